@@ -525,6 +525,137 @@ h3_status h3_linear_residual(const void* x, const void* w, float* resid, const f
                      reinterpret_cast<cudaStream_t>(stream), &ex);
 }
 
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The checks of h3_kv_cache and h3_kv_batch that all paged calls share.
+static h3_status check_paged(const h3_kv_cache* c, const h3_kv_batch* b, PagedBatch* out) {
+  H3_REQUIRE(c != nullptr && b != nullptr, H3_ERR_INVALID_ARG, "cache or batch is NULL");
+  H3_REQUIRE(c->k != nullptr && c->v != nullptr, H3_ERR_INVALID_ARG, "a cache pointer is NULL");
+  H3_REQUIRE(c->Dh == 128, H3_ERR_UNSUPPORTED, "head_dim %d unsupported (128 only)", c->Dh);
+  H3_REQUIRE(c->page_size == 16 || c->page_size == 32 || c->page_size == 64 || c->page_size == 128,
+             H3_ERR_UNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", c->page_size);
+  H3_REQUIRE(c->num_pages > 0 && c->Hkv > 0, H3_ERR_INVALID_ARG, "num_pages=%d, Hkv=%d",
+             c->num_pages, c->Hkv);
+  H3_REQUIRE(static_cast<int64_t>(c->num_pages) * c->page_size <= 0x7fffffff / c->Hkv,
+             H3_ERR_UNSUPPORTED, "num_pages * Hkv * page_size must be below 2^31");
+  H3_REQUIRE(aligned16(c->k) && aligned16(c->v), H3_ERR_MISALIGNED,
+             "the cache must be 16-byte aligned");
+  H3_REQUIRE(b->T >= 0 && b->B >= 0 && b->max_pages >= 0, H3_ERR_INVALID_ARG,
+             "negative size (T=%d, B=%d, max_pages=%d)", b->T, b->B, b->max_pages);
+  H3_REQUIRE(b->max_pages <= 0x7fffffff / c->page_size, H3_ERR_UNSUPPORTED,
+             "max_pages * page_size must be below 2^31");
+  H3_REQUIRE(b->B <= 65536, H3_ERR_UNSUPPORTED, "B=%d exceeds 65536 sequences", b->B);
+  H3_REQUIRE(b->T == 0 || b->B == 0 ||
+                 (b->cu_q != nullptr && b->kv_len != nullptr &&
+                  (b->page_table != nullptr || b->max_pages == 0)),
+             H3_ERR_INVALID_ARG, "cu_q, kv_len or page_table is NULL");
+  H3_REQUIRE(aligned4(b->cu_q) && aligned4(b->kv_len) && aligned4(b->page_table),
+             H3_ERR_MISALIGNED, "cu_q, kv_len and page_table must be 4-byte aligned");
+  int log2 = 4;
+  while ((1 << log2) < c->page_size) ++log2;
+  *out = PagedBatch{b->T, b->B, b->max_pages, c->num_pages, log2, b->cu_q, b->kv_len,
+                    b->page_table};
+  return H3_OK;
+}
+
+// A [T, H, 128] bf16 tensor with a row stride.
+static h3_status check_strided(const char* name, const void* p, int64_t ld, int64_t H) {
+  H3_REQUIRE(p != nullptr, H3_ERR_INVALID_ARG, "%s is NULL", name);
+  H3_REQUIRE(aligned16(p) && ld % 8 == 0, H3_ERR_MISALIGNED,
+             "%s and its row stride (%lld elements) must be 16-byte aligned", name,
+             static_cast<long long>(ld));
+  H3_REQUIRE(ld >= H * 128, H3_ERR_INVALID_ARG, "row stride %lld of %s is below its %lld elements",
+             static_cast<long long>(ld), name, static_cast<long long>(H * 128));
+  H3_REQUIRE(ld < (int64_t{1} << 31), H3_ERR_UNSUPPORTED, "row stride of %s is 2^31 or more", name);
+  return H3_OK;
+}
+
+h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                             const void* v, int64_t ld_v, void* q_out, int H, const float* q_gain,
+                             const float* k_gain, const int32_t* pos, const int* axis_dims,
+                             int pairing, float theta, float eps, const h3_kv_cache* cache,
+                             const h3_kv_batch* batch, h3_stream_t stream) {
+  clear_error();
+  PagedBatch b;
+  h3_status st = check_paged(cache, batch, &b);
+  if (st != H3_OK) return st;
+  H3_REQUIRE(H >= 0, H3_ERR_INVALID_ARG, "H=%d", H);
+  H3_REQUIRE(H <= 65535 && cache->Hkv <= 65535, H3_ERR_UNSUPPORTED, "H=%d, Hkv=%d exceed 65535", H,
+             cache->Hkv);
+  if ((st = check_axis_dims(axis_dims)) != H3_OK) return st;
+  if ((st = check_pairing(axis_dims, pairing)) != H3_OK) return st;
+  H3_REQUIRE(theta >= 1.f && eps >= 0.f, H3_ERR_INVALID_ARG, "theta must be >= 1 and eps >= 0");
+  if (b.T == 0 || b.B == 0) return H3_OK;
+  H3_REQUIRE((q == nullptr) == (q_out == nullptr), H3_ERR_INVALID_ARG,
+             "q and q_out come together");
+  H3_REQUIRE(q != nullptr ? H > 0 : H == 0, H3_ERR_INVALID_ARG, "H=%d query heads %s q", H,
+             q != nullptr ? "with" : "without");
+  if (q != nullptr) {
+    if ((st = check_strided("q", q, ld_q, H)) != H3_OK) return st;
+    H3_REQUIRE(aligned16(q_out), H3_ERR_MISALIGNED, "q_out must be 16-byte aligned");
+    H3_REQUIRE(q != q_out || ld_q == static_cast<int64_t>(H) * 128, H3_ERR_INVALID_ARG,
+               "q_out is q, but q has a row stride");
+  }
+  if ((st = check_strided("k", k, ld_k, cache->Hkv)) != H3_OK) return st;
+  if ((st = check_strided("v", v, ld_v, cache->Hkv)) != H3_OK) return st;
+  H3_REQUIRE(pos != nullptr, H3_ERR_INVALID_ARG, "pos is NULL");
+  H3_REQUIRE(q == nullptr || (q_gain == nullptr) == (k_gain == nullptr), H3_ERR_INVALID_ARG,
+             "q_gain and k_gain come together");
+  H3_REQUIRE(aligned16(q_gain) && aligned16(k_gain) && aligned4(pos), H3_ERR_MISALIGNED,
+             "the gains must be 16-byte, pos 4-byte aligned");
+  return launch_kv_append(q, ld_q, k, ld_k, v, ld_v, q_out, H, q_gain, k_gain, pos, axis_dims,
+                          pairing, theta, eps, cache->k, cache->v, cache->Hkv, b,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t h3_attention_paged_workspace_bytes(int T, int H, int prefix_len) {
+  clear_error();
+  if (T < 0 || H <= 0 || prefix_len < 0) {
+    fail(H3_ERR_INVALID_ARG, "T=%d, H=%d, prefix_len=%d", T, H, prefix_len);
+    return 0;
+  }
+  return paged_workspace_bytes(T, H, prefix_len);
+}
+
+h3_status h3_attention_paged_prefix(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
+                                    float softmax_scale, int causal, const h3_kv_cache* cache,
+                                    const h3_kv_batch* batch, const int32_t* prefix_pages,
+                                    int prefix_len, void* workspace, size_t workspace_bytes,
+                                    h3_stream_t stream) {
+  clear_error();
+  PagedBatch b;
+  h3_status st = check_paged(cache, batch, &b);
+  if (st != H3_OK) return st;
+  H3_REQUIRE(H > 0 && H % cache->Hkv == 0, H3_ERR_INVALID_ARG, "H=%d is no multiple of Hkv=%d", H,
+             cache->Hkv);
+  H3_REQUIRE(H <= 65535 && H / cache->Hkv <= 128, H3_ERR_UNSUPPORTED,
+             "H=%d heads on Hkv=%d: at most 128 per key head", H, cache->Hkv);
+  H3_REQUIRE(softmax_scale > 0.f, H3_ERR_INVALID_ARG, "softmax_scale must be > 0");
+  H3_REQUIRE(prefix_len >= 0, H3_ERR_INVALID_ARG, "prefix_len=%d", prefix_len);
+  if (b.T == 0 || b.B == 0) return H3_OK;
+  if ((st = check_strided("q", q, ld_q, H)) != H3_OK) return st;
+  if ((st = check_strided("o", o, ld_o, H)) != H3_OK) return st;
+  H3_REQUIRE(prefix_len == 0 || prefix_pages != nullptr, H3_ERR_INVALID_ARG,
+             "prefix_len=%d without prefix_pages", prefix_len);
+  H3_REQUIRE(aligned4(prefix_pages), H3_ERR_MISALIGNED, "prefix_pages must be 4-byte aligned");
+  const size_t need = paged_workspace_bytes(b.T, H, prefix_len);
+  H3_REQUIRE(workspace != nullptr && workspace_bytes >= need, H3_ERR_WORKSPACE,
+             "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  H3_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, H3_ERR_MISALIGNED,
+             "workspace must be 256-byte aligned");
+  return launch_paged_attention(q, ld_q, o, ld_o, H, softmax_scale, causal != 0, cache->k,
+                                cache->v, cache->Hkv, b, prefix_pages, prefix_len, workspace,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+h3_status h3_attention_paged(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
+                             float softmax_scale, int causal, const h3_kv_cache* cache,
+                             const h3_kv_batch* batch, void* workspace, size_t workspace_bytes,
+                             h3_stream_t stream) {
+  return h3_attention_paged_prefix(q, ld_q, o, ld_o, H, softmax_scale, causal, cache, batch,
+                                   nullptr, 0, workspace, workspace_bytes, stream);
+}
+
 static h3_status check_block_config(const h3_block_config* c) {
   H3_REQUIRE(c != nullptr, H3_ERR_INVALID_ARG, "config is NULL");
   h3_status st = check_rows(c->S, c->L);

@@ -162,4 +162,29 @@ h3_status launch_attention_fp8(const void* qc, const void* kc, const void* vc, i
                                int64_t ld_out, int L, int H, float scale, cudaStream_t s,
                                float skip_eps = -1.f, int* kept = nullptr);
 
+// ---- paged key/value cache (h3_paged.cu)
+// Rows and pages of one call (device arrays; see h3_kv_batch).
+struct PagedBatch {
+  int T, B;
+  int max_pages;
+  int num_pages, page_log2;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+};
+// q (optional, with q_out), k, v: rows of ld elements; pairing as
+// launch_qk_norm_rope; gains NULL: rotation only.
+h3_status launch_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                           int64_t ld_v, void* q_out, int H, const float* q_gain,
+                           const float* k_gain, const int32_t* pos, const int* axis_dims,
+                           int pairing, float theta, float eps, void* k_cache, void* v_cache,
+                           int Hkv, const PagedBatch& batch, cudaStream_t s);
+// prefix_len keys in prefix_pages (or 0) come before every sequence's own.
+size_t paged_workspace_bytes(int T, int H, int prefix_len);
+h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
+                                 float scale, bool causal, const void* k_cache,
+                                 const void* v_cache, int Hkv, const PagedBatch& batch,
+                                 const int32_t* prefix_pages, int prefix_len, void* workspace,
+                                 cudaStream_t s);
+
 }  // namespace h3

@@ -51,7 +51,19 @@ class BlockWeights(ctypes.Structure):
                 ("k_gain", ctypes.c_void_p)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("Dh", ctypes.c_int)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("B", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
 _P, _I, _F, _U64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64, ctypes.c_size_t
+_I64 = ctypes.c_int64
 _SIGS = {
     "h3_version": (_I, []),
     "h3_last_error": (ctypes.c_char_p, []),
@@ -91,6 +103,12 @@ _SIGS = {
     "h3_block_workspace_bytes_fp8": (_SZ, [ctypes.POINTER(BlockConfig)]),
     "h3_block_forward_fp8": (_I, [ctypes.POINTER(BlockConfig), ctypes.POINTER(BlockWeightsFp8),
                                   _P, _P, _P, _I, _P, _SZ, _P]),
+    "h3_kv_append_paged": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I, _P, _P, _P, _P, _I, _F, _F,
+                                _P, _P, _P]),
+    "h3_attention_paged_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "h3_attention_paged": (_I, [_P, _I64, _P, _I64, _I, _F, _I, _P, _P, _P, _SZ, _P]),
+    "h3_attention_paged_prefix": (_I, [_P, _I64, _P, _I64, _I, _F, _I, _P, _P, _P, _I, _P, _SZ,
+                                       _P]),
     "h3_stack_forward": (_I, [ctypes.POINTER(BlockConfig), ctypes.POINTER(BlockWeights), _I, _P,
                               _P, _I, _P, _P, _P, _SZ, _P]),
 }
@@ -288,6 +306,131 @@ def attention_fp8_skip(ops: dict, o, L=None, scale=None, skip_eps=0.0, kept=None
     _check("attention_fp8_skip", lib().h3_attention_fp8_skip(
         _p(ops["qc"]), _p(ops["kc"]), _p(ops["vc"]), _p(ops["sq"]), _p(ops["sk"]),
         _p(ops["sv"]), _p(o), S, L, H, Dh, scale, skip_eps, _p(kept), _s(stream)))
+
+
+def _on_current_device(t, name):
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, is on {t.device}")
+
+
+def _heads(t, name, T=None):
+    """Pointer, row stride and heads of a [T, heads, 128] bf16 tensor whose
+    rows may be strided (columns of a merged projection's output)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != 128 or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} must be [{'T' if T is None else T}, heads, 128], "
+                         f"got {list(t.shape)}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    _on_current_device(t, name)
+    heads = t.shape[1]
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * 128), heads
+
+
+def kv_cache(k, v) -> KvCache:
+    """A paged key/value cache on k, v [num_pages, Hkv, page_size, 128] bf16,
+    for kv_append_paged and attention_paged; it holds on to both tensors."""
+    for n, t in (("k", k), ("v", v)):
+        _need(t, torch.bfloat16, n)
+        _on_current_device(t, n)
+    if k.dim() != 4 or k.shape != v.shape:
+        raise ValueError(f"k and v must both be [num_pages, Hkv, page_size, 128], got "
+                         f"{list(k.shape)} and {list(v.shape)}")
+    c = KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], k.shape[1], k.shape[3])
+    c.tensors = (k, v)
+    return c
+
+
+def kv_batch(cu_q, kv_len, page_table, T: int) -> KvBatch:
+    """The rows of a call (T of them, sequence b's being [cu_q[b], cu_q[b+1]))
+    and their sequences: cu_q [B+1], kv_len [B] (with the call's rows in it),
+    page_table [B, max_pages], int32 on the device. It holds on to the tensors,
+    whose values are read when a call runs; one batch serves every layer."""
+    for n, t in (("cu_q", cu_q), ("kv_len", kv_len), ("page_table", page_table)):
+        _need(t, torch.int32, n)
+        _on_current_device(t, n)
+    B = kv_len.shape[0]
+    if cu_q.shape != (B + 1,) or kv_len.dim() != 1 or page_table.dim() != 2 \
+            or page_table.shape[0] != B:
+        raise ValueError(f"cu_q [B+1], kv_len [B], page_table [B, max_pages] wanted, got "
+                         f"{list(cu_q.shape)}, {list(kv_len.shape)}, {list(page_table.shape)}")
+    b = KvBatch(T, B, page_table.shape[1], cu_q.data_ptr(), kv_len.data_ptr(),
+                page_table.data_ptr())
+    b.tensors = (cu_q, kv_len, page_table)
+    return b
+
+
+def kv_append_paged(q, k, v, q_out, cache: KvCache, batch: KvBatch, pos, axis_dims, q_gain=None,
+                    k_gain=None, theta=1e4, eps=1e-6, pairing=0, stream=None):
+    """q_out <- RoPE(RMSNorm(q)); the rows' places in the cache get
+    RoPE(RMSNorm(k)) and v. q [T,H,128], k, v [T,Hkv,128] bf16 (rows may be
+    strided), q_out [T,H,128] contiguous (q and q_out None: cache only), pos
+    [T,3] int32, gains [128] f32 (None: no norm)."""
+    T, H, pq, ldq = batch.T, 0, None, 0
+    if q is not None:
+        pq, ldq, H = _heads(q, "q", T)
+        _need(q_out, torch.bfloat16, "q_out")
+        if q_out is None or q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        _on_current_device(q_out, "q_out")
+    pk, ldk, hk = _heads(k, "k", T)
+    pv, ldv, hv = _heads(v, "v", T)
+    if hk != cache.Hkv or hv != cache.Hkv:
+        raise ValueError(f"k and v have {hk} and {hv} heads, the cache {cache.Hkv}")
+    _need(pos, torch.int32, "pos")
+    if pos.shape != (T, 3):
+        raise ValueError(f"pos must be [{T}, 3], got {list(pos.shape)}")
+    _on_current_device(pos, "pos")
+    for n, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if g is not None:
+            _need(g, torch.float32, n)
+            _on_current_device(g, n)
+            if g.numel() != 128:
+                raise ValueError(f"{n} must have 128 values")
+    ax = (ctypes.c_int * 3)(*axis_dims)
+    _check("kv_append_paged", lib().h3_kv_append_paged(
+        pq, ldq, pk, ldk, pv, ldv, None if q_out is None else q_out.data_ptr(), H, _p(q_gain),
+        _p(k_gain), pos.data_ptr(), ctypes.addressof(ax), pairing, theta, eps,
+        ctypes.addressof(cache), ctypes.addressof(batch), _s(stream)))
+
+
+def attention_paged_workspace_bytes(T: int, H: int, prefix_len: int = 0) -> int:
+    n = lib().h3_attention_paged_workspace_bytes(T, H, prefix_len)
+    if n == 0:
+        raise H3Error("attention_paged_workspace_bytes", 1, last_error())
+    return n
+
+
+def attention_paged(q, o, cache: KvCache, batch: KvBatch, workspace, scale=None, causal=False,
+                    stream=None):
+    """o = softmax(q k^T * scale) v over the keys of every row's own sequence
+    (causal: those up to the row itself); q, o [T,H,128] bf16, rows may be
+    strided; workspace: device tensor of attention_paged_workspace_bytes."""
+    attention_paged_prefix(q, o, cache, batch, None, 0, workspace, scale, causal, stream)
+
+
+def attention_paged_prefix(q, o, cache: KvCache, batch: KvBatch, prefix_pages, prefix_len: int,
+                           workspace, scale=None, causal=False, stream=None):
+    """attention_paged with prefix_len keys in prefix_pages (int32) before the
+    own keys of every sequence, read once for the whole batch."""
+    pq, ldq, H = _heads(q, "q", batch.T)
+    po, ldo, Ho = _heads(o, "o", batch.T)
+    if Ho != H:
+        raise ValueError(f"q has {H} heads, o {Ho}")
+    if prefix_pages is not None:
+        _need(prefix_pages, torch.int32, "prefix_pages")
+        _on_current_device(prefix_pages, "prefix_pages")
+        if prefix_pages.numel() * cache.page_size < prefix_len:
+            raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of "
+                             f"{cache.page_size} keys, prefix_len is {prefix_len}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on_current_device(workspace, "workspace")
+    _check("attention_paged_prefix", lib().h3_attention_paged_prefix(
+        pq, ldq, po, ldo, H, 128 ** -0.5 if scale is None else scale, int(causal),
+        ctypes.addressof(cache), ctypes.addressof(batch), _p(prefix_pages), prefix_len,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _s(stream)))
 
 
 def swiglu(gate_up, out, L=None, stream=None):

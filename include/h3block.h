@@ -215,6 +215,110 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
                                 h3_stream_t stream);
 
 /*
+ * Paged key/value cache. The block reads keys and values of its own rows only
+ * (blog section 3.1); a server that keeps the keys and values of finished rows
+ * (prompt, reference and finished frames) over calls writes each call's rows
+ * to a cache and lets them read it. The three calls below take the same two
+ * descriptions.
+ *
+ * h3_kv_cache: the pool of pages of one layer, caller-owned.
+ *   k, v  [num_pages, Hkv, page_size, Dh] bf16
+ *   page_size 16, 32, 64 or 128; Dh == 128; num_pages * Hkv * page_size < 2^31
+ * h3_kv_batch: the rows of one call and where their sequences' keys lie.
+ *   T           rows of the call's q, k, v and o tensors; a call with T or B
+ *               0 does nothing (its row tensors and workspace may be NULL)
+ *   B           sequences, at most 65,536; rows [cu_q[b], cu_q[b+1]) belong to sequence b
+ *   cu_q        [B + 1] int32 device, non-decreasing, 0 <= cu_q[b] <= T; rows
+ *               outside [cu_q[0], cu_q[B]) are neither read nor written
+ *   kv_len      [B] int32 device: keys of sequence b with the call's rows in
+ *               it, so row i of its q_len rows is key kv_len[b] - q_len + i
+ *   page_table  [B, max_pages] int32 device: key j of sequence b is row
+ *               j % page_size of page page_table[b, j / page_size]
+ * The arrays are read on the device when the call runs, so a captured call
+ * replays with the lengths and pages that they hold then. What they hold is
+ * bounded there: a key index at or beyond max_pages * page_size or below 0 has
+ * no place (appending it writes nothing; lengths are taken as at most that),
+ * and a page outside [0, num_pages) is never touched (appending to it writes
+ * nothing; its keys and values read as zeros). Keys at and beyond kv_len may
+ * hold anything; keys below it must be finite.
+ */
+typedef struct h3_kv_cache {
+  void* k;
+  void* v;
+  int num_pages;
+  int page_size;
+  int Hkv;
+  int Dh;
+} h3_kv_cache;
+
+typedef struct h3_kv_batch {
+  int T;
+  int B;
+  int max_pages;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+} h3_kv_batch;
+
+/*
+ * a2 with the keys and values going to the cache in the same pass: for every
+ * row of a sequence, q_out <- RoPE(RMSNorm(q)) per head, and the row's place
+ * in the cache (see h3_kv_batch) gets RoPE(RMSNorm(k)) and v, as
+ * h3_qk_norm_rope_layout computes them and with one rounding to bf16.
+ *   q       [T, H, Dh] bf16, row stride ld_q elements, or NULL (then q_out is
+ *           NULL too, H is 0 and only the cache is written)
+ *   k, v    [T, Hkv, Dh] bf16, row strides ld_k, ld_v; q, k and v may be
+ *           columns of one [T, ld] buffer. Strides are multiples of 8.
+ *   q_out   [T, H, Dh] bf16 contiguous; may be q itself when ld_q == H * Dh,
+ *           else it does not overlap the inputs
+ *   q_gain, k_gain [Dh] float32, or both NULL: rotation without a norm
+ *   pos     [T, 3] int32; axis_dims, pairing, eps as h3_qk_norm_rope_layout;
+ *           theta >= 1
+ * Two rows of a call must not have the same place (sequences that are written
+ * to share no page); the cache does not overlap q, k, v or q_out.
+ */
+h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                             const void* v, int64_t ld_v, void* q_out, int H, const float* q_gain,
+                             const float* k_gain, const int32_t* pos, const int* axis_dims,
+                             int pairing, float theta, float eps, const h3_kv_cache* cache,
+                             const h3_kv_batch* batch, h3_stream_t stream);
+
+/*
+ * a3 over the cache: for every row i of sequence b and head h, with
+ * g = h / (H / Hkv),
+ *   o[row,h,:] = sum_j softmax_j(q[row,h,:] . k[b,j,g,:] * softmax_scale) v[b,j,g,:]
+ * over the keys j < kv_len[b], and with causal != 0 only those with
+ * j <= kv_len[b] - q_len + i (the row itself and what came before it). A row
+ * without any such key gives zeros.
+ *   q, o   [T, H, Dh] bf16, row strides ld_q, ld_o (multiples of 8); H a
+ *          multiple of cache->Hkv, at most 128 heads per key head
+ *   workspace  device memory of h3_attention_paged_workspace_bytes(T, H, 0)
+ *          bytes, 256-byte aligned, overwritten by the call; calls that may
+ *          overlap on the GPU need one each
+ * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out.
+ */
+size_t h3_attention_paged_workspace_bytes(int T, int H, int prefix_len);
+h3_status h3_attention_paged(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
+                             float softmax_scale, int causal, const h3_kv_cache* cache,
+                             const h3_kv_batch* batch, void* workspace, size_t workspace_bytes,
+                             h3_stream_t stream);
+
+/*
+ * h3_attention_paged for a batch whose sequences share their first prefix_len
+ * keys: every row sees all of them (causal or not), then its own sequence's
+ * keys as above (kv_len counts those only). The prefix's keys and values are
+ * read once for the rows of all sequences together.
+ *   prefix_pages [ceil(prefix_len / page_size)] int32 device, as a row of
+ *          page_table; may be NULL when prefix_len is 0
+ *   workspace  of h3_attention_paged_workspace_bytes(T, H, prefix_len) bytes
+ */
+h3_status h3_attention_paged_prefix(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
+                                    float softmax_scale, int causal, const h3_kv_cache* cache,
+                                    const h3_kv_batch* batch, const int32_t* prefix_pages,
+                                    int prefix_len, void* workspace, size_t workspace_bytes,
+                                    h3_stream_t stream);
+
+/*
  * a5 — SwiGLU (blog section 3.2, #6283): out[i,j] = SiLU(g) * u with
  * g = gate_up[i,j], u = gate_up[i,F+j], SiLU(g) = g / (1 + exp(-g)), for i < L.
  *   gate_up [S, 2F] bf16, out [S, F] bf16. F % 8 == 0.
