@@ -131,9 +131,7 @@ h3_status make_tmap_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint
                       box_inner, box_outer);
 }
 
-static h3_status make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base,
-                              uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
-                              uint32_t box_inner, uint32_t box_outer) {
+static h3_status load_encode() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -144,6 +142,14 @@ static h3_status make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void
   });
   if (g_encode == nullptr)
     return fail(H3_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  return H3_OK;
+}
+
+static h3_status make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base,
+                              uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
+                              uint32_t box_inner, uint32_t box_outer) {
+  h3_status st = load_encode();
+  if (st != H3_OK) return st;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {row_stride_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
@@ -157,6 +163,27 @@ static h3_status make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void
                 static_cast<int>(r), static_cast<unsigned long long>(inner),
                 static_cast<unsigned long long>(outer),
                 static_cast<unsigned long long>(row_stride_bytes));
+  return H3_OK;
+}
+
+h3_status make_tmap_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1,
+                            uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1,
+                            uint32_t b2) {
+  h3_status st = load_encode();
+  if (st != H3_OK) return st;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {s1, s2};
+  const cuuint32_t box[3] = {b0, b1, b2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(H3_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llux%llux%llu stride %llu",
+                static_cast<int>(r), static_cast<unsigned long long>(d0),
+                static_cast<unsigned long long>(d1), static_cast<unsigned long long>(d2),
+                static_cast<unsigned long long>(s2));
   return H3_OK;
 }
 
@@ -542,8 +569,8 @@ static h3_status check_paged(const h3_kv_cache* c, const h3_kv_batch* b, PagedBa
              "the cache must be 16-byte aligned");
   H3_REQUIRE(b->T >= 0 && b->B >= 0 && b->max_pages >= 0, H3_ERR_INVALID_ARG,
              "negative size (T=%d, B=%d, max_pages=%d)", b->T, b->B, b->max_pages);
-  H3_REQUIRE(b->max_pages <= 0x7fffffff / c->page_size, H3_ERR_UNSUPPORTED,
-             "max_pages * page_size must be below 2^31");
+  H3_REQUIRE(b->max_pages <= (1 << 30) / c->page_size, H3_ERR_UNSUPPORTED,
+             "max_pages * page_size must be at most 2^30");
   H3_REQUIRE(b->B <= 65536, H3_ERR_UNSUPPORTED, "B=%d exceeds 65536 sequences", b->B);
   H3_REQUIRE(b->T == 0 || b->B == 0 ||
                  (b->cu_q != nullptr && b->kv_len != nullptr &&
@@ -632,6 +659,9 @@ h3_status h3_attention_paged_prefix(const void* q, int64_t ld_q, void* o, int64_
              "H=%d heads on Hkv=%d: at most 128 per key head", H, cache->Hkv);
   H3_REQUIRE(softmax_scale > 0.f, H3_ERR_INVALID_ARG, "softmax_scale must be > 0");
   H3_REQUIRE(prefix_len >= 0, H3_ERR_INVALID_ARG, "prefix_len=%d", prefix_len);
+  H3_REQUIRE(prefix_len <= (1 << 30) && static_cast<int64_t>(b.T) * H <= (1 << 29),
+             H3_ERR_UNSUPPORTED, "prefix_len=%d exceeds 2^30 or T * H=%lld exceeds 2^29",
+             prefix_len, static_cast<long long>(b.T) * H);
   if (b.T == 0 || b.B == 0) return H3_OK;
   if ((st = check_strided("q", q, ld_q, H)) != H3_OK) return st;
   if ((st = check_strided("o", o, ld_o, H)) != H3_OK) return st;

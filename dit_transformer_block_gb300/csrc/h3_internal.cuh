@@ -46,6 +46,12 @@ h3_status make_tmap_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, ui
 h3_status make_tmap_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// A 3D bf16 tensor [d2, d1, d0] with row strides s1 and s2 in bytes, boxes of
+// b2 x b1 x b0, otherwise the same.
+h3_status make_tmap_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1,
+                            uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1,
+                            uint32_t b2);
+
 // ---- kernel launchers (arguments already validated)
 h3_status launch_swiglu(const void* gate_up, void* out, int L, int F, cudaStream_t s);
 // pairing: 0 interleaved pairs (2j, 2j + 1), 1 split-half pairs
@@ -162,7 +168,7 @@ h3_status launch_attention_fp8(const void* qc, const void* kc, const void* vc, i
                                int64_t ld_out, int L, int H, float scale, cudaStream_t s,
                                float skip_eps = -1.f, int* kept = nullptr);
 
-// ---- paged key/value cache (h3_paged.cu)
+// ---- paged key/value cache (h3_paged.cu, h3_paged_attention.cu)
 // Rows and pages of one call (device arrays; see h3_kv_batch).
 struct PagedBatch {
   int T, B;

@@ -1,5 +1,5 @@
-// Paged key/value cache: writing the rows of a call to it (with Q/K RMSNorm
-// and RoPE on the way) and attention of a ragged batch over it.
+// Paged key/value cache: writing the rows of a call to it, with Q/K RMSNorm and
+// RoPE on the way.
 //
 // A cache holds pages of `page` keys (a power of two from 16 to 128), laid out
 // [pages, Hkv, page, 128]: the keys of one page and head are one contiguous
@@ -178,70 +178,6 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32)
   }
 }
 
-// --------------------------------------------------------------- attention
-// One warp per (row, head), four channels per lane, the keys one after the
-// other with the running maximum and sum of an online softmax.
-struct PagedAttnArgs {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
-  __nv_bfloat16* o;
-  int64_t ld_q, ld_o;
-  int H, Hkv;
-  float scale_log2;
-  int causal;
-  const int32_t* prefix_pages;
-  int prefix_len;
-  PagedBatch b;
-};
-
-__global__ void __launch_bounds__(256) paged_attention_rows_kernel(const PagedAttnArgs a) {
-  const int64_t w = blockIdx.x * 8LL + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= static_cast<int64_t>(a.b.T) * a.H) return;
-  const int row = static_cast<int>(w / a.H), h = static_cast<int>(w % a.H);
-  const SeqRow s = find_row(a.b.cu_q, a.b.B, row);
-  if (s.b < 0) return;
-  const int hk = h / (a.H / a.Hkv);
-  const uint2 qw = *reinterpret_cast<const uint2*>(a.q + row * a.ld_q + h * DHP + lane * 4);
-  const float q0 = bf16_lo(qw.x), q1 = bf16_hi(qw.x), q2 = bf16_lo(qw.y), q3 = bf16_hi(qw.y);
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-  auto keys = [&](const int32_t* pages, int n) {
-    for (int j = 0; j < n; ++j) {
-      const int page = __ldg(pages + (j >> a.b.page_log2));
-      uint2 kw = make_uint2(0, 0), vw = make_uint2(0, 0);
-      if (page >= 0 && page < a.b.num_pages) {
-        const int64_t at = (((static_cast<int64_t>(page) * a.Hkv + hk) << a.b.page_log2) +
-                            (j & ((1 << a.b.page_log2) - 1))) * DHP + lane * 4;
-        kw = *reinterpret_cast<const uint2*>(a.k + at);
-        vw = *reinterpret_cast<const uint2*>(a.v + at);
-      }
-      float z = q0 * bf16_lo(kw.x) + q1 * bf16_hi(kw.x) + q2 * bf16_lo(kw.y) + q3 * bf16_hi(kw.y);
-#pragma unroll
-      for (int x = 16; x >= 1; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-      z *= a.scale_log2;
-      const float mn = fmaxf(m, z);
-      const float c = exp2f(m - mn), p = exp2f(z - mn);
-      m = mn;
-      l = l * c + p;
-      o0 = o0 * c + p * bf16_lo(vw.x);
-      o1 = o1 * c + p * bf16_hi(vw.x);
-      o2 = o2 * c + p * bf16_lo(vw.y);
-      o3 = o3 * c + p * bf16_hi(vw.y);
-    }
-  };
-  if (a.prefix_len > 0) keys(a.prefix_pages, a.prefix_len);
-  const int64_t cap = static_cast<int64_t>(a.b.max_pages) << a.b.page_log2;
-  const int64_t len = min(max(static_cast<int64_t>(__ldg(a.b.kv_len + s.b)), int64_t{0}), cap);
-  int64_t lim = len;
-  if (a.causal)
-    lim = min(len, max(static_cast<int64_t>(__ldg(a.b.kv_len + s.b)) - s.q_len + s.i + 1, int64_t{0}));
-  keys(a.b.page_table + static_cast<int64_t>(s.b) * a.b.max_pages, static_cast<int>(lim));
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(a.o + row * a.ld_o + h * DHP + lane * 4) =
-      make_uint2(pack_bf16x2(o0 * inv, o1 * inv), pack_bf16x2(o2 * inv, o3 * inv));
-}
-
 }  // namespace
 
 h3_status launch_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
@@ -279,32 +215,6 @@ h3_status launch_kv_append(const void* q, int64_t ld_q, const void* k, int64_t l
   else
     kv_append_kernel<false, U><<<static_cast<int>(blocks), APPEND_WARPS * 32, 0, s>>>(a, tab);
   return cuda_fail(cudaGetLastError(), "kv_append_paged launch");
-}
-
-size_t paged_workspace_bytes(int T, int H, int prefix_len) { return 16; }
-
-h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
-                                 float scale, bool causal, const void* k_cache,
-                                 const void* v_cache, int Hkv, const PagedBatch& batch,
-                                 const int32_t* prefix_pages, int prefix_len, void* workspace,
-                                 cudaStream_t s) {
-  PagedAttnArgs a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k = static_cast<const __nv_bfloat16*>(k_cache);
-  a.v = static_cast<const __nv_bfloat16*>(v_cache);
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.ld_q = ld_q;
-  a.ld_o = ld_o;
-  a.H = H;
-  a.Hkv = Hkv;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.causal = causal;
-  a.prefix_pages = prefix_pages;
-  a.prefix_len = prefix_len;
-  a.b = batch;
-  const int64_t blocks = (static_cast<int64_t>(batch.T) * H + 7) / 8;
-  paged_attention_rows_kernel<<<static_cast<int>(blocks), 256, 0, s>>>(a);
-  return cuda_fail(cudaGetLastError(), "paged attention launch");
 }
 
 }  // namespace h3

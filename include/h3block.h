@@ -233,7 +233,8 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
  *   kv_len      [B] int32 device: keys of sequence b with the call's rows in
  *               it, so row i of its q_len rows is key kv_len[b] - q_len + i
  *   page_table  [B, max_pages] int32 device: key j of sequence b is row
- *               j % page_size of page page_table[b, j / page_size]
+ *               j % page_size of page page_table[b, j / page_size];
+ *               max_pages * page_size at most 2^30
  * The arrays are read on the device when the call runs, so a captured call
  * replays with the lengths and pages that they hold then. What they hold is
  * bounded there: a key index at or beyond max_pages * page_size or below 0 has
@@ -291,7 +292,8 @@ h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t
  * j <= kv_len[b] - q_len + i (the row itself and what came before it). A row
  * without any such key gives zeros.
  *   q, o   [T, H, Dh] bf16, row strides ld_q, ld_o (multiples of 8); H a
- *          multiple of cache->Hkv, at most 128 heads per key head
+ *          multiple of cache->Hkv, at most 128 heads per key head; T * H at
+ *          most 2^29
  *   workspace  device memory of h3_attention_paged_workspace_bytes(T, H, 0)
  *          bytes, 256-byte aligned, overwritten by the call; calls that may
  *          overlap on the GPU need one each

@@ -144,7 +144,7 @@ def attend(h3lib, q, P, cu, causal=False, scale=None, o=None, ws=None, stream=No
     o = torch.full(q.shape, SENT, dtype=torch.bfloat16, device=dev) if o is None else o
     need = h3lib.attention_paged_workspace_bytes(T, q.shape[1], P.prefix)
     if ws is None:
-        ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=dev)
+        ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev)  # NaN floats
     c, b = h3lib.kv_cache(P.k, P.v), P.batch(h3lib, cu, T)
     if P.prefix:
         h3lib.attention_paged_prefix(q, o, c, b, P.prefix_pages, P.prefix, ws, scale, causal,

@@ -68,7 +68,7 @@ CACHE_AND_BATCH = [
     # 2^23 pages x 4 heads x 64 keys = 2^31 rows
     (dict(num_pages=1 << 23), {}, UNSUPPORTED),
     ({}, dict(T=-1), INVALID), ({}, dict(B=-1), INVALID), ({}, dict(max_pages=-1), INVALID),
-    ({}, dict(max_pages=1 << 25), UNSUPPORTED), ({}, dict(B=65537), UNSUPPORTED),
+    ({}, dict(max_pages=(1 << 24) + 1), UNSUPPORTED), ({}, dict(B=65537), UNSUPPORTED),
     ({}, dict(cu_q=None), INVALID), ({}, dict(kv_len=None), INVALID),
     ({}, dict(page_table=None), INVALID), ({}, dict(cu_q=A + 2), MISALIGNED),
 ]
@@ -87,7 +87,7 @@ def test_cache_and_batch_refusals(lib, c, b, want):
     (dict(ld_o=8 * 128 - 8), INVALID), (dict(ld_q=1 << 31), UNSUPPORTED),
     (dict(H=6), INVALID), (dict(H=0), INVALID), (dict(H=-4), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
-    (dict(prefix_len=-1), INVALID), (dict(prefix=NULL), INVALID), (dict(prefix=PM), MISALIGNED),
+    (dict(prefix_len=-1), INVALID), (dict(prefix_len=(1 << 30) + 1, bytes=1 << 50), UNSUPPORTED), (dict(prefix=NULL), INVALID), (dict(prefix=PM), MISALIGNED),
     (dict(ws=NULL), WORKSPACE), (dict(ws=ctypes.c_void_p(A + 16)), MISALIGNED),
 ])
 def test_attention_refusals(lib, kw, want):
@@ -97,6 +97,7 @@ def test_attention_refusals(lib, kw, want):
 def test_attention_workspace_and_group_limits(lib):
     need = lib.h3_attention_paged_workspace_bytes(6, 8, 100)
     assert attend(lib, bytes=need - 1) == WORKSPACE
+    assert attend(lib, b=batch(T=(1 << 26) + 1), bytes=1 << 50) == UNSUPPORTED  # T * H > 2^29
     # 129 query heads on one key head
     assert attend(lib, cache(Hkv=1), ld_q=129 * 128, ld_o=129 * 128, H=129,
                   bytes=1 << 40) == UNSUPPORTED
