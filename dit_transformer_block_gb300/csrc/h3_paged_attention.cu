@@ -12,7 +12,7 @@
 // and a second kernel joins the partials of each row. All lengths are read on
 // the device, so a captured call follows them.
 //
-// One CTA, 320 threads, the hand-off and tensor-memory layout of the FP8
+// One CTA, 384 threads (two warps idle), the hand-off and tensor-memory layout of the FP8
 // attention kernel:
 //   warp 8: walks the CTA's pieces of items, posts each in a ring in shared
 //     memory, and loads by TMA its query tiles and, key tile by key tile, K_t
@@ -34,6 +34,12 @@ constexpr int PA_SLOTS = 5;    // 32 KB each: K_t, V_t, K_t+1, ...
 constexpr int PA_PIECES = 8;   // pieces posted ahead
 constexpr int PA_MAX_CTAS = 160;
 constexpr int PA_CTRL_BYTES = 1024;
+// 12 warps: with three on each SM sub-partition the launch gives every thread
+// 168 registers; warps 8-11 hand most of theirs to the softmax warps, which
+// hold a row's 128 scores and 64 packed weights (168: 508 bytes of spills)
+constexpr int PA_THREADS = 384;
+constexpr int PA_REGS_SOFTMAX = 216, PA_REGS_OTHER = 72;
+static_assert(2 * PA_REGS_SOFTMAX + PA_REGS_OTHER <= 3 * 168, "registers of the launch");
 constexpr size_t PA_SMEM_BYTES = 1024 + (PA_SLOTS + 2) * TILE_BYTES + PA_CTRL_BYTES;
 static_assert(PA_SMEM_BYTES <= 227 * 1024, "paged attention shared memory");
 
@@ -213,7 +219,7 @@ __device__ __forceinline__ bool softmax_tile_paged(uint32_t (&sr)[128], uint32_t
   return true;
 }
 
-__global__ void __launch_bounds__(Q2_THREADS, 1)
+__global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PA_BARS + 1);
   Piece* ring = reinterpret_cast<Piece*>(ctrl + 384);                 // [PA_PIECES]
-  int64_t* warp_sum = reinterpret_cast<int64_t*>(ctrl + 640);         // [10]
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(ctrl + 640);         // [12]
   Share* share = reinterpret_cast<Share*>(ctrl + 736);                // [2]
   static_assert((PA_BARS + 1) * 8 + 16 <= 384 && 384 + PA_PIECES * 32 <= 640 &&
                     736 + 2 * sizeof(Share) <= PA_CTRL_BYTES,
@@ -255,7 +261,7 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
   const int first_seg = a.prefix_len > 0 ? 0 : 1;
   for (int seg = first_seg; seg < 2; ++seg) {
     const int n = seg == 0 ? 1 : a.b.B;
-    const int run = (n + Q2_THREADS - 1) / Q2_THREADS;
+    const int run = (n + PA_THREADS - 1) / PA_THREADS;
     const int b0 = min(static_cast<int>(threadIdx.x) * run, n), b1 = min(b0 + run, n);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += head_tiles(a, seg, seq_info(a, seg, b)) * a.Hkv;
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
     if (threadIdx.x == 0) share[seg] = Share{0, 0, 0, 0};
     __syncthreads();
     int64_t before = 0, W = 0;
-    for (int i = 0; i < Q2_THREADS / 32; ++i) {
+    for (int i = 0; i < PA_THREADS / 32; ++i) {
       if (i < warp) before += warp_sum[i];
       W += warp_sum[i];
     }
@@ -293,7 +299,8 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_REGS_OTHER));
   if (warp == 8) {
     // ------------------------------------------- pieces and TMA loads
     if (lane == 0) {
@@ -525,8 +532,10 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
     // frees them: commit and wait, bounded
     mma_commit_el(bar(PA_DRAIN));
     mbar_wait_drain(bar(PA_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(a.err));
+  }
   } else {
     // ---------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_REGS_SOFTMAX));
     const int tile = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -832,7 +841,7 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
       (st = make_tmap_bf16_2d(&tk, k_cache, DH, a.total_rows, DH * 2, 64, page)) != H3_OK ||
       (st = make_tmap_bf16_2d(&tv, v_cache, DH, a.total_rows, DH * 2, 64, page)) != H3_OK)
     return st;
-  paged_attention_kernel<<<a.ctas, Q2_THREADS, PA_SMEM_BYTES, s>>>(tq, tk, tv, a);
+  paged_attention_kernel<<<a.ctas, PA_THREADS, PA_SMEM_BYTES, s>>>(tq, tk, tv, a);
   if ((st = cuda_fail(cudaGetLastError(), "paged attention launch")) != H3_OK) return st;
   // the join kernel's blocks may take their places while the first kernel
   // runs; they wait for its end before they read anything
