@@ -12,11 +12,16 @@
 // and a second kernel joins the partials of each row. All lengths are read on
 // the device, so a captured call follows them.
 //
-// One CTA, 384 threads (two warps idle), the hand-off and tensor-memory layout of the FP8
-// attention kernel:
-//   warp 8: walks the CTA's pieces of items, posts each in a ring in shared
-//     memory, and loads by TMA its query tiles and, key tile by key tile, K_t
-//     and V_t (one box per page and 64 channels) into a ring of 32 KB slots;
+// Where a sequence has several items per key head, a team of CTAs takes
+// neighbouring ones over the same keys in step, so that a key tile comes from
+// HBM once for the team (pick_team).
+//
+// One CTA, 384 threads (warp 11 idle), the hand-off and tensor-memory layout
+// of the FP8 attention kernel:
+//   warp 10: walks the CTA's share and posts its pieces of items in a ring in
+//     shared memory, ahead of the others;
+//   warp 8: loads by TMA the pieces' query tiles and, key tile by key tile,
+//     K_t and V_t (one box per page and 64 channels) into a ring of 32 KB slots;
 //   warp 9: allocates TMEM and issues the products: S = Q_i K_t^T (SS) into
 //     one S buffer, O_i += P_i V_t (TS, P_i in tensor memory); Q K^T of the next
 //     key tile goes ahead of the P V of this one, also across pieces;
@@ -53,7 +58,7 @@ enum BarPA {
   PA_P = PA_SFREE + 2,         // P_i written (4 warp arrivals)
   PA_PVD = PA_P + 2,           // P_i V done (MMA commit)
   PA_PC_FULL = PA_PVD + 2,     // piece posted
-  PA_PC_EMPTY = PA_PC_FULL + PA_PIECES,  // piece read (8 softmax warps, MMA warp)
+  PA_PC_EMPTY = PA_PC_FULL + PA_PIECES,  // piece read (8 softmax warps, MMA warp, loads)
   PA_DRAIN = PA_PC_EMPTY + PA_PIECES,
   PA_BARS
 };
@@ -71,8 +76,11 @@ struct PagedArgs {
   const int32_t* prefix_pages;
   int prefix_len;
   // workspace
-  int64_t* totals;   // [2] key tiles of the two segments
-  int64_t* first;    // [T] tile offset of the sequence whose first row is t
+  int* teams;        // [2] CTAs per team of the two segments
+  int4* cut;         // [CTA] the item that goes on after the CTA's share: tok0, ntok (0: none),
+                     // key head, last CTA that has a part of it
+  int2* spread;      // with a prefix: [segment][T * Hkv] first and last CTA of the item that
+                     // begins with token t, at t * Hkv + key head
   float* part_o;     // split items: [slot][part_rows][128]
   float* part_ml;    // [slot][part_rows][2]
   int part_rows;
@@ -112,9 +120,11 @@ __device__ __forceinline__ int key_tiles(const SeqInfo& s, int end_tok) {
 
 __device__ __forceinline__ bool uneven(const PagedArgs& a, int seg) { return seg == 1 && a.causal; }
 
-// Key tiles of one key head of a sequence.
-__device__ __forceinline__ int64_t head_tiles(const PagedArgs& a, int seg, const SeqInfo& s) {
-  const int item = 2 * a.tok;
+// Key tiles of one key head of a sequence, for teams of g CTAs (the items of
+// a team run over as many as the one that sees most).
+__device__ __forceinline__ int64_t head_tiles(const PagedArgs& a, int seg, const SeqInfo& s,
+                                              int g) {
+  const int item = 2 * a.tok * g;
   const int n = (s.q_len + item - 1) / item;
   if (n == 0) return 0;
   if (!uneven(a, seg)) return static_cast<int64_t>(n) * key_tiles(s, s.q_len);
@@ -123,10 +133,25 @@ __device__ __forceinline__ int64_t head_tiles(const PagedArgs& a, int seg, const
   return sum;
 }
 
-// The CTAs' shares of a segment of W tiles: CTA c has [c W / n, (c + 1) W / n).
-__device__ __forceinline__ int64_t share_begin(int64_t W, int n, int c) { return c * W / n; }
-__device__ __forceinline__ int share_of(int64_t W, int n, int64_t w) {
-  return static_cast<int>(((w + 1) * n - 1) / W);
+// Team size for a segment whose tiles for teams of g are W[g - 1]: the least
+// time, with a tile of a lone CTA at 6 and of a team's at 5. A 64 KB key tile
+// takes a CTA about 2,300 cycles of products for two query tiles; read from
+// HBM by every CTA for itself it takes about 2,800.
+constexpr int PA_MAX_TEAM = 8;
+__device__ __forceinline__ int pick_team(const int64_t (&W)[PA_MAX_TEAM], int ctas, int most) {
+  int best = 1;
+  int64_t cost = 0;
+#pragma unroll
+  for (int g = 1; g <= PA_MAX_TEAM; ++g) {
+    if (g > most || g > ctas) break;
+    const int teams = ctas / g;
+    const int64_t c = (W[g - 1] + teams - 1) / teams * (g == 1 ? 6 : 5);
+    if (g == 1 || c < cost) {
+      cost = c;
+      best = g;
+    }
+  }
+  return best;
 }
 
 // A CTA's part of an item, as posted to the other warps.
@@ -137,14 +162,17 @@ struct Piece {
   int kv;          // keys of the sequence
   int lim0;        // token i of the piece sees min(lim0 + i, kv) keys
   int dest;        // >= 0: partial slot; -1: the output; -2 - seg: the segment's rows
+  int b;           // sequence, -1: the prefix
+  int pad[3];
 };
-static_assert(sizeof(Piece) == 32, "two 16-byte loads");
+static_assert(sizeof(Piece) == 48, "16-byte loads");
 
-// The first sequence of this CTA's share, found by all threads together.
+// This CTA's share of a segment: `tiles` key tiles from tile `at` of sequence
+// b on, found by all threads together. A share is the same number of tiles
+// (`per`) for every team but the last ones.
 struct Share {
-  int64_t begin, end;
-  int64_t base;  // tile offset of sequence b
-  int b;
+  int64_t tiles, at, per;
+  int b, g;
 };
 
 // One key tile of the online softmax of the calling thread's row, in base 2
@@ -231,11 +259,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   uint8_t* ctrl = sQ + 2 * TILE_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PA_BARS + 1);
-  Piece* ring = reinterpret_cast<Piece*>(ctrl + 384);                 // [PA_PIECES]
-  int64_t* warp_sum = reinterpret_cast<int64_t*>(ctrl + 640);         // [12]
-  Share* share = reinterpret_cast<Share*>(ctrl + 736);                // [2]
-  static_assert((PA_BARS + 1) * 8 + 16 <= 384 && 384 + PA_PIECES * 32 <= 640 &&
-                    736 + 2 * sizeof(Share) <= PA_CTRL_BYTES,
+  Piece* ring = reinterpret_cast<Piece*>(ctrl + 384);   // [PA_PIECES]
+  Share* share = reinterpret_cast<Share*>(ctrl + 768);  // [2]
+  // scratch of the share search, where the first key tiles land later
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(sKV);  // [PA_MAX_TEAM][warps]
+  static_assert((PA_BARS + 1) * 8 + 16 <= 384 && 384 + PA_PIECES * sizeof(Piece) <= 768 &&
+                    768 + 2 * sizeof(Share) <= PA_CTRL_BYTES,
                 "control region");
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int warp = threadIdx.x >> 5;
@@ -247,7 +276,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     for (int i = 0; i < PA_BARS; ++i) {
       uint32_t count = 1;
       if (i >= PA_SFREE && i < PA_PVD) count = 4;
-      if (i >= PA_PC_EMPTY && i < PA_DRAIN) count = 9;
+      if (i >= PA_PC_EMPTY && i < PA_DRAIN) count = 10;
       mbar_init(bar(i), count);
     }
     fence_mbar_init();
@@ -257,114 +286,251 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     tmem_relinquish();
   }
   // this CTA's share of each segment: every thread sums the tiles of a run of
-  // sequences, a scan over the threads gives the offsets
+  // sequences, for each team size; then the thread whose run holds the share's
+  // first tile finds its sequence
+  constexpr int WARPS = PA_THREADS / 32;
   const int first_seg = a.prefix_len > 0 ? 0 : 1;
+  const int most = a.b.T > 2 * a.tok ? PA_MAX_TEAM : 1;
   for (int seg = first_seg; seg < 2; ++seg) {
     const int n = seg == 0 ? 1 : a.b.B;
     const int run = (n + PA_THREADS - 1) / PA_THREADS;
     const int b0 = min(static_cast<int>(threadIdx.x) * run, n), b1 = min(b0 + run, n);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += head_tiles(a, seg, seq_info(a, seg, b)) * a.Hkv;
-    int64_t incl = mine;
+    int64_t mine[PA_MAX_TEAM] = {};
+    for (int b = b0; b < b1; ++b) {
+      const SeqInfo s = seq_info(a, seg, b);
+#pragma unroll
+      for (int g = 1; g <= PA_MAX_TEAM; ++g)
+        if (g <= most) mine[g - 1] += head_tiles(a, seg, s, g) * a.Hkv;
+    }
+    __syncthreads();  // warp_sum of the previous segment has been read
+    if (threadIdx.x == 0) share[seg] = Share{0, 0, 1, 0, 1};
+#pragma unroll
+    for (int g = 0; g < PA_MAX_TEAM; ++g) {
+      if (g >= most) break;
+      int64_t v = mine[g];
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+      if (lane == 0) warp_sum[g * WARPS + warp] = v;
+    }
+    __syncthreads();
+    int64_t W[PA_MAX_TEAM] = {};
+#pragma unroll
+    for (int g = 0; g < PA_MAX_TEAM; ++g) {
+      if (g >= most) break;
+      for (int i = 0; i < WARPS; ++i) W[g] += warp_sum[g * WARPS + i];
+    }
+    const int team = pick_team(W, a.ctas, most);
+    int64_t total = 0, own = 0, at = 0;
+#pragma unroll
+    for (int g = 0; g < PA_MAX_TEAM; ++g)
+      if (g + 1 == team) total = W[g], own = mine[g];
+    for (int i = 0; i < warp; ++i) at += warp_sum[(team - 1) * WARPS + i];
+    int64_t incl = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += v;
     }
-    __syncthreads();  // warp_sum of the previous segment has been read
-    if (lane == 31) warp_sum[warp] = incl;
-    if (threadIdx.x == 0) share[seg] = Share{0, 0, 0, 0};
-    __syncthreads();
-    int64_t before = 0, W = 0;
-    for (int i = 0; i < PA_THREADS / 32; ++i) {
-      if (i < warp) before += warp_sum[i];
-      W += warp_sum[i];
-    }
-    int64_t at = before + incl - mine;
-    const int64_t begin = share_begin(W, a.ctas, blockIdx.x);
-    const int64_t end = share_begin(W, a.ctas, blockIdx.x + 1);
-    const bool here = begin < end && begin >= at && begin < at + mine;
-    if (here || blockIdx.x == 0) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) a.totals[seg] = W;
+    at += incl - own;
+    const int teams = a.ctas / team;
+    const int64_t per = max((total + teams - 1) / teams, int64_t{1});
+    const int64_t begin = (blockIdx.x / team) * per;
+    const int64_t end = min(begin + per, total);
+    if (begin < end && begin >= at && begin < at + own && blockIdx.x / team < teams) {
       for (int b = b0; b < b1; ++b) {
-        const SeqInfo s = seq_info(a, seg, b);
-        const int64_t tiles = head_tiles(a, seg, s) * a.Hkv;
-        if (begin < end && begin >= at && begin < at + tiles) share[seg] = Share{begin, end, at, b};
-        if (blockIdx.x == 0 && seg == 1 && s.q_len > 0) a.first[s.c0] = at;
+        const int64_t tiles = head_tiles(a, seg, seq_info(a, seg, b), team) * a.Hkv;
+        if (begin < at + tiles) {
+          share[seg] = Share{end - begin, begin - at, per, b, team};
+          break;
+        }
         at += tiles;
       }
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.teams[seg] = team;
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // warp_sum, before TMA writes there
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_REGS_OTHER));
-  if (warp == 8) {
-    // ------------------------------------------- pieces and TMA loads
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
-    const int nbox = BKV >> a.b.page_log2;  // pages of a key tile
-    const int box = lane & (nbox - 1), half = lane / nbox;
-    const uint32_t box_dst = half * BOX_BYTES + ((box << a.b.page_log2) << 7);
-    const uint32_t q_bytes = static_cast<uint32_t>(a.tok * a.G) * 256;
-    int np = 0, seq = 0, nq[2] = {0, 0};
-    bool ok = true;
-    auto post = [&](const Piece& p) {
-      const int r = np % PA_PIECES;
-      if (!mbar_wait_warp(bar(PA_PC_EMPTY + r), ((np / PA_PIECES) & 1) ^ 1, a.err,
-                          ERR_WAIT_ATTN_PRODUCER))
-        return false;
-      if (lane == 0) {
-        ring[r] = p;
-        mbar_arrive(bar(PA_PC_FULL + r));
-      }
-      __syncwarp();
-      ++np;
-      return true;
-    };
-    auto run_piece = [&](const Piece& p, const int32_t* pages) {
-      const bool two = p.ntok > a.tok;
-      const int g0 = two ? 0 : np & 1;
-      if (!post(p)) return false;
-      for (int g = g0; g <= (two ? 1 : g0); ++g) {
-        if (!mbar_wait_warp(bar(PA_Q_EMPTY + g), (nq[g] & 1) ^ 1, a.err, ERR_WAIT_ATTN_PRODUCER))
+    if (warp == 10) {
+      // ------------------------------------------------------- the share
+      int np = 0;
+      auto post = [&](const Piece& p) {
+        const int r = np % PA_PIECES;
+        if (!mbar_wait_warp(bar(PA_PC_EMPTY + r), ((np / PA_PIECES) & 1) ^ 1, a.err,
+                            ERR_WAIT_ATTN_PRODUCER))
           return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(PA_Q_FULL + g), q_bytes);
-          const uint32_t dst = smem_u32(sQ + g * TILE_BYTES);
-          const int t0 = p.tok0 + (two ? g * a.tok : 0);
-          tma_load_3d(dst, &tmQ, bar(PA_Q_FULL + g), 0, p.hk * a.G, t0);
-          tma_load_3d(dst + BOX_BYTES, &tmQ, bar(PA_Q_FULL + g), 64, p.hk * a.G, t0);
+          ring[r] = p;
+          mbar_arrive(bar(PA_PC_FULL + r));
         }
-        ++nq[g];
-      }
-      // a page is loaded when it begins below the sequence's end
-      auto page_of = [&](int kt) {
-        const int i = kt * nbox + box;
-        return half < 2 && kt < p.kt1 && (static_cast<int64_t>(i) << a.b.page_log2) < p.kv
-                   ? __ldg(pages + i)
-                   : -1;
+        __syncwarp();
+        ++np;
+        return true;
       };
-      int page = page_of(p.kt0);
-      for (int kt = p.kt0; kt < p.kt1; ++kt) {
-        const int next = page_of(kt + 1);
-        const int live = min(nbox, (p.kv - kt * BKV + (1 << a.b.page_log2) - 1) >> a.b.page_log2);
+      bool ok = true;
+      for (int seg = first_seg; ok && seg < 2; ++seg) {
+        const Share sh = share[seg];
+        const int member = static_cast<int>(blockIdx.x) % sh.g;
+        const int item = 2 * a.tok;
+        const int n = seg == 0 ? 1 : a.b.B;
+        int4 cut = make_int4(0, 0, 0, 0);
+        int64_t left = sh.tiles;
+        int b = sh.b, hk = 0, qg = 0, kt = 0, items = 0, groups = 0;
+        SeqInfo s{};
+        auto group_tiles = [&]() { return key_tiles(s, min((qg + 1) * item * sh.g, s.q_len)); };
+        auto enter = [&]() {
+          s = seq_info(a, seg, b);
+          items = (s.q_len + item - 1) / item;
+          groups = (items + sh.g - 1) / sh.g;
+        };
+        if (left > 0) {
+          enter();
+          const int64_t per_head = max(head_tiles(a, seg, s, sh.g), int64_t{1});
+          hk = static_cast<int>(sh.at / per_head);
+          int64_t r = sh.at - hk * per_head;
+          if (!uneven(a, seg)) {
+            const int nk = group_tiles();
+            qg = static_cast<int>(r / nk);
+            r -= static_cast<int64_t>(qg) * nk;
+          } else {
+            for (int nk = group_tiles(); r >= nk && qg + 1 < groups; nk = group_tiles()) {
+              r -= nk;
+              ++qg;
+            }
+          }
+          kt = static_cast<int>(r);
+        }
+        while (ok && left > 0) {
+          const int take = static_cast<int>(min(static_cast<int64_t>(group_tiles() - kt), left));
+          const int qt = qg * sh.g + member;
+          const int nk = key_tiles(s, min((qt + 1) * item, s.q_len));  // of this CTA's item
+          if (qt < items && kt < nk) {
+            Piece p{};
+            p.hk = hk;
+            p.b = seg == 0 ? -1 : b;
+            p.kt0 = kt;
+            p.kt1 = min(kt + take, nk);
+            p.tok0 = s.c0 + qt * item;
+            p.ntok = min(item, s.q_len - qt * item);
+            p.kv = s.kv;
+            p.lim0 = uneven(a, seg) ? s.off + qt * item + 1 : s.kv;
+            const bool whole = p.kt0 == 0 && p.kt1 == nk;
+            p.dest = !whole ? ((seg - first_seg) * PA_MAX_CTAS + static_cast<int>(blockIdx.x)) * 2 +
+                                  (p.kt0 > 0 ? 0 : 1)
+                            : (first_seg == 0 ? -2 - seg : -1);
+            if (p.kt0 == 0) {
+              // the shares that the rest of the item falls into
+              const int more = static_cast<int>((nk - p.kt1 + sh.per - 1) / sh.per);
+              const int last = static_cast<int>(blockIdx.x) + more * sh.g;
+              if (!whole) cut = make_int4(p.tok0, p.ntok, hk, last);
+              if (first_seg == 0 && lane == 0)
+                a.spread[(static_cast<int64_t>(seg) * a.b.T + p.tok0) * a.Hkv + hk] =
+                    make_int2(blockIdx.x, last);
+            }
+            ok = post(p);
+          }
+          left -= take;
+          kt = 0;
+          if (++qg == groups) {
+            qg = 0;
+            if (++hk == a.Hkv) {
+              hk = 0;
+              groups = 0;
+              while (left > 0 && groups == 0 && ++b < n) enter();
+              if (b >= n) break;
+            }
+          }
+        }
+        if (seg == 1 && lane == 0) a.cut[blockIdx.x] = cut;
+      }
+      if (ok) post(Piece{});
+    } else if (warp == 8) {
+      // ------------------------------------------------------- TMA loads
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
+      const int nbox = BKV >> a.b.page_log2;  // pages of a key tile
+      const int box = lane & (nbox - 1), half = lane / nbox;
+      const uint32_t box_dst = half * BOX_BYTES + ((box << a.b.page_log2) << 7);
+      const uint32_t q_bytes = static_cast<uint32_t>(a.tok * a.G) * 256;
+      int np = 0, seq = 0, nq[2] = {0, 0};
+      bool ok = true;
+      struct Tile {
+        int kt, kt1, kv, hk;
+        const int32_t* pages;
+        int tok0, groups;  // of a piece's first tile: first token, query tiles (bit i: tile i)
+        int page;          // this lane's page, -1: none
+      };
+      // the key tile after d (of the next piece when d is its piece's last),
+      // with the lane's page on its way; false: no more, or a wait failed
+      auto advance = [&](Tile& d) {
+        d.groups = 0;
+        if (++d.kt >= d.kt1) {
+          const int r = np % PA_PIECES;
+          if (!mbar_wait_warp(bar(PA_PC_FULL + r), (np / PA_PIECES) & 1, a.err,
+                              ERR_WAIT_ATTN_PRODUCER))
+            return ok = false;
+          const Piece& p = ring[r];
+          const int ntok = p.ntok, b = p.b;
+          d.kt = p.kt0;
+          d.kt1 = p.kt1;
+          d.kv = p.kv;
+          d.hk = p.hk;
+          d.tok0 = p.tok0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
+          if (ntok == 0) return false;
+          d.pages = b < 0 ? a.prefix_pages
+                          : a.b.page_table + static_cast<int64_t>(b) * a.b.max_pages;
+          d.groups = ntok > a.tok ? 3 : 1 << (np & 1);
+          ++np;
+        }
+        // a page is loaded when it begins below the sequence's end
+        const int i = d.kt * nbox + box;
+        d.page = half < 2 && (static_cast<int64_t>(i) << a.b.page_log2) < d.kv ? __ldg(d.pages + i)
+                                                                              : -1;
+        return true;
+      };
+      Tile nxt{};
+      bool more = advance(nxt);
+      while (ok && more) {
+        const Tile cur = nxt;
+        more = advance(nxt);
+        if (!ok) break;
+        for (int g = 0; ok && g < 2; ++g) {
+          if (!(cur.groups >> g & 1)) continue;
+          ok = mbar_wait_warp(bar(PA_Q_EMPTY + g), (nq[g] & 1) ^ 1, a.err, ERR_WAIT_ATTN_PRODUCER);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(PA_Q_FULL + g), q_bytes);
+            const uint32_t dst = smem_u32(sQ + g * TILE_BYTES);
+            const int t0 = cur.tok0 + (cur.groups == 3 ? g * a.tok : 0);
+            tma_load_3d(dst, &tmQ, bar(PA_Q_FULL + g), 0, cur.hk * a.G, t0);
+            tma_load_3d(dst + BOX_BYTES, &tmQ, bar(PA_Q_FULL + g), 64, cur.hk * a.G, t0);
+          }
+          __syncwarp();
+          ++nq[g];
+        }
+        if (!ok) break;
+        const int live =
+            min(nbox, (cur.kv - cur.kt * BKV + (1 << a.b.page_log2) - 1) >> a.b.page_log2);
         const uint32_t bytes = static_cast<uint32_t>(max(live, 0)) << (a.b.page_log2 + 8);
         // a page outside the pool: a row past the map's end, which loads zeros
-        const int row = page >= 0 && page < a.b.num_pages
-                            ? (page * a.Hkv + p.hk) << a.b.page_log2
+        const int row = cur.page >= 0 && cur.page < a.b.num_pages
+                            ? (cur.page * a.Hkv + cur.hk) << a.b.page_log2
                             : a.total_rows;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++seq) {
           const int slot = seq % PA_SLOTS;
-          if (!mbar_wait_warp(bar(PA_KV_EMPTY + slot), ((seq / PA_SLOTS) & 1) ^ 1, a.err,
-                              ERR_WAIT_ATTN_PRODUCER))
-            return false;
+          ok = mbar_wait_warp(bar(PA_KV_EMPTY + slot), ((seq / PA_SLOTS) & 1) ^ 1, a.err,
+                              ERR_WAIT_ATTN_PRODUCER);
+          if (!ok) break;
           const uint32_t full = bar(PA_KV_FULL + slot);
           if (lane == 0) {
             if (bytes > 0)
@@ -377,162 +543,112 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             tma_load_2d(smem_u32(sKV + slot * TILE_BYTES) + box_dst, kv ? &tmV : &tmK, full,
                         half * 64, row);
         }
-        page = next;
       }
-      return true;
-    };
-    for (int seg = first_seg; ok && seg < 2; ++seg) {
-      const Share sh = share[seg];
-      int64_t w = sh.begin, base = sh.base;
-      int b = sh.b;
-      const int n = seg == 0 ? 1 : a.b.B;
-      const int item = 2 * a.tok;
-      if (w >= sh.end) continue;
-      SeqInfo s = seq_info(a, seg, b);
-      int64_t per_head = head_tiles(a, seg, s);
-      while (ok && w < sh.end) {
-        while (w >= base + per_head * a.Hkv && b + 1 < n) {
-          base += per_head * a.Hkv;
-          s = seq_info(a, seg, ++b);
-          per_head = head_tiles(a, seg, s);
+      // no copy of this CTA may still be landing when it exits
+      if (lane == 0) {
+        const uint64_t t0 = globaltimer_ns();
+        const uint64_t lim = drain_limit_ns(a.err);
+        for (int g = 0; g < 2; ++g)
+          if (nq[g] > 0) mbar_wait_drain(bar(PA_Q_FULL + g), (nq[g] - 1) & 1, t0, lim);
+        for (int i = max(seq - PA_SLOTS, 0); i < seq; ++i)
+          mbar_wait_drain(bar(PA_KV_FULL + i % PA_SLOTS), (i / PA_SLOTS) & 1, t0, lim);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(BQ, BKV, false);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(BQ, DH, true);
+      const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dk = sdesc_sw128(smem_u32(sKV), 16, 1024);
+      const uint64_t dv = sdesc_sw128(smem_u32(sKV), BOX_BYTES, 1024);
+      auto wait = [&](int b, int count) {
+        return mbar_wait_warp(bar(b), count & 1, a.err, ERR_WAIT_ATTN_MMA);
+      };
+      // 16-byte offset of K step kk (16 channels) in a K-major tile
+      auto kmaj = [](int kk) {
+        return static_cast<uint32_t>(((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4);
+      };
+      struct Tile {
+        int g0;      // query tile, or the first of two
+        bool two, first, last;
+        int t;       // key tiles of this CTA before it
+      };
+      int np = 0, left = 0, tiles = 0;
+      Tile proto{0, false, false, false, 0};
+      bool ok = true;
+      // the next key tile; false: no more, or a wait failed (ok false)
+      auto next_tile = [&](Tile& d) {
+        bool first = false;
+        if (left == 0) {
+          const int r = np % PA_PIECES;
+          if (!wait(PA_PC_FULL + r, np / PA_PIECES)) return ok = false;
+          const int ntok = ring[r].ntok;
+          left = ring[r].kt1 - ring[r].kt0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
+          if (ntok == 0) return false;
+          proto.two = ntok > a.tok;
+          proto.g0 = proto.two ? 0 : np & 1;
+          ++np;
+          first = true;
         }
-        if (per_head == 0 || w >= base + per_head * a.Hkv) break;
-        Piece p;
-        p.hk = static_cast<int>((w - base) / per_head);
-        int64_t r = (w - base) - p.hk * per_head;
-        int qt, nk;
-        if (uneven(a, seg)) {
-          for (qt = 0;; ++qt) {
-            nk = key_tiles(s, min((qt + 1) * item, s.q_len));
-            if (r < nk) break;
-            r -= nk;
-          }
-        } else {
-          nk = key_tiles(s, s.q_len);
-          qt = static_cast<int>(r / nk);
-          r -= static_cast<int64_t>(qt) * nk;
-        }
-        p.kt0 = static_cast<int>(r);
-        p.kt1 = static_cast<int>(min(static_cast<int64_t>(nk), r + (sh.end - w)));
-        w += p.kt1 - p.kt0;
-        p.tok0 = s.c0 + qt * item;
-        p.ntok = min(item, s.q_len - qt * item);
-        p.kv = s.kv;
-        p.lim0 = uneven(a, seg) ? s.off + qt * item + 1 : s.kv;
-        const bool whole = p.kt0 == 0 && p.kt1 == nk;
-        p.dest = !whole ? ((seg - first_seg) * PA_MAX_CTAS + static_cast<int>(blockIdx.x)) * 2 +
-                              (p.kt0 > 0 ? 0 : 1)
-                        : (first_seg == 0 ? -2 - seg : -1);
-        ok = run_piece(p, seg == 0 ? a.prefix_pages
-                                   : a.b.page_table + static_cast<int64_t>(b) * a.b.max_pages);
+        d = proto;
+        d.first = first;
+        d.last = --left == 0;
+        d.t = tiles++;
+        return true;
+      };
+      int nq[2] = {0, 0}, ns[2] = {0, 0}, npv[2] = {0, 0};
+      int last_s = -1;  // query tile whose S is in the buffer
+      auto qk = [&](const Tile& d, int g) {  // S = Q_g K_t^T
+        const int seq = 2 * d.t, slot = seq % PA_SLOTS;
+        if (d.first && !wait(PA_Q_FULL + g, nq[g]++)) return false;
+        if (!wait(PA_KV_FULL + slot, seq / PA_SLOTS)) return false;
+        if (last_s >= 0 && !wait(PA_SFREE + last_s, ns[last_s] - 1)) return false;
+        tc_fence_after();
+        const uint64_t qd = dq + static_cast<uint32_t>(g * (TILE_BYTES >> 4));
+        const uint64_t kd = dk + static_cast<uint32_t>(slot * (TILE_BYTES >> 4));
+  #pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk)
+          mma_ss_el(tmem + TPA_S, qd + kmaj(kk), kd + kmaj(kk), idesc_qk, kk > 0 ? 1u : 0u);
+        mma_commit_el(bar(PA_S + g));
+        if (d.last) mma_commit_el(bar(PA_Q_EMPTY + g));
+        if (!d.two || g == 1) mma_commit_el(bar(PA_KV_EMPTY + slot));
+        ++ns[g];
+        last_s = g;
+        return true;
+      };
+      auto pv = [&](const Tile& d, int g) {  // O_g (+)= P_g V_t
+        const int seq = 2 * d.t + 1, slot = seq % PA_SLOTS;
+        if (!wait(PA_P + g, npv[g]) || !wait(PA_KV_FULL + slot, seq / PA_SLOTS)) return false;
+        tc_fence_after();
+        const uint64_t vd = dv + static_cast<uint32_t>(slot * (TILE_BYTES >> 4));
+  #pragma unroll
+        for (int kk = 0; kk < BKV / 16; ++kk)
+          mma_ts_el(tmem + TPA_O + g * 128, tmem + TPA_P + g * 64 + kk * 8, vd + kk * (2048 >> 4),
+                    idesc_pv, (!d.first || kk > 0) ? 1u : 0u);
+        mma_commit_el(bar(PA_PVD + g));
+        if (!d.two || g == 1) mma_commit_el(bar(PA_KV_EMPTY + slot));
+        ++npv[g];
+        return true;
+      };
+      Tile cur, nxt;
+      bool more = next_tile(cur);
+      if (more) ok = qk(cur, cur.g0) && (!cur.two || qk(cur, 1));
+      // Q K^T of the next key tile before P V of this one; with two query tiles
+      // their products alternate, so one's softmax overlaps the other's products
+      while (ok && more) {
+        more = next_tile(nxt);
+        if (!ok) break;
+        ok = (!more || qk(nxt, nxt.g0)) && pv(cur, cur.g0);
+        if (ok && more && nxt.two) ok = qk(nxt, 1);
+        if (ok && cur.two) ok = pv(cur, 1);
+        cur = nxt;
       }
+      // every product must be done with shared and tensor memory before the CTA
+      // frees them: commit and wait, bounded
+      mma_commit_el(bar(PA_DRAIN));
+      mbar_wait_drain(bar(PA_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(a.err));
     }
-    if (ok) ok = post(Piece{0, 0, 0, 0, 0, 0, 0, 0});
-    // no copy of this CTA may still be landing when it exits
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer_ns();
-      const uint64_t lim = drain_limit_ns(a.err);
-      for (int g = 0; g < 2; ++g)
-        if (nq[g] > 0) mbar_wait_drain(bar(PA_Q_FULL + g), (nq[g] - 1) & 1, t0, lim);
-      for (int i = max(seq - PA_SLOTS, 0); i < seq; ++i)
-        mbar_wait_drain(bar(PA_KV_FULL + i % PA_SLOTS), (i / PA_SLOTS) & 1, t0, lim);
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(BQ, BKV, false);
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(BQ, DH, true);
-    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t dk = sdesc_sw128(smem_u32(sKV), 16, 1024);
-    const uint64_t dv = sdesc_sw128(smem_u32(sKV), BOX_BYTES, 1024);
-    auto wait = [&](int b, int count) {
-      return mbar_wait_warp(bar(b), count & 1, a.err, ERR_WAIT_ATTN_MMA);
-    };
-    // 16-byte offset of K step kk (16 channels) in a K-major tile
-    auto kmaj = [](int kk) {
-      return static_cast<uint32_t>(((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4);
-    };
-    struct Tile {
-      int g0;      // query tile, or the first of two
-      bool two, first, last;
-      int t;       // key tiles of this CTA before it
-    };
-    int np = 0, left = 0, tiles = 0;
-    Tile proto{0, false, false, false, 0};
-    bool ok = true;
-    // the next key tile; false: no more, or a wait failed (ok false)
-    auto next_tile = [&](Tile& d) {
-      bool first = false;
-      if (left == 0) {
-        const int r = np % PA_PIECES;
-        if (!wait(PA_PC_FULL + r, np / PA_PIECES)) return ok = false;
-        const int ntok = ring[r].ntok;
-        left = ring[r].kt1 - ring[r].kt0;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
-        if (ntok == 0) return false;
-        proto.two = ntok > a.tok;
-        proto.g0 = proto.two ? 0 : np & 1;
-        ++np;
-        first = true;
-      }
-      d = proto;
-      d.first = first;
-      d.last = --left == 0;
-      d.t = tiles++;
-      return true;
-    };
-    int nq[2] = {0, 0}, ns[2] = {0, 0}, npv[2] = {0, 0};
-    int last_s = -1;  // query tile whose S is in the buffer
-    auto qk = [&](const Tile& d, int g) {  // S = Q_g K_t^T
-      const int seq = 2 * d.t, slot = seq % PA_SLOTS;
-      if (d.first && !wait(PA_Q_FULL + g, nq[g]++)) return false;
-      if (!wait(PA_KV_FULL + slot, seq / PA_SLOTS)) return false;
-      if (last_s >= 0 && !wait(PA_SFREE + last_s, ns[last_s] - 1)) return false;
-      tc_fence_after();
-      const uint64_t qd = dq + static_cast<uint32_t>(g * (TILE_BYTES >> 4));
-      const uint64_t kd = dk + static_cast<uint32_t>(slot * (TILE_BYTES >> 4));
-#pragma unroll
-      for (int kk = 0; kk < DH / 16; ++kk)
-        mma_ss_el(tmem + TPA_S, qd + kmaj(kk), kd + kmaj(kk), idesc_qk, kk > 0 ? 1u : 0u);
-      mma_commit_el(bar(PA_S + g));
-      if (d.last) mma_commit_el(bar(PA_Q_EMPTY + g));
-      if (!d.two || g == 1) mma_commit_el(bar(PA_KV_EMPTY + slot));
-      ++ns[g];
-      last_s = g;
-      return true;
-    };
-    auto pv = [&](const Tile& d, int g) {  // O_g (+)= P_g V_t
-      const int seq = 2 * d.t + 1, slot = seq % PA_SLOTS;
-      if (!wait(PA_P + g, npv[g]) || !wait(PA_KV_FULL + slot, seq / PA_SLOTS)) return false;
-      tc_fence_after();
-      const uint64_t vd = dv + static_cast<uint32_t>(slot * (TILE_BYTES >> 4));
-#pragma unroll
-      for (int kk = 0; kk < BKV / 16; ++kk)
-        mma_ts_el(tmem + TPA_O + g * 128, tmem + TPA_P + g * 64 + kk * 8, vd + kk * (2048 >> 4),
-                  idesc_pv, (!d.first || kk > 0) ? 1u : 0u);
-      mma_commit_el(bar(PA_PVD + g));
-      if (!d.two || g == 1) mma_commit_el(bar(PA_KV_EMPTY + slot));
-      ++npv[g];
-      return true;
-    };
-    Tile cur, nxt;
-    bool more = next_tile(cur);
-    if (more) ok = qk(cur, cur.g0) && (!cur.two || qk(cur, 1));
-    // Q K^T of the next key tile before P V of this one; with two query tiles
-    // their products alternate, so one's softmax overlaps the other's products
-    while (ok && more) {
-      more = next_tile(nxt);
-      if (!ok) break;
-      ok = (!more || qk(nxt, nxt.g0)) && pv(cur, cur.g0);
-      if (ok && more && nxt.two) ok = qk(nxt, 1);
-      if (ok && cur.two) ok = pv(cur, 1);
-      cur = nxt;
-    }
-    // every product must be done with shared and tensor memory before the CTA
-    // frees them: commit and wait, bounded
-    mma_commit_el(bar(PA_DRAIN));
-    mbar_wait_drain(bar(PA_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(a.err));
-  }
   } else {
     // ---------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PA_REGS_SOFTMAX));
@@ -679,118 +795,158 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   }
 }
 
-// Joins the partial results of each row: one warp per (token, head), four
-// channels per lane, partials in the order of their keys (so the sums do not
-// depend on which CTA came first). Without a prefix only rows of split items
-// have any; with one, every row has those of the prefix and of its own keys.
+// A row's result while its partials are joined, four channels per lane.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+};
+
+// Adds up to 32 partial results to j: lane i holds the (maximum, sum) of the
+// i-th, src(i) is where its channels lie. In the order of their keys, so the
+// sums do not depend on which CTA came first.
+template <class Src>
+__device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& src) {
+  const int lane = threadIdx.x & 31;
+  float top = ml.x;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float m = fmaxf(j.m, top);
+  if (m == -INFINITY) return;  // no key so far
+  const float c = ex2_approx(j.m - m), w = ex2_approx(ml.x - m);
+  float l = ml.y * w;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  j.m = m;
+  j.l = j.l * c + l;
+  j.o.x *= c;
+  j.o.y *= c;
+  j.o.z *= c;
+  j.o.w *= c;
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(src(i0 + i)) + lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+      if (i0 + i < n) {
+        j.o.x = fmaf(x[i].x, wi, j.o.x);
+        j.o.y = fmaf(x[i].y, wi, j.o.y);
+        j.o.z = fmaf(x[i].z, wi, j.o.z);
+        j.o.w = fmaf(x[i].w, wi, j.o.w);
+      }
+    }
+  }
+}
+
+// Row r of an item that CTAs c0, c0 + g, .. c1 have parts of: the end of the
+// first one's share, the beginning of the others'.
+__device__ __forceinline__ void join_split(Joined& j, const PagedArgs& a, int seg, int c0, int c1,
+                                           int g, int r) {
+  const int lane = threadIdx.x & 31;
+  const int n = (c1 - c0) / g + 1;
+  auto slot = [&](int i) {
+    return static_cast<int64_t>((seg * PA_MAX_CTAS + c0 + i * g) * 2 + (i == 0 ? 1 : 0)) *
+               a.part_rows + r;
+  };
+  for (int base = 0; base < n; base += 32) {
+    const float2 ml = base + lane < n
+                          ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot(base + lane))
+                          : make_float2(-INFINITY, 0.f);
+    join_parts(j, min(n - base, 32), ml,
+               [&](int i) { return a.part_o + slot(base + i) * DH; });
+  }
+}
+
+__device__ __forceinline__ void store_joined(const Joined& j, const PagedArgs& a, int t, int head) {
+  const float inv = j.l == 0.f ? 0.f : 1.0f / j.l;  // no key: zeros
+  *reinterpret_cast<uint2*>(a.o + t * a.ld_o + head * DH + (threadIdx.x & 31) * 4) =
+      make_uint2(pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv));
+}
+
+// Without a prefix: block (c, y) joins rows of the item that goes on after CTA
+// c's share, a warp per row.
+constexpr int PA_JOIN_Y = 8;
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x;
+  const int4 cut = __ldcg(a.cut + c);
+  const int rows = cut.y * a.G;
+  const int g = rows > 0 ? __ldcg(a.teams + 1) : 1;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += PA_JOIN_Y * 8) {
+    Joined j;
+    join_split(j, a, 0, c, cut.w, g, r);
+    store_joined(j, a, cut.x + r / a.G, cut.z * a.G + r % a.G);
+  }
+}
+
+// With a prefix: every row is joined from its results of the prefix and of its
+// own keys, each whole or split; a warp per (token, head).
+__global__ void __launch_bounds__(256) paged_join_prefix_kernel(const PagedArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.b.T) * a.H;
-  const int first_seg = a.prefix_len > 0 ? 0 : 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int team[2] = {__ldcg(a.teams), __ldcg(a.teams + 1)};
   for (int64_t w = blockIdx.x * 8LL + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8LL) {
     const int t = static_cast<int>(w / a.H), head = static_cast<int>(w % a.H);
     const int hk = head / a.G;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool any = first_seg == 0;
-    auto add = [&](const float* po, const float* pml) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(pml));
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(po) + lane);
-      const float m_new = fmaxf(m, ml.x);
-      if (m_new == -INFINITY) return;  // no key so far
-      const float c = ex2_approx(m - m_new), d = ex2_approx(ml.x - m_new);
-      o.x = o.x * c + x.x * d;
-      o.y = o.y * c + x.y * d;
-      o.z = o.z * c + x.z * d;
-      o.w = o.w * c + x.w * d;
-      l = l * c + ml.y * d;
-      m = m_new;
-    };
     // the row's sequence: the number of ends at or below it
     int b = 0;
     for (int i = lane; i < a.b.B; i += 32) b += __ldg(a.b.cu_q + i + 1) <= t ? 1 : 0;
     b = __reduce_add_sync(0xffffffffu, b);
     if (b >= a.b.B) continue;
-    const SeqInfo own = seq_info(a, 1, b);
-    if (t < own.c0 || t >= own.c0 + own.q_len) continue;
-    for (int seg = first_seg; seg < 2; ++seg) {
-      const SeqInfo s = seg == 0 ? seq_info(a, 0, 0) : own;
-      if (t < s.c0 || t >= s.c0 + s.q_len) continue;  // only if cu_q is out of order
-      const int item = 2 * a.tok;
-      const int qt = (t - s.c0) / item, r = (t - s.c0 - qt * item) * a.G + head % a.G;
-      const int64_t W = __ldcg(reinterpret_cast<const long long*>(a.totals) + seg);
-      int64_t at = seg == 0 ? 0 : __ldcg(reinterpret_cast<const long long*>(a.first) + s.c0);
-      int nk = key_tiles(s, s.q_len);
-      if (uneven(a, seg)) {
-        int64_t sum = 0, all = 0;
-        const int n = (s.q_len + item - 1) / item;
-        for (int i = lane; i < n; i += 32) {
-          const int k = key_tiles(s, min((i + 1) * item, s.q_len));
-          all += k;
-          if (i < qt) sum += k;
-        }
+    Joined j;
+    bool any = false;
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          all += __shfl_xor_sync(0xffffffffu, all, d);
-        }
-        at += hk * all + sum;
-        nk = key_tiles(s, min((qt + 1) * item, s.q_len));
-      } else {
-        const int n = (s.q_len + item - 1) / item;
-        at += (static_cast<int64_t>(hk) * n + qt) * nk;
-      }
-      const int c0 = min(max(share_of(W, a.ctas, at), 0), a.ctas - 1);
-      const int c1 = min(max(share_of(W, a.ctas, at + nk - 1), c0), a.ctas - 1);
-      if (c0 == c1) {
-        if (first_seg == 0) {
-          const int64_t i = (static_cast<int64_t>(seg) * a.b.T + t) * a.H + head;
-          add(a.row_o + i * DH, a.row_ml + i * 2);
-        }
-        continue;
-      }
+    for (int seg = 0; seg < 2; ++seg) {
+      const SeqInfo s = seq_info(a, seg, b);
+      if (t < s.c0 || t >= s.c0 + s.q_len) continue;
+      const int item = 2 * a.tok;
+      const int first = (t - s.c0) / item * item;
+      const int2 at = __ldcg(a.spread + (static_cast<int64_t>(seg) * a.b.T + s.c0 + first) * a.Hkv + hk);
       any = true;
-      for (int c = c0; c <= c1; ++c) {
-        const int64_t begin = share_begin(W, a.ctas, c);
-        if (begin == share_begin(W, a.ctas, c + 1)) continue;  // fewer tiles than CTAs
-        const int slot = ((seg - first_seg) * PA_MAX_CTAS + c) * 2 + (begin > at ? 0 : 1);
-        const int64_t i = static_cast<int64_t>(slot) * a.part_rows + r;
-        add(a.part_o + i * DH, a.part_ml + i * 2);
+      if (at.x == at.y) {
+        const int64_t i = (static_cast<int64_t>(seg) * a.b.T + t) * a.H + head;
+        const float2 ml = lane == 0 ? __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i)
+                                    : make_float2(-INFINITY, 0.f);
+        join_parts(j, 1, ml, [&](int) { return a.row_o + i * DH; });
+      } else {
+        join_split(j, a, seg, min(max(at.x, 0), a.ctas - 1), min(max(at.y, 0), a.ctas - 1),
+                   team[seg], (t - s.c0 - first) * a.G + head % a.G);
       }
     }
-    if (!any) continue;
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    *reinterpret_cast<uint2*>(a.o + t * a.ld_o + head * DH + lane * 4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (any) store_joined(j, a, t, head);
   }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Workspace: the segments' totals, the sequences' offsets [T], the split
-// items' partials and, with a prefix, a result of every row per segment.
+// Workspace: team sizes and cut items; the split items' partials; with a
+// prefix, where each item lies and a result of every row per segment.
 struct PagedWs {
-  size_t first, part_o, part_ml, row_o, row_ml, total;
+  size_t cut, spread, part_o, part_ml, row_o, row_ml, total;
   int part_rows;
 };
 PagedWs paged_ws(int T, int H, int prefix_len) {
   PagedWs w;
   const size_t rows = static_cast<size_t>(T) * H;
+  const bool prefix = prefix_len > 0;
   // rows of one item: at most two query tiles, at most what the call has
   w.part_rows = static_cast<int>(std::min<size_t>(2 * BQ, rows));
-  const size_t slots = (prefix_len > 0 ? 2 : 1) * PA_MAX_CTAS * 2;
+  const size_t slots = (prefix ? 2 : 1) * PA_MAX_CTAS * 2;
   size_t off = 256;
-  w.first = off;
-  off += align256(static_cast<size_t>(T) * 8);
-  w.part_o = off;
-  off += align256(slots * w.part_rows * DH * 4);
-  w.part_ml = off;
-  off += align256(slots * w.part_rows * 8);
-  w.row_o = off;
-  if (prefix_len > 0) off += align256(2 * rows * DH * 4);
-  w.row_ml = off;
-  if (prefix_len > 0) off += align256(2 * rows * 8);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  w.cut = take(PA_MAX_CTAS * sizeof(int4));
+  w.part_o = take(slots * w.part_rows * DH * 4);
+  w.part_ml = take(slots * w.part_rows * 8);
+  w.spread = take(prefix ? 2 * rows * sizeof(int2) : 0);  // Hkv <= H
+  w.row_o = take(prefix ? 2 * rows * DH * 4 : 0);
+  w.row_ml = take(prefix ? 2 * rows * 8 : 0);
   w.total = off;
   return w;
 }
@@ -825,8 +981,9 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   a.causal = causal ? 1 : 0;
   a.prefix_pages = prefix_pages;
   a.prefix_len = prefix_len;
-  a.totals = reinterpret_cast<int64_t*>(base);
-  a.first = reinterpret_cast<int64_t*>(base + w.first);
+  a.teams = reinterpret_cast<int*>(base);
+  a.cut = reinterpret_cast<int4*>(base + w.cut);
+  a.spread = reinterpret_cast<int2*>(base + w.spread);
   a.part_o = reinterpret_cast<float*>(base + w.part_o);
   a.part_ml = reinterpret_cast<float*>(base + w.part_ml);
   a.part_rows = w.part_rows;
@@ -849,12 +1006,17 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  const int64_t want = (static_cast<int64_t>(batch.T) * H + 7) / 8;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, a.ctas * 8)));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (prefix_len > 0) {
+    const int64_t want = (static_cast<int64_t>(batch.T) * H + 7) / 8;
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, a.ctas * 8)));
+    return cuda_fail(cudaLaunchKernelEx(&cfg, paged_join_prefix_kernel, a),
+                     "paged attention join launch");
+  }
+  cfg.gridDim = dim3(a.ctas, PA_JOIN_Y);
   return cuda_fail(cudaLaunchKernelEx(&cfg, paged_join_kernel, a), "paged attention join launch");
 }
 
