@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       const int box = lane & (nbox - 1), half = lane / nbox;
       const uint32_t box_dst = half * BOX_BYTES + ((box << a.b.page_log2) << 7);
       const uint32_t q_bytes = static_cast<uint32_t>(a.tok * a.G) * 256;
-      int np = 0, seq = 0, nq[2] = {0, 0};
+      int np = 0, seq = 0;
+      uint32_t q_phase = 3, q_used = 0;  // per query tile: parity of Q_EMPTY; loaded at all
       bool ok = true;
       struct Tile {
         int kt, kt1, kv, hk;
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (!ok) break;
         for (int g = 0; ok && g < 2; ++g) {
           if (!(cur.groups >> g & 1)) continue;
-          ok = mbar_wait_warp(bar(PA_Q_EMPTY + g), (nq[g] & 1) ^ 1, a.err, ERR_WAIT_ATTN_PRODUCER);
+          ok = mbar_wait_warp(bar(PA_Q_EMPTY + g), q_phase >> g & 1u, a.err, ERR_WAIT_ATTN_PRODUCER);
           if (!ok) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(bar(PA_Q_FULL + g), q_bytes);
@@ -515,7 +516,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             tma_load_3d(dst + BOX_BYTES, &tmQ, bar(PA_Q_FULL + g), 64, cur.hk * a.G, t0);
           }
           __syncwarp();
-          ++nq[g];
+          q_phase ^= 1u << g;
+          q_used |= 1u << g;
         }
         if (!ok) break;
         const int live =
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         const uint64_t t0 = globaltimer_ns();
         const uint64_t lim = drain_limit_ns(a.err);
         for (int g = 0; g < 2; ++g)
-          if (nq[g] > 0) mbar_wait_drain(bar(PA_Q_FULL + g), (nq[g] - 1) & 1, t0, lim);
+          if (q_used >> g & 1u) mbar_wait_drain(bar(PA_Q_FULL + g), q_phase >> g & 1u, t0, lim);
         for (int i = max(seq - PA_SLOTS, 0); i < seq; ++i)
           mbar_wait_drain(bar(PA_KV_FULL + i % PA_SLOTS), (i / PA_SLOTS) & 1, t0, lim);
       }
@@ -560,27 +562,33 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk = sdesc_sw128(smem_u32(sKV), 16, 1024);
       const uint64_t dv = sdesc_sw128(smem_u32(sKV), BOX_BYTES, 1024);
-      auto wait = [&](int b, int count) {
-        return mbar_wait_warp(bar(b), count & 1, a.err, ERR_WAIT_ATTN_MMA);
+      // parities of the phases waited for next, one bit per barrier (an array
+      // indexed by query tile would live in local memory, on the issue path)
+      uint32_t phase = 0;
+      auto wait = [&](int b) {
+        const bool done = mbar_wait_warp(bar(b), phase >> b & 1u, a.err, ERR_WAIT_ATTN_MMA);
+        phase ^= 1u << b;
+        return done;
       };
+      static_assert(PA_PVD <= 32, "a bit per barrier");
       // 16-byte offset of K step kk (16 channels) in a K-major tile
       auto kmaj = [](int kk) {
         return static_cast<uint32_t>(((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4);
       };
       struct Tile {
-        int g0;      // query tile, or the first of two
+        int g0;  // query tile, or the first of two
         bool two, first, last;
-        int t;       // key tiles of this CTA before it
       };
-      int np = 0, left = 0, tiles = 0;
-      Tile proto{0, false, false, false, 0};
+      int np = 0, left = 0;
+      Tile proto{0, false, false, false};
       bool ok = true;
       // the next key tile; false: no more, or a wait failed (ok false)
       auto next_tile = [&](Tile& d) {
         bool first = false;
         if (left == 0) {
           const int r = np % PA_PIECES;
-          if (!wait(PA_PC_FULL + r, np / PA_PIECES)) return ok = false;
+          if (!mbar_wait_warp(bar(PA_PC_FULL + r), (np / PA_PIECES) & 1, a.err, ERR_WAIT_ATTN_MMA))
+            return ok = false;
           const int ntok = ring[r].ntok;
           left = ring[r].kt1 - ring[r].kt0;
           __syncwarp();
@@ -594,41 +602,46 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         d = proto;
         d.first = first;
         d.last = --left == 0;
-        d.t = tiles++;
         return true;
       };
-      int nq[2] = {0, 0}, ns[2] = {0, 0}, npv[2] = {0, 0};
+      // slots of the next K_t and V_t to be used: every other one of the ring
+      int k_slot = 0, v_slot = 1;
+      auto step = [](int& slot) { slot += slot < PA_SLOTS - 2 ? 2 : 2 - PA_SLOTS; };
       int last_s = -1;  // query tile whose S is in the buffer
       auto qk = [&](const Tile& d, int g) {  // S = Q_g K_t^T
-        const int seq = 2 * d.t, slot = seq % PA_SLOTS;
-        if (d.first && !wait(PA_Q_FULL + g, nq[g]++)) return false;
-        if (!wait(PA_KV_FULL + slot, seq / PA_SLOTS)) return false;
-        if (last_s >= 0 && !wait(PA_SFREE + last_s, ns[last_s] - 1)) return false;
+        if (d.first && !wait(PA_Q_FULL + g)) return false;
+        if (g == d.g0 && !wait(PA_KV_FULL + k_slot)) return false;
+        if (last_s >= 0 && !wait(PA_SFREE + last_s)) return false;
         tc_fence_after();
         const uint64_t qd = dq + static_cast<uint32_t>(g * (TILE_BYTES >> 4));
-        const uint64_t kd = dk + static_cast<uint32_t>(slot * (TILE_BYTES >> 4));
-  #pragma unroll
+        const uint64_t kd = dk + static_cast<uint32_t>(k_slot * (TILE_BYTES >> 4));
+#pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk)
           mma_ss_el(tmem + TPA_S, qd + kmaj(kk), kd + kmaj(kk), idesc_qk, kk > 0 ? 1u : 0u);
         mma_commit_el(bar(PA_S + g));
         if (d.last) mma_commit_el(bar(PA_Q_EMPTY + g));
-        if (!d.two || g == 1) mma_commit_el(bar(PA_KV_EMPTY + slot));
-        ++ns[g];
+        if (!d.two || g == 1) {
+          mma_commit_el(bar(PA_KV_EMPTY + k_slot));
+          step(k_slot);
+        }
         last_s = g;
         return true;
       };
       auto pv = [&](const Tile& d, int g) {  // O_g (+)= P_g V_t
-        const int seq = 2 * d.t + 1, slot = seq % PA_SLOTS;
-        if (!wait(PA_P + g, npv[g]) || !wait(PA_KV_FULL + slot, seq / PA_SLOTS)) return false;
+        if (g == d.g0 && !wait(PA_KV_FULL + v_slot)) return false;
+        if (!wait(PA_P + g)) return false;
         tc_fence_after();
-        const uint64_t vd = dv + static_cast<uint32_t>(slot * (TILE_BYTES >> 4));
-  #pragma unroll
+        const uint64_t vd = dv + static_cast<uint32_t>(v_slot * (TILE_BYTES >> 4));
+        const uint32_t to = tmem + TPA_O + g * 128, tp = tmem + TPA_P + g * 64;
+#pragma unroll
         for (int kk = 0; kk < BKV / 16; ++kk)
-          mma_ts_el(tmem + TPA_O + g * 128, tmem + TPA_P + g * 64 + kk * 8, vd + kk * (2048 >> 4),
-                    idesc_pv, (!d.first || kk > 0) ? 1u : 0u);
+          mma_ts_el(to, tp + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
+                    (!d.first || kk > 0) ? 1u : 0u);
         mma_commit_el(bar(PA_PVD + g));
-        if (!d.two || g == 1) mma_commit_el(bar(PA_KV_EMPTY + slot));
-        ++npv[g];
+        if (!d.two || g == 1) {
+          mma_commit_el(bar(PA_KV_EMPTY + v_slot));
+          step(v_slot);
+        }
         return true;
       };
       Tile cur, nxt;
