@@ -43,7 +43,7 @@ constexpr int PA_CTRL_BYTES = 1024;
 // 168 registers; warps 8-11 hand most of theirs to the softmax warps, which
 // hold a row's 128 scores and 64 packed weights (168: 508 bytes of spills)
 constexpr int PA_THREADS = 384;
-constexpr int PA_REGS_SOFTMAX = 216, PA_REGS_OTHER = 72;
+constexpr int PA_REGS_SOFTMAX = 192, PA_REGS_OTHER = 120;
 static_assert(2 * PA_REGS_SOFTMAX + PA_REGS_OTHER <= 3 * 168, "registers of the launch");
 constexpr size_t PA_SMEM_BYTES = 1024 + (PA_SLOTS + 2) * TILE_BYTES + PA_CTRL_BYTES;
 static_assert(PA_SMEM_BYTES <= 227 * 1024, "paged attention shared memory");
@@ -589,8 +589,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           const int r = np % PA_PIECES;
           if (!mbar_wait_warp(bar(PA_PC_FULL + r), (np / PA_PIECES) & 1, a.err, ERR_WAIT_ATTN_MMA))
             return ok = false;
-          const int ntok = ring[r].ntok;
-          left = ring[r].kt1 - ring[r].kt0;
+          // through a warp reduction, whose result is a uniform value: what
+          // follows from it, the products' operands included, then stays in
+          // the uniform datapath
+          const int ntok = __reduce_max_sync(0xffffffffu, ring[r].ntok);
+          left = __reduce_max_sync(0xffffffffu, ring[r].kt1 - ring[r].kt0);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
           if (ntok == 0) return false;
@@ -608,10 +611,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       int k_slot = 0, v_slot = 1;
       auto step = [](int& slot) { slot += slot < PA_SLOTS - 2 ? 2 : 2 - PA_SLOTS; };
       int last_s = -1;  // query tile whose S is in the buffer
-      auto qk = [&](const Tile& d, int g) {  // S = Q_g K_t^T
-        if (d.first && !wait(PA_Q_FULL + g)) return false;
-        if (g == d.g0 && !wait(PA_KV_FULL + k_slot)) return false;
-        if (last_s >= 0 && !wait(PA_SFREE + last_s)) return false;
+      auto qk = [&](int g, int prev, bool lead, bool tail, bool first, bool last) {  // S = Q_g K_t^T
+        if (first && !wait(PA_Q_FULL + g)) return false;
+        if (lead && !wait(PA_KV_FULL + k_slot)) return false;
+        if (prev >= 0 && !wait(PA_SFREE + prev)) return false;
         tc_fence_after();
         const uint64_t qd = dq + static_cast<uint32_t>(g * (TILE_BYTES >> 4));
         const uint64_t kd = dk + static_cast<uint32_t>(k_slot * (TILE_BYTES >> 4));
@@ -619,42 +622,61 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         for (int kk = 0; kk < DH / 16; ++kk)
           mma_ss_el(tmem + TPA_S, qd + kmaj(kk), kd + kmaj(kk), idesc_qk, kk > 0 ? 1u : 0u);
         mma_commit_el(bar(PA_S + g));
-        if (d.last) mma_commit_el(bar(PA_Q_EMPTY + g));
-        if (!d.two || g == 1) {
+        if (last) mma_commit_el(bar(PA_Q_EMPTY + g));
+        if (tail) {
           mma_commit_el(bar(PA_KV_EMPTY + k_slot));
           step(k_slot);
         }
-        last_s = g;
         return true;
       };
-      auto pv = [&](const Tile& d, int g) {  // O_g (+)= P_g V_t
-        if (g == d.g0 && !wait(PA_KV_FULL + v_slot)) return false;
+      auto pv = [&](int g, bool lead, bool tail, uint32_t acc) {  // O_g (+)= P_g V_t
+        if (lead && !wait(PA_KV_FULL + v_slot)) return false;
         if (!wait(PA_P + g)) return false;
         tc_fence_after();
         const uint64_t vd = dv + static_cast<uint32_t>(v_slot * (TILE_BYTES >> 4));
         const uint32_t to = tmem + TPA_O + g * 128, tp = tmem + TPA_P + g * 64;
 #pragma unroll
         for (int kk = 0; kk < BKV / 16; ++kk)
-          mma_ts_el(to, tp + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
-                    (!d.first || kk > 0) ? 1u : 0u);
+          mma_ts_el(to, tp + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1u : acc);
         mma_commit_el(bar(PA_PVD + g));
-        if (!d.two || g == 1) {
+        if (tail) {
           mma_commit_el(bar(PA_KV_EMPTY + v_slot));
           step(v_slot);
         }
         return true;
       };
+      auto qk_of = [&](const Tile& d, int g) {
+        const int prev = last_s;
+        last_s = g;
+        return qk(g, prev, g == d.g0, !d.two || g == 1, d.first, d.last);
+      };
+      auto pv_of = [&](const Tile& d, int g) {
+        return pv(g, g == d.g0, !d.two || g == 1, d.first ? 0u : 1u);
+      };
       Tile cur, nxt;
       bool more = next_tile(cur);
-      if (more) ok = qk(cur, cur.g0) && (!cur.two || qk(cur, 1));
+      if (more) ok = qk_of(cur, cur.g0) && (!cur.two || qk_of(cur, 1));
       // Q K^T of the next key tile before P V of this one; with two query tiles
       // their products alternate, so one's softmax overlaps the other's products
       while (ok && more) {
+        if (cur.two && left >= 2) {
+          // the next key tile is of the same piece and not its last: the same
+          // four products with everything but the slots known
+          uint32_t acc = cur.first ? 0u : 1u;
+          do {
+            ok = qk(0, 1, true, false, false, false) && pv(0, true, false, acc) &&
+                 qk(1, 0, false, true, false, false) && pv(1, false, true, acc);
+            acc = 1u;
+            --left;
+          } while (ok && left >= 2);
+          cur.first = false;
+          continue;
+        }
         more = next_tile(nxt);
         if (!ok) break;
-        ok = (!more || qk(nxt, nxt.g0)) && pv(cur, cur.g0);
-        if (ok && more && nxt.two) ok = qk(nxt, 1);
-        if (ok && cur.two) ok = pv(cur, 1);
+        ok = (!more || qk_of(nxt, nxt.g0)) && pv_of(cur, cur.g0);
+        if (ok && more && nxt.two) ok = qk_of(nxt, 1);
+        if (ok && cur.two) ok = pv_of(cur, 1);
         cur = nxt;
       }
       // every product must be done with shared and tensor memory before the CTA
@@ -697,55 +719,68 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       const bool active = quarter * 32 < rows;
       const int tok = tok0 + row / a.G;
       const int lim = min(max(p.lim0 + tok, 0), p.kv);
-      float m = -INFINITY, l = 0.f;
-      for (int kt = p.kt0; kt < p.kt1; ++kt, ++tiles, ++n) {
-        if (!mbar_wait_warp(bar(PA_S + tile), n & 1, a.err, ERR_WAIT_ATTN_SOFTMAX)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t sr[128];
-        if (active) {
-          tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-          tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-          tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
-          tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
-          tmem_ld_wait();
-          tmem_reg_fence(sr);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PA_SFREE + tile));
+      // keys past the sequence's end hold anything: their weights are 0, and so
+      // their values have to be finite
+      auto clear_values = [&](int kt) {
         const int live = p.kv - kt * BKV;  // keys of the tile that exist
-        if (live < BKV) {
-          // places behind the last key hold anything: their weights are 0, and
-          // so their values have to be finite
-          const int seq = 2 * tiles + 1, slot = seq % PA_SLOTS;
-          if (!mbar_wait_warp(bar(PA_KV_FULL + slot), (seq / PA_SLOTS) & 1, a.err,
-                              ERR_WAIT_ATTN_SOFTMAX)) {
+        if (live >= BKV) return true;
+        const int seq = 2 * tiles + 1, slot = seq % PA_SLOTS;
+        if (!mbar_wait_warp(bar(PA_KV_FULL + slot), (seq / PA_SLOTS) & 1, a.err,
+                            ERR_WAIT_ATTN_SOFTMAX))
+          return false;
+        if (row >= live) {
+          uint4* v = reinterpret_cast<uint4*>(sKV + slot * TILE_BYTES + row * 128);
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i)
+            v[i] = v[BOX_BYTES / 16 + i] = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        return true;
+      };
+      float m = -INFINITY, l = 0.f;
+      if (!active) {
+        // no row of this warp exists: it takes part in the hand-offs only (and
+        // waits for the P V, so that its arrivals stay in step)
+        for (int kt = p.kt0; ok && kt < p.kt1; ++kt, ++tiles, ++n) {
+          ok = mbar_wait_warp(bar(PA_S + tile), n & 1, a.err, ERR_WAIT_ATTN_SOFTMAX);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(bar(PA_SFREE + tile));
+          ok = clear_values(kt) && (kt == p.kt0 || wait_pv(n - 1));
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PA_P + tile));
+        }
+      } else {
+        for (int kt = p.kt0; kt < p.kt1; ++kt, ++tiles, ++n) {
+          if (!mbar_wait_warp(bar(PA_S + tile), n & 1, a.err, ERR_WAIT_ATTN_SOFTMAX)) {
             ok = false;
             break;
           }
-          if (row >= live) {
-            uint8_t* v = sKV + slot * TILE_BYTES + row * 128;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              reinterpret_cast<uint4*>(v)[i] = make_uint4(0, 0, 0, 0);
-              reinterpret_cast<uint4*>(v + BOX_BYTES)[i] = make_uint4(0, 0, 0, 0);
-            }
+          tc_fence_after();
+          uint32_t sr[128];
+          {
+            uint32_t (&c0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+            uint32_t (&c1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
+            uint32_t (&c2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[64]);
+            uint32_t (&c3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[96]);
+            tmem_ld32(tS + 0, c0);
+            tmem_ld32(tS + 32, c1);
+            tmem_ld32(tS + 64, c2);
+            tmem_ld32(tS + 96, c3);
+            tmem_ld_wait();
+            tmem_reg_fence(sr);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PA_SFREE + tile));
+          ok = softmax_tile_paged(sr, tP, tO, lim - kt * BKV, kt > p.kt0, a.scale_log2, m, l,
+                                  [&] { return wait_pv(n - 1); }) &&
+               clear_values(kt);
+          if (!ok) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PA_P + tile));
         }
-        const bool o_live = kt > p.kt0;
-        if (active)
-          ok = softmax_tile_paged(sr, tP, tO, lim - kt * BKV, o_live, a.scale_log2, m, l,
-                                  [&] { return wait_pv(n - 1); });
-        else  // this warp's P barrier phase must not run ahead of the others'
-          ok = !o_live || wait_pv(n - 1);
-        if (!ok) break;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PA_P + tile));
       }
       if (!ok || !wait_pv(n - 1)) break;
       if (!active) continue;
