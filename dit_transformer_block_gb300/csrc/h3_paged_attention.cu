@@ -14,14 +14,15 @@
 //
 // Where a sequence has several items per key head, a team of CTAs takes
 // neighbouring ones over the same keys in step, so that a key tile comes from
-// HBM once for the team (pick_team).
+// HBM once for the team (find_share).
 //
-// One CTA, 384 threads (warp 11 idle), the hand-off and tensor-memory layout
-// of the FP8 attention kernel:
+// One CTA, 384 threads, the hand-off and tensor-memory layout of the FP8
+// attention kernel:
 //   warp 10: walks the CTA's share and posts its pieces of items in a ring in
 //     shared memory, ahead of the others;
-//   warp 8: loads by TMA the pieces' query tiles and, key tile by key tile,
-//     K_t and V_t (one box per page and 64 channels) into a ring of 32 KB slots;
+//   warp 11: loads the pieces' query tiles by TMA;
+//   warp 8: loads K_t and V_t, key tile by key tile (one box per page and 64
+//     channels), into a ring of 32 KB slots, past the ends of pieces;
 //   warp 9: allocates TMEM and issues the products: S = Q_i K_t^T (SS) into
 //     one S buffer, O_i += P_i V_t (TS, P_i in tensor memory); Q K^T of the next
 //     key tile goes ahead of the P V of this one, also across pieces;
@@ -35,10 +36,15 @@
 namespace h3 {
 namespace {
 
-constexpr int PA_SLOTS = 5;    // 32 KB each: K_t, V_t, K_t+1, ...
+// Ring of 32 KB slots in the order K_0 K_1 V_0 K_2 V_1 ..: the order of use, so
+// that no V waits in the ring for longer than the products need it.
+constexpr int PA_SLOTS = 5;
+__device__ __forceinline__ int k_seq(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int v_seq(int t) { return 2 * t + 2; }
 constexpr int PA_PIECES = 8;   // pieces posted ahead
 constexpr int PA_MAX_CTAS = 160;
 constexpr int PA_CTRL_BYTES = 1024;
+constexpr int PA_FEW_TOKENS = 4, PA_FEW_ROWS = 8;
 // 12 warps: with three on each SM sub-partition the launch gives every thread
 // 168 registers; warps 8-11 hand most of theirs to the softmax warps, which
 // hold a row's 128 scores and 64 packed weights (168: 508 bytes of spills)
@@ -120,39 +126,28 @@ __device__ __forceinline__ int key_tiles(const SeqInfo& s, int end_tok) {
 
 __device__ __forceinline__ bool uneven(const PagedArgs& a, int seg) { return seg == 1 && a.causal; }
 
-// Key tiles of one key head of a sequence, for teams of g CTAs (the items of
-// a team run over as many as the one that sees most).
-__device__ __forceinline__ int64_t head_tiles(const PagedArgs& a, int seg, const SeqInfo& s,
+// What beginning an item costs, in key tiles, in the shares: its first scores
+// and its output are not hidden behind other products.
+constexpr int PA_ITEM_COST = 2;
+// An item of up to so many key tiles is not split: it goes to the CTA in whose
+// share it begins.
+constexpr int PA_WHOLE = 4;
+
+// Cost of one key head of a sequence, for teams of g CTAs (the items of a team
+// run over as many key tiles as the one that sees most).
+__device__ __forceinline__ int64_t head_cost(const PagedArgs& a, int seg, const SeqInfo& s,
                                               int g) {
   const int item = 2 * a.tok * g;
   const int n = (s.q_len + item - 1) / item;
   if (n == 0) return 0;
-  if (!uneven(a, seg)) return static_cast<int64_t>(n) * key_tiles(s, s.q_len);
-  int64_t sum = 0;
+  if (!uneven(a, seg)) return static_cast<int64_t>(n) * (key_tiles(s, s.q_len) + PA_ITEM_COST);
+  int64_t sum = static_cast<int64_t>(n) * PA_ITEM_COST;
   for (int i = 1; i <= n; ++i) sum += key_tiles(s, min(i * item, s.q_len));
   return sum;
 }
 
-// Team size for a segment whose tiles for teams of g are W[g - 1]: the least
-// time, with a tile of a lone CTA at 6 and of a team's at 5. A 64 KB key tile
-// takes a CTA about 2,300 cycles of products for two query tiles; read from
-// HBM by every CTA for itself it takes about 2,800.
+// Teams of up to so many CTAs (find_share picks the size).
 constexpr int PA_MAX_TEAM = 8;
-__device__ __forceinline__ int pick_team(const int64_t (&W)[PA_MAX_TEAM], int ctas, int most) {
-  int best = 1;
-  int64_t cost = 0;
-#pragma unroll
-  for (int g = 1; g <= PA_MAX_TEAM; ++g) {
-    if (g > most || g > ctas) break;
-    const int teams = ctas / g;
-    const int64_t c = (W[g - 1] + teams - 1) / teams * (g == 1 ? 6 : 5);
-    if (g == 1 || c < cost) {
-      cost = c;
-      best = g;
-    }
-  }
-  return best;
-}
 
 // A CTA's part of an item, as posted to the other warps.
 struct Piece {
@@ -167,11 +162,19 @@ struct Piece {
 };
 static_assert(sizeof(Piece) == 48, "16-byte loads");
 
-// This CTA's share of a segment: `tiles` key tiles from tile `at` of sequence
-// b on, found by all threads together. A share is the same number of tiles
-// (`per`) for every team but the last ones.
+// a / b for a >= 0, b > 0; in 32 bits where they fit.
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+  return a / b;
+}
+
+// This CTA's share of a segment: `cost` units from unit `at` of sequence b on. A
+// share is the same cost (`per`) for every
+// team but the last ones. An item of n key tiles is PA_ITEM_COST + n units, of
+// which the last n are its key tiles.
 struct Share {
-  int64_t tiles, at, per;
+  int64_t cost, at, per;
   int b, g;
 };
 
@@ -179,14 +182,17 @@ struct Share {
 // with the scale folded in; the scores are in sr, columns >= valid are masked.
 // The running maximum is raised only when a row exceeds it by more than
 // RESCALE_THRESHOLD (then O and the sum are rescaled), so a weight can be up
-// to 2^8; a row that has seen no key yet keeps maximum -inf and sum 0. The
+// to 2^8; a row that has seen no key yet keeps maximum -inf and sum 0.
+// Only rows that exist (row_ok) ask for it: the others hold what was left in
+// shared memory, whose scores would have the tiles of a lone row rescaled. The
 // weights go to tensor memory rounded to bf16 (the type of V in the product);
 // the sum is of the unrounded ones, in FP32. wait_pv: the tile's previous P V
 // is done with P and O. Returns false when a wait failed.
 template <class WaitPV>
 __device__ __forceinline__ bool softmax_tile_paged(uint32_t (&sr)[128], uint32_t tP, uint32_t tO,
-                                                   int valid, bool o_live, float scale_log2,
-                                                   float& m, float& l, WaitPV&& wait_pv) {
+                                                   int valid, bool o_live, bool row_ok,
+                                                   float scale_log2, float& m, float& l,
+                                                   WaitPV&& wait_pv) {
   if (__any_sync(0xffffffffu, valid < BKV)) {
 #pragma unroll
     for (int c = 0; c < 128; ++c)
@@ -202,7 +208,7 @@ __device__ __forceinline__ bool softmax_tile_paged(uint32_t (&sr)[128], uint32_t
   }
   const float mx = max3f(ma, mb, fmaxf(mc, md)) * scale_log2;
   bool pv_done = !o_live;
-  if (__any_sync(0xffffffffu, mx > m + RESCALE_THRESHOLD)) {
+  if (__any_sync(0xffffffffu, row_ok && mx > m + RESCALE_THRESHOLD)) {
     const float m_new = fmaxf(m, mx);
     const float alpha = m_new == m ? 1.0f : ex2_approx(m - m_new);  // 0 from -inf
     l *= alpha;
@@ -247,8 +253,78 @@ __device__ __forceinline__ bool softmax_tile_paged(uint32_t (&sr)[128], uint32_t
   return true;
 }
 
+// Writes 64 bytes (four 16-byte units, w) of every lane's row at byte `at`, with
+// stores of 64 bytes of eight rows each: one that takes 16 bytes of 32 rows
+// touches 32 lines and holds the load/store unit for as many cycles. For
+// PA_FEW_ROWS rows of a warp and fewer there is nothing to gain.
+// How:
+// groups of four lanes transpose their units, then to[j] (the row of lane j of
+// the group, at this lane's unit) gets what is now in unit j, for j < left.
+__device__ __forceinline__ void store_transposed(uint32_t (&w)[16], char* const (&to)[4], int left,
+                                                 int at) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s <= 2; ++s) {  // partner lane ^ s holds the other half of each pair of units
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & s) continue;
+      const bool hi = (lane & s) != 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t &lo_w = w[i * 4 + k], &hi_w = w[(i + s) * 4 + k];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? lo_w : hi_w, s);
+        if (hi)
+          lo_w = got;
+        else
+          hi_w = got;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < left)
+      *reinterpret_cast<uint4*>(to[j] + at) =
+          make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
+// A whole product of a key tile, eight instructions of K = 16, issued by one
+// elected lane of the warp from one asm block: an election and descriptors of
+// its own for each instruction are 45 machine instructions a piece here.
+// D[tmem] = A[smem] B[smem]^T, both K-major tiles of two 64-channel boxes.
+__device__ __forceinline__ void mma_ss8_el(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  static_assert(BOX_BYTES >> 4 == 1024, "descriptor offset of the second box");
+  asm volatile(
+      "{\n\t.reg .pred e, n, y;\n\t.reg .b64 u, v;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 n, 0, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
+#define H3_SS(pred) "@e tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, " pred ";\n\t"
+#define H3_AT(off) "add.s64 u, %1, " off ";\n\tadd.s64 v, %2, " off ";\n\t"
+      H3_AT("0") H3_SS("n") H3_AT("2") H3_SS("y") H3_AT("4") H3_SS("y") H3_AT("6") H3_SS("y")
+      H3_AT("1024") H3_SS("y") H3_AT("1026") H3_SS("y") H3_AT("1028") H3_SS("y") H3_AT("1030")
+      H3_SS("y") "}"
+#undef H3_SS
+#undef H3_AT
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem], B an MN-major tile (16 keys are 2 KB).
+__device__ __forceinline__ void mma_ts8_el(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, n, y;\n\t.reg .b64 v;\n\t.reg .b32 u;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %4, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
+#define H3_TS(i, pred)                                                          \
+  "add.s32 u, %1, 8 * " i ";\n\tadd.s64 v, %2, 128 * " i ";\n\t"               \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], v, %3, " pred ";\n\t"
+      H3_TS("0", "n") H3_TS("1", "y") H3_TS("2", "y") H3_TS("3", "y") H3_TS("4", "y")
+      H3_TS("5", "y") H3_TS("6", "y") H3_TS("7", "y") "}"
+#undef H3_TS
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
+                           const __grid_constant__ CUtensorMap tmQ1,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -260,11 +336,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PA_BARS + 1);
   Piece* ring = reinterpret_cast<Piece*>(ctrl + 384);   // [PA_PIECES]
-  Share* share = reinterpret_cast<Share*>(ctrl + 768);  // [2]
-  // scratch of the share search, where the first key tiles land later
-  int64_t* warp_sum = reinterpret_cast<int64_t*>(sKV);  // [PA_MAX_TEAM][warps]
-  static_assert((PA_BARS + 1) * 8 + 16 <= 384 && 384 + PA_PIECES * sizeof(Piece) <= 768 &&
-                    768 + 2 * sizeof(Share) <= PA_CTRL_BYTES,
+  static_assert((PA_BARS + 1) * 8 + 16 <= 384 && 384 + PA_PIECES * sizeof(Piece) <= PA_CTRL_BYTES,
                 "control region");
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int warp = threadIdx.x >> 5;
@@ -276,79 +348,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     for (int i = 0; i < PA_BARS; ++i) {
       uint32_t count = 1;
       if (i >= PA_SFREE && i < PA_PVD) count = 4;
-      if (i >= PA_PC_EMPTY && i < PA_DRAIN) count = 10;
+      if (i >= PA_PC_EMPTY && i < PA_DRAIN) count = 11;
       mbar_init(bar(i), count);
     }
     fence_mbar_init();
+  }
+  if (threadIdx.x == PA_THREADS - 32) {
+    tma_prefetch_desc(&tmQ1);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmQ);
   }
   if (warp == 9) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  // this CTA's share of each segment: every thread sums the tiles of a run of
-  // sequences, for each team size; then the thread whose run holds the share's
-  // first tile finds its sequence
-  constexpr int WARPS = PA_THREADS / 32;
-  const int first_seg = a.prefix_len > 0 ? 0 : 1;
-  const int most = a.b.T > 2 * a.tok ? PA_MAX_TEAM : 1;
-  for (int seg = first_seg; seg < 2; ++seg) {
-    const int n = seg == 0 ? 1 : a.b.B;
-    const int run = (n + PA_THREADS - 1) / PA_THREADS;
-    const int b0 = min(static_cast<int>(threadIdx.x) * run, n), b1 = min(b0 + run, n);
-    int64_t mine[PA_MAX_TEAM] = {};
-    for (int b = b0; b < b1; ++b) {
-      const SeqInfo s = seq_info(a, seg, b);
-#pragma unroll
-      for (int g = 1; g <= PA_MAX_TEAM; ++g)
-        if (g <= most) mine[g - 1] += head_tiles(a, seg, s, g) * a.Hkv;
-    }
-    __syncthreads();  // warp_sum of the previous segment has been read
-    if (threadIdx.x == 0) share[seg] = Share{0, 0, 1, 0, 1};
-#pragma unroll
-    for (int g = 0; g < PA_MAX_TEAM; ++g) {
-      if (g >= most) break;
-      int64_t v = mine[g];
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-      if (lane == 0) warp_sum[g * WARPS + warp] = v;
-    }
-    __syncthreads();
-    int64_t W[PA_MAX_TEAM] = {};
-#pragma unroll
-    for (int g = 0; g < PA_MAX_TEAM; ++g) {
-      if (g >= most) break;
-      for (int i = 0; i < WARPS; ++i) W[g] += warp_sum[g * WARPS + i];
-    }
-    const int team = pick_team(W, a.ctas, most);
-    int64_t total = 0, own = 0, at = 0;
-#pragma unroll
-    for (int g = 0; g < PA_MAX_TEAM; ++g)
-      if (g + 1 == team) total = W[g], own = mine[g];
-    for (int i = 0; i < warp; ++i) at += warp_sum[(team - 1) * WARPS + i];
-    int64_t incl = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
-    }
-    at += incl - own;
-    const int teams = a.ctas / team;
-    const int64_t per = max((total + teams - 1) / teams, int64_t{1});
-    const int64_t begin = (blockIdx.x / team) * per;
-    const int64_t end = min(begin + per, total);
-    if (begin < end && begin >= at && begin < at + own && blockIdx.x / team < teams) {
-      for (int b = b0; b < b1; ++b) {
-        const int64_t tiles = head_tiles(a, seg, seq_info(a, seg, b), team) * a.Hkv;
-        if (begin < at + tiles) {
-          share[seg] = Share{end - begin, begin - at, per, b, team};
-          break;
-        }
-        at += tiles;
-      }
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.teams[seg] = team;
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // warp_sum, before TMA writes there
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -357,6 +371,65 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PA_REGS_OTHER));
     if (warp == 10) {
       // ------------------------------------------------------- the share
+      // Every lane sums the cost of a run of sequences; the lane whose run holds
+      // the share's beginning finds where. Teams are of the size with the least
+      // time, a tile of a lone CTA taken as 6 and of a team's as 5: a 64 KB key
+      // tile takes a CTA about 2,300 cycles of products for two query tiles, and
+      // about 2,800 where every CTA reads it from HBM for itself. (Loops are
+      // kept rolled: the instruction cache is short for this kernel.)
+      const int most = a.b.T > 2 * a.tok ? min(PA_MAX_TEAM, a.ctas) : 1;
+      auto find_share = [&](int seg) {
+        const int n = seg == 0 ? 1 : a.b.B;
+        const int run = (n + 31) / 32;
+        const int b0 = min(lane * run, n), b1 = min(b0 + run, n);
+        Share sh{0, 0, 1, 0, 1};
+        int64_t total = 0, mine = 0;
+        float least = 0.f;
+#pragma unroll 1
+        for (int g = 1; g <= most; ++g) {
+          int64_t own = 0;
+#pragma unroll 1
+          for (int b = b0; b < b1; ++b) own += head_cost(a, seg, seq_info(a, seg, b), g);
+          own *= a.Hkv;
+          int64_t W = own;
+#pragma unroll
+          for (int d = 16; d >= 1; d >>= 1) W += __shfl_xor_sync(0xffffffffu, W, d);
+          const float cost = ceilf(static_cast<float>(W) / static_cast<float>(a.ctas / g)) *
+                             (g == 1 ? 6.f : 5.f);
+          if (g == 1 || cost < least) {
+            least = cost;
+            total = W;
+            mine = own;
+            sh.g = g;
+          }
+        }
+        const int teams = a.ctas / sh.g, team = static_cast<int>(blockIdx.x) / sh.g;
+        sh.per = max(div64(total + teams - 1, teams), int64_t{1});
+        const int64_t begin = team * sh.per;
+        if (team >= teams || begin >= total) return sh;
+        sh.cost = min(sh.per, total - begin);
+        int64_t at = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, at, d);
+          if (lane >= d) at += v;
+        }
+        at -= mine;
+        const uint32_t who = __ballot_sync(0xffffffffu, begin >= at && begin < at + mine);
+        int b = b0;
+        if (who >> lane & 1u) {
+#pragma unroll 1
+          for (; b < b1; ++b) {
+            const int64_t c = head_cost(a, seg, seq_info(a, seg, b), sh.g) * a.Hkv;
+            if (begin < at + c) break;
+            at += c;
+          }
+        }
+        const int src = __ffs(who) - 1;
+        sh.b = __shfl_sync(0xffffffffu, b, src & 31);
+        sh.at = begin - __shfl_sync(0xffffffffu, at, src & 31);
+        return sh;
+      };
       int np = 0;
       auto post = [&](const Piece& p) {
         const int r = np % PA_PIECES;
@@ -372,16 +445,20 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         return true;
       };
       bool ok = true;
+      const int first_seg = a.prefix_len > 0 ? 0 : 1;
       for (int seg = first_seg; ok && seg < 2; ++seg) {
-        const Share sh = share[seg];
+        const Share sh = find_share(seg);
+        if (blockIdx.x == 0 && lane == 0) a.teams[seg] = sh.g;
         const int member = static_cast<int>(blockIdx.x) % sh.g;
         const int item = 2 * a.tok;
         const int n = seg == 0 ? 1 : a.b.B;
         int4 cut = make_int4(0, 0, 0, 0);
-        int64_t left = sh.tiles;
-        int b = sh.b, hk = 0, qg = 0, kt = 0, items = 0, groups = 0;
+        int64_t left = sh.cost;
+        int b = sh.b, hk = 0, qg = 0, u = 0, items = 0, groups = 0;  // u: unit of the item
         SeqInfo s{};
-        auto group_tiles = [&]() { return key_tiles(s, min((qg + 1) * item * sh.g, s.q_len)); };
+        auto group_cost = [&]() {
+          return key_tiles(s, min((qg + 1) * item * sh.g, s.q_len)) + PA_ITEM_COST;
+        };
         auto enter = [&]() {
           s = seq_info(a, seg, b);
           items = (s.q_len + item - 1) / item;
@@ -389,31 +466,35 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         };
         if (left > 0) {
           enter();
-          const int64_t per_head = max(head_tiles(a, seg, s, sh.g), int64_t{1});
-          hk = static_cast<int>(sh.at / per_head);
+          const int64_t per_head = max(head_cost(a, seg, s, sh.g), int64_t{1});
+          hk = static_cast<int>(div64(sh.at, per_head));
           int64_t r = sh.at - hk * per_head;
           if (!uneven(a, seg)) {
-            const int nk = group_tiles();
-            qg = static_cast<int>(r / nk);
+            const int nk = group_cost();
+            qg = static_cast<int>(div64(r, nk));
             r -= static_cast<int64_t>(qg) * nk;
           } else {
-            for (int nk = group_tiles(); r >= nk && qg + 1 < groups; nk = group_tiles()) {
+            for (int nk = group_cost(); r >= nk && qg + 1 < groups; nk = group_cost()) {
               r -= nk;
               ++qg;
             }
           }
-          kt = static_cast<int>(r);
+          u = static_cast<int>(r);
         }
         while (ok && left > 0) {
-          const int take = static_cast<int>(min(static_cast<int64_t>(group_tiles() - kt), left));
+          const bool small = group_cost() <= PA_WHOLE + PA_ITEM_COST;
+          const int rest = group_cost() - u;
+          const int take = small ? rest : static_cast<int>(min(static_cast<int64_t>(rest), left));
           const int qt = qg * sh.g + member;
           const int nk = key_tiles(s, min((qt + 1) * item, s.q_len));  // of this CTA's item
-          if (qt < items && kt < nk) {
+          const int kt0 = small ? 0 : max(u - PA_ITEM_COST, 0);
+          const int kt1 = min(max(u + take - PA_ITEM_COST, 0), nk);
+          if (qt < items && kt0 < kt1 && !(small && u > 0)) {
             Piece p{};
             p.hk = hk;
             p.b = seg == 0 ? -1 : b;
-            p.kt0 = kt;
-            p.kt1 = min(kt + take, nk);
+            p.kt0 = kt0;
+            p.kt1 = kt1;
             p.tok0 = s.c0 + qt * item;
             p.ntok = min(item, s.q_len - qt * item);
             p.kv = s.kv;
@@ -424,7 +505,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                             : (first_seg == 0 ? -2 - seg : -1);
             if (p.kt0 == 0) {
               // the shares that the rest of the item falls into
-              const int more = static_cast<int>((nk - p.kt1 + sh.per - 1) / sh.per);
+              const int more = static_cast<int>(div64(nk - p.kt1 + sh.per - 1, sh.per));
               const int last = static_cast<int>(blockIdx.x) + more * sh.g;
               if (!whole) cut = make_int4(p.tok0, p.ntok, hk, last);
               if (first_seg == 0 && lane == 0)
@@ -434,7 +515,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             ok = post(p);
           }
           left -= take;
-          kt = 0;
+          u += take;
+          if (u < group_cost()) break;  // the end of the share
+          u = 0;
           if (++qg == groups) {
             qg = 0;
             if (++hk == a.Hkv) {
@@ -450,28 +533,19 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       if (ok) post(Piece{});
     } else if (warp == 8) {
       // ------------------------------------------------------- TMA loads
-      if (lane == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-      }
       const int nbox = BKV >> a.b.page_log2;  // pages of a key tile
       const int box = lane & (nbox - 1), half = lane / nbox;
       const uint32_t box_dst = half * BOX_BYTES + ((box << a.b.page_log2) << 7);
-      const uint32_t q_bytes = static_cast<uint32_t>(a.tok * a.G) * 256;
-      int np = 0, seq = 0;
-      uint32_t q_phase = 3, q_used = 0;  // per query tile: parity of Q_EMPTY; loaded at all
+      int np = 0;
       bool ok = true;
       struct Tile {
         int kt, kt1, kv, hk;
         const int32_t* pages;
-        int tok0, groups;  // of a piece's first tile: first token, query tiles (bit i: tile i)
-        int page;          // this lane's page, -1: none
+        int page;  // this lane's page, -1: none
       };
       // the key tile after d (of the next piece when d is its piece's last),
       // with the lane's page on its way; false: no more, or a wait failed
       auto advance = [&](Tile& d) {
-        d.groups = 0;
         if (++d.kt >= d.kt1) {
           const int r = np % PA_PIECES;
           if (!mbar_wait_warp(bar(PA_PC_FULL + r), (np / PA_PIECES) & 1, a.err,
@@ -483,13 +557,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           d.kt1 = p.kt1;
           d.kv = p.kv;
           d.hk = p.hk;
-          d.tok0 = p.tok0;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
           if (ntok == 0) return false;
           d.pages = b < 0 ? a.prefix_pages
                           : a.b.page_table + static_cast<int64_t>(b) * a.b.max_pages;
-          d.groups = ntok > a.tok ? 3 : 1 << (np & 1);
           ++np;
         }
         // a page is loaded when it begins below the sequence's end
@@ -498,62 +570,96 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                                                                               : -1;
         return true;
       };
-      Tile nxt{};
-      bool more = advance(nxt);
-      while (ok && more) {
-        const Tile cur = nxt;
-        more = advance(nxt);
-        if (!ok) break;
-        for (int g = 0; ok && g < 2; ++g) {
-          if (!(cur.groups >> g & 1)) continue;
-          ok = mbar_wait_warp(bar(PA_Q_EMPTY + g), q_phase >> g & 1u, a.err, ERR_WAIT_ATTN_PRODUCER);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(PA_Q_FULL + g), q_bytes);
-            const uint32_t dst = smem_u32(sQ + g * TILE_BYTES);
-            const int t0 = cur.tok0 + (cur.groups == 3 ? g * a.tok : 0);
-            tma_load_3d(dst, &tmQ, bar(PA_Q_FULL + g), 0, cur.hk * a.G, t0);
-            tma_load_3d(dst + BOX_BYTES, &tmQ, bar(PA_Q_FULL + g), 64, cur.hk * a.G, t0);
-          }
-          __syncwarp();
-          q_phase ^= 1u << g;
-          q_used |= 1u << g;
-        }
-        if (!ok) break;
-        const int live =
-            min(nbox, (cur.kv - cur.kt * BKV + (1 << a.b.page_log2) - 1) >> a.b.page_log2);
+      uint32_t used = 0, parity = 0;  // per slot: loaded at all; phase of its last load
+      // K or V of key tile d, the seq-th load
+      auto load = [&](const Tile& d, const CUtensorMap* map, int seq) {
+        const int live = min(nbox, (d.kv - d.kt * BKV + (1 << a.b.page_log2) - 1) >> a.b.page_log2);
         const uint32_t bytes = static_cast<uint32_t>(max(live, 0)) << (a.b.page_log2 + 8);
         // a page outside the pool: a row past the map's end, which loads zeros
-        const int row = cur.page >= 0 && cur.page < a.b.num_pages
-                            ? (cur.page * a.Hkv + cur.hk) << a.b.page_log2
+        const int row = d.page >= 0 && d.page < a.b.num_pages
+                            ? (d.page * a.Hkv + d.hk) << a.b.page_log2
                             : a.total_rows;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++seq) {
-          const int slot = seq % PA_SLOTS;
-          ok = mbar_wait_warp(bar(PA_KV_EMPTY + slot), ((seq / PA_SLOTS) & 1) ^ 1, a.err,
-                              ERR_WAIT_ATTN_PRODUCER);
-          if (!ok) break;
-          const uint32_t full = bar(PA_KV_FULL + slot);
-          if (lane == 0) {
-            if (bytes > 0)
-              mbar_arrive_expect_tx(full, bytes);
-            else
-              mbar_arrive(full);
-          }
-          __syncwarp();
-          if (half < 2 && box < live)
-            tma_load_2d(smem_u32(sKV + slot * TILE_BYTES) + box_dst, kv ? &tmV : &tmK, full,
-                        half * 64, row);
+        const int slot = seq % PA_SLOTS;
+        if (!mbar_wait_warp(bar(PA_KV_EMPTY + slot), ((seq / PA_SLOTS) & 1) ^ 1, a.err,
+                            ERR_WAIT_ATTN_PRODUCER))
+          return false;
+        const uint32_t full = bar(PA_KV_FULL + slot);
+        if (lane == 0) {
+          if (bytes > 0)
+            mbar_arrive_expect_tx(full, bytes);
+          else
+            mbar_arrive(full);
         }
+        __syncwarp();
+        used |= 1u << slot;
+        parity = (parity & ~(1u << slot)) | static_cast<uint32_t>((seq / PA_SLOTS) & 1) << slot;
+        if (half < 2 && box < live)
+          tma_load_2d(smem_u32(sKV + slot * TILE_BYTES) + box_dst, map, full, half * 64, row);
+        return true;
+      };
+      Tile cur{}, nxt{};
+      int t = 0;  // key tiles loaded
+      bool more = advance(nxt);
+      if (more) ok = load(nxt, &tmK, k_seq(0));
+      while (ok && more) {
+        cur = nxt;
+        more = advance(nxt);
+        ok = ok && (!more || load(nxt, &tmK, k_seq(t + 1))) && load(cur, &tmV, v_seq(t));
+        ++t;
       }
       // no copy of this CTA may still be landing when it exits
       if (lane == 0) {
         const uint64_t t0 = globaltimer_ns();
         const uint64_t lim = drain_limit_ns(a.err);
+        for (int slot = 0; slot < PA_SLOTS; ++slot)
+          if (used >> slot & 1u) mbar_wait_drain(bar(PA_KV_FULL + slot), parity >> slot & 1u, t0, lim);
+      }
+    } else if (warp == 11) {
+      // ------------------------------------------------------ query tiles
+      // a query tile of few tokens is loaded token by token (tmQ1): the box of a
+      // whole tile would read up to 128 rows for one (64 single rows behind a
+      // shared prefix, 42 heads: its loads held up those of the keys)
+      uint32_t phase = 3, used = 0;  // per query tile: parity of Q_EMPTY; loaded at all
+      bool ok = true;
+      for (int np = 0; ok; ++np) {
+        const int r = np % PA_PIECES;
+        if (!mbar_wait_warp(bar(PA_PC_FULL + r), (np / PA_PIECES) & 1, a.err,
+                            ERR_WAIT_ATTN_PRODUCER))
+          break;
+        const int tok0 = ring[r].tok0, ntok = ring[r].ntok, hk = ring[r].hk;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
+        if (ntok == 0) break;
+        const bool two = ntok > a.tok;
+        for (int g = two ? 0 : np & 1; g <= (two ? 1 : np & 1); ++g) {
+          ok = mbar_wait_warp(bar(PA_Q_EMPTY + g), phase >> g & 1u, a.err, ERR_WAIT_ATTN_PRODUCER);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t dst = smem_u32(sQ + g * TILE_BYTES), full = bar(PA_Q_FULL + g);
+            const int t0 = tok0 + g * (two ? a.tok : 0);
+            const int n = min(ntok - (t0 - tok0), a.tok);
+            if (n <= PA_FEW_TOKENS) {
+              mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * a.G) * 256);
+              for (int i = 0; i < n; ++i) {
+                tma_load_3d(dst + i * a.G * 128, &tmQ1, full, 0, hk * a.G, t0 + i);
+                tma_load_3d(dst + i * a.G * 128 + BOX_BYTES, &tmQ1, full, 64, hk * a.G, t0 + i);
+              }
+            } else {
+              mbar_arrive_expect_tx(full, static_cast<uint32_t>(a.tok * a.G) * 256);
+              tma_load_3d(dst, &tmQ, full, 0, hk * a.G, t0);
+              tma_load_3d(dst + BOX_BYTES, &tmQ, full, 64, hk * a.G, t0);
+            }
+          }
+          __syncwarp();
+          phase ^= 1u << g;
+          used |= 1u << g;
+        }
+      }
+      if (lane == 0) {  // no copy may still be landing when the CTA exits
+        const uint64_t t0 = globaltimer_ns();
         for (int g = 0; g < 2; ++g)
-          if (q_used >> g & 1u) mbar_wait_drain(bar(PA_Q_FULL + g), q_phase >> g & 1u, t0, lim);
-        for (int i = max(seq - PA_SLOTS, 0); i < seq; ++i)
-          mbar_wait_drain(bar(PA_KV_FULL + i % PA_SLOTS), (i / PA_SLOTS) & 1, t0, lim);
+          if (used >> g & 1u)
+            mbar_wait_drain(bar(PA_Q_FULL + g), phase >> g & 1u, t0, drain_limit_ns(a.err));
       }
     } else if (warp == 9) {
       // ------------------------------------------------------ MMA issuer
@@ -571,10 +677,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         return done;
       };
       static_assert(PA_PVD <= 32, "a bit per barrier");
-      // 16-byte offset of K step kk (16 channels) in a K-major tile
-      auto kmaj = [](int kk) {
-        return static_cast<uint32_t>(((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4);
-      };
       struct Tile {
         int g0;  // query tile, or the first of two
         bool two, first, last;
@@ -607,8 +709,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         d.last = --left == 0;
         return true;
       };
-      // slots of the next K_t and V_t to be used: every other one of the ring
-      int k_slot = 0, v_slot = 1;
+      // slots of the next K_t and V_t to be used: from K_1 and V_0 on every
+      // other one of the ring
+      int k_slot = k_seq(0), v_slot = v_seq(0);
+      bool k_first = true;
       auto step = [](int& slot) { slot += slot < PA_SLOTS - 2 ? 2 : 2 - PA_SLOTS; };
       int last_s = -1;  // query tile whose S is in the buffer
       auto qk = [&](int g, int prev, bool lead, bool tail, bool first, bool last) {  // S = Q_g K_t^T
@@ -618,14 +722,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         tc_fence_after();
         const uint64_t qd = dq + static_cast<uint32_t>(g * (TILE_BYTES >> 4));
         const uint64_t kd = dk + static_cast<uint32_t>(k_slot * (TILE_BYTES >> 4));
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          mma_ss_el(tmem + TPA_S, qd + kmaj(kk), kd + kmaj(kk), idesc_qk, kk > 0 ? 1u : 0u);
+        mma_ss8_el(tmem + TPA_S, qd, kd, idesc_qk);
         mma_commit_el(bar(PA_S + g));
         if (last) mma_commit_el(bar(PA_Q_EMPTY + g));
         if (tail) {
           mma_commit_el(bar(PA_KV_EMPTY + k_slot));
-          step(k_slot);
+          if (k_first)
+            k_slot = k_seq(1), k_first = false;
+          else
+            step(k_slot);
         }
         return true;
       };
@@ -634,10 +739,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (!wait(PA_P + g)) return false;
         tc_fence_after();
         const uint64_t vd = dv + static_cast<uint32_t>(v_slot * (TILE_BYTES >> 4));
-        const uint32_t to = tmem + TPA_O + g * 128, tp = tmem + TPA_P + g * 64;
-#pragma unroll
-        for (int kk = 0; kk < BKV / 16; ++kk)
-          mma_ts_el(to, tp + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1u : acc);
+        mma_ts8_el(tmem + TPA_O + g * 128, tmem + TPA_P + g * 64, vd, idesc_pv, acc);
         mma_commit_el(bar(PA_PVD + g));
         if (tail) {
           mma_commit_el(bar(PA_KV_EMPTY + v_slot));
@@ -645,21 +747,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         }
         return true;
       };
-      auto qk_of = [&](const Tile& d, int g) {
-        const int prev = last_s;
-        last_s = g;
-        return qk(g, prev, g == d.g0, !d.two || g == 1, d.first, d.last);
-      };
-      auto pv_of = [&](const Tile& d, int g) {
-        return pv(g, g == d.g0, !d.two || g == 1, d.first ? 0u : 1u);
-      };
-      Tile cur, nxt;
-      bool more = next_tile(cur);
-      if (more) ok = qk_of(cur, cur.g0) && (!cur.two || qk_of(cur, 1));
       // Q K^T of the next key tile before P V of this one; with two query tiles
       // their products alternate, so one's softmax overlaps the other's products
-      while (ok && more) {
-        if (cur.two && left >= 2) {
+      Tile cur{}, nxt{};
+      bool have = false, more = true;  // cur, nxt exist
+      while (ok) {
+        if (have && cur.two && left >= 2) {
           // the next key tile is of the same piece and not its last: the same
           // four products with everything but the slots known
           uint32_t acc = cur.first ? 0u : 1u;
@@ -673,11 +766,26 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           continue;
         }
         more = next_tile(nxt);
-        if (!ok) break;
-        ok = (!more || qk_of(nxt, nxt.g0)) && pv_of(cur, cur.g0);
-        if (ok && more && nxt.two) ok = qk_of(nxt, 1);
-        if (ok && cur.two) ok = pv_of(cur, 1);
+        if (!ok || !(have || more)) break;
+        // a new piece on a query tile that is still in use: its output first
+        const bool out_first = have && more && nxt.first && (cur.two || nxt.two);
+#pragma unroll 1
+        for (int i = 0; ok && i < 4; ++i) {
+          const bool is_qk = out_first ? i >= 2 : (i & 1) == 0;
+          const int second = out_first ? i & 1 : i >> 1;
+          if (is_qk) {
+            if (more && (!second || nxt.two)) {
+              const int g = second ? 1 : nxt.g0, prev = last_s;
+              last_s = g;
+              ok = qk(g, prev, !second, second || !nxt.two, nxt.first, nxt.last);
+            }
+          } else if (have && (!second || cur.two)) {
+            ok = pv(second ? 1 : cur.g0, !second, second || !cur.two, cur.first ? 0u : 1u);
+          }
+        }
         cur = nxt;
+        have = more;
+        if (!have) break;
       }
       // every product must be done with shared and tensor memory before the CTA
       // frees them: commit and wait, bounded
@@ -724,16 +832,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       auto clear_values = [&](int kt) {
         const int live = p.kv - kt * BKV;  // keys of the tile that exist
         if (live >= BKV) return true;
-        const int seq = 2 * tiles + 1, slot = seq % PA_SLOTS;
+        const int seq = v_seq(tiles), slot = seq % PA_SLOTS;
         if (!mbar_wait_warp(bar(PA_KV_FULL + slot), (seq / PA_SLOTS) & 1, a.err,
                             ERR_WAIT_ATTN_SOFTMAX))
           return false;
-        if (row >= live) {
-          uint4* v = reinterpret_cast<uint4*>(sKV + slot * TILE_BYTES + row * 128);
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i)
-            v[i] = v[BOX_BYTES / 16 + i] = make_uint4(0, 0, 0, 0);
-        }
+        // eight lanes per 128-byte half of a row
+        uint4* v = reinterpret_cast<uint4*>(sKV + slot * TILE_BYTES) + (lane & 7);
+        for (int r = max(live, 0) + quarter * 4 + (lane >> 3); r < BKV; r += 16)
+          v[r * 8] = v[BOX_BYTES / 16 + r * 8] = make_uint4(0, 0, 0, 0);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         return true;
       };
@@ -773,7 +879,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(PA_SFREE + tile));
-          ok = softmax_tile_paged(sr, tP, tO, lim - kt * BKV, kt > p.kt0, a.scale_log2, m, l,
+          ok = softmax_tile_paged(sr, tP, tO, lim - kt * BKV, kt > p.kt0, row < rows,
+                                  a.scale_log2, m, l,
                                   [&] { return wait_pv(n - 1); }) &&
                clear_values(kt);
           if (!ok) break;
@@ -784,51 +891,81 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (!ok || !wait_pv(n - 1)) break;
       if (!active) continue;
-      const bool row_ok = row < rows;
       const int64_t orow = static_cast<int64_t>(p.tok0 + tok);
       const int head = p.hk * a.G + row % a.G;
+      char* dst;
       if (p.dest == -1) {
-        const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key: zeros
-        __nv_bfloat16* dst = a.o + orow * a.ld_o + head * DH;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t ov[16], pk[8];
-          tmem_ld16(tO + c * 16, ov);
-          tmem_ld_wait();
-          tmem_reg_fence(ov);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
-          if (row_ok) {
-            reinterpret_cast<uint4*>(dst)[2 * c] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            reinterpret_cast<uint4*>(dst)[2 * c + 1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          }
-        }
+        dst = reinterpret_cast<char*>(a.o + orow * a.ld_o + head * DH);
       } else {
-        float *po, *pml;
+        int64_t at;
+        float* ml;
         if (p.dest >= 0) {
-          const int64_t at = static_cast<int64_t>(p.dest) * a.part_rows + tok0 * a.G + row;
-          po = a.part_o + at * DH;
-          pml = a.part_ml + at * 2;
+          at = static_cast<int64_t>(p.dest) * a.part_rows + tok0 * a.G + row;
+          dst = reinterpret_cast<char*>(a.part_o + at * DH);
+          ml = a.part_ml;
         } else {
-          const int64_t at = (static_cast<int64_t>(-2 - p.dest) * a.b.T + orow) * a.H + head;
-          po = a.row_o + at * DH;
-          pml = a.row_ml + at * 2;
+          at = (static_cast<int64_t>(-2 - p.dest) * a.b.T + orow) * a.H + head;
+          dst = reinterpret_cast<char*>(a.row_o + at * DH);
+          ml = a.row_ml;
         }
+        if (row < rows) *reinterpret_cast<float2*>(ml + at * 2) = make_float2(m, l);
+      }
+      const float inv = p.dest == -1 ? (l == 0.f ? 0.f : 1.0f / l) : 1.0f;  // no key: zeros
+      if (rows - quarter * 32 <= PA_FEW_ROWS) {
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           uint32_t ov[16];
           tmem_ld16(tO + c * 16, ov);
           tmem_ld_wait();
           tmem_reg_fence(ov);
-          if (row_ok) {
+          if (row < rows) {
+            uint4* to = reinterpret_cast<uint4*>(dst);
+            if (p.dest == -1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<uint4*>(po)[4 * c + i] =
-                  make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+              for (int i = 0; i < 8; ++i)
+                ov[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv,
+                                    __uint_as_float(ov[2 * i + 1]) * inv);
+              to[2 * c] = make_uint4(ov[0], ov[1], ov[2], ov[3]);
+              to[2 * c + 1] = make_uint4(ov[4], ov[5], ov[6], ov[7]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                to[4 * c + i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+            }
           }
         }
-        if (row_ok) *reinterpret_cast<float2*>(pml) = make_float2(m, l);
+      } else {
+        char* to[4];  // the four lanes' rows, at this lane's unit
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          to[j] = reinterpret_cast<char*>(
+                      __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst),
+                                  (lane & ~3) + j)) + (lane & 3) * 16;
+        const int have = rows - (row & ~3);  // rows of the four that exist
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t ov[16];
+          tmem_ld16(tO + c * 16, ov);
+          tmem_ld_wait();
+          tmem_reg_fence(ov);
+          if (p.dest == -1) {  // 32 columns to 64 bytes
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv,
+                                 __uint_as_float(ov[2 * i + 1]) * inv);
+            tmem_ld16(tO + ++c * 16, ov);
+            tmem_ld_wait();
+            tmem_reg_fence(ov);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[8 + i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv,
+                                     __uint_as_float(ov[2 * i + 1]) * inv);
+            store_transposed(w, to, have, (c >> 1) * 64);
+          } else {
+            store_transposed(ov, to, have, c * 64);
+          }
+        }
       }
       // O has been read before a later piece's P V overwrites it
       tc_fence_before();
@@ -1039,14 +1176,16 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   a.row_ml = reinterpret_cast<float*>(base + w.row_ml);
   a.ctas = std::min(num_sms(), PA_MAX_CTAS);
   if ((st = dev_err(&a.err)) != H3_OK) return st;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tq1, tk, tv;
   const uint32_t page = 1u << batch.page_log2;
   if ((st = make_tmap_bf16_3d(&tq, q, DH, H, batch.T, DH * 2, static_cast<uint64_t>(ld_q) * 2, 64,
                               a.G, a.tok)) != H3_OK ||
+      (st = make_tmap_bf16_3d(&tq1, q, DH, H, batch.T, DH * 2, static_cast<uint64_t>(ld_q) * 2, 64,
+                              a.G, 1)) != H3_OK ||
       (st = make_tmap_bf16_2d(&tk, k_cache, DH, a.total_rows, DH * 2, 64, page)) != H3_OK ||
       (st = make_tmap_bf16_2d(&tv, v_cache, DH, a.total_rows, DH * 2, 64, page)) != H3_OK)
     return st;
-  paged_attention_kernel<<<a.ctas, PA_THREADS, PA_SMEM_BYTES, s>>>(tq, tk, tv, a);
+  paged_attention_kernel<<<a.ctas, PA_THREADS, PA_SMEM_BYTES, s>>>(tq, tq1, tk, tv, a);
   if ((st = cuda_fail(cudaGetLastError(), "paged attention launch")) != H3_OK) return st;
   // the join kernel's blocks may take their places while the first kernel
   // runs; they wait for its end before they read anything

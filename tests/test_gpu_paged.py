@@ -209,6 +209,20 @@ def test_many_sequences_of_one_key(h3lib):
     run_attention(h3lib, [1] * 700, [1] * 700, 2, 2, 16)
 
 
+def test_no_wait_runs_out_at_the_end_of_a_call(h3lib):
+    # many key tiles per SM: a wait for copies that have long landed would show
+    # as its 2 s limit
+    P = Paged([20000, 7000, 12345], 8, 16, k_std=1.0)
+    q = rnd(gen(40), 3, 8, DH)
+    attend(h3lib, q, P, [0, 1, 2, 3])
+    e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    e[0].record()
+    attend(h3lib, q, P, [0, 1, 2, 3])
+    e[1].record()
+    torch.cuda.synchronize()
+    assert e[0].elapsed_time(e[1]) < 500
+
+
 def test_empty_sequences_and_masked_rows(h3lib):
     # sequences without rows, without keys, with more rows than keys (causal:
     # the first rows see nothing and give zeros)
