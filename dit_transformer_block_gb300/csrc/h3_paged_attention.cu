@@ -44,7 +44,7 @@ __device__ __forceinline__ int v_seq(int t) { return 2 * t + 2; }
 constexpr int PA_PIECES = 8;   // pieces posted ahead
 constexpr int PA_MAX_CTAS = 160;
 constexpr int PA_CTRL_BYTES = 1024;
-constexpr int PA_FEW_TOKENS = 4, PA_FEW_ROWS = 8;
+constexpr int PA_FEW_TOKENS = 4, PA_FEW_ROWS = 8, PA_QUAD_ROWS = 8;
 // 12 warps: with three on each SM sub-partition the launch gives every thread
 // 168 registers; warps 8-11 hand most of theirs to the softmax warps, which
 // hold a row's 128 scores and 64 packed weights (168: 508 bytes of spills)
@@ -58,14 +58,15 @@ enum BarPA {
   PA_KV_FULL = 0,
   PA_KV_EMPTY = PA_KV_FULL + PA_SLOTS,
   PA_Q_FULL = PA_KV_EMPTY + PA_SLOTS,
-  PA_Q_EMPTY = PA_Q_FULL + 2,
+  PA_Q_EMPTY = PA_Q_FULL + 2,  // last Q K^T done (commit), its shared memory not needed (4 warps)
   PA_S = PA_Q_EMPTY + 2,       // S written for query tile i (MMA commit)
   PA_SFREE = PA_S + 2,         // S read by its softmax (4 warp arrivals)
   PA_P = PA_SFREE + 2,         // P_i written (4 warp arrivals)
   PA_PVD = PA_P + 2,           // P_i V done (MMA commit)
   PA_PC_FULL = PA_PVD + 2,     // piece posted
   PA_PC_EMPTY = PA_PC_FULL + PA_PIECES,  // piece read (8 softmax warps, MMA warp, loads)
-  PA_DRAIN = PA_PC_EMPTY + PA_PIECES,
+  PA_JOIN = PA_PC_EMPTY + PA_PIECES,     // a quarter's result is in shared memory (4 arrivals)
+  PA_DRAIN = PA_JOIN + 2,
   PA_BARS
 };
 constexpr uint32_t TPA_S = 0, TPA_O = 128, TPA_P = 384;
@@ -142,6 +143,7 @@ __device__ __forceinline__ int64_t head_cost(const PagedArgs& a, int seg, const 
   if (n == 0) return 0;
   if (!uneven(a, seg)) return static_cast<int64_t>(n) * (key_tiles(s, s.q_len) + PA_ITEM_COST);
   int64_t sum = static_cast<int64_t>(n) * PA_ITEM_COST;
+#pragma unroll 1
   for (int i = 1; i <= n; ++i) sum += key_tiles(s, min(i * item, s.q_len));
   return sum;
 }
@@ -253,6 +255,75 @@ __device__ __forceinline__ bool softmax_tile_paged(uint32_t (&sr)[128], uint32_t
   return true;
 }
 
+// The same for a piece of at most PA_QUAD_ROWS rows, which lie in all four lane
+// quarters of the query tile: warp w takes keys 32 w .. 32 w + 31 of the key
+// tile, with a maximum, sum and O of its own (its other weights in tensor memory
+// are 0); the four are joined when the piece ends. A quarter of the latency and
+// of the code of a warp that takes a row's 128 keys alone. The code counts: short
+// items run every path of this kernel once in a few microseconds, and it is
+// longer than what an SM keeps of it (64 rows of 256 keys, 42 heads: 64 % of the
+// instruction fetches hit in the SM's own cache before, 82 % after).
+template <class WaitPV, class FreeS>
+__device__ __forceinline__ bool softmax_tile_quad(uint32_t tS, uint32_t tP, uint32_t tO, int valid,
+                                                  bool o_live, bool row_ok, float scale_log2,
+                                                  float& m, float& l, WaitPV&& wait_pv,
+                                                  FreeS&& free_s) {
+  uint32_t x[32];
+  tmem_ld32(tS, x);
+  tmem_ld_wait();
+  tmem_reg_fence(x);
+  free_s();
+  if (__any_sync(0xffffffffu, valid < 32)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= valid) x[i] = 0xff800000u;
+  }
+  float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    ma = max3f(ma, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+    mb = max3f(mb, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+  }
+  const float mx = fmaxf(ma, mb) * scale_log2;
+  const bool raise = __any_sync(0xffffffffu, row_ok && mx > m + RESCALE_THRESHOLD);
+  float alpha = 1.0f;
+  if (raise) {
+    const float m_new = fmaxf(m, mx);
+    if (m_new != m) alpha = ex2_approx(m - m_new);  // 0 from -inf
+    l *= alpha;
+    m = m_new;
+  }
+  const float neg_m = m == -INFINITY ? 0.f : -m;
+  float la = 0.f, lb = 0.f;
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
+    ffma2_bc(x0, x1, __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), scale_log2, neg_m);
+    const float p0 = ex2_approx(x0);
+    const float p1 = ex2_approx(x1);
+    fadd2(la, lb, p0, p1);
+    pk[i] = pack_bf16x2(p0, p1);
+  }
+  l += la + lb;
+  if (o_live && !wait_pv()) return false;
+  if (raise && o_live) {
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 16) {
+      uint32_t ov[16];
+      tmem_ld16(tO + c, ov);
+      tmem_ld_wait();
+      tmem_reg_fence(ov);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+      tmem_st16(tO + c, ov);
+    }
+  }
+  tmem_st16(tP, pk);
+  tmem_st_wait();
+  return true;
+}
+
 // Writes 64 bytes (four 16-byte units, w) of every lane's row at byte `at`, with
 // stores of 64 bytes of eight rows each: one that takes 16 bytes of 32 rows
 // touches 32 lines and holds the load/store unit for as many cycles. For
@@ -287,41 +358,6 @@ __device__ __forceinline__ void store_transposed(uint32_t (&w)[16], char* const 
           make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-// A whole product of a key tile, eight instructions of K = 16, issued by one
-// elected lane of the warp from one asm block: an election and descriptors of
-// its own for each instruction are 45 machine instructions a piece here.
-// D[tmem] = A[smem] B[smem]^T, both K-major tiles of two 64-channel boxes.
-__device__ __forceinline__ void mma_ss8_el(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-  static_assert(BOX_BYTES >> 4 == 1024, "descriptor offset of the second box");
-  asm volatile(
-      "{\n\t.reg .pred e, n, y;\n\t.reg .b64 u, v;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 n, 0, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
-#define H3_SS(pred) "@e tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, " pred ";\n\t"
-#define H3_AT(off) "add.s64 u, %1, " off ";\n\tadd.s64 v, %2, " off ";\n\t"
-      H3_AT("0") H3_SS("n") H3_AT("2") H3_SS("y") H3_AT("4") H3_SS("y") H3_AT("6") H3_SS("y")
-      H3_AT("1024") H3_SS("y") H3_AT("1026") H3_SS("y") H3_AT("1028") H3_SS("y") H3_AT("1030")
-      H3_SS("y") "}"
-#undef H3_SS
-#undef H3_AT
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] B[smem], B an MN-major tile (16 keys are 2 KB).
-__device__ __forceinline__ void mma_ts8_el(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred e, n, y;\n\t.reg .b64 v;\n\t.reg .b32 u;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %4, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
-#define H3_TS(i, pred)                                                          \
-  "add.s32 u, %1, 8 * " i ";\n\tadd.s64 v, %2, 128 * " i ";\n\t"               \
-  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], v, %3, " pred ";\n\t"
-      H3_TS("0", "n") H3_TS("1", "y") H3_TS("2", "y") H3_TS("3", "y") H3_TS("4", "y")
-      H3_TS("5", "y") H3_TS("6", "y") H3_TS("7", "y") "}"
-#undef H3_TS
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmQ1,
@@ -348,7 +384,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     for (int i = 0; i < PA_BARS; ++i) {
       uint32_t count = 1;
       if (i >= PA_SFREE && i < PA_PVD) count = 4;
-      if (i >= PA_PC_EMPTY && i < PA_DRAIN) count = 11;
+      if (i >= PA_PC_EMPTY && i < PA_JOIN) count = 11;
+      if (i >= PA_JOIN && i < PA_DRAIN) count = 4;
+      if (i >= PA_Q_EMPTY && i < PA_S) count = 5;
       mbar_init(bar(i), count);
     }
     fence_mbar_init();
@@ -446,6 +484,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       };
       bool ok = true;
       const int first_seg = a.prefix_len > 0 ? 0 : 1;
+#pragma unroll 1
       for (int seg = first_seg; ok && seg < 2; ++seg) {
         const Share sh = find_share(seg);
         if (blockIdx.x == 0 && lane == 0) a.teams[seg] = sh.g;
@@ -474,6 +513,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             qg = static_cast<int>(div64(r, nk));
             r -= static_cast<int64_t>(qg) * nk;
           } else {
+#pragma unroll 1
             for (int nk = group_cost(); r >= nk && qg + 1 < groups; nk = group_cost()) {
               r -= nk;
               ++qg;
@@ -481,9 +521,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
           u = static_cast<int>(r);
         }
+#pragma unroll 1
         while (ok && left > 0) {
-          const bool small = group_cost() <= PA_WHOLE + PA_ITEM_COST;
-          const int rest = group_cost() - u;
+          const int cost = group_cost();
+          const bool small = cost <= PA_WHOLE + PA_ITEM_COST;
+          const int rest = cost - u;
           const int take = small ? rest : static_cast<int>(min(static_cast<int64_t>(rest), left));
           const int qt = qg * sh.g + member;
           const int nk = key_tiles(s, min((qt + 1) * item, s.q_len));  // of this CTA's item
@@ -516,13 +558,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
           left -= take;
           u += take;
-          if (u < group_cost()) break;  // the end of the share
+          if (u < cost) break;  // the end of the share
           u = 0;
           if (++qg == groups) {
             qg = 0;
             if (++hk == a.Hkv) {
               hk = 0;
               groups = 0;
+#pragma unroll 1
               while (left > 0 && groups == 0 && ++b < n) enter();
               if (b >= n) break;
             }
@@ -598,14 +641,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         return true;
       };
       Tile cur{}, nxt{};
-      int t = 0;  // key tiles loaded
-      bool more = advance(nxt);
-      if (more) ok = load(nxt, &tmK, k_seq(0));
-      while (ok && more) {
+      bool have = false;
+      for (int t = -1; ok; ++t) {  // K of tile t + 1, then V of tile t
+        const bool more = advance(nxt);
+        if (!ok || !(have || more)) break;
+#pragma unroll 1
+        for (int v = more ? 0 : 1; ok && v <= (have ? 1 : 0); ++v)
+          ok = load(v ? cur : nxt, v ? &tmV : &tmK, v ? v_seq(t) : k_seq(t + 1));
         cur = nxt;
-        more = advance(nxt);
-        ok = ok && (!more || load(nxt, &tmK, k_seq(t + 1))) && load(cur, &tmV, v_seq(t));
-        ++t;
+        have = more;
+        if (!have) break;
       }
       // no copy of this CTA may still be landing when it exits
       if (lane == 0) {
@@ -631,15 +676,25 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
         if (ntok == 0) break;
         const bool two = ntok > a.tok;
+#pragma unroll 1
         for (int g = two ? 0 : np & 1; g <= (two ? 1 : np & 1); ++g) {
           ok = mbar_wait_warp(bar(PA_Q_EMPTY + g), phase >> g & 1u, a.err, ERR_WAIT_ATTN_PRODUCER);
           if (!ok) break;
-          if (lane == 0) {
-            const uint32_t dst = smem_u32(sQ + g * TILE_BYTES), full = bar(PA_Q_FULL + g);
-            const int t0 = tok0 + g * (two ? a.tok : 0);
-            const int n = min(ntok - (t0 - tok0), a.tok);
+          const uint32_t dst = smem_u32(sQ + g * TILE_BYTES), full = bar(PA_Q_FULL + g);
+          const int t0 = tok0 + g * (two ? a.tok : 0);
+          const int n = min(ntok - (t0 - tok0), a.tok);
+          if (n * a.G <= PA_QUAD_ROWS) {  // in all four lane quarters
+            if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * a.G) * 1024);
+            __syncwarp();
+            const int w = lane & 3, h = lane >> 2 & 1;
+#pragma unroll 1
+            for (int i = lane >> 3; i < n; i += 4)
+              tma_load_3d(dst + h * BOX_BYTES + w * 4096 + i * a.G * 128, &tmQ1, full, h * 64,
+                          hk * a.G, t0 + i);
+          } else if (lane == 0) {
             if (n <= PA_FEW_TOKENS) {
               mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * a.G) * 256);
+#pragma unroll 1
               for (int i = 0; i < n; ++i) {
                 tma_load_3d(dst + i * a.G * 128, &tmQ1, full, 0, hk * a.G, t0 + i);
                 tma_load_3d(dst + i * a.G * 128 + BOX_BYTES, &tmQ1, full, 64, hk * a.G, t0 + i);
@@ -722,7 +777,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         tc_fence_after();
         const uint64_t qd = dq + static_cast<uint32_t>(g * (TILE_BYTES >> 4));
         const uint64_t kd = dk + static_cast<uint32_t>(k_slot * (TILE_BYTES >> 4));
-        mma_ss8_el(tmem + TPA_S, qd, kd, idesc_qk);
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          // 16-byte offset of K step kk (16 channels) in a K-major tile
+          const uint32_t off = ((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4;
+          mma_ss_el(tmem + TPA_S, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+        }
         mma_commit_el(bar(PA_S + g));
         if (last) mma_commit_el(bar(PA_Q_EMPTY + g));
         if (tail) {
@@ -739,7 +799,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (!wait(PA_P + g)) return false;
         tc_fence_after();
         const uint64_t vd = dv + static_cast<uint32_t>(v_slot * (TILE_BYTES >> 4));
-        mma_ts8_el(tmem + TPA_O + g * 128, tmem + TPA_P + g * 64, vd, idesc_pv, acc);
+#pragma unroll
+        for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of V
+          mma_ts_el(tmem + TPA_O + g * 128, tmem + TPA_P + g * 64 + kk * 8,
+                    vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1u : acc);
         mma_commit_el(bar(PA_PVD + g));
         if (tail) {
           mma_commit_el(bar(PA_KV_EMPTY + v_slot));
@@ -769,6 +832,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (!ok || !(have || more)) break;
         // a new piece on a query tile that is still in use: its output first
         const bool out_first = have && more && nxt.first && (cur.two || nxt.two);
+        // (rolled: the instruction cache holds the short items' path better, 371
+        // against 402 thousand cycles for 64 rows behind a 29,034-key prefix; the
+        // steady loop of a long chunk loses 4 %)
 #pragma unroll 1
         for (int i = 0; ok && i < 4; ++i) {
           const bool is_qk = out_first ? i >= 2 : (i & 1) == 0;
@@ -801,6 +867,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     const uint32_t tS = tmem + lane_base + TPA_S;
     const uint32_t tO = tmem + lane_base + TPA_O + tile * 128;
     const uint32_t tP = tmem + lane_base + TPA_P + tile * 64;
+    const int row_tok = row / a.G, row_head = row % a.G, lane_tok = lane / a.G;
+    bool p_clear = false;  // this warp's weights outside its 32 keys are 0
+    int joins = 0;   // pieces joined from the four quarters
     int n = 0;       // S tiles of this query tile so far
     int tiles = 0;   // key tiles of this CTA so far
     bool ok = true;
@@ -824,9 +893,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       const int tok0 = two ? tile * a.tok : 0;                        // within the piece
       const int rows = (two ? (tile ? p.ntok - a.tok : a.tok) : p.ntok) * a.G;
-      const bool active = quarter * 32 < rows;
-      const int tok = tok0 + row / a.G;
-      const int lim = min(max(p.lim0 + tok, 0), p.kv);
+      // rows of this lane quarter's own numbering; a few rows are in all quarters
+      const bool quad = rows <= PA_QUAD_ROWS;
+      const bool active = quad || quarter * 32 < rows;
+      const bool row_ok = (quad ? lane : row) < rows;
+      const int tok = tok0 + (quad ? lane_tok : row_tok);
+      const int lim = min(max(p.lim0 + tok, 0), p.kv) - (quad ? quarter * 32 : 0);
+      // only the results of few rows need the query tile's shared memory
+      if (!quad && lane == 0) mbar_arrive(bar(PA_Q_EMPTY + tile));
       // keys past the sequence's end hold anything: their weights are 0, and so
       // their values have to be finite
       auto clear_values = [&](int kt) {
@@ -844,25 +918,35 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         return true;
       };
       float m = -INFINITY, l = 0.f;
-      if (!active) {
-        // no row of this warp exists: it takes part in the hand-offs only (and
-        // waits for the P V, so that its arrivals stay in step)
-        for (int kt = p.kt0; ok && kt < p.kt1; ++kt, ++tiles, ++n) {
-          ok = mbar_wait_warp(bar(PA_S + tile), n & 1, a.err, ERR_WAIT_ATTN_SOFTMAX);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(bar(PA_SFREE + tile));
-          ok = clear_values(kt) && (kt == p.kt0 || wait_pv(n - 1));
-          if (!ok) break;
+      for (int kt = p.kt0; kt < p.kt1; ++kt, ++tiles, ++n) {
+        ok = mbar_wait_warp(bar(PA_S + tile), n & 1, a.err, ERR_WAIT_ATTN_SOFTMAX);
+        if (!ok) break;
+        tc_fence_after();
+        auto free_s = [&] {
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(PA_P + tile));
-        }
-      } else {
-        for (int kt = p.kt0; kt < p.kt1; ++kt, ++tiles, ++n) {
-          if (!mbar_wait_warp(bar(PA_S + tile), n & 1, a.err, ERR_WAIT_ATTN_SOFTMAX)) {
-            ok = false;
-            break;
+          if (lane == 0) mbar_arrive(bar(PA_SFREE + tile));
+        };
+        auto pv_before = [&] { return wait_pv(n - 1); };
+        const int valid = lim - kt * BKV;
+        const bool o_live = kt > p.kt0;
+        if (!active) {
+          // no row of this warp exists: it takes part in the hand-offs only (and
+          // waits for the P V, so that its arrivals stay in step)
+          free_s();
+          ok = !o_live || pv_before();
+        } else if (quad) {
+          if (!p_clear) {
+            const uint32_t z[16] = {};
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) tmem_st16(tP + c, z);
+            tmem_st_wait();
+            p_clear = true;
           }
-          tc_fence_after();
+          ok = softmax_tile_quad(tS + quarter * 32, tP + quarter * 16, tO, valid, o_live, row_ok,
+                                 a.scale_log2, m, l, pv_before, free_s);
+        } else {
+          p_clear = false;
           uint32_t sr[128];
           {
             uint32_t (&c0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
@@ -876,23 +960,94 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             tmem_ld_wait();
             tmem_reg_fence(sr);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(PA_SFREE + tile));
-          ok = softmax_tile_paged(sr, tP, tO, lim - kt * BKV, kt > p.kt0, row < rows,
-                                  a.scale_log2, m, l,
-                                  [&] { return wait_pv(n - 1); }) &&
-               clear_values(kt);
-          if (!ok) break;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(PA_P + tile));
+          free_s();
+          ok = softmax_tile_paged(sr, tP, tO, valid, o_live, row_ok, a.scale_log2, m, l,
+                                  pv_before);
         }
+        ok = ok && clear_values(kt);
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PA_P + tile));
       }
       if (!ok || !wait_pv(n - 1)) break;
+      if (quad) {
+        // the four quarters' results meet in the part of the query tile that
+        // few rows leave free: row r of quarter w, 512 bytes in the order of
+        // 16-byte units XOR r
+        uint8_t* sj = sQ + tile * TILE_BYTES + 1024;
+        auto unit = [&](int w, int r, int c) {
+          return reinterpret_cast<float4*>(sj + (r >> 2) * BOX_BYTES + w * 4096 + (r & 3) * 512) +
+                 (c ^ r);
+        };
+        float2* sml = reinterpret_cast<float2*>(sj + 2048);  // + w * 4096: [row]
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t ov[16];
+          tmem_ld16(tO + c * 16, ov);
+          tmem_ld_wait();
+          tmem_reg_fence(ov);
+          if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *unit(quarter, lane, 4 * c + i) =
+                  make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
+                              __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+          }
+        }
+        if (row_ok) sml[quarter * 512 + lane] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PA_JOIN + tile));
+        ok = mbar_wait_warp(bar(PA_JOIN + tile), joins & 1, a.err, ERR_WAIT_ATTN_SOFTMAX);
+        ++joins;
+        if (!ok) break;
+        for (int r = quarter; r < rows; r += 4) {
+          float2 ml[4];
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            ml[w] = sml[w * 512 + r];
+            top = fmaxf(top, ml[w].x);
+          }
+          float sum = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float f = top == -INFINITY ? 0.f : ex2_approx(ml[w].x - top);
+            const float4 x = *unit(w, r, lane);
+            sum = fmaf(ml[w].y, f, sum);
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+          }
+          const int64_t orow = static_cast<int64_t>(p.tok0 + tok0 + r / a.G);
+          const int head = p.hk * a.G + r % a.G;
+          if (p.dest == -1) {
+            const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // no key: zeros
+            *reinterpret_cast<uint2*>(a.o + orow * a.ld_o + head * DH + lane * 4) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+          } else {
+            const int64_t at = p.dest >= 0
+                                   ? static_cast<int64_t>(p.dest) * a.part_rows + tok0 * a.G + r
+                                   : (static_cast<int64_t>(-2 - p.dest) * a.b.T + orow) * a.H + head;
+            reinterpret_cast<float4*>((p.dest >= 0 ? a.part_o : a.row_o) + at * DH)[lane] = o;
+            if (lane == 0)
+              *reinterpret_cast<float2*>((p.dest >= 0 ? a.part_ml : a.row_ml) + at * 2) =
+                  make_float2(top, sum);
+          }
+        }
+        // O has been read before a later piece's P V overwrites it, and the query
+        // tile may be loaded again
+        tc_fence_before();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PA_Q_EMPTY + tile));
+        continue;
+      }
       if (!active) continue;
       const int64_t orow = static_cast<int64_t>(p.tok0 + tok);
-      const int head = p.hk * a.G + row % a.G;
+      const int head = p.hk * a.G + row_head;
       char* dst;
       if (p.dest == -1) {
         dst = reinterpret_cast<char*>(a.o + orow * a.ld_o + head * DH);
@@ -967,8 +1122,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
         }
       }
-      // O has been read before a later piece's P V overwrites it
-      tc_fence_before();
+      tc_fence_before();  // O has been read before a later piece's P V overwrites it
     }
   }
 
