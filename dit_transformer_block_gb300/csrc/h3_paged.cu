@@ -204,7 +204,16 @@ h3_status launch_kv_append(const void* q, int64_t ld_q, const void* k, int64_t l
   a.Hkv = Hkv;
   a.units = (H + 2 * Hkv + 2 * U - 1) / (2 * U);
   a.b = batch;
-  const RopeTable tab = rope_table(axis_dims, theta);
+  // the table of 64 powers takes longer to form than the launch; it depends on
+  // these four numbers alone, which a model never changes
+  thread_local RopeTable tab;
+  thread_local int tab_axis[3] = {0, 0, 0};
+  thread_local float tab_theta = 0.f;
+  if (tab_theta != theta || !std::equal(axis_dims, axis_dims + 3, tab_axis)) {
+    tab = rope_table(axis_dims, theta);
+    std::copy(axis_dims, axis_dims + 3, tab_axis);
+    tab_theta = theta;
+  }
   const int64_t blocks =
       (static_cast<int64_t>(batch.T) * a.units + APPEND_WARPS - 1) / APPEND_WARPS;
   if (blocks > 0x7fffffff)

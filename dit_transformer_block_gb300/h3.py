@@ -308,32 +308,54 @@ def attention_fp8_skip(ops: dict, o, L=None, scale=None, skip_eps=0.0, kept=None
         _p(ops["sv"]), _p(o), S, L, H, Dh, scale, skip_eps, _p(kept), _s(stream)))
 
 
-def _on_current_device(t, name):
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+# The paged calls run once per layer and token: their checks are kept to a few
+# attribute reads, and the device and stream are asked for by number.
+_INT3 = ctypes.c_int * 3
+
+
+def _device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _on(t, name, dev):
+    if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be on the current CUDA device, is on {t.device}")
 
 
-def _heads(t, name, T=None):
-    """Pointer, row stride and heads of a [T, heads, 128] bf16 tensor whose
-    rows may be strided (columns of a merged projection's output)."""
-    if t.dtype != torch.bfloat16:
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _heads(t, name, T, dev):
+    """Row stride and heads of a [T, heads, 128] bf16 tensor whose rows may be
+    strided (columns of a merged projection's output)."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != 128 or (T is not None and t.shape[0] != T):
-        raise ValueError(f"{name} must be [{'T' if T is None else T}, heads, 128], "
-                         f"got {list(t.shape)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128 or shape[0] != T:
+        raise ValueError(f"{name} must be [{T}, heads, 128], got {list(shape)}")
+    ld, head, one = t.stride()
+    heads = shape[1]
+    if one != 1 or (head != 128 and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    _on_current_device(t, name)
-    heads = t.shape[1]
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * 128), heads
+    _on(t, name, dev)
+    return (ld if T > 1 else heads * 128), heads
+
+
+def _flat(t, name, dtype, dev):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    _on(t, name, dev)
 
 
 def kv_cache(k, v) -> KvCache:
     """A paged key/value cache on k, v [num_pages, Hkv, page_size, 128] bf16,
     for kv_append_paged and attention_paged; it holds on to both tensors."""
+    dev = _device()
     for n, t in (("k", k), ("v", v)):
-        _need(t, torch.bfloat16, n)
-        _on_current_device(t, n)
+        _flat(t, n, torch.bfloat16, dev)
     if k.dim() != 4 or k.shape != v.shape:
         raise ValueError(f"k and v must both be [num_pages, Hkv, page_size, 128], got "
                          f"{list(k.shape)} and {list(v.shape)}")
@@ -347,9 +369,9 @@ def kv_batch(cu_q, kv_len, page_table, T: int) -> KvBatch:
     and their sequences: cu_q [B+1], kv_len [B] (with the call's rows in it),
     page_table [B, max_pages], int32 on the device. It holds on to the tensors,
     whose values are read when a call runs; one batch serves every layer."""
+    dev = _device()
     for n, t in (("cu_q", cu_q), ("kv_len", kv_len), ("page_table", page_table)):
-        _need(t, torch.int32, n)
-        _on_current_device(t, n)
+        _flat(t, n, torch.int32, dev)
     B = kv_len.shape[0]
     if cu_q.shape != (B + 1,) or kv_len.dim() != 1 or page_table.dim() != 2 \
             or page_table.shape[0] != B:
@@ -367,32 +389,35 @@ def kv_append_paged(q, k, v, q_out, cache: KvCache, batch: KvBatch, pos, axis_di
     RoPE(RMSNorm(k)) and v. q [T,H,128], k, v [T,Hkv,128] bf16 (rows may be
     strided), q_out [T,H,128] contiguous (q and q_out None: cache only), pos
     [T,3] int32, gains [128] f32 (None: no norm)."""
-    T, H, pq, ldq = batch.T, 0, None, 0
+    dev, T = _device(), batch.T
+    H, pq, ldq, po = 0, None, 0, None
     if q is not None:
-        pq, ldq, H = _heads(q, "q", T)
-        _need(q_out, torch.bfloat16, "q_out")
+        ldq, H = _heads(q, "q", T, dev)
         if q_out is None or q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
-        _on_current_device(q_out, "q_out")
-    pk, ldk, hk = _heads(k, "k", T)
-    pv, ldv, hv = _heads(v, "v", T)
+        _flat(q_out, "q_out", torch.bfloat16, dev)
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    ldk, hk = _heads(k, "k", T, dev)
+    ldv, hv = _heads(v, "v", T, dev)
     if hk != cache.Hkv or hv != cache.Hkv:
         raise ValueError(f"k and v have {hk} and {hv} heads, the cache {cache.Hkv}")
-    _need(pos, torch.int32, "pos")
     if pos.shape != (T, 3):
         raise ValueError(f"pos must be [{T}, 3], got {list(pos.shape)}")
-    _on_current_device(pos, "pos")
-    for n, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+    _flat(pos, "pos", torch.int32, dev)
+    pg = [None, None]
+    for i, g in enumerate((q_gain, k_gain)):
         if g is not None:
-            _need(g, torch.float32, n)
-            _on_current_device(g, n)
+            _flat(g, "a gain", torch.float32, dev)
             if g.numel() != 128:
-                raise ValueError(f"{n} must have 128 values")
-    ax = (ctypes.c_int * 3)(*axis_dims)
+                raise ValueError(f"a gain must have 128 values, has {g.numel()}")
+            pg[i] = g.data_ptr()
+    ax = _INT3(*axis_dims)
     _check("kv_append_paged", lib().h3_kv_append_paged(
-        pq, ldq, pk, ldk, pv, ldv, None if q_out is None else q_out.data_ptr(), H, _p(q_gain),
-        _p(k_gain), pos.data_ptr(), ctypes.addressof(ax), pairing, theta, eps,
-        ctypes.addressof(cache), ctypes.addressof(batch), _s(stream)))
+        pq, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, po, H, pg[0], pg[1], pos.data_ptr(),
+        ctypes.addressof(ax), pairing, theta, eps, ctypes.addressof(cache),
+        ctypes.addressof(batch), _raw_stream(stream, dev)))
 
 
 def attention_paged_workspace_bytes(T: int, H: int, prefix_len: int = 0) -> int:
@@ -414,23 +439,23 @@ def attention_paged_prefix(q, o, cache: KvCache, batch: KvBatch, prefix_pages, p
                            workspace, scale=None, causal=False, stream=None):
     """attention_paged with prefix_len keys in prefix_pages (int32) before the
     own keys of every sequence, read once for the whole batch."""
-    pq, ldq, H = _heads(q, "q", batch.T)
-    po, ldo, Ho = _heads(o, "o", batch.T)
+    dev, T = _device(), batch.T
+    ldq, H = _heads(q, "q", T, dev)
+    ldo, Ho = _heads(o, "o", T, dev)
     if Ho != H:
         raise ValueError(f"q has {H} heads, o {Ho}")
+    pages = None
     if prefix_pages is not None:
-        _need(prefix_pages, torch.int32, "prefix_pages")
-        _on_current_device(prefix_pages, "prefix_pages")
+        _flat(prefix_pages, "prefix_pages", torch.int32, dev)
         if prefix_pages.numel() * cache.page_size < prefix_len:
             raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of "
                              f"{cache.page_size} keys, prefix_len is {prefix_len}")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on_current_device(workspace, "workspace")
+        pages = prefix_pages.data_ptr()
+    _flat(workspace, "workspace", workspace.dtype, dev)
     _check("attention_paged_prefix", lib().h3_attention_paged_prefix(
-        pq, ldq, po, ldo, H, 128 ** -0.5 if scale is None else scale, int(causal),
-        ctypes.addressof(cache), ctypes.addressof(batch), _p(prefix_pages), prefix_len,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _s(stream)))
+        q.data_ptr(), ldq, o.data_ptr(), ldo, H, 128 ** -0.5 if scale is None else scale,
+        int(causal), ctypes.addressof(cache), ctypes.addressof(batch), pages, prefix_len,
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)))
 
 
 def swiglu(gate_up, out, L=None, stream=None):
