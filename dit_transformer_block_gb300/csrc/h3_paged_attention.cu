@@ -133,6 +133,8 @@ constexpr int PA_ITEM_COST = 2;
 // An item of up to so many key tiles is not split: it goes to the CTA in whose
 // share it begins.
 constexpr int PA_WHOLE = 4;
+// Least share of a CTA: a partial result costs more than a few tiles' time.
+constexpr int PA_MIN_SHARE = 2;
 
 // Cost of one key head of a sequence, for teams of g CTAs (the items of a team
 // run over as many key tiles as the one that sees most).
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
         }
         const int teams = a.ctas / sh.g, team = static_cast<int>(blockIdx.x) / sh.g;
-        sh.per = max(div64(total + teams - 1, teams), int64_t{1});
+        sh.per = max(div64(total + teams - 1, teams), int64_t{PA_MIN_SHARE});
         const int64_t begin = team * sh.per;
         if (team >= teams || begin >= total) return sh;
         sh.cost = min(sh.per, total - begin);
@@ -1161,13 +1163,14 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& sr
   j.o.y *= c;
   j.o.z *= c;
   j.o.w *= c;
-  for (int i0 = 0; i0 < n; i0 += 4) {
-    float4 x[4];
+  constexpr int N = 8;  // partials in flight
+  for (int i0 = 0; i0 < n; i0 += N) {
+    float4 x[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
       if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(src(i0 + i)) + lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
       if (i0 + i < n) {
         j.o.x = fmaf(x[i].x, wi, j.o.x);
@@ -1341,6 +1344,9 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
     return st;
   paged_attention_kernel<<<a.ctas, PA_THREADS, PA_SMEM_BYTES, s>>>(tq, tq1, tk, tv, a);
   if ((st = cuda_fail(cudaGetLastError(), "paged attention launch")) != H3_OK) return st;
+  // items that cannot be split leave nothing to join
+  if (prefix_len == 0 && (static_cast<int64_t>(batch.max_pages) << batch.page_log2) <= PA_WHOLE * BKV)
+    return H3_OK;
   // the join kernel's blocks may take their places while the first kernel
   // runs; they wait for its end before they read anything
   cudaLaunchAttribute attr{};
