@@ -1100,27 +1100,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                                   (lane & ~3) + j)) + (lane & 3) * 16;
         const int have = rows - (row & ~3);  // rows of the four that exist
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t ov[16];
-          tmem_ld16(tO + c * 16, ov);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
           tmem_ld_wait();
           tmem_reg_fence(ov);
-          if (p.dest == -1) {  // 32 columns to 64 bytes
+          if (p.dest == -1) {
             uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 16; ++i)
               w[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv,
                                  __uint_as_float(ov[2 * i + 1]) * inv);
-            tmem_ld16(tO + ++c * 16, ov);
-            tmem_ld_wait();
-            tmem_reg_fence(ov);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              w[8 + i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv,
-                                     __uint_as_float(ov[2 * i + 1]) * inv);
-            store_transposed(w, to, have, (c >> 1) * 64);
+            store_transposed(w, to, have, c * 64);
           } else {
-            store_transposed(ov, to, have, c * 64);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              store_transposed(*reinterpret_cast<uint32_t(*)[16]>(&ov[h * 16]), to, have,
+                               c * 128 + h * 64);
           }
         }
       }
