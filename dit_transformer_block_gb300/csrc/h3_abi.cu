@@ -569,8 +569,9 @@ static h3_status check_paged(const h3_kv_cache* c, const h3_kv_batch* b, PagedBa
              "the cache must be 16-byte aligned");
   H3_REQUIRE(b->T >= 0 && b->B >= 0 && b->max_pages >= 0, H3_ERR_INVALID_ARG,
              "negative size (T=%d, B=%d, max_pages=%d)", b->T, b->B, b->max_pages);
-  H3_REQUIRE(b->max_pages <= (1 << 30) / c->page_size, H3_ERR_UNSUPPORTED,
-             "max_pages * page_size must be at most 2^30");
+  // (a CTA's part of that many keys takes about half of the default wait limit)
+  H3_REQUIRE(b->max_pages <= (1 << 26) / c->page_size, H3_ERR_UNSUPPORTED,
+             "max_pages * page_size must be at most 2^26");
   H3_REQUIRE(b->B <= 65536, H3_ERR_UNSUPPORTED, "B=%d exceeds 65536 sequences", b->B);
   H3_REQUIRE(b->T == 0 || b->B == 0 ||
                  (b->cu_q != nullptr && b->kv_len != nullptr &&
@@ -659,8 +660,8 @@ h3_status h3_attention_paged_prefix(const void* q, int64_t ld_q, void* o, int64_
              "H=%d heads on Hkv=%d: at most 128 per key head", H, cache->Hkv);
   H3_REQUIRE(softmax_scale > 0.f, H3_ERR_INVALID_ARG, "softmax_scale must be > 0");
   H3_REQUIRE(prefix_len >= 0, H3_ERR_INVALID_ARG, "prefix_len=%d", prefix_len);
-  H3_REQUIRE(prefix_len <= (1 << 30) && static_cast<int64_t>(b.T) * H <= (1 << 29),
-             H3_ERR_UNSUPPORTED, "prefix_len=%d exceeds 2^30 or T * H=%lld exceeds 2^29",
+  H3_REQUIRE(prefix_len <= (1 << 26) && static_cast<int64_t>(b.T) * H <= (1 << 29),
+             H3_ERR_UNSUPPORTED, "prefix_len=%d exceeds 2^26 or T * H=%lld exceeds 2^29",
              prefix_len, static_cast<long long>(b.T) * H);
   if (b.T == 0 || b.B == 0) return H3_OK;
   if ((st = check_strided("q", q, ld_q, H)) != H3_OK) return st;

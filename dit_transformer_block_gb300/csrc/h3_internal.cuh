@@ -178,6 +178,23 @@ struct PagedBatch {
   const int32_t* kv_len;
   const int32_t* page_table;
 };
+#ifdef __CUDACC__
+// The number of sequence ends cu_q[1..B] at or below row t, by a whole warp: 32
+// of them at a time, so three reads for any B up to 32,768. Arrays that are out
+// of order give some number in [0, B].
+__device__ __forceinline__ int ends_up_to(const int32_t* cu_q, int B, int t) {
+  int at = 0, n = B;  // the answer is in [at, at + n]
+  while (n > 0) {
+    const int step = (n + 31) >> 5;
+    const int i = (static_cast<int>(threadIdx.x & 31) + 1) * step;  // the i-th end from at on
+    const uint32_t below = __ballot_sync(0xffffffffu, i <= n && __ldg(cu_q + at + min(i, n)) <= t);
+    const int skip = __popc(below) * step;
+    at += skip;
+    n = min(step - 1, n - skip);
+  }
+  return at;
+}
+#endif
 // q (optional, with q_out), k, v: rows of ld elements; pairing as
 // launch_qk_norm_rope; gains NULL: rotation only.
 h3_status launch_kv_append(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,

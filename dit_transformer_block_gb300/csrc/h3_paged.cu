@@ -24,12 +24,9 @@ struct SeqRow {
   int q_len;  // rows of the sequence
 };
 
-// The sequence of row t: the number of ends cu_q[1..B] at or below t, counted
-// by the whole warp.
+// The sequence of row t, by the whole warp.
 __device__ __forceinline__ SeqRow find_row(const int32_t* __restrict__ cu_q, int B, int t) {
-  int n = 0;
-  for (int i = threadIdx.x & 31; i < B; i += 32) n += __ldg(cu_q + i + 1) <= t ? 1 : 0;
-  n = __reduce_add_sync(0xffffffffu, n);
+  const int n = ends_up_to(cu_q, B, t);
   SeqRow r{-1, 0, 0};
   if (n < B) {
     const int first = __ldg(cu_q + n), end = __ldg(cu_q + n + 1);

@@ -417,7 +417,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       // tile takes a CTA about 2,300 cycles of products for two query tiles, and
       // about 2,800 where every CTA reads it from HBM for itself. (Loops are
       // kept rolled: the instruction cache is short for this kernel.)
-      const int most = a.b.T > 2 * a.tok ? min(PA_MAX_TEAM, a.ctas) : 1;
       auto find_share = [&](int seg) {
         const int n = seg == 0 ? 1 : a.b.B;
         const int run = (n + 31) / 32;
@@ -425,11 +424,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         Share sh{0, 0, 1, 0, 1};
         int64_t total = 0, mine = 0;
         float least = 0.f;
+        int most = 1;  // no team is larger than the items of a sequence
 #pragma unroll 1
         for (int g = 1; g <= most; ++g) {
           int64_t own = 0;
+          int rows = 0;
 #pragma unroll 1
-          for (int b = b0; b < b1; ++b) own += head_cost(a, seg, seq_info(a, seg, b), g);
+          for (int b = b0; b < b1; ++b) {
+            const SeqInfo s = seq_info(a, seg, b);
+            own += head_cost(a, seg, s, g);
+            rows = max(rows, s.q_len);
+          }
+          if (g == 1) {
+            rows = __reduce_max_sync(0xffffffffu, rows);
+            most = min(min(PA_MAX_TEAM, a.ctas), (rows + 2 * a.tok - 1) / (2 * a.tok));
+          }
           own *= a.Hkv;
           int64_t W = own;
 #pragma unroll
@@ -1229,10 +1238,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const PagedArgs 
   for (int64_t w = blockIdx.x * 8LL + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8LL) {
     const int t = static_cast<int>(w / a.H), head = static_cast<int>(w % a.H);
     const int hk = head / a.G;
-    // the row's sequence: the number of ends at or below it
-    int b = 0;
-    for (int i = lane; i < a.b.B; i += 32) b += __ldg(a.b.cu_q + i + 1) <= t ? 1 : 0;
-    b = __reduce_add_sync(0xffffffffu, b);
+    const int b = ends_up_to(a.b.cu_q, a.b.B, t);  // the row's sequence
     if (b >= a.b.B) continue;
     Joined j;
     bool any = false;

@@ -52,11 +52,15 @@ class BlockWeights(ctypes.Structure):
 
 
 class KvCache(ctypes.Structure):
+    device = None  # of the tensors, where kv_cache made it
+
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("Dh", ctypes.c_int)]
 
 
 class KvBatch(ctypes.Structure):
+    device = None
+
     _fields_ = [("T", ctypes.c_int), ("B", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
                 ("page_table", ctypes.c_void_p)]
@@ -326,6 +330,12 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _made_on(cache, batch, dev):
+    for n, s in (("cache", cache), ("batch", batch)):
+        if s.device is not None and s.device != dev:
+            raise ValueError(f"the {n} must be on the current CUDA device, is on device {s.device}")
+
+
 def _heads(t, name, T, dev):
     """Row stride and heads of a [T, heads, 128] bf16 tensor whose rows may be
     strided (columns of a merged projection's output)."""
@@ -360,7 +370,7 @@ def kv_cache(k, v) -> KvCache:
         raise ValueError(f"k and v must both be [num_pages, Hkv, page_size, 128], got "
                          f"{list(k.shape)} and {list(v.shape)}")
     c = KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], k.shape[1], k.shape[3])
-    c.tensors = (k, v)
+    c.tensors, c.device = (k, v), dev
     return c
 
 
@@ -379,7 +389,7 @@ def kv_batch(cu_q, kv_len, page_table, T: int) -> KvBatch:
                          f"{list(cu_q.shape)}, {list(kv_len.shape)}, {list(page_table.shape)}")
     b = KvBatch(T, B, page_table.shape[1], cu_q.data_ptr(), kv_len.data_ptr(),
                 page_table.data_ptr())
-    b.tensors = (cu_q, kv_len, page_table)
+    b.tensors, b.device = (cu_q, kv_len, page_table), dev
     return b
 
 
@@ -390,6 +400,7 @@ def kv_append_paged(q, k, v, q_out, cache: KvCache, batch: KvBatch, pos, axis_di
     strided), q_out [T,H,128] contiguous (q and q_out None: cache only), pos
     [T,3] int32, gains [128] f32 (None: no norm)."""
     dev, T = _device(), batch.T
+    _made_on(cache, batch, dev)
     H, pq, ldq, po = 0, None, 0, None
     if q is not None:
         ldq, H = _heads(q, "q", T, dev)
@@ -440,6 +451,7 @@ def attention_paged_prefix(q, o, cache: KvCache, batch: KvBatch, prefix_pages, p
     """attention_paged with prefix_len keys in prefix_pages (int32) before the
     own keys of every sequence, read once for the whole batch."""
     dev, T = _device(), batch.T
+    _made_on(cache, batch, dev)
     ldq, H = _heads(q, "q", T, dev)
     ldo, Ho = _heads(o, "o", T, dev)
     if Ho != H:

@@ -228,13 +228,13 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
  *   T           rows of the call's q, k, v and o tensors; a call with T or B
  *               0 does nothing (its row tensors and workspace may be NULL)
  *   B           sequences, at most 65,536; rows [cu_q[b], cu_q[b+1]) belong to sequence b
- *   cu_q        [B + 1] int32 device, non-decreasing, 0 <= cu_q[b] <= T; rows
- *               outside [cu_q[0], cu_q[B]) are neither read nor written
+ *   cu_q        [B + 1] int32 device, non-decreasing, 0 <= cu_q[b] <= T; the
+ *               outputs' rows outside [cu_q[0], cu_q[B]) are left as they were
  *   kv_len      [B] int32 device: keys of sequence b with the call's rows in
  *               it, so row i of its q_len rows is key kv_len[b] - q_len + i
  *   page_table  [B, max_pages] int32 device: key j of sequence b is row
  *               j % page_size of page page_table[b, j / page_size];
- *               max_pages * page_size at most 2^30
+ *               max_pages * page_size at most 2^26
  * The arrays are read on the device when the call runs, so a captured call
  * replays with the lengths and pages that they hold then. What they hold is
  * bounded there: a key index at or beyond max_pages * page_size or below 0 has
@@ -311,7 +311,8 @@ h3_status h3_attention_paged(const void* q, int64_t ld_q, void* o, int64_t ld_o,
  * keys as above (kv_len counts those only). The prefix's keys and values are
  * read once for the rows of all sequences together.
  *   prefix_pages [ceil(prefix_len / page_size)] int32 device, as a row of
- *          page_table; may be NULL when prefix_len is 0
+ *          page_table; may be NULL when prefix_len is 0. prefix_len is at
+ *          most 2^26
  *   workspace  of h3_attention_paged_workspace_bytes(T, H, prefix_len) bytes
  */
 h3_status h3_attention_paged_prefix(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,

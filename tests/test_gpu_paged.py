@@ -254,6 +254,56 @@ def test_prefix_chunks(h3lib, causal):
     run_attention(h3lib, [300, 300], [300, 300], 2, 1, 128, causal, prefix=300)
 
 
+@pytest.mark.parametrize("G", [1, 4, 32])
+def test_second_query_tile_of_few_rows(h3lib, G):
+    # a piece of two query tiles whose second one has one token, between pieces
+    # of one tile and of two full ones
+    t = 128 // G
+    run_attention(h3lib, [t + 1, 2 * t, 1, t + 2, 3 * t + 1, t], [700, 700, 300, 1500, 4000, 129],
+                  2 * G, 2, 32, causal=True)
+    run_attention(h3lib, [t + 1, 1, 2 * t + 1], [700, 3, 1500], 2 * G, 2, 16, prefix=400)
+
+
+def test_a_page_in_several_places(h3lib):
+    # the same page twice in a sequence, in two sequences and in the prefix
+    P = Paged([200, 150, 64], 2, 32, prefix=96)
+    P.table[0, 3] = P.table[0, 1]
+    P.table[1, 0] = P.table[0, 1]
+    P.prefix_pages[2] = P.table[0, 0]
+    P.prefix_pages[1] = P.prefix_pages[0]
+    q = rnd(gen(31), 8, 6, DH)
+    check_attention(attend(h3lib, q, P, [0, 3, 7, 8]), q, P, [0, 3, 7, 8], False, DH ** -0.5)
+
+
+def test_many_sequences(h3lib):
+    # more than 32 ends per step of the search for a row's sequence, empty ones
+    # among them
+    B = 2100
+    q_len = [0 if i % 3 == 1 else 1 + (i % 97 == 0) * 2 for i in range(B)]
+    kv = [(i * 7) % 50 + q_len[i] for i in range(B)]
+    run_attention(h3lib, q_len, kv, 2, 1, 16, causal=True, prefix=40)
+    run_attention(h3lib, q_len, kv, 2, 1, 16, first=2, behind=3, prefix=40)
+
+
+def test_nothing_but_the_rows_is_written(h3lib):
+    # the columns beside o's rows, the memory behind the workspace and the pool
+    for prefix in (0, 300):
+        P = Paged([900, 40, 2000], 2, 16, prefix=prefix)
+        k, v = P.k.clone(), P.v.clone()
+        H, cu = 6, [0, 1, 30, 200]
+        q = rnd(gen(32), 200, H, DH)
+        wide = torch.full((200, H * DH + 24), SENT, dtype=torch.bfloat16, device=dev)
+        o = wide[:, 8:8 + H * DH].unflatten(1, (H, DH))
+        need = h3lib.attention_paged_workspace_bytes(200, H, prefix)
+        ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=dev)
+        h3lib_o = attend(h3lib, q, P, cu, causal=True, o=o, ws=ws[:need])
+        check_attention(h3lib_o, q, P, cu, True, DH ** -0.5)
+        assert bool((wide[:, :8] == SENT).all()) and bool((wide[:, 8 + H * DH:] == SENT).all())
+        assert bool((ws[need:] == 0x5A).all())
+        for now, then in ((P.k, k), (P.v, v)):
+            assert torch.equal(now.view(torch.int16), then.view(torch.int16))
+
+
 def test_large_scores(h3lib):
     # sharply peaked softmax: the running maximum moves by more than one
     # rescale threshold many times
@@ -621,3 +671,46 @@ def test_variants_behind_one_prefix_equal_separate_sequences(h3lib):
         alone = attend(h3lib, q_out, own, cu, causal)
         rel = float((o.double() - alone.double()).norm() / alone.double().norm())
         assert rel <= 2 * U, rel
+
+
+@pytest.mark.parametrize("prefix", [0, 260])
+def test_two_captured_calls_in_turn(h3lib, prefix):
+    # two graphs of one padded size with a workspace of their own, replayed in
+    # turn on two streams while the batch shrinks and grows
+    P = Paged([300, 40, 600], 2, 32, prefix=prefix)
+    T, H = 160, 6
+    c = h3lib.kv_cache(P.k, P.v)
+    cu, kv = torch.zeros(4, dtype=torch.int32, device=dev), i32(P.kv)
+    b = h3lib.kv_batch(cu, kv, P.table, T)
+    q = rnd(gen(33), T, H, DH)
+    need = h3lib.attention_paged_workspace_bytes(T, H, prefix)
+    ws = [torch.full((need,), 0xFF, dtype=torch.uint8, device=dev) for _ in range(2)]
+    o = [torch.empty_like(q) for _ in range(2)]
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            h3lib.attention_paged_prefix(q, o[i], c, b, P.prefix_pages if prefix else None, prefix,
+                                         ws[i], causal=i == 1)
+    for ends in ([0, 1, 1, 2], [0, 100, 140, 160], [0, 0, 0, 0], [0, 40, 70, 71], [3, 3, 30, 150]):
+        cu.copy_(i32(ends))
+        for x in o:
+            x.fill_(SENT)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        h3lib.check_device_error()
+        for i in range(2):
+            if ends[-1] > ends[0]:
+                check_attention(o[i], q, P, ends, i == 1, DH ** -0.5, f"ends {ends} causal {i}")
+            assert bool((o[i][:ends[0]] == SENT).all()) and bool((o[i][ends[-1]:] == SENT).all())
+
+
+def test_append_many_sequences(h3lib):
+    B = 2100
+    q_len = [0 if i % 3 == 1 else 1 for i in range(B)]
+    run_append(h3lib, q_len, [(i * 7) % 50 + q_len[i] for i in range(B)], 1, 1, 16, first=1, behind=2)

@@ -160,3 +160,27 @@ def test_binding_checks_before_the_library():
     with pytest.raises(TypeError):
         h3.kv_append_paged(x.float(), x[:, :4], x[:, :4], x, c, b,
                            torch.zeros(6, 3, dtype=torch.int32), (128, 0, 0))
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_longest_table_and_prefix(lib, page):
+    c, most = cache(page_size=page), (1 << 26) // page
+    assert attend(lib, c, batch(max_pages=most + 1)) == UNSUPPORTED
+    assert append(lib, c, batch(max_pages=most + 1)) == UNSUPPORTED
+    assert attend(lib, c, prefix_len=(1 << 26) + 1, bytes=1 << 50) == UNSUPPORTED
+    # at the limit the next check is the first to refuse
+    assert attend(lib, c, batch(max_pages=most), q=NULL) == INVALID
+    assert attend(lib, c, prefix_len=1 << 26, bytes=1 << 50, prefix=NULL) == INVALID
+
+
+def test_cache_and_batch_of_another_device_are_refused(monkeypatch):
+    x = torch.zeros(6, 8, 128, dtype=torch.bfloat16)
+    for at in ("cache", "batch"):
+        c, b = cache(), batch()
+        (c if at == "cache" else b).device = 1
+        monkeypatch.setattr(h3, "_device", lambda: 0)
+        with pytest.raises(ValueError, match=f"the {at} must be on the current CUDA device"):
+            h3.attention_paged(x, x, c, b, torch.zeros(16, dtype=torch.uint8))
+        with pytest.raises(ValueError, match=f"the {at} must be on the current CUDA device"):
+            h3.kv_append_paged(None, x[:, :4], x[:, :4], None, c, b,
+                               torch.zeros(6, 3, dtype=torch.int32), (128, 0, 0))
