@@ -291,12 +291,16 @@ h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t
  * over the keys j < kv_len[b], and with causal != 0 only those with
  * j <= kv_len[b] - q_len + i (the row itself and what came before it). A row
  * without any such key gives zeros.
- *   q, o   [T, H, Dh] bf16, row strides ld_q, ld_o (multiples of 8); H a
+ *   q, o   [T, H, Dh] bf16, not overlapping, row strides ld_q, ld_o (multiples of 8); H a
  *          multiple of cache->Hkv, at most 128 heads per key head; T * H at
  *          most 2^29
  *   workspace  device memory of h3_attention_paged_workspace_bytes(T, H, 0)
  *          bytes, 256-byte aligned, overwritten by the call; calls that may
  *          overlap on the GPU need one each
+ * A batch of short tables (max_pages * page_size) and few rows is taken row by
+ * row, a cluster of CTAs each, others by tiles of rows and keys; both give
+ * the same up to the order of the sums, which in the second also goes by the
+ * lengths of the whole batch.
  * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out.
  */
 size_t h3_attention_paged_workspace_bytes(int T, int H, int prefix_len);

@@ -26,6 +26,7 @@ dev = "cuda"
 U = 2.0 ** -8
 DH = 128
 SENT = -7.25
+LEAST_KEYS = 0  # that a page table has room for: the choice of kernel goes by it
 
 
 def gen(seed):
@@ -56,7 +57,8 @@ class Paged:
         self.v = torch.full((self.pages, Hkv, page, DH), float("inf"), device=dev).to(torch.bfloat16)
         self.v[..., ::2] = float("nan")
         order = torch.randperm(self.pages, generator=g, device=dev).to(torch.int32)
-        self.table = torch.full((len(kv_len), max(need + [1])), -1, dtype=torch.int32, device=dev)
+        self.table = torch.full((len(kv_len), max(need + [1, -(-LEAST_KEYS // page)])), -1,
+                                dtype=torch.int32, device=dev)
         at = npre
         for b, n in enumerate(need):
             self.table[b, :n] = order[at:at + n]
@@ -302,6 +304,28 @@ def test_nothing_but_the_rows_is_written(h3lib):
         assert bool((ws[need:] == 0x5A).all())
         for now, then in ((P.k, k), (P.v, v)):
             assert torch.equal(now.view(torch.int16), then.view(torch.int16))
+
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (8, 4), (21, 3), (8, 1), (9, 1), (20, 2), (128, 1)])
+@pytest.mark.parametrize("kv", [255, 257, 511, 513, 1023, 1100, 2048, 2100, 4096, 9000, 10240, 11000])
+def test_single_rows_of_growing_tables(h3lib, H, Hkv, kv):
+    # lengths about those where a row's keys go to more CTAs or to the other kernel
+    run_attention(h3lib, [1], [kv], H, Hkv, 16 if kv % 2 else 64)
+    run_attention(h3lib, [1, 1, 0, 1], [kv, 1, 5, kv // 3], H, Hkv, 32, prefix=70 if kv < 2000 else 0)
+
+
+@pytest.mark.parametrize("B", [14, 15, 16, 33, 35, 75, 77, 151, 153, 305, 700])
+def test_single_rows_of_growing_batches(h3lib, B):
+    run_attention(h3lib, [1] * B, [(i * 131) % 1100 for i in range(B)], 2, 1, 64)
+    run_attention(h3lib, [1] * B, [(i * 131) % 300 for i in range(B)], 18, 2, 16)
+    run_attention(h3lib, [1] * B, [(i * 131) % 90 for i in range(B)], 1, 1, 16, prefix=130, causal=True)
+
+
+def test_short_chunks(h3lib):
+    # a few rows of a sequence, each taken by itself
+    run_attention(h3lib, [4, 1, 7], [900, 40, 7], 6, 2, 32, causal=True)
+    run_attention(h3lib, [4, 1, 7], [900, 40, 7], 10, 1, 16, prefix=33)
+    run_attention(h3lib, [30], [20], 4, 4, 16, causal=True, first=2, behind=3)
 
 
 def test_large_scores(h3lib):

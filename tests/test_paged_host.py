@@ -162,6 +162,10 @@ def test_binding_checks_before_the_library():
                            torch.zeros(6, 3, dtype=torch.int32), (128, 0, 0))
 
 
+def test_attention_in_place_is_refused(lib):
+    assert attend(lib, q=P, o=P) == INVALID and "o is q" in h3.last_error()
+
+
 @pytest.mark.parametrize("page", [16, 128])
 def test_longest_table_and_prefix(lib, page):
     c, most = cache(page_size=page), (1 << 26) // page
