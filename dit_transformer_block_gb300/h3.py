@@ -315,6 +315,7 @@ def attention_fp8_skip(ops: dict, o, L=None, scale=None, skip_eps=0.0, kept=None
 # The paged calls run once per layer and token: their checks are kept to a few
 # attribute reads, and the device and stream are asked for by number.
 _INT3 = ctypes.c_int * 3
+_AXES = {}  # axis_dims as the library takes them
 
 
 def _device() -> int:
@@ -331,9 +332,10 @@ def _raw_stream(stream, dev):
 
 
 def _made_on(cache, batch, dev):
-    for n, s in (("cache", cache), ("batch", batch)):
-        if s.device is not None and s.device != dev:
-            raise ValueError(f"the {n} must be on the current CUDA device, is on device {s.device}")
+    if cache.device != dev and cache.device is not None:
+        raise ValueError(f"the cache must be on the current CUDA device, is on device {cache.device}")
+    if batch.device != dev and batch.device is not None:
+        raise ValueError(f"the batch must be on the current CUDA device, is on device {batch.device}")
 
 
 def _heads(t, name, T, dev):
@@ -348,7 +350,8 @@ def _heads(t, name, T, dev):
     heads = shape[1]
     if one != 1 or (head != 128 and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    _on(t, name, dev)
+    if t.get_device() != dev or dev < 0:
+        _on(t, name, dev)
     return (ld if T > 1 else heads * 128), heads
 
 
@@ -358,6 +361,13 @@ def _flat(t, name, dtype, dev):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     _on(t, name, dev)
+
+
+def _gain(g, dev):
+    _flat(g, "a gain", torch.float32, dev)
+    if g.numel() != 128:
+        raise ValueError(f"a gain must have 128 values, has {g.numel()}")
+    return g.data_ptr()
 
 
 def kv_cache(k, v) -> KvCache:
@@ -418,13 +428,14 @@ def kv_append_paged(q, k, v, q_out, cache: KvCache, batch: KvBatch, pos, axis_di
         raise ValueError(f"pos must be [{T}, 3], got {list(pos.shape)}")
     _flat(pos, "pos", torch.int32, dev)
     pg = [None, None]
-    for i, g in enumerate((q_gain, k_gain)):
-        if g is not None:
-            _flat(g, "a gain", torch.float32, dev)
-            if g.numel() != 128:
-                raise ValueError(f"a gain must have 128 values, has {g.numel()}")
-            pg[i] = g.data_ptr()
-    ax = _INT3(*axis_dims)
+    if q_gain is not None:
+        pg[0] = _gain(q_gain, dev)
+    if k_gain is not None:
+        pg[1] = _gain(k_gain, dev)
+    axis = tuple(axis_dims)
+    ax = _AXES.get(axis)
+    if ax is None:
+        ax = _AXES[axis] = _INT3(*axis)
     _check("kv_append_paged", lib().h3_kv_append_paged(
         pq, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, po, H, pg[0], pg[1], pos.data_ptr(),
         ctypes.addressof(ax), pairing, theta, eps, ctypes.addressof(cache),
