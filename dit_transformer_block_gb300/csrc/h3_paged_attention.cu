@@ -29,6 +29,18 @@
 //   warps 0-3 / 4-7: softmax of query tile 0 / 1 (thread = query row = TMEM
 //     lane). A piece of one query tile takes the two groups in turn, so the
 //     output of one piece overlaps the products of the next.
+//
+// Measured and bound by (152 SMs): single rows, HBM: 8 of up to 58,758 keys, 42
+// heads, 1.40 ms (7.2 TB/s); 64 of 4,096 keys, 40 heads on 8, 165 us (6.5 TB/s).
+// Pages of 16 keys, the loading warp: a box of 2 KB takes it about 100 cycles (96
+// rows of up to 8,191 keys, 32 heads on 4: 165 us; pages of 32 and more 139 us, 6.2
+// TB/s). Chunks, the chain
+// through the one S buffer: product 512 cycles, seen 200, read 250, seen 200, twice
+// per key tile and two query tiles, 2,700 cycles against 2,048 of products (1,896
+// rows of 58,758 keys, 42 heads: 1.54 ms, 1,560 TFLOP/s; of 16,384 keys, 1,515).
+// Short items, instruction fetch: the kernel is 125 KB, and an item runs most of a
+// small part of it once (64 rows of up to 512 keys behind a prefix of 29,034, 42
+// heads: 194 us, of which the prefix's bytes take 92).
 #include <algorithm>
 
 #include "h3_attn_common.cuh"
@@ -44,6 +56,9 @@ __device__ __forceinline__ int v_seq(int t) { return 2 * t + 2; }
 constexpr int PA_PIECES = 8;   // pieces posted ahead
 constexpr int PA_MAX_CTAS = 160;
 constexpr int PA_CTRL_BYTES = 1024;
+// A query tile of so many tokens is loaded token by token; so many rows of a warp
+// are stored by themselves (store_transposed); so many rows of a query tile lie in
+// all four lane quarters (softmax_tile_quad).
 constexpr int PA_FEW_TOKENS = 4, PA_FEW_ROWS = 8, PA_QUAD_ROWS = 8;
 // 12 warps: with three on each SM sub-partition the launch gives every thread
 // 168 registers; warps 8-11 hand most of theirs to the softmax warps, which
@@ -133,7 +148,8 @@ constexpr int PA_ITEM_COST = 2;
 // An item of up to so many key tiles is not split: it goes to the CTA in whose
 // share it begins.
 constexpr int PA_WHOLE = 4;
-// Least share of a CTA: a partial result costs more than a few tiles' time.
+// Least share of a CTA: a partial result costs more than a tile's time (8 rows
+// behind 4,099 keys, 16 heads on 2: 21.2 us for 2, 22.9 for 1, 24.0 for 4).
 constexpr int PA_MIN_SHARE = 2;
 
 // Cost of one key head of a sequence, for teams of g CTAs (the items of a team
@@ -174,8 +190,7 @@ __device__ __noinline__ int64_t div64(int64_t a, int64_t b) {
 }
 
 // This CTA's share of a segment: `cost` units from unit `at` of sequence b on. A
-// share is the same cost (`per`) for every
-// team but the last ones. An item of n key tiles is PA_ITEM_COST + n units, of
+// share is the same cost (`per`) for every team but the last ones. An item of n key tiles is PA_ITEM_COST + n units, of
 // which the last n are its key tiles.
 struct Share {
   int64_t cost, at, per;
@@ -329,10 +344,9 @@ __device__ __forceinline__ bool softmax_tile_quad(uint32_t tS, uint32_t tP, uint
 // Writes 64 bytes (four 16-byte units, w) of every lane's row at byte `at`, with
 // stores of 64 bytes of eight rows each: one that takes 16 bytes of 32 rows
 // touches 32 lines and holds the load/store unit for as many cycles. For
-// PA_FEW_ROWS rows of a warp and fewer there is nothing to gain.
-// How:
-// groups of four lanes transpose their units, then to[j] (the row of lane j of
-// the group, at this lane's unit) gets what is now in unit j, for j < left.
+// PA_FEW_ROWS rows of a warp and fewer there is nothing to gain. Groups of four
+// lanes transpose their units, then to[j] (the row of lane j of the group, at this
+// lane's unit) gets what is now in unit j, for j < left.
 __device__ __forceinline__ void store_transposed(uint32_t (&w)[16], char* const (&to)[4], int left,
                                                  int at) {
   const int lane = threadIdx.x & 31;

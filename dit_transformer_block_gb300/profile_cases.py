@@ -1,6 +1,6 @@
 """Small, fixed cases for ncu captures of the library's kernels.
 
-    python -m dit_transformer_block_gb300.profile_cases [attention] [gemm] [elementwise] [fp8] [sage]
+    python -m dit_transformer_block_gb300.profile_cases [attention] [gemm] [elementwise] [fp8] [sage] [paged]
 
 Each selected kernel runs twice on inputs larger than L2 (129 MB) but a few
 hundred MB in total, so that an `ncu --set full -k <kernel> -s 1 -c 1`
@@ -17,6 +17,9 @@ capture of the second launch ends within a minute or two:
               8192 x 5376, SAGE quantisation and FP8 attention at S = L = 16384
   sage        SAGE quantisation alone (K mean, V absmax, Q/K tile and V codes)
               at S = L = 16384, 42 heads
+  paged       the paged cache: 16384 rows appended (42 heads, interleaved pairs),
+              1896 rows against 16384 keys (42 heads), 64 rows of 4096 keys (40
+              heads on 8), and 512 rows of 256 keys (32 heads on 8)
 """
 from __future__ import annotations
 
@@ -28,7 +31,7 @@ from dit_transformer_block_gb300 import build, h3
 
 
 def main(argv):
-    which = set(argv) or {"attention", "gemm", "elementwise", "fp8", "sage"}
+    which = set(argv) or {"attention", "gemm", "elementwise", "fp8", "sage", "paged"}
     build.build()
     h3.lib()
     dev = "cuda"
@@ -91,6 +94,34 @@ def main(argv):
         S = 16384
         qs, ks, vs = rnd(S, 42, 128), rnd(S, 42, 128), rnd(S, 42, 128)
         runs.append(lambda: h3.sage_quantize(qs, ks, vs, S))
+    if "paged" in which:
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+
+        def pool(B, keys, Hkv, page=64):
+            n = keys // page
+            c = h3.kv_cache(rnd(B * n, Hkv, page, 128), rnd(B * n, Hkv, page, 128))
+            order = torch.randperm(B * n, generator=g, device=dev).to(torch.int32).view(B, n)
+            return c, order
+
+        def attend(B, rows, keys, H, Hkv):
+            c, table = pool(B, keys, Hkv)
+            T = B * rows
+            b = h3.kv_batch(i32([i * rows for i in range(B + 1)]), i32([keys] * B), table, T)
+            q, o = rnd(T, H, 128), torch.empty(T, H, 128, device=dev, dtype=torch.bfloat16)
+            ws = torch.empty(h3.attention_paged_workspace_bytes(T, H), device=dev, dtype=torch.uint8)
+            runs.append(lambda: h3.attention_paged(q, o, c, b, ws))
+
+        T = 16384
+        ca, table = pool(1, T, 42)
+        ba = h3.kv_batch(i32([0, T]), i32([T]), table, T)
+        qkv = rnd(T, 3, 42, 128)
+        qp, ones3 = torch.empty(T, 42, 128, device=dev, dtype=torch.bfloat16), torch.ones(128, device=dev)
+        pos3 = torch.zeros(T, 3, dtype=torch.int32, device=dev)
+        runs.append(lambda: h3.kv_append_paged(qkv[:, 0], qkv[:, 1], qkv[:, 2], qp, ca, ba, pos3,
+                                               (32, 48, 48), ones3, ones3))
+        attend(1, 1896, 16384, 42, 42)
+        attend(64, 1, 4096, 40, 8)
+        attend(512, 1, 256, 32, 8)
     for _ in range(2):
         for fn in runs:
             fn()
