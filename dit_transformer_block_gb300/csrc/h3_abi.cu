@@ -678,7 +678,7 @@ h3_status h3_attention_paged_prefix(const void* q, int64_t ld_q, void* o, int64_
   const int64_t keys = (static_cast<int64_t>(b.max_pages) << b.page_log2) + prefix_len;
   if (paged_rows_fit(b.T, H, cache->Hkv, b.B, keys, prefix_len))
     return launch_paged_rows(q, ld_q, o, ld_o, H, softmax_scale, causal != 0, cache->k, cache->v,
-                             cache->Hkv, b, prefix_pages, prefix_len,
+                             cache->Hkv, b, prefix_pages, prefix_len, nullptr, nullptr,
                              reinterpret_cast<cudaStream_t>(stream));
   return launch_paged_attention(q, ld_q, o, ld_o, H, softmax_scale, causal != 0, cache->k,
                                 cache->v, cache->Hkv, b, prefix_pages, prefix_len, workspace,

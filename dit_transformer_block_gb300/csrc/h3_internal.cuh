@@ -210,11 +210,12 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
                                  const int32_t* prefix_pages, int prefix_len, void* workspace,
                                  cudaStream_t s);
 // The same for single rows over at most so many keys (h3_paged_rows.cu), where
-// paged_rows_fit; no workspace.
+// paged_rows_fit; no workspace. With part_o and part_ml, sums and (maximum, sum) of
+// every row and head go there instead of the output.
 bool paged_rows_fit(int T, int H, int Hkv, int B, int64_t keys, int prefix_len);
 h3_status launch_paged_rows(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H, float scale,
                             bool causal, const void* k_cache, const void* v_cache, int Hkv,
                             const PagedBatch& batch, const int32_t* prefix_pages, int prefix_len,
-                            cudaStream_t s);
+                            float* part_o, float* part_ml, cudaStream_t s);
 
 }  // namespace h3

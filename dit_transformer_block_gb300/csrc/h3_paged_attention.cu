@@ -34,13 +34,12 @@
 // heads, 1.40 ms (7.2 TB/s); 64 of 4,096 keys, 40 heads on 8, 165 us (6.5 TB/s).
 // Pages of 16 keys, the loading warp: a box of 2 KB takes it about 100 cycles (96
 // rows of up to 8,191 keys, 32 heads on 4: 165 us; pages of 32 and more 139 us, 6.2
-// TB/s). Chunks, the chain
-// through the one S buffer: product 512 cycles, seen 200, read 250, seen 200, twice
-// per key tile and two query tiles, 2,700 cycles against 2,048 of products (1,896
-// rows of 58,758 keys, 42 heads: 1.54 ms, 1,560 TFLOP/s; of 16,384 keys, 1,515).
-// Short items, instruction fetch: the kernel is 125 KB, and an item runs most of a
-// small part of it once (64 rows of up to 512 keys behind a prefix of 29,034, 42
-// heads: 194 us, of which the prefix's bytes take 92).
+// TB/s). Chunks, the chain through the one S buffer: product 512 cycles, seen 200,
+// read 250, seen 200, twice per key tile and two query tiles, 2,700 cycles against
+// 2,048 of products (1,896 rows of 58,758 keys, 42 heads: 1.54 ms, 1,560 TFLOP/s; of
+// 16,384 keys, 1,515). Short items, instruction fetch: the kernel is 125 KB, and an
+// item runs a small part of it once (6 causal chunks of up to 901 rows and 6,007
+// keys, 32 heads on 8: 141 us, products 69).
 #include <algorithm>
 
 #include "h3_attn_common.cuh"
@@ -97,6 +96,7 @@ struct PagedArgs {
   int causal;
   const int32_t* prefix_pages;
   int prefix_len;
+  int rows_own;      // the rows' own keys are another kernel's: its results are in row_o, row_ml
   // workspace
   int* teams;        // [2] CTAs per team of the two segments
   int4* cut;         // [CTA] the item that goes on after the CTA's share: tok0, ntok (0: none),
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       bool ok = true;
       const int first_seg = a.prefix_len > 0 ? 0 : 1;
 #pragma unroll 1
-      for (int seg = first_seg; ok && seg < 2; ++seg) {
+      for (int seg = first_seg; ok && seg < (a.rows_own ? 1 : 2); ++seg) {
         const Share sh = find_share(seg);
         if (blockIdx.x == 0 && lane == 0) a.teams[seg] = sh.g;
         const int member = static_cast<int>(blockIdx.x) % sh.g;
@@ -1152,6 +1152,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+    // the join, which waits for this kernel's end, has to find the rows' results too
+    if (a.rows_own) asm volatile("griddepcontrol.wait;" ::: "memory");
   }
 }
 
@@ -1243,12 +1245,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
 }
 
 // With a prefix: every row is joined from its results of the prefix and of its
-// own keys, each whole or split; a warp per (token, head).
+// own keys, each whole or split, or the second by h3_paged_rows.cu; a warp per
+// (token, head).
 __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const PagedArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.b.T) * a.H;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int team[2] = {__ldcg(a.teams), __ldcg(a.teams + 1)};
+  const int team[2] = {__ldcg(a.teams), a.rows_own ? 1 : __ldcg(a.teams + 1)};
   for (int64_t w = blockIdx.x * 8LL + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8LL) {
     const int t = static_cast<int>(w / a.H), head = static_cast<int>(w % a.H);
     const int hk = head / a.G;
@@ -1262,7 +1265,9 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const PagedArgs 
       if (t < s.c0 || t >= s.c0 + s.q_len) continue;
       const int item = 2 * a.tok;
       const int first = (t - s.c0) / item * item;
-      const int2 at = __ldcg(a.spread + (static_cast<int64_t>(seg) * a.b.T + s.c0 + first) * a.Hkv + hk);
+      int2 at = make_int2(0, 0);
+      if (seg == 0 || !a.rows_own)
+        at = __ldcg(a.spread + (static_cast<int64_t>(seg) * a.b.T + s.c0 + first) * a.Hkv + hk);
       any = true;
       if (at.x == at.y) {
         const int64_t i = (static_cast<int64_t>(seg) * a.b.T + t) * a.H + head;
@@ -1358,21 +1363,40 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
       (st = make_tmap_bf16_2d(&tk, k_cache, DH, a.total_rows, DH * 2, 64, page)) != H3_OK ||
       (st = make_tmap_bf16_2d(&tv, v_cache, DH, a.total_rows, DH * 2, 64, page)) != H3_OK)
     return st;
-  paged_attention_kernel<<<a.ctas, PA_THREADS, PA_SMEM_BYTES, s>>>(tq, tq1, tk, tv, a);
-  if ((st = cuda_fail(cudaGetLastError(), "paged attention launch")) != H3_OK) return st;
-  // items that cannot be split leave nothing to join
-  if (prefix_len == 0 && (static_cast<int64_t>(batch.max_pages) << batch.page_log2) <= PA_WHOLE * BKV)
-    return H3_OK;
-  // the join kernel's blocks may take their places while the first kernel
-  // runs; they wait for its end before they read anything
+  // The rows' own keys behind a prefix, many items of few keys, go to the kernel of
+  // short rows (64 rows of up to 512 keys behind 29,034, 42 heads: 172 us against 194;
+  // 128 rows of up to 200 keys behind 12,000, 8 heads: 43 / 50; of up to 1,000 behind
+  // 40,000: 98 / 96). With fewer items its launch costs what it saves (64 rows of up
+  // to 200 keys behind 40,000, 32 heads on 4: 55 / 53).
+  const int64_t own = static_cast<int64_t>(batch.max_pages) << batch.page_log2;
+  a.rows_own = prefix_len > 0 && static_cast<int64_t>(batch.T) * Hkv > 2 * num_sms() &&
+               paged_rows_fit(batch.T, H, Hkv, batch.B, own, 0);
+  if (a.rows_own &&
+      (st = launch_paged_rows(q, ld_q, o, ld_o, H, scale, causal, k_cache, v_cache, Hkv, batch,
+                              nullptr, 0, a.row_o + static_cast<int64_t>(batch.T) * H * DH,
+                              a.row_ml + static_cast<int64_t>(batch.T) * H * 2, s)) != H3_OK)
+    return st;
+  // the next kernel's blocks may take their places while the one before runs; they
+  // wait for its end before they read what it wrote
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = &attr;
+  cfg.numAttrs = a.rows_own;
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(PA_THREADS);
+  cfg.dynamicSmemBytes = PA_SMEM_BYTES;
+  st = cuda_fail(cudaLaunchKernelEx(&cfg, paged_attention_kernel, tq, tq1, tk, tv, a),
+                 "paged attention launch");
+  if (st != H3_OK) return st;
+  // items that cannot be split leave nothing to join
+  if (prefix_len == 0 && (static_cast<int64_t>(batch.max_pages) << batch.page_log2) <= PA_WHOLE * BKV)
+    return H3_OK;
   cfg.numAttrs = 1;
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
   if (prefix_len > 0) {
     const int64_t want = (static_cast<int64_t>(batch.T) * H + 7) / 8;
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, a.ctas * 8)));

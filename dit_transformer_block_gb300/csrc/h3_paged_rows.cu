@@ -44,6 +44,8 @@ struct RowsArgs {
   int causal;
   const int32_t* prefix_pages;
   int prefix_len;
+  float* part_o;   // not NULL: [T * H][128] sums and
+  float* part_ml;  // [T * H] (maximum, sum) go there instead of the output
 };
 
 // D += A B of one warp: A 16 x 16, B 16 x 8, bf16 in, FP32 out.
@@ -89,6 +91,12 @@ struct Joined {
     add(p, y);
   }
   __device__ __forceinline__ void store(const RowsArgs& a, int t, int head, int lane) const {
+    if (a.part_o != nullptr) {
+      const int64_t at = static_cast<int64_t>(t) * (a.Hkv * a.G) + head;
+      reinterpret_cast<float4*>(a.part_o + at * PR_DH)[lane] = o;
+      if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m, l);
+      return;
+    }
     const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key: zeros
     *reinterpret_cast<uint2*>(a.o + t * a.ld_o + head * PR_DH + lane * 4) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -108,6 +116,8 @@ __global__ void __launch_bounds__(32 * PR_MAX_WARPS, CTAS)
   const int heads = min(PR_HEADS, (hk + 1) * a.G - head0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int warp0 = rank * warps + warp, step = a.cluster * warps;
+  // a kernel that goes on from the partial results may take SMs that become free
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // In a product this lane has row (of A and D; also row n + 8) or column (of B) n,
   // and of the contraction the places 2 c, 2 c + 1, 2 c + 8 and 2 c + 9; of D columns
   // 2 c and 2 c + 1. Scores are q k^T (rows: heads), and which channel has which place
@@ -311,7 +321,7 @@ bool paged_rows_fit(int T, int H, int Hkv, int B, int64_t keys, int prefix_len) 
 h3_status launch_paged_rows(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H, float scale,
                             bool causal, const void* k_cache, const void* v_cache, int Hkv,
                             const PagedBatch& batch, const int32_t* prefix_pages, int prefix_len,
-                            cudaStream_t s) {
+                            float* part_o, float* part_ml, cudaStream_t s) {
   RowsArgs a{};
   a.b = batch;
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -326,6 +336,8 @@ h3_status launch_paged_rows(const void* q, int64_t ld_q, void* o, int64_t ld_o, 
   a.causal = causal ? 1 : 0;
   a.prefix_pages = prefix_pages;
   a.prefix_len = prefix_len;
+  a.part_o = part_o;
+  a.part_ml = part_ml;
   const int64_t keys = (static_cast<int64_t>(batch.max_pages) << batch.page_log2) + prefix_len;
   a.groups = rows_groups(H, Hkv);
   a.sets = a.groups * Hkv;

@@ -734,6 +734,43 @@ def test_two_captured_calls_in_turn(h3lib, prefix):
             assert bool((o[i][:ends[0]] == SENT).all()) and bool((o[i][ends[-1]:] == SENT).all())
 
 
+def test_calls_one_after_another_share_a_workspace(h3lib):
+    # rows of many sequences behind a prefix (two kernels and a join), a chunk, and a
+    # long row, in turn on one stream with one workspace, directly and captured
+    B = 170
+    calls, want = [], []
+    need = 0
+    for q_len, kv, prefix, seed in (([1] * B, [(i * 37) % 230 for i in range(B)], 1500, 1),
+                                    ([200], [1500], 0, 2), ([1], [15000], 0, 3),
+                                    ([1] * B, [(i * 53) % 120 + 1 for i in range(B)], 900, 4)):
+        P, cu = Paged(kv, 2, 16, seed, prefix), cumul(q_len)
+        q = rnd(gen(seed), cu[-1], 4, DH)
+        need = max(need, h3lib.attention_paged_workspace_bytes(cu[-1], 4, prefix))
+        calls.append((q, torch.empty_like(q), h3lib.kv_cache(P.k, P.v), P.batch(h3lib, cu, cu[-1]),
+                      P.prefix_pages if prefix else None, prefix))
+        want.append(attend(h3lib, q, P, cu))
+        check_attention(want[-1], q, P, cu, False, DH ** -0.5, f"call {seed}")
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+
+    def run():
+        for _ in range(4):
+            for q, o, c, b, pages, n in calls:
+                h3lib.attention_paged_prefix(q, o, c, b, pages, n, ws)
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run()
+    for go in (run, graph.replay, run):
+        for c in calls:
+            c[1].fill_(SENT)
+        go()
+        torch.cuda.synchronize()
+        h3lib.check_device_error()
+        assert all(torch.equal(c[1], w) for c, w in zip(calls, want))
+
+
 def test_append_many_sequences(h3lib):
     B = 2100
     q_len = [0 if i % 3 == 1 else 1 for i in range(B)]
