@@ -91,6 +91,8 @@ struct PagedArgs {
   __nv_bfloat16* o;
   int H, Hkv, G;
   int tok;           // tokens of one query tile: floor(128 / G)
+  int item;          // tokens of an item: those of two query tiles, or of one
+  int max_team;      // CTAs of a team, at most
   int total_rows;    // rows of the cache's tensor map: num_pages * Hkv * page_size
   float scale_log2;  // softmax_scale * log2(e)
   int causal;
@@ -156,7 +158,7 @@ constexpr int PA_MIN_SHARE = 2;
 // run over as many key tiles as the one that sees most).
 __device__ __forceinline__ int64_t head_cost(const PagedArgs& a, int seg, const SeqInfo& s,
                                               int g) {
-  const int item = 2 * a.tok * g;
+  const int item = a.item * g;
   const int n = (s.q_len + item - 1) / item;
   if (n == 0) return 0;
   if (!uneven(a, seg)) return static_cast<int64_t>(n) * (key_tiles(s, s.q_len) + PA_ITEM_COST);
@@ -396,15 +398,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 
   // the joining kernel may be set up while this one runs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < PA_BARS; ++i) {
-      uint32_t count = 1;
-      if (i >= PA_SFREE && i < PA_PVD) count = 4;
-      if (i >= PA_PC_EMPTY && i < PA_JOIN) count = 11;
-      if (i >= PA_JOIN && i < PA_DRAIN) count = 4;
-      if (i >= PA_Q_EMPTY && i < PA_S) count = 5;
-      mbar_init(bar(i), count);
-    }
+  // a barrier per thread (one thread for all of them: 2,400 cycles)
+  if (threadIdx.x < PA_BARS) {
+    const int i = threadIdx.x;
+    uint32_t count = 1;
+    if (i >= PA_SFREE && i < PA_PVD) count = 4;
+    if (i >= PA_PC_EMPTY && i < PA_JOIN) count = 11;
+    if (i >= PA_JOIN && i < PA_DRAIN) count = 4;
+    if (i >= PA_Q_EMPTY && i < PA_S) count = 5;
+    mbar_init(bar(i), count);
     fence_mbar_init();
   }
   if (threadIdx.x == PA_THREADS - 32) {
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
           if (g == 1) {
             rows = __reduce_max_sync(0xffffffffu, rows);
-            most = min(min(PA_MAX_TEAM, a.ctas), (rows + 2 * a.tok - 1) / (2 * a.tok));
+            most = min(min(a.max_team, a.ctas), (rows + a.item - 1) / a.item);
           }
           own *= a.Hkv;
           int64_t W = own;
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         const Share sh = find_share(seg);
         if (blockIdx.x == 0 && lane == 0) a.teams[seg] = sh.g;
         const int member = static_cast<int>(blockIdx.x) % sh.g;
-        const int item = 2 * a.tok;
+        const int item = a.item;
         const int n = seg == 0 ? 1 : a.b.B;
         int4 cut = make_int4(0, 0, 0, 0);
         int64_t left = sh.cost;
@@ -1263,7 +1265,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const PagedArgs 
     for (int seg = 0; seg < 2; ++seg) {
       const SeqInfo s = seq_info(a, seg, b);
       if (t < s.c0 || t >= s.c0 + s.q_len) continue;
-      const int item = 2 * a.tok;
+      const int item = a.item;
       const int first = (t - s.c0) / item * item;
       int2 at = make_int2(0, 0);
       if (seg == 0 || !a.rows_own)
@@ -1339,6 +1341,15 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   a.Hkv = Hkv;
   a.G = H / Hkv;
   a.tok = BQ / a.G;
+  const int64_t own = static_cast<int64_t>(batch.max_pages) << batch.page_log2;
+  // One query tile per item, and no teams, where none is split and there is a CTA for
+  // each of them (2 sequences of 185 rows and 446 keys, 32 heads on 8: 14.4 us against
+  // 16.5; one of 512 rows and keys, 4 heads: 13.3 / 15.6).
+  const bool whole = prefix_len == 0 && own <= PA_WHOLE * BKV;
+  const int ctas = std::min(num_sms(), PA_MAX_CTAS);
+  const bool one = whole && (batch.T / a.tok + static_cast<int64_t>(batch.B)) * Hkv <= ctas;
+  a.item = one ? a.tok : 2 * a.tok;
+  a.max_team = one ? 1 : PA_MAX_TEAM;
   a.total_rows = (batch.num_pages * Hkv) << batch.page_log2;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.causal = causal ? 1 : 0;
@@ -1352,7 +1363,7 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   a.part_rows = w.part_rows;
   a.row_o = reinterpret_cast<float*>(base + w.row_o);
   a.row_ml = reinterpret_cast<float*>(base + w.row_ml);
-  a.ctas = std::min(num_sms(), PA_MAX_CTAS);
+  a.ctas = ctas;
   if ((st = dev_err(&a.err)) != H3_OK) return st;
   CUtensorMap tq, tq1, tk, tv;
   const uint32_t page = 1u << batch.page_log2;
@@ -1368,7 +1379,6 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   // 128 rows of up to 200 keys behind 12,000, 8 heads: 43 / 50; of up to 1,000 behind
   // 40,000: 98 / 96). With fewer items its launch costs what it saves (64 rows of up
   // to 200 keys behind 40,000, 32 heads on 4: 55 / 53).
-  const int64_t own = static_cast<int64_t>(batch.max_pages) << batch.page_log2;
   a.rows_own = prefix_len > 0 && static_cast<int64_t>(batch.T) * Hkv > 2 * num_sms() &&
                paged_rows_fit(batch.T, H, Hkv, batch.B, own, 0);
   if (a.rows_own &&
@@ -1391,9 +1401,7 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   st = cuda_fail(cudaLaunchKernelEx(&cfg, paged_attention_kernel, tq, tq1, tk, tv, a),
                  "paged attention launch");
   if (st != H3_OK) return st;
-  // items that cannot be split leave nothing to join
-  if (prefix_len == 0 && (static_cast<int64_t>(batch.max_pages) << batch.page_log2) <= PA_WHOLE * BKV)
-    return H3_OK;
+  if (whole) return H3_OK;  // nothing is split, nothing to join
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
