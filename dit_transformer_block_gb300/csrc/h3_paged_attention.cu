@@ -148,8 +148,14 @@ __device__ __forceinline__ bool uneven(const PagedArgs& a, int seg) { return seg
 // and its output are not hidden behind other products.
 constexpr int PA_ITEM_COST = 2;
 // An item of up to so many key tiles is not split: it goes to the CTA in whose
-// share it begins.
-constexpr int PA_WHOLE = 4;
+// share it begins. One of more than a query tile's rows leaves a large partial result
+// (256 KB written and read for two query tiles), so it is kept whole up to more tiles,
+// and up to a share's worth, which leaves the CTAs within an item of one another.
+// (Against 4 for all: a causal chunk of 618 rows, 64 heads on 8, 33.6 -> 27.6 us; 4 of
+// 500 rows and 2,000 keys, 32 on 8, 75 -> 64; 7 of up to 1,469 rows and 2,203 keys, 12
+// heads, 85 -> 71; 6 of up to 901 rows and 1,500 keys, 8 heads, 47.6 -> 50.7. Up to a
+// share and 4 tiles more: 2 of up to 1,623 rows and 2,230 keys, 12 heads, 46 -> 59.)
+constexpr int PA_WHOLE = 4, PA_WHOLE_ROWS = 8, PA_WHOLE_SHARE = 32;
 // Least share of a CTA: a partial result costs more than a tile's time (8 rows
 // behind 4,099 keys, 16 heads on 2: 21.2 us for 2, 22.9 for 1, 24.0 for 4).
 constexpr int PA_MIN_SHARE = 2;
@@ -551,7 +557,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll 1
         while (ok && left > 0) {
           const int cost = group_cost();
-          const bool small = cost <= PA_WHOLE + PA_ITEM_COST;
+          const int most = s.q_len * a.G > BQ
+                               ? max(PA_WHOLE_ROWS, static_cast<int>(min(sh.per, int64_t{PA_WHOLE_SHARE})))
+                               : PA_WHOLE;
+          const bool small = cost <= most + PA_ITEM_COST;
           const int rest = cost - u;
           const int take = small ? rest : static_cast<int>(min(static_cast<int64_t>(rest), left));
           const int qt = qg * sh.g + member;
