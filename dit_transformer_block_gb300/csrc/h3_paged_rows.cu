@@ -307,15 +307,19 @@ static int rows_cluster(int64_t units, int64_t keys) {
 //     17.9 / 16.8; 84 CTAs of 4,000 keys in pairs 24 / 27; 126 CTAs of 2,000 keys
 //     26 / 35; 16 rows of one sequence, 1,000 keys, 12 heads on 4: 8.3 / 14.8
 //   more CTAs than SMs (a row's keys are read for itself, and once more per group of
-//     its heads): 1,024 rows of 256 keys, 32 heads on 8: 180 / 250; 96 rows of up to
+//     its heads): 1,024 rows of 256 keys, 32 heads on 8: 175 / 250; 96 rows of up to
 //     1,000 keys: 50 / 54, of 1,000 keys 83 / 74, of 2,000 keys 157 / 130; 512 rows of
-//     1,000 keys, 16 heads on 1: 74 / 61, of 60 keys 9 / 28; several rows of one
-//     sequence (8 of 1,000 keys, 42 heads): 29 / 17; behind a shared prefix of 900
-//     keys, 24 rows of 12 heads 20 / 22, 64 rows of 42 heads 155 / 82
+//     1,000 keys, 16 heads on 1: 74 / 61, of 60 keys 9 / 28. Several rows of one
+//     sequence read its keys several times: 8 sequences of 64 rows and keys, 4 heads
+//     8.5 / 10.5, 2 of 40 rows and 500 keys 17 / 13. So does every row a prefix, where
+//     the other kernel takes longer too: 32 rows of 42 heads behind 100 keys, 120 of
+//     their own 32 / 36, behind 900 keys 90 / 49
 bool paged_rows_fit(int T, int H, int Hkv, int B, int64_t keys, int prefix_len) {
   const int64_t groups = rows_groups(H, Hkv), units = groups * T * Hkv, sms = num_sms();
   if (units <= sms) return keys <= std::min(2048 * rows_cluster(units, keys), 10240);
-  return keys * groups * groups <= 1024 && T <= B && (prefix_len == 0 || units <= 2 * sms);
+  if (keys * groups * groups > 1024) return false;
+  if (prefix_len > 0) return units * keys <= 2048 * sms;
+  return T <= B || units * keys <= 900 * sms;
 }
 
 h3_status launch_paged_rows(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H, float scale,
