@@ -1168,16 +1168,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   }
 }
 
+// With a prefix every row passes the join, so warps in flight count: four CTAs per
+// SM (64 registers) and four partials at a time (6 chunks of 300 rows behind 1,000
+// keys, 42 heads: 132 us; three CTAs 142, three and eight partials 160; 48 rows behind
+// 58,758 keys, whose partials are many: 91.6, 89.8, 93.2).
+constexpr int PA_JOIN_CTAS = 4, PA_JOIN_PREFIX = 4;
 // A row's result while its partials are joined, four channels per lane.
 struct Joined {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 };
 
-// Adds up to 32 partial results to j: lane i holds the (maximum, sum) of the
+// Adds up to 32 partial results to j, N of them in flight: lane i holds the (maximum, sum) of the
 // i-th, src(i) is where its channels lie. In the order of their keys, so the
 // sums do not depend on which CTA came first.
-template <class Src>
+template <int N, class Src>
 __device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& src) {
   const int lane = threadIdx.x & 31;
   float top = ml.x;
@@ -1195,7 +1200,6 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& sr
   j.o.y *= c;
   j.o.z *= c;
   j.o.w *= c;
-  constexpr int N = 8;  // partials in flight
   for (int i0 = 0; i0 < n; i0 += N) {
     float4 x[N];
 #pragma unroll
@@ -1216,6 +1220,7 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& sr
 
 // Row r of an item that CTAs c0, c0 + g, .. c1 have parts of: the end of the
 // first one's share, the beginning of the others'.
+template <int N>
 __device__ __forceinline__ void join_split(Joined& j, const PagedArgs& a, int seg, int c0, int c1,
                                            int g, int r) {
   const int lane = threadIdx.x & 31;
@@ -1228,7 +1233,7 @@ __device__ __forceinline__ void join_split(Joined& j, const PagedArgs& a, int se
     const float2 ml = base + lane < n
                           ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot(base + lane))
                           : make_float2(-INFINITY, 0.f);
-    join_parts(j, min(n - base, 32), ml,
+    join_parts<N>(j, min(n - base, 32), ml,
                [&](int i) { return a.part_o + slot(base + i) * DH; });
   }
 }
@@ -1250,15 +1255,16 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
   const int g = rows > 0 ? __ldcg(a.teams + 1) : 1;
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += PA_JOIN_Y * 8) {
     Joined j;
-    join_split(j, a, 0, c, cut.w, g, r);
+    join_split<8>(j, a, 0, c, cut.w, g, r);
     store_joined(j, a, cut.x + r / a.G, cut.z * a.G + r % a.G);
   }
 }
 
 // With a prefix: every row is joined from its results of the prefix and of its
 // own keys, each whole or split, or the second by h3_paged_rows.cu; a warp per
-// (token, head).
-__global__ void __launch_bounds__(256) paged_join_prefix_kernel(const PagedArgs a) {
+// (token, head). What bounds it is the chain of loads of a row (sequence, ranges,
+// places, results), so those of both segments are in flight together.
+__global__ void __launch_bounds__(256, PA_JOIN_CTAS) paged_join_prefix_kernel(const PagedArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.b.T) * a.H;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1268,29 +1274,50 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const PagedArgs 
     const int hk = head / a.G;
     const int b = ends_up_to(a.b.cu_q, a.b.B, t);  // the row's sequence
     if (b >= a.b.B) continue;
-    Joined j;
-    bool any = false;
+    bool in[2];
+    int2 at[2];  // first and last CTA that has a part of the row's item
+    int row[2];  // of the item
 #pragma unroll
     for (int seg = 0; seg < 2; ++seg) {
       const SeqInfo s = seq_info(a, seg, b);
-      if (t < s.c0 || t >= s.c0 + s.q_len) continue;
-      const int item = a.item;
-      const int first = (t - s.c0) / item * item;
-      int2 at = make_int2(0, 0);
-      if (seg == 0 || !a.rows_own)
-        at = __ldcg(a.spread + (static_cast<int64_t>(seg) * a.b.T + s.c0 + first) * a.Hkv + hk);
-      any = true;
-      if (at.x == at.y) {
-        const int64_t i = (static_cast<int64_t>(seg) * a.b.T + t) * a.H + head;
-        const float2 ml = lane == 0 ? __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i)
-                                    : make_float2(-INFINITY, 0.f);
-        join_parts(j, 1, ml, [&](int) { return a.row_o + i * DH; });
-      } else {
-        join_split(j, a, seg, min(max(at.x, 0), a.ctas - 1), min(max(at.y, 0), a.ctas - 1),
-                   team[seg], (t - s.c0 - first) * a.G + head % a.G);
+      in[seg] = t >= s.c0 && t < s.c0 + s.q_len;
+      const int first = in[seg] ? (t - s.c0) / a.item * a.item : 0;
+      row[seg] = (t - s.c0 - first) * a.G + head % a.G;
+      at[seg] = make_int2(0, 0);
+      if (in[seg] && (seg == 0 || !a.rows_own))
+        at[seg] = __ldcg(a.spread + (static_cast<int64_t>(seg) * a.b.T + s.c0 + first) * a.Hkv + hk);
+    }
+    if (!in[0] && !in[1]) continue;
+    const int64_t i1 = rows + w;
+    Joined j;
+    if (in[0] && in[1] && at[0].x == at[0].y && at[1].x == at[1].y) {  // both whole
+      const float2 ml0 = __ldcg(reinterpret_cast<const float2*>(a.row_ml) + w);
+      const float2 ml1 = __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i1);
+      const float4 x0 = __ldcg(reinterpret_cast<const float4*>(a.row_o + w * DH) + lane);
+      const float4 x1 = __ldcg(reinterpret_cast<const float4*>(a.row_o + i1 * DH) + lane);
+      const float m = fmaxf(ml0.x, ml1.x);
+      const float f0 = m == -INFINITY ? 0.f : ex2_approx(ml0.x - m);
+      const float f1 = m == -INFINITY ? 0.f : ex2_approx(ml1.x - m);
+      j.l = ml0.y * f0 + ml1.y * f1;
+      j.o = make_float4(x0.x * f0 + x1.x * f1, x0.y * f0 + x1.y * f1, x0.z * f0 + x1.z * f1,
+                        x0.w * f0 + x1.w * f1);
+    } else {
+#pragma unroll 1
+      for (int seg = 0; seg < 2; ++seg) {
+        if (!(seg ? in[1] : in[0])) continue;
+        const int2 p = seg ? at[1] : at[0];
+        if (p.x == p.y) {
+          const int64_t i = seg ? i1 : w;
+          const float2 ml = lane == 0 ? __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i)
+                                      : make_float2(-INFINITY, 0.f);
+          join_parts<1>(j, 1, ml, [&](int) { return a.row_o + i * DH; });
+        } else {
+          join_split<PA_JOIN_PREFIX>(j, a, seg, min(max(p.x, 0), a.ctas - 1), min(max(p.y, 0), a.ctas - 1),
+                     seg ? team[1] : team[0], seg ? row[1] : row[0]);
+        }
       }
     }
-    if (any) store_joined(j, a, t, head);
+    store_joined(j, a, t, head);
   }
 }
 
