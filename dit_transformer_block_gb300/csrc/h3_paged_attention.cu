@@ -1168,23 +1168,25 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   }
 }
 
-// With a prefix every row passes the join, so warps in flight count: four CTAs per
-// SM (64 registers) and four partials at a time (6 chunks of 300 rows behind 1,000
-// keys, 42 heads: 132 us; three CTAs 142, three and eight partials 160; 48 rows behind
-// 58,758 keys, whose partials are many: 91.6, 89.8, 93.2).
-constexpr int PA_JOIN_CTAS = 4, PA_JOIN_PREFIX = 4;
+// Joins. With a prefix every row passes one, so warps in flight count: four CTAs per SM
+// (64 registers) and four partials at a time (6 chunks of 300 rows behind 1,000 keys, 42
+// heads: 132 us; three CTAs 142, three and eight partials 160). Where the items are so
+// few that a row has more than PA_JOIN_MANY partials, up to eight warps of a CTA share
+// them: 2 sequences of up to 6 rows and 27,758 keys, 24 heads on 1, 22 us against 38
+// with a warp per row (and 2 of up to 3 rows and 8,277 keys, 32 heads on 4, about 19
+// partials, 19.7 against 18.5).
+constexpr int PA_JOIN_CTAS = 4, PA_JOIN_N = 4, PA_JOIN_WARPS = 8, PA_JOIN_MANY = 32;
 // A row's result while its partials are joined, four channels per lane.
 struct Joined {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 };
 
-// Adds up to 32 partial results to j, N of them in flight: lane i holds the (maximum, sum) of the
-// i-th, src(i) is where its channels lie. In the order of their keys, so the
-// sums do not depend on which CTA came first.
-template <int N, class Src>
-__device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& src) {
-  const int lane = threadIdx.x & 31;
+// Adds up to 32 partial results to j, N of them in flight: lane i holds the (maximum,
+// sum) of the i-th, load(i) gives this lane's channels of it. In the order of their
+// keys, so the sums do not depend on which CTA came first.
+template <int N, class Load>
+__device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Load&& load) {
   float top = ml.x;
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -1204,7 +1206,7 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& sr
     float4 x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(src(i0 + i)) + lane);
+      if (i0 + i < n) x[i] = load(i0 + i);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
@@ -1218,24 +1220,52 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, float2 ml, Src&& sr
   }
 }
 
-// Row r of an item that CTAs c0, c0 + g, .. c1 have parts of: the end of the
-// first one's share, the beginning of the others'.
+__device__ __forceinline__ float4 load_part(const float* row) {
+  return __ldcg(reinterpret_cast<const float4*>(row) + (threadIdx.x & 31));
+}
+
+// Row r of an item that CTAs c0, c0 + g, .. c1 have parts of (the end of the first
+// one's share, the beginning of the others'): the sub-th of `subs` equal runs of them.
 template <int N>
 __device__ __forceinline__ void join_split(Joined& j, const PagedArgs& a, int seg, int c0, int c1,
-                                           int g, int r) {
+                                           int g, int r, int sub, int subs) {
   const int lane = threadIdx.x & 31;
-  const int n = (c1 - c0) / g + 1;
+  const int n = (c1 - c0) / g + 1, run = (n + subs - 1) / subs;
+  const int end = min((sub + 1) * run, n);
   auto slot = [&](int i) {
     return static_cast<int64_t>((seg * PA_MAX_CTAS + c0 + i * g) * 2 + (i == 0 ? 1 : 0)) *
                a.part_rows + r;
   };
-  for (int base = 0; base < n; base += 32) {
-    const float2 ml = base + lane < n
+  for (int base = sub * run; base < end; base += 32) {
+    const float2 ml = base + lane < end
                           ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot(base + lane))
                           : make_float2(-INFINITY, 0.f);
-    join_parts<N>(j, min(n - base, 32), ml,
-               [&](int i) { return a.part_o + slot(base + i) * DH; });
+    join_parts<N>(j, min(end - base, 32), ml,
+                  [&](int i) { return load_part(a.part_o + slot(base + i) * DH); });
   }
+}
+
+// Warps of a CTA that share a row, when the grid's warps are for so many rows.
+__device__ __forceinline__ int join_subs(int64_t rows) {
+  int n = 1;
+  while (n < PA_JOIN_WARPS && rows * n * 2 <= static_cast<int64_t>(gridDim.x) * PA_JOIN_WARPS) n *= 2;
+  return n;
+}
+
+// Adds what the other warps of the row have to the first one's. All of the CTA.
+__device__ __forceinline__ void join_warps(Joined& j, float4 (&part)[PA_JOIN_WARPS][32],
+                                           float2 (&ml)[PA_JOIN_WARPS], int subs) {
+  if (subs == 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (subs - 1);
+  __syncthreads();  // the row before has been read
+  part[warp][lane] = j.o;
+  if (lane == 0) ml[warp] = make_float2(j.m, j.l);
+  __syncthreads();
+  if (sub != 0) return;
+  const float2 mine = lane < subs ? ml[warp + lane] : make_float2(-INFINITY, 0.f);
+  Joined all;
+  join_parts<PA_JOIN_N>(all, subs, mine, [&](int i) { return part[warp + i][lane]; });
+  j = all;
 }
 
 __device__ __forceinline__ void store_joined(const Joined& j, const PagedArgs& a, int t, int head) {
@@ -1247,16 +1277,75 @@ __device__ __forceinline__ void store_joined(const Joined& j, const PagedArgs& a
 // Without a prefix: block (c, y) joins rows of the item that goes on after CTA
 // c's share, a warp per row.
 constexpr int PA_JOIN_Y = 8;
-__global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(32 * PA_JOIN_WARPS) paged_join_kernel(const PagedArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const int4 cut = __ldcg(a.cut + c);
   const int rows = cut.y * a.G;
   const int g = rows > 0 ? __ldcg(a.teams + 1) : 1;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += PA_JOIN_Y * 8) {
+  for (int r = blockIdx.y * PA_JOIN_WARPS + (threadIdx.x >> 5); r < rows;
+       r += PA_JOIN_Y * PA_JOIN_WARPS) {
     Joined j;
-    join_split<8>(j, a, 0, c, cut.w, g, r);
+    join_split<8>(j, a, 0, c, cut.w, g, r, 0, 1);
     store_joined(j, a, cut.x + r / a.G, cut.z * a.G + r % a.G);
+  }
+}
+
+// The same where rows have many partials: the rows of those items, laid end to end,
+// are spread over the grid's CTAs, several warps to a row.
+__global__ void __launch_bounds__(32 * PA_JOIN_WARPS)
+    paged_join_many_kernel(const PagedArgs a) {
+  __shared__ int start[PA_MAX_CTAS + 1];  // first row of every CTA's cut item
+  __shared__ float4 part[PA_JOIN_WARPS][32];
+  __shared__ float2 ml[PA_JOIN_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    constexpr int RUN = PA_MAX_CTAS / 32;
+    int rows[RUN], sum = 0;
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      const int c = lane * RUN + i;
+      rows[i] = c < a.ctas ? __ldcg(a.cut + c).y * a.G : 0;
+      sum += rows[i];
+    }
+    int at = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, d);
+      if (lane >= d) at += v;
+    }
+    if (lane == 31) start[PA_MAX_CTAS] = at;
+    at -= sum;
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      start[lane * RUN + i] = at;
+      at += rows[i];
+    }
+  }
+  __syncthreads();
+  const int total = start[PA_MAX_CTAS];
+  const int subs = join_subs(total), each = PA_JOIN_WARPS / subs;
+  const int sub = warp & (subs - 1);
+  const int g = total > 0 ? __ldcg(a.teams + 1) : 1;
+  for (int base = blockIdx.x * each; base < total; base += gridDim.x * each) {
+    const int w = base + warp / subs;
+    Joined j;
+    int4 cut{};
+    int r = 0;
+    if (w < total) {
+      // the last CTA whose item begins at or before the row (those without rows
+      // begin where the next one does)
+      int before = 0;
+#pragma unroll
+      for (int i = 0; i < PA_MAX_CTAS / 32; ++i) before += start[i * 32 + lane + 1] <= w ? 1 : 0;
+      const int c = __reduce_add_sync(0xffffffffu, before);
+      cut = __ldcg(a.cut + c);
+      r = w - start[c];
+      join_split<8>(j, a, 0, c, cut.w, g, r, sub, subs);
+    }
+    join_warps(j, part, ml, subs);
+    if (w < total && sub == 0) store_joined(j, a, cut.x + r / a.G, cut.z * a.G + r % a.G);
   }
 }
 
@@ -1264,60 +1353,74 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
 // own keys, each whole or split, or the second by h3_paged_rows.cu; a warp per
 // (token, head). What bounds it is the chain of loads of a row (sequence, ranges,
 // places, results), so those of both segments are in flight together.
-__global__ void __launch_bounds__(256, PA_JOIN_CTAS) paged_join_prefix_kernel(const PagedArgs a) {
-  const int lane = threadIdx.x & 31;
+// MANY: several warps to a row.
+template <bool MANY>
+__global__ void __launch_bounds__(32 * PA_JOIN_WARPS, MANY ? 1 : PA_JOIN_CTAS)
+    paged_join_prefix_kernel(const PagedArgs a) {
+  __shared__ float4 part[PA_JOIN_WARPS][32];
+  __shared__ float2 ml[PA_JOIN_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.b.T) * a.H;
+  const int subs = MANY ? join_subs(rows) : 1, each = PA_JOIN_WARPS / subs;
+  const int sub = warp & (subs - 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int team[2] = {__ldcg(a.teams), a.rows_own ? 1 : __ldcg(a.teams + 1)};
-  for (int64_t w = blockIdx.x * 8LL + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8LL) {
-    const int t = static_cast<int>(w / a.H), head = static_cast<int>(w % a.H);
-    const int hk = head / a.G;
-    const int b = ends_up_to(a.b.cu_q, a.b.B, t);  // the row's sequence
-    if (b >= a.b.B) continue;
-    bool in[2];
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * each; base < rows;
+       base += static_cast<int64_t>(gridDim.x) * each) {
+    const int64_t w = base + warp / subs;
+    const int t = static_cast<int>(min(w, rows - 1) / a.H);
+    const int head = static_cast<int>(min(w, rows - 1) % a.H), hk = head / a.G;
+    const int b = w < rows ? ends_up_to(a.b.cu_q, a.b.B, t) : a.b.B;  // the row's sequence
+    bool in[2] = {false, false};
     int2 at[2];  // first and last CTA that has a part of the row's item
     int row[2];  // of the item
 #pragma unroll
     for (int seg = 0; seg < 2; ++seg) {
+      at[seg] = make_int2(0, 0);
+      row[seg] = 0;
+      if (b >= a.b.B) continue;
       const SeqInfo s = seq_info(a, seg, b);
       in[seg] = t >= s.c0 && t < s.c0 + s.q_len;
       const int first = in[seg] ? (t - s.c0) / a.item * a.item : 0;
       row[seg] = (t - s.c0 - first) * a.G + head % a.G;
-      at[seg] = make_int2(0, 0);
       if (in[seg] && (seg == 0 || !a.rows_own))
         at[seg] = __ldcg(a.spread + (static_cast<int64_t>(seg) * a.b.T + s.c0 + first) * a.Hkv + hk);
     }
-    if (!in[0] && !in[1]) continue;
-    const int64_t i1 = rows + w;
     Joined j;
+    const int64_t i1 = rows + w;
     if (in[0] && in[1] && at[0].x == at[0].y && at[1].x == at[1].y) {  // both whole
-      const float2 ml0 = __ldcg(reinterpret_cast<const float2*>(a.row_ml) + w);
-      const float2 ml1 = __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i1);
-      const float4 x0 = __ldcg(reinterpret_cast<const float4*>(a.row_o + w * DH) + lane);
-      const float4 x1 = __ldcg(reinterpret_cast<const float4*>(a.row_o + i1 * DH) + lane);
-      const float m = fmaxf(ml0.x, ml1.x);
-      const float f0 = m == -INFINITY ? 0.f : ex2_approx(ml0.x - m);
-      const float f1 = m == -INFINITY ? 0.f : ex2_approx(ml1.x - m);
-      j.l = ml0.y * f0 + ml1.y * f1;
-      j.o = make_float4(x0.x * f0 + x1.x * f1, x0.y * f0 + x1.y * f1, x0.z * f0 + x1.z * f1,
-                        x0.w * f0 + x1.w * f1);
+      if (sub == 0) {
+        const float2 ml0 = __ldcg(reinterpret_cast<const float2*>(a.row_ml) + w);
+        const float2 ml1 = __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i1);
+        const float4 x0 = load_part(a.row_o + w * DH), x1 = load_part(a.row_o + i1 * DH);
+        const float m = fmaxf(ml0.x, ml1.x);
+        const float f0 = m == -INFINITY ? 0.f : ex2_approx(ml0.x - m);
+        const float f1 = m == -INFINITY ? 0.f : ex2_approx(ml1.x - m);
+        j.m = m;
+        j.l = ml0.y * f0 + ml1.y * f1;
+        j.o = make_float4(x0.x * f0 + x1.x * f1, x0.y * f0 + x1.y * f1, x0.z * f0 + x1.z * f1,
+                          x0.w * f0 + x1.w * f1);
+      }
     } else {
 #pragma unroll 1
       for (int seg = 0; seg < 2; ++seg) {
         if (!(seg ? in[1] : in[0])) continue;
         const int2 p = seg ? at[1] : at[0];
         if (p.x == p.y) {
+          if (sub != 0) continue;
           const int64_t i = seg ? i1 : w;
-          const float2 ml = lane == 0 ? __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i)
-                                      : make_float2(-INFINITY, 0.f);
-          join_parts<1>(j, 1, ml, [&](int) { return a.row_o + i * DH; });
+          const float2 v = lane == 0 ? __ldcg(reinterpret_cast<const float2*>(a.row_ml) + i)
+                                     : make_float2(-INFINITY, 0.f);
+          join_parts<1>(j, 1, v, [&](int) { return load_part(a.row_o + i * DH); });
         } else {
-          join_split<PA_JOIN_PREFIX>(j, a, seg, min(max(p.x, 0), a.ctas - 1), min(max(p.y, 0), a.ctas - 1),
-                     seg ? team[1] : team[0], seg ? row[1] : row[0]);
+          join_split<MANY ? 8 : PA_JOIN_N>(
+                     j, a, seg, min(max(p.x, 0), a.ctas - 1), min(max(p.y, 0), a.ctas - 1),
+                     seg ? team[1] : team[0], seg ? row[1] : row[0], sub, subs);
         }
       }
     }
-    store_joined(j, a, t, head);
+    if constexpr (MANY) join_warps(j, part, ml, subs);
+    if (sub == 0 && (in[0] || in[1])) store_joined(j, a, t, head);
   }
 }
 
@@ -1439,16 +1542,27 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   if (st != H3_OK) return st;
   if (whole) return H3_OK;  // nothing is split, nothing to join
   cfg.numAttrs = 1;
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * PA_JOIN_WARPS);
   cfg.dynamicSmemBytes = 0;
-  if (prefix_len > 0) {
-    const int64_t want = (static_cast<int64_t>(batch.T) * H + 7) / 8;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, a.ctas * 8)));
-    return cuda_fail(cudaLaunchKernelEx(&cfg, paged_join_prefix_kernel, a),
-                     "paged attention join launch");
+  // items of the prefix, or at least so many of the sequences' own keys
+  const int64_t tiles = (batch.T + a.item - 1) / a.item;
+  const int64_t items = (prefix_len > 0 ? tiles : std::max<int64_t>(tiles, batch.B)) * Hkv;
+  const bool many = items * PA_JOIN_MANY <= a.ctas;
+  const int64_t rows = static_cast<int64_t>(batch.T) * H;
+  cudaError_t e;
+  if (many) {
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, a.ctas * 3)));
+    e = prefix_len > 0 ? cudaLaunchKernelEx(&cfg, paged_join_prefix_kernel<true>, a)
+                       : cudaLaunchKernelEx(&cfg, paged_join_many_kernel, a);
+  } else if (prefix_len > 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(
+        std::min<int64_t>((rows + PA_JOIN_WARPS - 1) / PA_JOIN_WARPS, a.ctas * 8)));
+    e = cudaLaunchKernelEx(&cfg, paged_join_prefix_kernel<false>, a);
+  } else {
+    cfg.gridDim = dim3(a.ctas, PA_JOIN_Y);
+    e = cudaLaunchKernelEx(&cfg, paged_join_kernel, a);
   }
-  cfg.gridDim = dim3(a.ctas, PA_JOIN_Y);
-  return cuda_fail(cudaLaunchKernelEx(&cfg, paged_join_kernel, a), "paged attention join launch");
+  return cuda_fail(e, "paged attention join launch");
 }
 
 }  // namespace h3
