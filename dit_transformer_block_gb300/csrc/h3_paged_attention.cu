@@ -444,16 +444,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         const int run = (n + 31) / 32;
         const int b0 = min(lane * run, n), b1 = min(b0 + run, n);
         Share sh{0, 0, 1, 0, 1};
-        int64_t total = 0, mine = 0;
+        int64_t mine = 0;
         float least = 0.f;
         int most = 1;  // no team is larger than the items of a sequence
+        SeqInfo s{};
 #pragma unroll 1
-        for (int g = 1; g <= most; ++g) {
+        for (int g = 1; g <= most; g += g < 4 ? 1 : 2) {
           int64_t own = 0;
           int rows = 0;
 #pragma unroll 1
           for (int b = b0; b < b1; ++b) {
-            const SeqInfo s = seq_info(a, seg, b);
+            if (g == 1 || run > 1) s = seq_info(a, seg, b);
             own += head_cost(a, seg, s, g);
             rows = max(rows, s.q_len);
           }
@@ -462,18 +463,19 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             most = min(min(a.max_team, a.ctas), (rows + a.item - 1) / a.item);
           }
           own *= a.Hkv;
-          int64_t W = own;
+          float W = static_cast<float>(own);
 #pragma unroll
           for (int d = 16; d >= 1; d >>= 1) W += __shfl_xor_sync(0xffffffffu, W, d);
-          const float cost = ceilf(static_cast<float>(W) / static_cast<float>(a.ctas / g)) *
-                             (g == 1 ? 6.f : 5.f);
+          const float cost = ceilf(W / static_cast<float>(a.ctas / g)) * (g == 1 ? 6.f : 5.f);
           if (g == 1 || cost < least) {
             least = cost;
-            total = W;
             mine = own;
             sh.g = g;
           }
         }
+        int64_t total = mine;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
         const int teams = a.ctas / sh.g, team = static_cast<int>(blockIdx.x) / sh.g;
         sh.per = max(div64(total + teams - 1, teams), int64_t{PA_MIN_SHARE});
         const int64_t begin = team * sh.per;
