@@ -260,10 +260,11 @@ h3_status launch_kv_append(const void* q, int64_t ld_q, const void* k, int64_t l
     std::copy(axis_dims, axis_dims + 3, tab_axis);
     tab_theta = theta;
   }
-  // several rows per CTA once every SM has a few CTAs of them; the heads of few
-  // rows are spread over two CTAs per SM
+  // several rows per CTA once every SM has 16 CTAs of them (2,600 rows of 42 + 84 heads:
+  // one row 38 us, two 44; 58,758: 667, 642); the heads of few rows are spread over two
+  // CTAs per SM
   const int heads = H + 2 * Hkv, sms = num_sms();
-  a.rows = batch.T >= 8 * APPEND_ROWS * sms ? APPEND_ROWS : 1;
+  a.rows = batch.T >= 16 * APPEND_ROWS * sms ? APPEND_ROWS : 1;
   const int slices = std::min(std::max(2 * sms / batch.T, 1), (heads + APPEND_STEP - 1) / APPEND_STEP);
   a.slice = (heads + slices - 1) / slices;
   a.slice = (a.slice + APPEND_STEP - 1) / APPEND_STEP * APPEND_STEP;
