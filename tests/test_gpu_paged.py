@@ -17,6 +17,7 @@ within 2^-23). In the mean, over inputs of random sign: the two bf16 roundings
 are independent and uniform within half a step, so the relative L2 error is at
 most u sqrt(2 / 3), and the other terms do not add to u: rel-L2 <= u."""
 import math
+import random
 
 import pytest
 import torch
@@ -326,6 +327,22 @@ def test_short_chunks(h3lib):
     run_attention(h3lib, [4, 1, 7], [900, 40, 7], 6, 2, 32, causal=True)
     run_attention(h3lib, [4, 1, 7], [900, 40, 7], 10, 1, 16, prefix=33)
     run_attention(h3lib, [30], [20], 4, 4, 16, causal=True, first=2, behind=3)
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_drawn_batches(h3lib, seed):
+    r = random.Random(seed)
+    log = lambda lo, hi: round(math.exp(r.uniform(math.log(lo), math.log(hi))))  # noqa: E731
+    G, Hkv = r.choice([1, 1, 2, 3, 5, 8, 12, 17, 40]), r.choice([1, 2, 3, 7])
+    B, prefix = log(1, 60), r.choice([0, 0, 0, log(1, 3000)])
+    q_len = [r.choice([0, 1, 1, 1, log(1, max(2, 700 // B))]) for _ in range(B)]
+    kv = [0 if r.random() < 0.1 else log(1, r.choice([100, 1000, max(2, 40000 // B)])) for _ in q_len]
+    if r.random() < 0.4:
+        q_len = [min(n, 1) for n in q_len]
+    if not sum(q_len):
+        q_len[0] = 1
+    run_attention(h3lib, q_len, kv, G * Hkv, Hkv, r.choice([16, 32, 64, 128]), r.random() < 0.4, prefix,
+                  seed, first=r.choice([0, 3]), behind=r.choice([0, 5]))
 
 
 def test_large_scores(h3lib):

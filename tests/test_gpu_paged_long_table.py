@@ -12,7 +12,8 @@ from test_gpu_paged import (  # noqa: F401
     test_repeats_are_bit_identical, test_another_stream_and_two_at_once,
     test_captured_calls_follow_the_device_arrays, test_two_captured_calls_in_turn,
     test_append_rows_without_a_place, test_short_chunks,
-    test_row_ranges_out_of_order_stay_inside, test_offsets_past_32_bits)
+    test_row_ranges_out_of_order_stay_inside, test_offsets_past_32_bits, test_drawn_batches,
+    test_calls_one_after_another_share_a_workspace)
 
 pytestmark = pytest.mark.gpu
 
