@@ -291,12 +291,16 @@ __global__ void __launch_bounds__(32 * PR_MAX_WARPS, CTAS)
 static int rows_groups(int H, int Hkv) { return (H / Hkv + PR_HEADS - 1) / PR_HEADS; }
 
 // CTAs for a row and group of heads: several, a cluster, where that leaves none of
-// them waiting for a place. (Of 152 SMs, clusters of eight find 120 to be resident
-// on at once: 16 of them take 16.1 us for 4,000 keys, 15 take 9.0.)
+// them waiting for a place, and 128 keys for each. Of 152 SMs, clusters of eight (and
+// of seven) find 120 to be resident on at once, of six 132, of five, four and three
+// 135: 2,000 keys of 15 rows take 7.1 us with eight, 8.1 with six, of 16 rows 12.4
+// and 8.2; of 45 rows 13.6 with two, 11.9 with three, 17.5 with four.
 static int rows_cluster(int64_t units, int64_t keys) {
   const int sms = num_sms();
   if (keys >= 1024 && units * 8 <= sms * 4 / 5) return 8;
-  if (keys >= 512 && units * 4 <= sms * 9 / 10) return 4;
+  if (keys >= 768 && units * 6 <= sms * 7 / 8) return 6;
+  for (int n = 5; n >= 3; --n)
+    if (keys >= 128 * n && units * n <= sms * 8 / 9) return n;
   return keys >= 256 && units * 2 <= sms ? 2 : 1;
 }
 

@@ -315,7 +315,7 @@ def test_single_rows_of_growing_tables(h3lib, H, Hkv, kv):
     run_attention(h3lib, [1, 1, 0, 1], [kv, 1, 5, kv // 3], H, Hkv, 32, prefix=70 if kv < 2000 else 0)
 
 
-@pytest.mark.parametrize("B", [14, 15, 16, 33, 35, 75, 77, 151, 153, 305, 700])
+@pytest.mark.parametrize("B", [10, 14, 15, 16, 22, 23, 27, 28, 33, 35, 45, 46, 75, 77, 151, 153, 305, 700])
 def test_single_rows_of_growing_batches(h3lib, B):
     run_attention(h3lib, [1] * B, [(i * 131) % 1100 for i in range(B)], 2, 1, 64)
     run_attention(h3lib, [1] * B, [(i * 131) % 300 for i in range(B)], 18, 2, 16)
