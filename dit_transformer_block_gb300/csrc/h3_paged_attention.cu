@@ -37,7 +37,7 @@
 // TB/s). Chunks, the chain through the one S buffer: product 512 cycles, seen 200,
 // read 250, seen 200, twice per key tile and two query tiles, 2,700 cycles against
 // 2,048 of products (1,896 rows of 58,758 keys, 42 heads: 1.54 ms, 1,560 TFLOP/s; of
-// 16,384 keys, 1,515). Short items, instruction fetch: the kernel is 125 KB, and an
+// 16,384 keys, 1,500). Short items, instruction fetch: the kernel is 125 KB, and an
 // item runs a small part of it once (6 causal chunks of up to 901 rows and 6,007
 // keys, 32 heads on 8: 141 us, products 69).
 #include <algorithm>
