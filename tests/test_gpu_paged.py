@@ -267,6 +267,17 @@ def test_second_query_tile_of_few_rows(h3lib, G):
     run_attention(h3lib, [t + 1, 1, 2 * t + 1], [700, 3, 1500], 2 * G, 2, 16, prefix=400)
 
 
+@pytest.mark.parametrize("prefix", [0, 300, 13000])
+def test_a_table_without_pages(h3lib, prefix):
+    # no sequence has a place for a key: nothing, or the prefix alone
+    P = Paged([0, 0], 2, 16, prefix=prefix)
+    P.table = torch.zeros(2, 0, dtype=torch.int32, device=dev)
+    q = rnd(gen(34), 5, 6, DH)
+    o = attend(h3lib, q, P, [0, 2, 5], causal=True)
+    check_attention(o, q, P, [0, 2, 5], True, DH ** -0.5)
+    assert prefix or bool((o == 0).all())
+
+
 def test_a_page_in_several_places(h3lib):
     # the same page twice in a sequence, in two sequences and in the prefix
     P = Paged([200, 150, 64], 2, 32, prefix=96)
