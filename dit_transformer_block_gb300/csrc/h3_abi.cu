@@ -627,8 +627,9 @@ h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t
   if ((st = check_strided("k", k, ld_k, cache->Hkv)) != H3_OK) return st;
   if ((st = check_strided("v", v, ld_v, cache->Hkv)) != H3_OK) return st;
   H3_REQUIRE(pos != nullptr, H3_ERR_INVALID_ARG, "pos is NULL");
-  H3_REQUIRE(q == nullptr || (q_gain == nullptr) == (k_gain == nullptr), H3_ERR_INVALID_ARG,
-             "q_gain and k_gain come together");
+  // (without q its gain may be left out)
+  H3_REQUIRE(k_gain != nullptr ? q == nullptr || q_gain != nullptr : q_gain == nullptr,
+             H3_ERR_INVALID_ARG, "q_gain and k_gain come together");
   H3_REQUIRE(aligned16(q_gain) && aligned16(k_gain) && aligned4(pos), H3_ERR_MISALIGNED,
              "the gains must be 16-byte, pos 4-byte aligned");
   return launch_kv_append(q, ld_q, k, ld_k, v, ld_v, q_out, H, q_gain, k_gain, pos, axis_dims,

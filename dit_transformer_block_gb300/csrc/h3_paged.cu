@@ -61,8 +61,8 @@ struct AppendArgs {
   __nv_bfloat16* q_out;
   __nv_bfloat16* k_cache;
   __nv_bfloat16* v_cache;
-  const float* q_gain;  // NULL: no norm
-  const float* k_gain;
+  const float* q_gain;  // given with k_gain where there is a q
+  const float* k_gain;  // NULL: no norm
   const int32_t* pos;
   float eps;
   int H, Hkv;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, APPEND_CTAS<HALF>)
     rope_angle(__ldg(a.pos + 3 * (row0 + r) + tab.axis[pr]), tab.turn[pr], sn, cs);
     turn[r][pr] = make_float2(cs, sn);
   }
-  const bool norm = a.k_gain != nullptr || a.q_gain != nullptr;
+  const bool norm = a.k_gain != nullptr;
   float gq[8] = {}, gk[8] = {};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {

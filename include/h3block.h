@@ -272,7 +272,8 @@ typedef struct h3_kv_batch {
  *           columns of one [T, ld] buffer. Strides are multiples of 8.
  *   q_out   [T, H, Dh] bf16 contiguous; may be q itself when ld_q == H * Dh,
  *           else it does not overlap the inputs
- *   q_gain, k_gain [Dh] float32, or both NULL: rotation without a norm
+ *   q_gain, k_gain [Dh] float32, or both NULL: rotation without a norm. Without
+ *          q, k_gain alone may be given
  *   pos     [T, 3] int32; axis_dims, pairing, eps as h3_qk_norm_rope_layout;
  *           theta >= 1
  * Two rows of a call must not have the same place (sequences that are written

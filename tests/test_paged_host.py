@@ -188,3 +188,9 @@ def test_cache_and_batch_of_another_device_are_refused(monkeypatch):
         with pytest.raises(ValueError, match=f"the {at} must be on the current CUDA device"):
             h3.kv_append_paged(None, x[:, :4], x[:, :4], None, c, b,
                                torch.zeros(6, 3, dtype=torch.int32), (128, 0, 0))
+
+
+def test_append_of_keys_alone_needs_their_gain(lib):
+    # a gain for the queries that the call does not have, none for its keys
+    kw = dict(q=NULL, q_out=NULL, H=0)
+    assert append(lib, kg=NULL, **kw) == INVALID and "k_gain" in h3.last_error()
