@@ -179,6 +179,13 @@ struct PagedBatch {
   const int32_t* page_table;
 };
 #ifdef __CUDACC__
+// A partial result of a row is (maximum, sum, O). A maximum of -inf says that the
+// row has seen no key, and nothing else does: of rows whose scores are all NaN
+// (which a maximum drops) or all -inf it is this, the least float. Their sums (NaN,
+// 0) then go through the joins with weights like any other's, and the row has no
+// value, NaN, however its keys were split.
+constexpr float KEYS_SEEN = -3.402823466e+38f;
+
 // The number of sequence ends cu_q[1..B] at or below row t, by a whole warp: 32
 // of them at a time, so three reads for any B up to 32,768. Arrays that are out
 // of order give some number in [0, B].

@@ -1009,6 +1009,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (lane == 0) mbar_arrive(bar(PA_P + tile));
       }
       if (!ok || !wait_pv(n - 1)) break;
+      if (lim > p.kt0 * BKV) m = fmaxf(m, KEYS_SEEN);
       if (quad) {
         // the four quarters' results meet in the part of the query tile that
         // few rows leave free: row r of quarter w, 512 bytes in the order of
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           const int64_t orow = static_cast<int64_t>(p.tok0 + tok0 + r / a.G);
           const int head = p.hk * a.G + r % a.G;
           if (p.dest == -1) {
-            const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // no key: zeros
+            const float inv = top == -INFINITY ? 0.f : 1.0f / sum;  // no key: zeros
             *reinterpret_cast<uint2*>(a.o + orow * a.ld_o + head * DH + lane * 4) =
                 make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
           } else {
@@ -1103,7 +1104,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         }
         if (row < rows) *reinterpret_cast<float2*>(ml + at * 2) = make_float2(m, l);
       }
-      const float inv = p.dest == -1 ? (l == 0.f ? 0.f : 1.0f / l) : 1.0f;  // no key: zeros
+      const float inv = p.dest == -1 ? (m == -INFINITY ? 0.f : 1.0f / l) : 1.0f;  // no key: zeros
       if (rows - quarter * 32 <= PA_FEW_ROWS) {
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
@@ -1180,7 +1181,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 constexpr int PA_JOIN_CTAS = 4, PA_JOIN_N = 4, PA_JOIN_WARPS = 8, PA_JOIN_MANY = 32;
 // A row's result while its partials are joined, four channels per lane.
 struct Joined {
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f;  // maximum -inf: no key (see KEYS_SEEN)
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 };
 
@@ -1271,7 +1272,7 @@ __device__ __forceinline__ void join_warps(Joined& j, float4 (&part)[PA_JOIN_WAR
 }
 
 __device__ __forceinline__ void store_joined(const Joined& j, const PagedArgs& a, int t, int head) {
-  const float inv = j.l == 0.f ? 0.f : 1.0f / j.l;  // no key: zeros
+  const float inv = j.m == -INFINITY ? 0.f : 1.0f / j.l;  // no key: zeros
   *reinterpret_cast<uint2*>(a.o + t * a.ld_o + head * DH + (threadIdx.x & 31) * 4) =
       make_uint2(pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv));
 }

@@ -59,7 +59,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
 
 // A (row, head)'s result while its parts are joined, four channels per lane.
 struct Joined {
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f;  // maximum -inf: no key (see KEYS_SEEN)
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 
   __device__ __forceinline__ void add(float2 ml, const float4& y) {
@@ -97,7 +97,7 @@ struct Joined {
       if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m, l);
       return;
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key: zeros
+    const float inv = m == -INFINITY ? 0.f : 1.0f / l;  // no key: zeros
     *reinterpret_cast<uint2*>(a.o + t * a.ld_o + head * PR_DH + lane * 4) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   }
@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(32 * PR_MAX_WARPS, CTAS)
   float2* ml = reinterpret_cast<float2*>(sm + warps * heads * PR_DH);
   l += __shfl_xor_sync(0xffffffffu, l, 1);
   l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (warp0 < chunks) m = fmaxf(m, KEYS_SEEN);
   if (c == 0 && n < heads) ml[warp * heads + n] = make_float2(m, l);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

@@ -291,7 +291,8 @@ h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t
  *   o[row,h,:] = sum_j softmax_j(q[row,h,:] . k[b,j,g,:] * softmax_scale) v[b,j,g,:]
  * over the keys j < kv_len[b], and with causal != 0 only those with
  * j <= kv_len[b] - q_len + i (the row itself and what came before it). A row
- * without any such key gives zeros.
+ * without any such key gives zeros; one with a score of NaN or +inf, or whose
+ * scores are all -inf, gives NaN.
  *   q, o   [T, H, Dh] bf16, not overlapping, row strides ld_q, ld_o (multiples of 8); H a
  *          multiple of cache->Hkv, at most 128 heads per key head; T * H at
  *          most 2^29
