@@ -569,7 +569,7 @@ static h3_status check_paged(const h3_kv_cache* c, const h3_kv_batch* b, PagedBa
              "the cache must be 16-byte aligned");
   H3_REQUIRE(b->T >= 0 && b->B >= 0 && b->max_pages >= 0, H3_ERR_INVALID_ARG,
              "negative size (T=%d, B=%d, max_pages=%d)", b->T, b->B, b->max_pages);
-  // (a CTA's part of that many keys takes about half of the default wait limit)
+  // (the longest that is tested; the kernels keep key indices in 32 bits)
   H3_REQUIRE(b->max_pages <= (1 << 26) / c->page_size, H3_ERR_UNSUPPORTED,
              "max_pages * page_size must be at most 2^26");
   H3_REQUIRE(b->B <= 65536, H3_ERR_UNSUPPORTED, "B=%d exceeds 65536 sequences", b->B);

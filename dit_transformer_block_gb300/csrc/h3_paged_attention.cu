@@ -78,7 +78,8 @@ enum BarPA {
   PA_P = PA_SFREE + 2,         // P_i written (4 warp arrivals)
   PA_PVD = PA_P + 2,           // P_i V done (MMA commit)
   PA_PC_FULL = PA_PVD + 2,     // piece posted
-  PA_PC_EMPTY = PA_PC_FULL + PA_PIECES,  // piece read (8 softmax warps, MMA warp, loads)
+  PA_PC_EMPTY = PA_PC_FULL + PA_PIECES,  // piece read (8 softmax warps, MMA warp, loads); of
+                                         // several runs: done with their place
   PA_JOIN = PA_PC_EMPTY + PA_PIECES,     // a quarter's result is in shared memory (4 arrivals)
   PA_DRAIN = PA_JOIN + 2,
   PA_BARS
@@ -174,10 +175,19 @@ __device__ __forceinline__ int64_t head_cost(const PagedArgs& a, int seg, const 
   return sum;
 }
 
+// Key tiles that are summed in one accumulator. The tensor cores cut an FP32
+// accumulator off, towards zero, with every 16 keys: for values of one sign a sum
+// over n keys comes out low by up to n 2^-27 of it, and by 4.3 n 10^-9 on average (on
+// 2^24 keys of one CTA 7 %; 1.8 % where a quarter of the keys is summed for itself).
+// So a part of an item of more tiles is several pieces, one after the other, each of
+// which adds its result to that of those before it, in FP32 rounded to nearest (then
+// 0.08 and 0.02 %).
+constexpr int PA_RUN = 1024;
+
 // Teams of up to so many CTAs (find_share picks the size).
 constexpr int PA_MAX_TEAM = 8;
 
-// A CTA's part of an item, as posted to the other warps.
+// A CTA's part of an item, or a run of it, as posted to the other warps.
 struct Piece {
   int tok0, ntok;  // tokens (ntok 0: no more pieces)
   int hk;          // key head
@@ -186,7 +196,8 @@ struct Piece {
   int lim0;        // token i of the piece sees min(lim0 + i, kv) keys
   int dest;        // >= 0: partial slot; -1: the output; -2 - seg: the segment's rows
   int b;           // sequence, -1: the prefix
-  int pad[3];
+  int before, more;  // runs of the part before and after this one
+  int pad;
 };
 static_assert(sizeof(Piece) == 48, "16-byte loads");
 
@@ -347,6 +358,52 @@ __device__ __forceinline__ bool softmax_tile_quad(uint32_t tS, uint32_t tP, uint
   tmem_st16(tP, pk);
   tmem_st_wait();
   return true;
+}
+
+// Adds what the runs of a part before this one have of the calling thread's row, at
+// `to` and `ml` in the workspace, to what this one has, maximum and sum (m, l) and O in
+// tensor memory (`first`: there is none before it), and leaves that there for the next
+// run (keep) or as this one's result. By the whole warp.
+__device__ __noinline__ float2 join_runs(uint32_t tO, float* to, float2* ml, bool row_ok, bool first,
+                                         bool keep, float m, float l) {
+  float c = 0.f, w = 1.f;  // weights of the runs before and of this one
+  if (!first && row_ok) {
+    const float2 x = *ml;
+    const float top = fmaxf(x.x, m);
+    c = x.x == top ? 1.f : ex2_approx(x.x - top);  // (equal: -inf too, no key so far)
+    w = m == top ? 1.f : ex2_approx(m - top);
+    m = top;
+    l = fmaf(x.y, c, l * w);
+  }
+  if (keep && row_ok) *ml = make_float2(m, l);
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    uint32_t ov[16];
+    tmem_ld16(tO + i * 16, ov);
+    tmem_ld_wait();
+    tmem_reg_fence(ov);
+    float4* at = reinterpret_cast<float4*>(to) + i * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(ov[4 * j + e]) * w;
+      if (!first && row_ok) {
+        const float4 y = at[j];
+        x[0] = fmaf(y.x, c, x[0]);
+        x[1] = fmaf(y.y, c, x[1]);
+        x[2] = fmaf(y.z, c, x[2]);
+        x[3] = fmaf(y.w, c, x[3]);
+      }
+      if (keep && row_ok) at[j] = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ov[4 * j + e] = __float_as_uint(x[e]);
+    }
+    if (!keep) tmem_st16(tO + i * 16, ov);
+  }
+  if (!keep) tmem_st_wait();
+  __syncwarp();  // another lane may write to the place next
+  return make_float2(m, l);
 }
 
 // Writes 64 bytes (four 16-byte units, w) of every lane's row at byte `at`, with
@@ -592,7 +649,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 a.spread[(static_cast<int64_t>(seg) * a.b.T + p.tok0) * a.Hkv + hk] =
                     make_int2(blockIdx.x, last);
             }
-            ok = post(p);
+            // runs of at most PA_RUN tiles, as even as they can be
+            const int runs = (kt1 - kt0 + PA_RUN - 1) / PA_RUN, len = (kt1 - kt0 + runs - 1) / runs;
+            p.more = runs;
+#pragma unroll 1
+            for (; ok && p.more > 0; ++p.before, p.kt0 = p.kt1) {
+              --p.more;
+              p.kt1 = min(p.kt0 + len, kt1);
+              ok = post(p);
+            }
           }
           left -= take;
           u += take;
@@ -908,6 +973,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     const int row_tok = row / a.G, row_head = row % a.G, lane_tok = lane / a.G;
     bool p_clear = false;  // this warp's weights outside its 32 keys are 0
     int joins = 0;   // pieces joined from the four quarters
+    // the last piece of several runs, if this warp has not seen it done with their place,
+    // which may be this piece's too
+    int run_piece = -1;
     int n = 0;       // S tiles of this query tile so far
     int tiles = 0;   // key tiles of this CTA so far
     bool ok = true;
@@ -921,11 +989,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       if (!mbar_wait_warp(bar(PA_PC_FULL + r), (np / PA_PIECES) & 1, a.err, ERR_WAIT_ATTN_SOFTMAX))
         break;
       const Piece p = ring[r];
+      const bool two = p.ntok > a.tok, mine = two || (np & 1) == tile;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
+      if (lane == 0 && !(mine && p.before + p.more > 0)) mbar_arrive(bar(PA_PC_EMPTY + r));
       if (p.ntok == 0) break;
-      const bool two = p.ntok > a.tok;
-      if (!two && (np & 1) != tile) {
+      if (!mine) {
+        if (p.before + p.more > 0) run_piece = np;
         tiles += p.kt1 - p.kt0;
         continue;
       }
@@ -1010,6 +1079,34 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (!ok || !wait_pv(n - 1)) break;
       if (lim > p.kt0 * BKV) m = fmaxf(m, KEYS_SEEN);
+      if (run_piece >= 0) {
+        ok = mbar_wait_warp(bar(PA_PC_EMPTY + run_piece % PA_PIECES), (run_piece / PA_PIECES) & 1,
+                            a.err, ERR_WAIT_ATTN_SOFTMAX);
+        if (!ok) break;
+        run_piece = -1;
+      }
+      if (p.before + p.more > 0) {
+        if (active) {
+          // a part's runs meet where its partial result goes, or where this CTA's last one
+          // of the segment will; rows in all lane quarters have four places
+          const int slot = p.dest >= 0 ? p.dest
+                                       : ((p.dest == -1 ? 0 : -2 - p.dest) * PA_MAX_CTAS +
+                                          static_cast<int>(blockIdx.x)) * 2 + 1;
+          const int64_t at = static_cast<int64_t>(slot) * a.part_rows + tok0 * a.G +
+                             (quad ? quarter * rows + lane : row);
+          const float2 x = join_runs(tO, a.part_o + at * DH, reinterpret_cast<float2*>(a.part_ml) + at,
+                                     row_ok, p.before == 0, p.more > 0, m, l);
+          m = x.x;
+          l = x.y;
+        }
+        run_piece = np;
+        if (lane == 0) mbar_arrive(bar(PA_PC_EMPTY + r));
+        if (p.more > 0) {
+          tc_fence_before();  // O has been read
+          if (quad && lane == 0) mbar_arrive(bar(PA_Q_EMPTY + tile));
+          continue;
+        }
+      }
       if (quad) {
         // the four quarters' results meet in the part of the query tile that
         // few rows leave free: row r of quarter w, 512 bytes in the order of
@@ -1439,8 +1536,9 @@ PagedWs paged_ws(int T, int H, int prefix_len) {
   PagedWs w;
   const size_t rows = static_cast<size_t>(T) * H;
   const bool prefix = prefix_len > 0;
-  // rows of one item: at most two query tiles, at most what the call has
-  w.part_rows = static_cast<int>(std::min<size_t>(2 * BQ, rows));
+  // rows of one item: at most two query tiles, at most what the call has; where the
+  // runs of a part meet, up to PA_QUAD_ROWS of them in every lane quarter
+  w.part_rows = static_cast<int>(std::min<size_t>(2 * BQ, rows + 3 * std::min<size_t>(PA_QUAD_ROWS, rows)));
   const size_t slots = (prefix ? 2 : 1) * PA_MAX_CTAS * 2;
   size_t off = 256;
   auto take = [&](size_t bytes) {

@@ -303,7 +303,10 @@ h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t
  * row, a cluster of CTAs each, others by tiles of rows and keys; both give
  * the same up to the order of the sums, which in the second also goes by the
  * lengths of the whole batch.
- * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out.
+ * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out. A tensor core
+ * sums at most 131,072 keys in one accumulator, longer sums are of such runs, so the
+ * error does not grow with the keys from there on: relative to the sum of weight
+ * times |v|, 2^-8 for the weights' rounding and 2^-10 for the sums, at most.
  */
 size_t h3_attention_paged_workspace_bytes(int T, int H, int prefix_len);
 h3_status h3_attention_paged(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
