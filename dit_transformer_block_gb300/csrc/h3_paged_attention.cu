@@ -181,7 +181,9 @@ __device__ __forceinline__ int64_t head_cost(const PagedArgs& a, int seg, const 
 // 2^24 keys of one CTA 7 %; 1.8 % where a quarter of the keys is summed for itself).
 // So a part of an item of more tiles is several pieces, one after the other, each of
 // which adds its result to that of those before it, in FP32 rounded to nearest (then
-// 0.08 and 0.02 %).
+// 0.08 and 0.02 %). An instance of the kernel for itself, for tables and prefixes with
+// room for so many keys: the code for runs is fetched with every short item (1,024
+// rows of 256 keys, 32 heads on 8: 255 us with it, 234 without).
 constexpr int PA_RUN = 1024;
 
 // Teams of up to so many CTAs (find_share picks the size).
@@ -196,7 +198,7 @@ struct Piece {
   int lim0;        // token i of the piece sees min(lim0 + i, kv) keys
   int dest;        // >= 0: partial slot; -1: the output; -2 - seg: the segment's rows
   int b;           // sequence, -1: the prefix
-  int before, more;  // runs of the part before and after this one
+  int before, more;  // RUNS: 0, or there are runs of the part before and after this one
   int pad;
 };
 static_assert(sizeof(Piece) == 48, "16-byte loads");
@@ -439,6 +441,8 @@ __device__ __forceinline__ void store_transposed(uint32_t (&w)[16], char* const 
           make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
+// RUNS: parts may be longer than PA_RUN.
+template <bool RUNS>
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmQ1,
@@ -649,13 +653,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 a.spread[(static_cast<int64_t>(seg) * a.b.T + p.tok0) * a.Hkv + hk] =
                     make_int2(blockIdx.x, last);
             }
-            // runs of at most PA_RUN tiles, as even as they can be
-            const int runs = (kt1 - kt0 + PA_RUN - 1) / PA_RUN, len = (kt1 - kt0 + runs - 1) / runs;
-            p.more = runs;
+            if constexpr (RUNS) {
 #pragma unroll 1
-            for (; ok && p.more > 0; ++p.before, p.kt0 = p.kt1) {
-              --p.more;
-              p.kt1 = min(p.kt0 + len, kt1);
+              do {
+                p.kt1 = min(p.kt0 + PA_RUN, kt1);
+                p.more = kt1 - p.kt1;
+                ok = post(p);
+                p.before = 1;
+                p.kt0 = p.kt1;
+              } while (ok && p.more > 0);
+            } else {
               ok = post(p);
             }
           }
@@ -990,11 +997,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         break;
       const Piece p = ring[r];
       const bool two = p.ntok > a.tok, mine = two || (np & 1) == tile;
+      const bool run = RUNS && p.before + p.more > 0;
       __syncwarp();
-      if (lane == 0 && !(mine && p.before + p.more > 0)) mbar_arrive(bar(PA_PC_EMPTY + r));
+      if (lane == 0 && !(mine && run)) mbar_arrive(bar(PA_PC_EMPTY + r));
       if (p.ntok == 0) break;
       if (!mine) {
-        if (p.before + p.more > 0) run_piece = np;
+        if (run) run_piece = np;
         tiles += p.kt1 - p.kt0;
         continue;
       }
@@ -1079,13 +1087,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (!ok || !wait_pv(n - 1)) break;
       if (lim > p.kt0 * BKV) m = fmaxf(m, KEYS_SEEN);
-      if (run_piece >= 0) {
+      if (RUNS && run_piece >= 0) {
         ok = mbar_wait_warp(bar(PA_PC_EMPTY + run_piece % PA_PIECES), (run_piece / PA_PIECES) & 1,
                             a.err, ERR_WAIT_ATTN_SOFTMAX);
         if (!ok) break;
         run_piece = -1;
       }
-      if (p.before + p.more > 0) {
+      if (run) {
         if (active) {
           // a part's runs meet where its partial result goes, or where this CTA's last one
           // of the segment will; rows in all lane quarters have four places
@@ -1567,8 +1575,11 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
                                  const void* v_cache, int Hkv, const PagedBatch& batch,
                                  const int32_t* prefix_pages, int prefix_len, void* workspace,
                                  cudaStream_t s) {
-  static std::atomic<bool> done[64];
-  h3_status st = set_smem_limit(done, paged_attention_kernel, PA_SMEM_BYTES,
+  const int64_t own = static_cast<int64_t>(batch.max_pages) << batch.page_log2;
+  const bool runs = std::max<int64_t>(own, prefix_len) > PA_RUN * BKV;
+  const auto kernel = runs ? paged_attention_kernel<true> : paged_attention_kernel<false>;
+  static std::atomic<bool> done[2][64];
+  h3_status st = set_smem_limit(done[runs], kernel, PA_SMEM_BYTES,
                                 "paged attention: set shared memory size");
   if (st != H3_OK) return st;
   const PagedWs w = paged_ws(batch.T, H, prefix_len);
@@ -1581,7 +1592,6 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   a.Hkv = Hkv;
   a.G = H / Hkv;
   a.tok = BQ / a.G;
-  const int64_t own = static_cast<int64_t>(batch.max_pages) << batch.page_log2;
   // One query tile per item, and no teams, where none is split and there is a CTA for
   // each of them (2 sequences of 185 rows and 446 keys, 32 heads on 8: 14.4 us against
   // 16.5; one of 512 rows and keys, 4 heads: 13.3 / 15.6).
@@ -1638,7 +1648,7 @@ h3_status launch_paged_attention(const void* q, int64_t ld_q, void* o, int64_t l
   cfg.gridDim = dim3(a.ctas);
   cfg.blockDim = dim3(PA_THREADS);
   cfg.dynamicSmemBytes = PA_SMEM_BYTES;
-  st = cuda_fail(cudaLaunchKernelEx(&cfg, paged_attention_kernel, tq, tq1, tk, tv, a),
+  st = cuda_fail(cudaLaunchKernelEx(&cfg, kernel, tq, tq1, tk, tv, a),
                  "paged attention launch");
   if (st != H3_OK) return st;
   if (whole) return H3_OK;  // nothing is split, nothing to join
