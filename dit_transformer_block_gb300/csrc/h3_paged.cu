@@ -175,7 +175,9 @@ __global__ void __launch_bounds__(APPEND_THREADS, APPEND_CTAS<HALF>)
     rope_angle(__ldg(a.pos + 3 * (row0 + r) + tab.axis[pr]), tab.turn[pr], sn, cs);
     turn[r][pr] = make_float2(cs, sn);
   }
-  const bool norm = a.k_gain != nullptr;
+  // (k_gain is there whenever q_gain is; asked for it alone, 58,758 split-half rows of
+  // 126 heads take 762 us, not 754)
+  const bool norm = a.k_gain != nullptr || a.q_gain != nullptr;
   float gq[8] = {}, gk[8] = {};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
