@@ -45,9 +45,10 @@ __device__ __forceinline__ SeqRow find_row(const int32_t* __restrict__ cu_q, int
 // life on the three dependent loads of that: 1.06 ms for 58,758 rows of 126
 // heads.)
 // Measured at 58,758 rows of 42 + 84 heads, interleaved pairs: 642 us (5.9 TB/s
-// of 3.8 GB); 256 threads with 4 rows 665-776, batches of 8 heads 675. Split-half
-// pairs, with a shuffle per channel: 759 us at six CTAs per SM (eight spill:
-// 1,069; five 797).
+// of 3.8 GB; at the 64 registers of eight CTAs per SM 28 bytes are spilled); 256
+// threads with 4 rows 665-776, batches of 8 heads 675. Split-half pairs, with a
+// shuffle per channel: 754 us at six CTAs per SM (80 registers, no spills; eight
+// CTAs 1,069, five 797).
 constexpr int APPEND_THREADS = 128, APPEND_ROWS = 2, APPEND_BATCH = 4;
 template <bool HALF>
 constexpr int APPEND_CTAS = HALF ? 6 : 8;  // per SM
@@ -71,8 +72,8 @@ struct AppendArgs {
 };
 
 // 8 channels (one lane's) of a head: normed by its RMS and gain if there is one,
-// its pairs turned by (cos, sin) from cs on. The roundings are those that the
-// in-place Q/K kernel's expressions are compiled to.
+// its pairs turned by (cos, sin) from cs on. Which products are fused is written out,
+// so that the result has the bits of the in-place Q/K kernel.
 template <bool HALF>
 __device__ __forceinline__ uint4 norm_turn(uint4 w, bool norm, const float (&gain)[8], float eps,
                                            const float2* turn, bool first, int src_lane) {

@@ -36,8 +36,9 @@
 // rows of up to 8,191 keys, 32 heads on 4: 165 us; pages of 32 and more 139 us, 6.2
 // TB/s). Chunks, the chain through the one S buffer: product 512 cycles, seen 200,
 // read 250, seen 200, twice per key tile and two query tiles, 2,700 cycles against
-// 2,048 of products (1,896 rows of 58,758 keys, 42 heads: 1.54 ms, 1,560 TFLOP/s; of
-// 16,384 keys, 1,500). Short items, instruction fetch: the kernel is 125 KB, and an
+// 2,048 of products (1,896 rows of 58,758 keys, 42 heads: 2,853 thousand cycles, 1.54 to
+// 1.82 ms with the clock that the power cap leaves, 1,560 to 1,320 TFLOP/s; of 16,384
+// keys, 840 thousand, 1,500). Short items, instruction fetch: the kernel is 125 KB, and an
 // item runs a small part of it once (6 causal chunks of up to 901 rows and 6,007
 // keys, 32 heads on 8: 141 us, products 69).
 #include <algorithm>
@@ -158,7 +159,8 @@ constexpr int PA_ITEM_COST = 2;
 // share and 4 tiles more: 2 of up to 1,623 rows and 2,230 keys, 12 heads, 46 -> 59.)
 constexpr int PA_WHOLE = 4, PA_WHOLE_ROWS = 8, PA_WHOLE_SHARE = 32;
 // Least share of a CTA: a partial result costs more than a tile's time (8 rows
-// behind 4,099 keys, 16 heads on 2: 21.2 us for 2, 22.9 for 1, 24.0 for 4).
+// behind 12,000 keys, 16 heads on 2: 18.8 us for 2, 19.6 for 1, 22.8 for 4, 29.8 for 8;
+// a row of 12,000 keys, 4 heads: 16.1, 16.3, 17.3, 21.6).
 constexpr int PA_MIN_SHARE = 2;
 
 // Cost of one key head of a sequence, for teams of g CTAs (the items of a team
@@ -299,8 +301,9 @@ __device__ __forceinline__ bool softmax_tile_paged(uint32_t (&sr)[128], uint32_t
 // are 0); the four are joined when the piece ends. A quarter of the latency and
 // of the code of a warp that takes a row's 128 keys alone. The code counts: short
 // items run every path of this kernel once in a few microseconds, and it is
-// longer than what an SM keeps of it (64 rows of 256 keys, 42 heads: 64 % of the
-// instruction fetches hit in the SM's own cache before, 82 % after).
+// longer than what an SM keeps of it (64 rows of 256 keys, 42 heads, under a table of
+// more: 73 us against 90 without; 1,024 of them, 32 heads on 8: 237 / 320; 32 rows behind
+// 6,000 keys, 32 on 8: 27.6 / 29.3; 96 rows of up to 8,191 keys, 32 on 4: 164 / 170).
 template <class WaitPV, class FreeS>
 __device__ __forceinline__ bool softmax_tile_quad(uint32_t tS, uint32_t tP, uint32_t tO, int valid,
                                                   bool o_live, bool row_ok, float scale_log2,

@@ -305,8 +305,12 @@ static int rows_cluster(int64_t units, int64_t keys) {
   return keys >= 256 && units * 2 <= sms ? 2 : 1;
 }
 
-// Whether rows are taken one by one: `keys` is what a row can see at most. Measured
-// against the tensor-core kernel, us (here / there):
+// Whether rows are taken one by one: `keys` is what a row can see at most, the room in
+// its table and the prefix (how many it sees is known on the device only). Measured with
+// tables as wide as the sequences are long, against the tensor-core kernel, us (here /
+// there; it takes 11, 73, 235 and 963 where the tables of 1 row of 250 keys, 64 of 256,
+// 42 heads, 1,024 of 256, 32 on 8, and 16,384 of 64, 8 on 2, have room for more, this one
+// 5, 65, 173 and 193):
 //   a CTA or a cluster per row and group of heads, all at once: one row, 4 heads, 250
 //     keys 5.3 / 10.7, 1,000 keys 5.6 / 13.2, 8,000 keys 13.1 / 15.7, 12,000 keys
 //     17.9 / 16.8; 84 CTAs of 4,000 keys in pairs 24 / 27; 126 CTAs of 2,000 keys

@@ -388,7 +388,9 @@ def kv_batch(cu_q, kv_len, page_table, T: int) -> KvBatch:
     """The rows of a call (T of them, sequence b's being [cu_q[b], cu_q[b+1]))
     and their sequences: cu_q [B+1], kv_len [B] (with the call's rows in it),
     page_table [B, max_pages], int32 on the device. It holds on to the tensors,
-    whose values are read when a call runs; one batch serves every layer."""
+    whose values are read when a call runs; one batch serves every layer. The
+    attention's kernel is chosen by max_pages * page_size: a table no wider than the
+    sequences can get is faster where they are short."""
     dev = _device()
     for n, t in (("cu_q", cu_q), ("kv_len", kv_len), ("page_table", page_table)):
         _flat(t, n, torch.int32, dev)
@@ -460,7 +462,8 @@ def attention_paged(q, o, cache: KvCache, batch: KvBatch, workspace, scale=None,
 def attention_paged_prefix(q, o, cache: KvCache, batch: KvBatch, prefix_pages, prefix_len: int,
                            workspace, scale=None, causal=False, stream=None):
     """attention_paged with prefix_len keys in prefix_pages (int32) before the
-    own keys of every sequence, read once for the whole batch."""
+    own keys of every sequence, read once for the whole batch (by few rows behind
+    a short prefix once for each)."""
     dev, T = _device(), batch.T
     _made_on(cache, batch, dev)
     ldq, H = _heads(q, "q", T, dev)

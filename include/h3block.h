@@ -299,10 +299,10 @@ h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t
  *   workspace  device memory of h3_attention_paged_workspace_bytes(T, H, 0)
  *          bytes, 256-byte aligned, overwritten by the call; calls that may
  *          overlap on the GPU need one each
- * A batch of short tables (max_pages * page_size) and few rows is taken row by
- * row, a cluster of CTAs each, others by tiles of rows and keys; both give
- * the same up to the order of the sums, which in the second also goes by the
- * lengths of the whole batch.
+ * A batch of short tables (max_pages * page_size, whatever the lengths are: they
+ * are known on the device only) and few rows is taken row by row, a cluster of
+ * CTAs each, others by tiles of rows and keys; both give the same up to the order
+ * of the sums, which in the second also goes by the lengths of the whole batch.
  * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out. A tensor core
  * sums at most 131,072 keys in one accumulator, longer sums are of such runs, so the
  * error does not grow with the keys from there on: relative to the sum of weight
@@ -317,8 +317,10 @@ h3_status h3_attention_paged(const void* q, int64_t ld_q, void* o, int64_t ld_o,
 /*
  * h3_attention_paged for a batch whose sequences share their first prefix_len
  * keys: every row sees all of them (causal or not), then its own sequence's
- * keys as above (kv_len counts those only). The prefix's keys and values are
- * read once for the rows of all sequences together.
+ * keys as above (kv_len counts those only). By tiles, the prefix's keys and values
+ * are read once for the rows of all sequences together; what is taken row by row
+ * (prefix_len counts as room in the table, so few rows behind a short prefix) reads
+ * them for every row.
  *   prefix_pages [ceil(prefix_len / page_size)] int32 device, as a row of
  *          page_table; may be NULL when prefix_len is 0. prefix_len is at
  *          most 2^26
