@@ -306,7 +306,8 @@ h3_status h3_kv_append_paged(const void* q, int64_t ld_q, const void* k, int64_t
  * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out. A tensor core
  * sums at most 131,072 keys in one accumulator, longer sums are of such runs, so the
  * error does not grow with the keys from there on: relative to the sum of weight
- * times |v|, 2^-8 for the weights' rounding and 2^-10 for the sums, at most.
+ * times |v|, at most 2^-8 for the weights' rounding and little over 2^-10 for the
+ * sums, beside what the FP32 scores have.
  */
 size_t h3_attention_paged_workspace_bytes(int T, int H, int prefix_len);
 h3_status h3_attention_paged(const void* q, int64_t ld_q, void* o, int64_t ld_o, int H,
