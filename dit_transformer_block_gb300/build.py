@@ -17,7 +17,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libh3block.so")
 SOURCES = ["h3_abi.cu", "h3_elementwise.cu", "h3_gemm.cu", "h3_attention.cu",
            "h3_attention_tiles.cu", "h3_sage.cu", "h3_paged.cu",
-           "h3_paged_attention.cu", "h3_paged_rows.cu"]
+           "h3_paged_attention.cu", "h3_paged_rows.cu", "h3_norms.cu", "h3_fp4.cu",
+           "h3_fp4_gemm.cu", "h3_blocks.cu", "h3_block_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-Wall"]

@@ -5,11 +5,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 
+#include "h3_blocks.cuh"
+#include "h3_fp4.cuh"
 #include "h3_internal.cuh"
 
 namespace h3 {
@@ -271,6 +274,53 @@ h3_status h3_mod_norm_residual(float* resid, const void* delta, const float* gat
   if (L == 0) return H3_OK;
   return launch_mod_norm_residual(resid, delta, gate, shift, scale, normed, L, D, eps,
                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+h3_status h3_sandwich_norm(const float* resid, const void* delta, float* resid_out, void* normed,
+                           int post_norm, const float* post_gain, const float* gate,
+                           float resid_scale, const float* pre_gain, const float* shift,
+                           const float* scale, const int32_t* seg, int num_seg,
+                           int64_t seg_stride, int rms, int S, int L, int D, float eps,
+                           h3_stream_t stream) {
+  clear_error();
+  h3_status st = check_rows(S, L);
+  if (st != H3_OK) return st;
+  H3_REQUIRE(resid != nullptr, H3_ERR_INVALID_ARG, "resid is NULL");
+  H3_REQUIRE(resid_out != nullptr || normed != nullptr, H3_ERR_INVALID_ARG,
+             "neither resid_out nor normed given: nothing to do");
+  H3_REQUIRE(resid_out != nullptr || (delta == nullptr && resid_scale == 1.f), H3_ERR_INVALID_ARG,
+             "delta or resid_scale changes the residual, but resid_out is NULL");
+  H3_REQUIRE(normed != nullptr || delta != nullptr || resid_scale != 1.f, H3_ERR_INVALID_ARG,
+             "neither normed nor delta nor a resid_scale: nothing to do");
+  H3_REQUIRE(delta != nullptr || (!post_norm && gate == nullptr), H3_ERR_INVALID_ARG,
+             "post_norm or gate given without delta");
+  H3_REQUIRE(post_norm || post_gain == nullptr, H3_ERR_INVALID_ARG,
+             "post_gain given without post_norm");
+  H3_REQUIRE(normed != nullptr || (pre_gain == nullptr && shift == nullptr && scale == nullptr),
+             H3_ERR_INVALID_ARG, "pre_gain, shift or scale given without normed");
+  H3_REQUIRE(D > 0 && D % 8 == 0, H3_ERR_UNSUPPORTED, "D=%d must be a positive multiple of 8", D);
+  H3_REQUIRE(D <= 8192, H3_ERR_UNSUPPORTED, "D=%d exceeds 8192", D);
+  H3_REQUIRE(eps >= 0.f, H3_ERR_INVALID_ARG, "eps must be >= 0");
+  H3_REQUIRE(std::isfinite(resid_scale), H3_ERR_INVALID_ARG, "resid_scale must be finite");
+  H3_REQUIRE(aligned16(resid) && aligned16(delta) && aligned16(resid_out) && aligned16(normed) &&
+                 aligned16(post_gain) && aligned16(gate) && aligned16(pre_gain) &&
+                 aligned16(shift) && aligned16(scale),
+             H3_ERR_MISALIGNED, "a pointer is not 16-byte aligned");
+  if (seg != nullptr) {
+    H3_REQUIRE(num_seg >= 1, H3_ERR_INVALID_ARG, "num_seg=%d", num_seg);
+    H3_REQUIRE(seg_stride >= D && seg_stride % 4 == 0, H3_ERR_INVALID_ARG,
+               "seg_stride=%lld must be a multiple of 4, at least D=%d",
+               static_cast<long long>(seg_stride), D);
+    H3_REQUIRE((reinterpret_cast<uintptr_t>(seg) & 3u) == 0, H3_ERR_MISALIGNED,
+               "seg must be 4-byte aligned");
+  }
+  H3_REQUIRE(normed == nullptr || (normed != resid && normed != delta && normed != resid_out),
+             H3_ERR_INVALID_ARG, "normed overlaps another tensor");
+  H3_REQUIRE(resid_out == nullptr || resid_out != delta, H3_ERR_INVALID_ARG, "resid_out is delta");
+  if (L == 0) return H3_OK;
+  return launch_sandwich_norm(resid, delta, resid_out, normed, post_norm != 0, post_gain, gate,
+                              resid_scale, pre_gain, shift, scale, seg, num_seg, seg_stride,
+                              rms != 0, L, D, eps, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // pairing 0: interleaved pairs; 1: split-half pairs, every section a
@@ -694,6 +744,122 @@ h3_status h3_attention_paged(const void* q, int64_t ld_q, void* o, int64_t ld_o,
                                    nullptr, 0, workspace, workspace_bytes, stream);
 }
 
+// ---- attention over chosen key blocks
+static int query_blocks(int Lq) {
+  return static_cast<int>((static_cast<int64_t>(Lq) + H3_QUERY_BLOCK - 1) / H3_QUERY_BLOCK);
+}
+static int key_blocks(int Lk, int k_block) {
+  return static_cast<int>((static_cast<int64_t>(Lk) + k_block - 1) / k_block);
+}
+
+static h3_status check_block_sizes(int Lq, int Lk, int H, int Hkv, int k_block) {
+  H3_REQUIRE(Lq >= 0 && Lk >= 0, H3_ERR_INVALID_ARG, "negative length (Lq=%d, Lk=%d)", Lq, Lk);
+  H3_REQUIRE(H > 0 && Hkv > 0 && H % Hkv == 0, H3_ERR_INVALID_ARG,
+             "H=%d is no multiple of Hkv=%d", H, Hkv);
+  H3_REQUIRE(H <= 65535, H3_ERR_UNSUPPORTED, "H=%d exceeds 65535", H);
+  H3_REQUIRE(k_block == 64 || k_block == 128, H3_ERR_UNSUPPORTED, "k_block=%d (64 or 128)",
+             k_block);
+  H3_REQUIRE(key_blocks(Lk, k_block) <= (1 << 20), H3_ERR_UNSUPPORTED,
+             "Lk=%d has more than 2^20 blocks of %d keys", Lk, k_block);
+  H3_REQUIRE(query_blocks(Lq) <= (1 << 20), H3_ERR_UNSUPPORTED,
+             "Lq=%d has more than 2^20 blocks of %d rows", Lq, H3_QUERY_BLOCK);
+  return H3_OK;
+}
+
+size_t h3_block_scores_workspace_bytes(int Lq, int Lk, int H, int Hkv, int k_block) {
+  clear_error();
+  if (check_block_sizes(Lq, Lk, H, Hkv, k_block) != H3_OK) return 0;
+  return std::max<size_t>(
+      256, block_scores_workspace_bytes(query_blocks(Lq), key_blocks(Lk, k_block), H, Hkv));
+}
+
+h3_status h3_block_scores(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                          float* scores, int Lq, int Lk, int H, int Hkv, int Dh, int k_block,
+                          float softmax_scale, void* workspace, size_t workspace_bytes,
+                          h3_stream_t stream) {
+  clear_error();
+  h3_status st = check_block_sizes(Lq, Lk, H, Hkv, k_block);
+  if (st != H3_OK) return st;
+  H3_REQUIRE(Dh == 128, H3_ERR_UNSUPPORTED, "head_dim %d unsupported (128 only)", Dh);
+  H3_REQUIRE(std::isfinite(softmax_scale), H3_ERR_INVALID_ARG, "softmax_scale must be finite");
+  const int nq = query_blocks(Lq), nk = key_blocks(Lk, k_block);
+  H3_REQUIRE(static_cast<int64_t>(nq) * H <= 0x7fffffffLL / std::max(nk, 1), H3_ERR_UNSUPPORTED,
+             "2^31 scores or more (%d heads, %d x %d blocks)", H, nq, nk);
+  if (Lq == 0 || Lk == 0) return H3_OK;
+  if ((st = check_strided("q", q, ld_q, H)) != H3_OK) return st;
+  if ((st = check_strided("k", k, ld_k, Hkv)) != H3_OK) return st;
+  H3_REQUIRE(scores != nullptr, H3_ERR_INVALID_ARG, "scores is NULL");
+  H3_REQUIRE(aligned16(scores), H3_ERR_MISALIGNED, "scores must be 16-byte aligned");
+  const size_t need = block_scores_workspace_bytes(nq, nk, H, Hkv);
+  H3_REQUIRE(workspace != nullptr && workspace_bytes >= need, H3_ERR_WORKSPACE,
+             "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  H3_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, H3_ERR_MISALIGNED,
+             "workspace must be 256-byte aligned");
+  return launch_block_scores(q, ld_q, k, ld_k, scores, Lq, Lk, H, Hkv, k_block, softmax_scale,
+                             workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static h3_status check_lists(int64_t rows, int nk, int max_blocks) {
+  H3_REQUIRE(max_blocks >= 1, H3_ERR_INVALID_ARG, "max_blocks=%d", max_blocks);
+  H3_REQUIRE(rows <= 0x7fffffffLL / max_blocks && rows <= 0x7fffffffLL / std::max(nk, 1),
+             H3_ERR_UNSUPPORTED, "rows=%lld lists of %d out of %d blocks: 2^31 or more",
+             static_cast<long long>(rows), max_blocks, nk);
+  return H3_OK;
+}
+
+h3_status h3_block_select(const float* scores, int32_t* ids, int32_t* counts, int rows, int nk,
+                          int max_blocks, int keep_first, int keep_last, h3_stream_t stream) {
+  clear_error();
+  H3_REQUIRE(rows >= 0 && nk >= 0, H3_ERR_INVALID_ARG, "rows=%d, nk=%d", rows, nk);
+  H3_REQUIRE(nk <= (1 << 20), H3_ERR_UNSUPPORTED, "nk=%d exceeds 2^20", nk);
+  h3_status st = check_lists(rows, nk, max_blocks);
+  if (st != H3_OK) return st;
+  H3_REQUIRE(keep_first >= 0 && keep_last >= 0 && keep_first <= max_blocks - keep_last,
+             H3_ERR_INVALID_ARG, "keep_first=%d and keep_last=%d exceed max_blocks=%d", keep_first,
+             keep_last, max_blocks);
+  if (rows == 0 || nk == 0) return H3_OK;
+  H3_REQUIRE(scores && ids && counts, H3_ERR_INVALID_ARG, "a required pointer is NULL");
+  H3_REQUIRE(aligned4(scores) && aligned4(ids) && aligned4(counts), H3_ERR_MISALIGNED,
+             "scores, ids and counts must be 4-byte aligned");
+  return launch_block_select(scores, ids, counts, rows, nk, max_blocks, keep_first, keep_last,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+h3_status h3_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                              const void* v, int64_t ld_v, void* o, int64_t ld_o,
+                              const int32_t* ids, const int32_t* counts, int max_blocks, int Lq,
+                              int Lk, int H, int Hkv, int Dh, int k_block, float softmax_scale,
+                              h3_stream_t stream) {
+  clear_error();
+  h3_status st = check_block_sizes(Lq, Lk, H, Hkv, k_block);
+  if (st != H3_OK) return st;
+  H3_REQUIRE(Dh == 128, H3_ERR_UNSUPPORTED, "head_dim %d unsupported (128 only)", Dh);
+  H3_REQUIRE(softmax_scale > 0.f && std::isfinite(softmax_scale), H3_ERR_INVALID_ARG,
+             "softmax_scale must be > 0 and finite");
+  st = check_lists(static_cast<int64_t>(query_blocks(Lq)) * H, key_blocks(Lk, k_block), max_blocks);
+  if (st != H3_OK) return st;
+  if (Lq == 0) return H3_OK;
+  if ((st = check_strided("q", q, ld_q, H)) != H3_OK) return st;
+  if ((st = check_strided("o", o, ld_o, H)) != H3_OK) return st;
+  if (Lk > 0) {
+    if ((st = check_strided("k", k, ld_k, Hkv)) != H3_OK) return st;
+    if ((st = check_strided("v", v, ld_v, Hkv)) != H3_OK) return st;
+    H3_REQUIRE(o != k && o != v, H3_ERR_INVALID_ARG, "o is k or v");
+  }
+  H3_REQUIRE(o != q, H3_ERR_INVALID_ARG, "o is q");
+  H3_REQUIRE(ids && counts, H3_ERR_INVALID_ARG, "ids or counts is NULL");
+  H3_REQUIRE(aligned4(ids) && aligned4(counts), H3_ERR_MISALIGNED,
+             "ids and counts must be 4-byte aligned");
+  if (Lk == 0)  // no key anywhere
+    return cuda_fail(cudaMemset2DAsync(o, static_cast<size_t>(ld_o) * 2, 0,
+                                       static_cast<size_t>(H) * 256, Lq,
+                                       reinterpret_cast<cudaStream_t>(stream)),
+                     "block attention without keys");
+  return launch_attention_blocks(q, ld_q, k, ld_k, v, ld_v, o, ld_o, ids, counts, max_blocks, Lq,
+                                 Lk, H, Hkv, k_block, softmax_scale,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
 static h3_status check_block_config(const h3_block_config* c) {
   H3_REQUIRE(c != nullptr, H3_ERR_INVALID_ARG, "config is NULL");
   h3_status st = check_rows(c->S, c->L);
@@ -1003,6 +1169,92 @@ h3_status h3_linear_swiglu_fp8(const void* qx, const float* sx, const void* qw_g
   if (L == 0) return H3_OK;
   return launch_gemm_fp8(qx, K, sx, qw_gu, K, sw_gu, out, F, L, F, K, GEMM_SWIGLU,
                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---- 4-bit rows and their products
+static h3_status check_fp4(int K, int format) {
+  H3_REQUIRE(format == H3_FP4_MX || format == H3_FP4_NV, H3_ERR_INVALID_ARG,
+             "format %d (H3_FP4_MX or H3_FP4_NV)", format);
+  H3_REQUIRE(K > 0 && K % 32 == 0, H3_ERR_UNSUPPORTED, "K=%d must be a positive multiple of 32", K);
+  return H3_OK;
+}
+
+static bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
+
+size_t h3_fp4_scale_bytes(int R, int K, int format) {
+  clear_error();
+  if (R < 0) {
+    fail(H3_ERR_INVALID_ARG, "R=%d", R);
+    return 0;
+  }
+  if (check_fp4(K, format) != H3_OK) return 0;
+  const size_t blocks = std::max<size_t>(1, (static_cast<size_t>(R) + 127) / 128);
+  return blocks * fp4_tiles(K, format == H3_FP4_NV) * 512;
+}
+
+h3_status h3_quantize_fp4_rows(const void* x, int64_t ld_x, void* codes, void* scales,
+                               float* row_scale, int R, int K, int format, h3_stream_t stream) {
+  clear_error();
+  h3_status st = check_fp4(K, format);
+  if (st != H3_OK) return st;
+  H3_REQUIRE(R >= 0, H3_ERR_INVALID_ARG, "R=%d", R);
+  H3_REQUIRE(K <= 16384, H3_ERR_UNSUPPORTED, "K=%d exceeds 16384", K);
+  H3_REQUIRE((row_scale != nullptr) == (format == H3_FP4_NV) || R == 0, H3_ERR_INVALID_ARG,
+             "row_scale belongs to H3_FP4_NV, and only to it");
+  if (R == 0) return H3_OK;
+  H3_REQUIRE(x && codes && scales, H3_ERR_INVALID_ARG, "a required pointer is NULL");
+  H3_REQUIRE(ld_x >= K, H3_ERR_INVALID_ARG, "row stride %lld of x is below K=%d",
+             static_cast<long long>(ld_x), K);
+  H3_REQUIRE(aligned16(x) && ld_x % 8 == 0 && aligned16(codes) && aligned128(scales) &&
+                 aligned4(row_scale),
+             H3_ERR_MISALIGNED,
+             "x, its row stride and codes must be 16-byte, scales 128-byte aligned");
+  H3_REQUIRE(x != codes && x != scales && codes != scales, H3_ERR_INVALID_ARG,
+             "x, codes and scales overlap");
+  return launch_quantize_fp4_rows(x, ld_x, codes, scales, row_scale, R, K, format == H3_FP4_NV,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+static h3_status fp4_product(const Fp4Operand& x, const Fp4Operand& w, void* y, int S, int L, int N,
+                             int K, int format, bool swiglu, h3_stream_t stream) {
+  h3_status st = check_rows(S, L);
+  if (st != H3_OK) return st;
+  if ((st = check_fp4(K, format)) != H3_OK) return st;
+  H3_REQUIRE(K <= (1 << 20) && N <= (1 << 24), H3_ERR_UNSUPPORTED,
+             "K=%d exceeds 2^20 or N=%d exceeds 2^24", K, N);
+  H3_REQUIRE(x.codes && x.scales && w.codes && w.scales && y, H3_ERR_INVALID_ARG,
+             "a required pointer is NULL");
+  const bool nv = format == H3_FP4_NV;
+  H3_REQUIRE((x.row_scale != nullptr) == nv && (w.row_scale != nullptr) == nv, H3_ERR_INVALID_ARG,
+             "row scales belong to H3_FP4_NV, and only to it");
+  H3_REQUIRE(aligned16(x.codes) && aligned16(w.codes) && aligned16(y) && aligned128(x.scales) &&
+                 aligned128(w.scales) && aligned4(x.row_scale) && aligned16(w.row_scale),
+             H3_ERR_MISALIGNED,
+             "codes, y and the weights' row scales must be 16-byte, scales 128-byte aligned");
+  H3_REQUIRE(y != x.codes && y != w.codes, H3_ERR_INVALID_ARG, "y overlaps an operand");
+  const int64_t tiles = ((static_cast<int64_t>(L) + 255) / 256) * ((static_cast<int64_t>(N) + 127) / 128);
+  H3_REQUIRE(tiles < (int64_t{1} << 30), H3_ERR_UNSUPPORTED, "L=%d x N=%d is too large", L, N);
+  if (L == 0) return H3_OK;
+  return launch_gemm_fp4(x, w, y, L, N, K, nv, swiglu, reinterpret_cast<cudaStream_t>(stream));
+}
+
+h3_status h3_linear_fp4(const void* x_codes, const void* x_scales, const float* rx,
+                        const void* w_codes, const void* w_scales, const float* rw, void* y,
+                        int S, int L, int N, int K, int format, h3_stream_t stream) {
+  clear_error();
+  H3_REQUIRE(N > 0 && N % 8 == 0, H3_ERR_UNSUPPORTED, "N=%d must be a positive multiple of 8", N);
+  return fp4_product({x_codes, x_scales, rx}, {w_codes, w_scales, rw}, y, S, L, N, K, format, false,
+                     stream);
+}
+
+h3_status h3_linear_swiglu_fp4(const void* x_codes, const void* x_scales, const float* rx,
+                               const void* w_codes, const void* w_scales, const float* rw,
+                               void* out, int S, int L, int F, int K, int format,
+                               h3_stream_t stream) {
+  clear_error();
+  H3_REQUIRE(F > 0 && F % 128 == 0, H3_ERR_UNSUPPORTED, "F=%d must be a positive multiple of 128", F);
+  return fp4_product({x_codes, x_scales, rx}, {w_codes, w_scales, rw}, out, S, L, F, K, format, true,
+                     stream);
 }
 
 // FP8 block workspace: the BF16 block's slices, one FP8 code buffer

@@ -1,0 +1,497 @@
+// Block-sparse attention: every block of 256 query rows attends over its own list of key
+// blocks (64 or 128 keys), on tcgen05 with S, P and O in tensor memory.
+//
+// One CTA per (query block, head): two query tiles of 128 rows share each key tile, so
+// a 64 KB key and value tile feeds four products (2,048 cycles) and a CTA draws 32 bytes
+// per cycle from L2. Two tiles with lists of their own would need twice that, which is
+// what an SM gets at best: hence lists of 256 rows. A key tile is one listed block of 128
+// keys, or two of 64.
+//   * tensor memory: S (128 columns, the two query tiles in turn), O and P (bf16) of both;
+//     a softmax reads S into registers and frees it at once, so the other tile's Q K^T
+//     overlaps it, and P V reads P from tensor memory;
+//   * warps 0-3 / 4-7: softmax of query tile 0 / 1 (thread = row); warp 8: lists and TMA loads,
+//     keys and values in five 32 KB slots in the order in which they are used; warp 9:
+//     issues the products;
+//   * the lists may hold anything: an id outside the keys is loaded from past the last
+//     row (zeros) and its keys are masked, as are those past the end of the last block.
+// Where the (query block, head)s are fewer than the SMs, a cluster of CTAs shares a list
+// and joins its partial results through distributed shared memory, in rank order.
+#include <algorithm>
+
+#include "h3_attn_common.cuh"
+#include "h3_blocks.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int BS_SLOTS = 5;
+constexpr int BS_COUNTS = 8;  // key tiles whose key counts are kept
+constexpr size_t BS_SMEM_BYTES = 1024 + BS_SLOTS * TILE_BYTES + 2 * TILE_BYTES + 512;
+static_assert(BS_SMEM_BYTES <= 227 * 1024, "block attention shared memory");
+constexpr float BS_KEYS_SEEN = -3.402823466e+38f;
+
+enum BarB {
+  BB_Q = 0,
+  BB_FULL = 1,
+  BB_EMPTY = BB_FULL + BS_SLOTS,
+  BB_S = BB_EMPTY + BS_SLOTS,  // S_i written (MMA commit)
+  BB_SFREE = BB_S + 2,         // S_i read by the softmax (4 warp arrivals)
+  BB_P = BB_SFREE + 2,         // P_i written (4 warp arrivals)
+  BB_PVD = BB_P + 2,           // P_i V_j done (MMA commit)
+  BB_O = BB_PVD + 2,
+  BB_DRAIN = BB_O + 1,
+  BB_NUM = BB_DRAIN + 1
+};
+constexpr uint32_t TB_S = 0, TB_O = 128, TB_P = 384;
+// barriers, the TMEM address word, key counts of the tiles under way
+static_assert(BB_NUM * 8 + 16 + BS_COUNTS * 4 <= 512, "barrier + count region");
+// the join: O of 256 rows in the slots, (maximum, sum) behind it
+static_assert(2 * BQ * DH * 4 + 2 * BQ * 8 <= BS_SLOTS * TILE_BYTES, "join region");
+
+struct BlockAttnArgs {
+  __nv_bfloat16* o;
+  int64_t ld_o;
+  const int32_t* ids;
+  const int32_t* counts;
+  int Lq, Lk, nq, nk;
+  int most;        // entries of a list
+  int kb;          // keys of a block
+  int group;       // query heads per key head
+  int cluster;     // CTAs per list
+  float scale_log2;
+  DevErr err;
+};
+
+// Number of the load, in slot order, of K_j and V_j of n tiles: K0 K1 V0 K2 V1 ...
+__device__ __forceinline__ int load_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int load_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+
+// One key tile of the online softmax for the calling thread's row, as in the dense
+// kernel (base 2, the scale folded in, the running maximum raised only when exceeded by
+// more than RESCALE_THRESHOLD). v0, v1: real keys among the tile's first and last 64. A
+// maximum of -inf says that the row has seen no key; rows whose scores are all NaN or
+// -inf have the least float instead, so that they end as NaN.
+template <class WaitPV>
+__device__ __forceinline__ bool softmax_blocks(uint32_t (&sr)[128], uint32_t tP, uint32_t tO,
+                                               int v0, int v1, bool o_live, float scale_log2,
+                                               float& m, float& l, WaitPV&& wait_pv) {
+  if ((v0 & v1) != 64) {  // (both are at most 64)
+#pragma unroll
+    for (int c = 0; c < 64; ++c) {
+      if (c >= v0) sr[c] = 0xff800000u;
+      if (c >= v1) sr[64 + c] = 0xff800000u;
+    }
+  }
+  float ma = -INFINITY, mb = -INFINITY, mc = -INFINITY, md = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 128; c += 8) {
+    ma = max3f(ma, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+    mb = max3f(mb, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+    mc = max3f(mc, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
+    md = max3f(md, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
+  }
+  float mx = max3f(ma, mb, fmaxf(mc, md)) * scale_log2;
+  if (v0 + v1 > 0) mx = fmaxf(mx, BS_KEYS_SEEN);
+  bool pv_done = !o_live;
+  if (__any_sync(0xffffffffu, mx > m + RESCALE_THRESHOLD)) {
+    const float m_new = fmaxf(m, mx);
+    const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+    l *= alpha;
+    if (o_live) {
+      if (!wait_pv()) return false;
+      pv_done = true;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t ov[16];
+        tmem_ld16(tO + c * 16, ov);
+        tmem_ld_wait();
+        tmem_reg_fence(ov);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+        tmem_st16(tO + c * 16, ov);
+      }
+      tmem_st_wait();
+    }
+    m = m_new;
+  }
+  const float neg_m = m == -INFINITY ? 0.f : -m;  // no key so far: weights of exp2(-inf)
+  float la = 0.f, lb = 0.f, lc = 0.f, ld = 0.f;
+  uint32_t pk[64];
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    float x0, x1;
+    ffma2_bc(x0, x1, __uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]), scale_log2, neg_m);
+    const float p0 = ex2_approx(x0);
+    const float p1 = ex2_approx(x1);
+    if (i & 1)
+      fadd2(lc, ld, p0, p1);
+    else
+      fadd2(la, lb, p0, p1);
+    pk[i] = pack_bf16x2(p0, p1);
+  }
+  l += (la + lb) + (lc + ld);
+  if (!pv_done && !wait_pv()) return false;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    tmem_st16(tP + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[c * 16]));
+  tmem_st_wait();
+  return true;
+}
+
+__global__ void __launch_bounds__(Q2_THREADS, 1)
+    attention_blocks_kernel(const __grid_constant__ CUtensorMap tmQ,
+                            const __grid_constant__ CUtensorMap tmK,
+                            const __grid_constant__ CUtensorMap tmV, const BlockAttnArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sKV = smem;
+  uint8_t* sQ = smem + BS_SLOTS * TILE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + 2 * TILE_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BB_NUM);
+  // real keys of key tile j: low half its first 64, high half its last 64
+  volatile uint32_t* keys = tmem_slot + 4;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % a.cluster;
+  const int qb = static_cast<int>(blockIdx.x) / a.cluster;
+  const int h = blockIdx.y;
+  const int q0 = qb * 2 * BQ;
+  const bool two = q0 + BQ < a.Lq;  // the second query tile has rows
+  const int64_t item = static_cast<int64_t>(h) * a.nq + qb;
+  const int32_t* list = a.ids + item * a.most;
+  const int per_tile = BKV / a.kb;  // listed blocks of a key tile
+  const int count = min(max(__ldg(a.counts + item), 0), a.most);
+  // this CTA's key tiles
+  const int tiles = (count + per_tile - 1) / per_tile;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / a.cluster);
+  const int n = static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / a.cluster) - tile0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < BB_NUM; ++i) mbar_init(bar(i), (i >= BB_SFREE && i < BB_PVD) ? 4 : 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  float m = -INFINITY, l = 0.f;  // softmax warps: the row's maximum and sum
+  bool ok = true;
+  if (warp == 8) {
+    // ---------------------------------------------------------- lists and loads
+    if (lane == 0 && n > 0) {
+      const int colq = h * DH, colk = h / a.group * DH;
+      mbar_arrive_expect_tx(bar(BB_Q), (two ? 2 : 1) * TILE_BYTES);
+      for (int i = 0; i < (two ? 2 : 1); ++i)
+        for (int c = 0; c < 2; ++c)
+          tma_load_2d(smem_u32(sQ + i * TILE_BYTES + c * BOX_BYTES), &tmQ, bar(BB_Q), colq + c * 64,
+                      q0 + i * BQ);
+      int issued = 0;
+      // the first rows of a tile's blocks; past the last key where there is none
+      auto rows_of = [&](int j, int (&row)[2], int (&real)[2]) {
+        for (int e = 0; e < per_tile; ++e) {
+          const int at = (tile0 + j) * per_tile + e;
+          const int id = at < count ? __ldg(list + at) : -1;
+          const bool in = id >= 0 && id < a.nk;
+          row[e] = in ? id * a.kb : a.Lk;
+          real[e] = in ? min(a.kb, a.Lk - row[e]) : 0;
+        }
+      };
+      auto load = [&](const CUtensorMap* map, const int (&row)[2]) {
+        const int st = issued % BS_SLOTS;
+        if (!mbar_wait(bar(BB_EMPTY + st), (static_cast<uint32_t>(issued / BS_SLOTS) & 1u) ^ 1u,
+                       a.err, ERR_WAIT_ATTN_PRODUCER))
+          return false;
+        const uint32_t full = bar(BB_FULL + st);
+        mbar_arrive_expect_tx(full, TILE_BYTES);
+        const uint32_t dst = smem_u32(sKV + st * TILE_BYTES);
+        for (int e = 0; e < per_tile; ++e)
+          for (int c = 0; c < 2; ++c)
+            tma_load_2d(dst + c * BOX_BYTES + e * a.kb * 128, map, full, colk + c * 64, row[e]);
+        ++issued;
+        return true;
+      };
+      int row[2][2] = {}, real[2] = {};
+      for (int j = 0; j <= n; ++j) {  // K_j, then V_{j-1}
+        if (j < n) {
+          rows_of(j, row[j & 1], real);
+          keys[j % BS_COUNTS] = a.kb == 64
+                                    ? static_cast<uint32_t>(real[0]) | static_cast<uint32_t>(real[1]) << 16
+                                    : static_cast<uint32_t>(min(real[0], 64)) |
+                                          static_cast<uint32_t>(max(real[0] - 64, 0)) << 16;
+          if (!load(&tmK, row[j & 1])) break;
+        }
+        if (j > 0 && !load(&tmV, row[(j - 1) & 1])) break;
+      }
+      // no copy of this CTA may still be landing when it exits
+      const uint64_t t0 = globaltimer_ns();
+      const uint64_t lim = drain_limit_ns(a.err);
+      mbar_wait_drain(bar(BB_Q), 0u, t0, lim);
+      for (int i = issued > BS_SLOTS ? issued - BS_SLOTS : 0; i < issued; ++i)
+        mbar_wait_drain(bar(BB_FULL + i % BS_SLOTS), static_cast<uint32_t>(i / BS_SLOTS) & 1u, t0,
+                        lim);
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(BQ, BKV, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(BQ, DH, true);
+    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dk = sdesc_sw128(smem_u32(sKV), 16, 1024);
+    const uint64_t dv = sdesc_sw128(smem_u32(sKV), BOX_BYTES, 1024);
+    auto wait = [&](int b, uint32_t parity) {
+      return mbar_wait_warp(bar(b), parity, a.err, ERR_WAIT_ATTN_MMA);
+    };
+    auto wait_load = [&](int i) {
+      return wait(BB_FULL + i % BS_SLOTS, static_cast<uint32_t>(i / BS_SLOTS) & 1u);
+    };
+    auto slot = [](int i) { return static_cast<uint32_t>((i % BS_SLOTS) * (TILE_BYTES >> 4)); };
+    auto qk = [&](int i, int j) {  // S = Q_i K_j^T
+      const uint64_t qd = dq + static_cast<uint32_t>(i * (TILE_BYTES >> 4));
+      const uint64_t kd = dk + slot(load_k(j));
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        const uint32_t off = static_cast<uint32_t>(((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4);
+        mma_ss_el(tmem + TB_S, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_el(bar(BB_S + i));
+    };
+    auto pv = [&](int i, int j) {  // O_i += P_i V_j
+      const uint64_t vd = dv + slot(load_v(j, n));
+#pragma unroll
+      for (int kk = 0; kk < BKV / 16; ++kk)
+        mma_ts_el(tmem + TB_O + i * 128, tmem + TB_P + i * 64 + kk * 8, vd + kk * (2048 >> 4),
+                  idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+      mma_commit_el(bar(BB_PVD + i));
+    };
+    auto free_load = [&](int i) { mma_commit_el(bar(BB_EMPTY + i % BS_SLOTS)); };
+    if (n > 0) {
+      bool go = wait(BB_Q, 0u) && wait_load(0);
+      if (go) {
+        tc_fence_after();
+        qk(0, 0);
+        if (two) {
+          go = wait(BB_SFREE, 0u);
+          if (go) {
+            tc_fence_after();
+            qk(1, 0);
+          }
+        }
+        if (go) free_load(load_k(0));
+      }
+      // per key tile QK0(j+1) once S1(j) is read, PV0(j), QK1(j+1) once S0(j+1) is, PV1(j);
+      // with one query tile QK0(j+1) once S0(j) is read, PV0(j)
+      for (int j = 0; go && j < n; ++j) {
+        const uint32_t par = static_cast<uint32_t>(j) & 1u;
+        const bool more = j + 1 < n;
+        if (more) {
+          if (!wait_load(load_k(j + 1)) || !wait(BB_SFREE + (two ? 1 : 0), par)) break;
+          tc_fence_after();
+          qk(0, j + 1);
+          if (!two) free_load(load_k(j + 1));
+        }
+        if (!wait_load(load_v(j, n)) || !wait(BB_P, par)) break;
+        tc_fence_after();
+        pv(0, j);
+        if (two) {
+          if (more) {
+            if (!wait(BB_SFREE, par ^ 1u)) break;
+            tc_fence_after();
+            qk(1, j + 1);
+            free_load(load_k(j + 1));
+          }
+          if (!wait(BB_P + 1, par)) break;
+          tc_fence_after();
+          pv(1, j);
+        }
+        free_load(load_v(j, n));
+      }
+    }
+    mma_commit_el(bar(BB_O));
+    // every product must be done with shared and tensor memory before the CTA frees them
+    mma_commit_el(bar(BB_DRAIN));
+    mbar_wait_drain(bar(BB_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(a.err));
+  } else if (two || warp < 4) {
+    // ---------------------------------------------------------- softmax
+    const int tile = warp >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + TB_S;
+    const uint32_t tO = tmem + lane_base + TB_O + tile * 128;
+    const uint32_t tP = tmem + lane_base + TB_P + tile * 64;
+    for (int j = 0; j < n; ++j) {
+      if (!mbar_wait_warp(bar(BB_S + tile), static_cast<uint32_t>(j) & 1u, a.err,
+                          ERR_WAIT_ATTN_SOFTMAX)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t real = keys[j % BS_COUNTS];
+      uint32_t sr[128];
+      {
+        uint32_t (&c0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+        uint32_t (&c1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
+        uint32_t (&c2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[64]);
+        uint32_t (&c3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[96]);
+        tmem_ld32(tS + 0, c0);
+        tmem_ld32(tS + 32, c1);
+        tmem_ld32(tS + 64, c2);
+        tmem_ld32(tS + 96, c3);
+        tmem_ld_wait();
+        tmem_reg_fence(sr);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BB_SFREE + tile));
+      auto wait_pv = [&]() {  // P_i V_{j-1} done with P_i and O_i
+        const bool done = mbar_wait_warp(bar(BB_PVD + tile), static_cast<uint32_t>(j - 1) & 1u,
+                                         a.err, ERR_WAIT_ATTN_SOFTMAX);
+        tc_fence_after();
+        return done;
+      };
+      if (!softmax_blocks(sr, tP, tO, static_cast<int>(real & 0xffffu),
+                          static_cast<int>(real >> 16), j > 0, a.scale_log2, m, l, wait_pv)) {
+        ok = false;
+        break;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BB_P + tile));
+    }
+    if (ok) ok = mbar_wait_warp(bar(BB_O), 0u, a.err, ERR_WAIT_ATTN_SOFTMAX);
+    tc_fence_after();
+    const int row = tile * BQ + (warp & 3) * 32 + lane;
+    const bool row_ok = q0 + row < a.Lq;
+    if (a.cluster == 1) {
+      __nv_bfloat16* orow = a.o + static_cast<int64_t>(q0 + row) * a.ld_o + h * DH;
+      if (n == 0) {  // no key: zeros
+        if (row_ok)
+          for (int c = 0; c < DH / 8; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0, 0, 0, 0);
+      } else if (ok) {
+        // (a list of nothing but ids outside the keys: O is 0, and stays so)
+        store_o_row(tO, m == -INFINITY ? 1.f : l, orow, row_ok, nullptr);
+      }
+    } else {
+      // partial results to shared memory, where no load and no product is under way any
+      // more: float4 c of row r at c ^ (r & 31), so that a warp's stores spread over the banks
+      float4* po = reinterpret_cast<float4*>(sKV) + row * (DH / 4);
+      if (n > 0) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tmem_ld_wait();
+          tmem_reg_fence(ov);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            po[(c * 8 + i) ^ lane] =
+                make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
+                            __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+        }
+      }
+      reinterpret_cast<float2*>(sKV + 2 * BQ * DH * 4)[row] =
+          make_float2(n > 0 ? m : -INFINITY, l);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (a.cluster == 1) {
+    __syncthreads();
+  } else {
+    cluster_sync_all();
+    // rows in turn over the cluster's warps, a lane four channels
+    const int rows = min(2 * BQ, a.Lq - q0);
+    const uint32_t base = smem_u32(sKV);
+    for (int r = rank * 10 + warp; r < rows; r += a.cluster * 10) {
+      float top = -INFINITY, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < a.cluster; ++p) {
+        float pm, pl;
+        const uint32_t ml = mapa_shared(base + 2 * BQ * DH * 4 + r * 8, p);
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(pm), "=f"(pl) : "r"(ml) : "memory");
+        if (pm == -INFINITY) continue;  // no key there
+        float4 y;
+        const uint32_t at = mapa_shared(base + r * (DH * 4) + ((lane ^ (r & 31)) * 16), p);
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                     : "r"(at)
+                     : "memory");
+        const float next = fmaxf(top, pm);
+        const float f = top == -INFINITY ? 0.f : ex2_approx(top - next), w = ex2_approx(pm - next);
+        top = next;
+        sum = fmaf(pl, w, sum * f);
+        acc.x = fmaf(y.x, w, acc.x * f);
+        acc.y = fmaf(y.y, w, acc.y * f);
+        acc.z = fmaf(y.z, w, acc.z * f);
+        acc.w = fmaf(y.w, w, acc.w * f);
+      }
+      const float inv = top == -INFINITY ? 0.f : 1.0f / sum;
+      *reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(q0 + r) * a.ld_o + h * DH + lane * 4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    cluster_sync_all();  // a peer may still be reading this CTA's results
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+h3_status launch_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                                  const void* v, int64_t ld_v, void* o, int64_t ld_o,
+                                  const int32_t* ids, const int32_t* counts, int max_blocks, int Lq,
+                                  int Lk, int H, int Hkv, int k_block, float scale,
+                                  cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  h3_status st = set_smem_limit(done, attention_blocks_kernel, BS_SMEM_BYTES,
+                                "block attention: set shared memory size");
+  if (st != H3_OK) return st;
+  BlockAttnArgs a{};
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.ld_o = ld_o;
+  a.ids = ids;
+  a.counts = counts;
+  a.Lq = Lq;
+  a.Lk = Lk;
+  a.nq = (Lq + 2 * BQ - 1) / (2 * BQ);
+  a.nk = (Lk + k_block - 1) / k_block;
+  a.most = max_blocks;
+  a.kb = k_block;
+  a.group = H / Hkv;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if ((st = dev_err(&a.err)) != H3_OK) return st;
+  // a list is shared by as many CTAs as there are SMs for, of two key tiles each at least
+  const int64_t items = static_cast<int64_t>(a.nq) * H;
+  const int64_t tiles = (static_cast<int64_t>(max_blocks) * k_block + BKV - 1) / BKV;
+  a.cluster = 1;
+  while (a.cluster < 8 && items * a.cluster * 2 <= num_sms() && tiles >= a.cluster * 4) a.cluster *= 2;
+  CUtensorMap tq, tk, tv;
+  const uint64_t wq = static_cast<uint64_t>(H) * DH, wk = static_cast<uint64_t>(Hkv) * DH;
+  if ((st = make_tmap_bf16_2d(&tq, q, wq, Lq, ld_q * 2, 64, BQ)) != H3_OK) return st;
+  if ((st = make_tmap_bf16_2d(&tk, k, wk, Lk, ld_k * 2, 64, k_block)) != H3_OK) return st;
+  if ((st = make_tmap_bf16_2d(&tv, v, wk, Lk, ld_v * 2, 64, k_block)) != H3_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.nq) * a.cluster, H);
+  cfg.blockDim = dim3(Q2_THREADS);
+  cfg.dynamicSmemBytes = BS_SMEM_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_fail(cudaLaunchKernelEx(&cfg, attention_blocks_kernel, tq, tk, tv, a),
+                   "block attention launch");
+}
+
+}  // namespace h3

@@ -1,0 +1,454 @@
+// Block-scaled 4-bit GEMM on CTA pairs: C[:L] = epilogue(A[:L] B^T), E2M1 operands whose
+// scales the tensor cores apply (tcgen05 kind::mxf4 / kind::mxf4nvf4, cta_group::2), FP32
+// accumulation in tensor memory, bf16 output.
+//
+// A pair takes 256 x 256 of the output: a CTA holds 128 rows of A and of B (half of the
+// columns) in shared memory and 128 x 256 of the accumulator in tensor memory. One
+// CTA's tile of 128 x 256 would read 12 KB of shared memory per instruction and
+// 128 cycles, three quarters of what it can; as a pair it is 8 KB.
+//   * stage: 256 values of K (128 bytes per row, 128-byte swizzle) of both operands and
+//     their scales, which lie in memory as the tensor cores want them (tiles of 128 rows x
+//     4 scales, 512 bytes), so a stage's are one contiguous copy per 128 rows;
+//   * warp 0: TMA producer (one lane); warp 1 of the even CTA: issues, per stage, the
+//     copies of the scales from shared to tensor memory (both CTAs' at once) and four
+//     products of K = 64; of the odd CTA: tells the even one when its stage has landed;
+//     warps 2-9: epilogue, two per lane quarter;
+//   * tensor memory: the scales of two stages (2 x 48 columns) leave 416 columns for two
+//     accumulators of 256, so they share 96: a tile's epilogue reads the shared columns
+//     first, and the next tile's products start when they are read. A buffer of scales
+//     is written again when the products of the stage before last are done.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "h3_fp4.cuh"
+#include "h3_internal.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int ROWS = 128;                    // rows of A, and of B, per CTA
+constexpr int BN4 = 256;                     // output columns of a pair
+constexpr int STAGE_CODES = 256;             // values of K per stage
+constexpr int OP_BYTES = ROWS * STAGE_CODES / 2;  // 16 KB
+constexpr int SFA_BYTES = 2048, SFB_BYTES = 2 * 2048;
+constexpr int STAGE4_BYTES = 2 * OP_BYTES + SFA_BYTES + SFB_BYTES;
+constexpr int STAGES4 = 5;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS4 = 64 + EPI_WARPS * 32;
+constexpr int GROUP_M4 = 16;                 // raster: 16 x 256 rows per sweep of the columns
+constexpr size_t SMEM4_BYTES = 1024 + STAGES4 * STAGE4_BYTES + 256;
+static_assert(SMEM4_BYTES <= 227 * 1024, "fp4 gemm shared memory");
+
+// tensor-memory columns
+constexpr uint32_t T4_ACC1 = 160, T4_SF = 416, T4_SF_COLS = 48, T4_SFB = 16;
+constexpr int SHARED_CHUNKS = 3;             // 32-column chunks the accumulators share
+
+enum Bar4 {
+  B4_FULL = 0,
+  B4_EMPTY = B4_FULL + STAGES4,
+  B4_TFULL = B4_EMPTY + STAGES4,  // accumulator written [2]
+  B4_SHARED = B4_TFULL + 2,       // shared columns read (16 warps)
+  B4_DRAIN = B4_SHARED + 1,
+  B4_NUM = B4_DRAIN + 1
+};
+static_assert(B4_NUM * 8 + 8 <= 256, "barrier region");
+
+// Instruction descriptor of the 4-bit kinds with E2M1 operands and an f32 accumulator:
+// [4,6) scale id of B, [7,10) and [10,12) operand formats (1 = E2M1), [17,23) N >> 3, bit
+// 23 scale format (0 = E4M3, 1 = E8M0), [24,29) M >> 4, [29,31) scale id of A, bit 31 0
+// for K = 64. A scale id is the byte of its 32-bit column where a product's scales begin.
+__host__ __device__ constexpr uint32_t idesc_e2m1(int M, int N, bool e8m0, uint32_t scale_id) {
+  return (scale_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         ((e8m0 ? 1u : 0u) << 23) | (static_cast<uint32_t>(M >> 4) << 24) | (scale_id << 29);
+}
+
+// Descriptor of 32 rows x 16 contiguous bytes without swizzle (8-row groups 128 bytes
+// apart): the source of a scale copy.
+__device__ __forceinline__ uint64_t sdesc_rows16(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+// 512 bytes of scales (32 rows of 16 bytes) to 4 columns of tensor memory, the same in
+// every lane quarter, in both CTAs from their own shared memory.
+__device__ __forceinline__ void scale_copy_pair_el(uint32_t taddr, uint64_t desc) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc)
+      : "memory");
+}
+template <bool NV>
+__device__ __forceinline__ void mma_fp4_pair_el(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (NV)
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// Untiled copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+struct Gemm4Args {
+  __nv_bfloat16* C;
+  const uint8_t* sfa;
+  const uint8_t* sfb;
+  const float* ra;  // row scales (NV)
+  const float* rb;
+  int M, N, K;
+  int num_m, num_n, num_k;  // tiles of 256 rows, of columns, stages
+  int num_tiles;
+  int sf_tiles;             // scale tiles along K
+  int a_blocks, b_blocks;   // scale tiles along the rows
+  int up_rows;              // SwiGLU: first row of the up half of B
+  DevErr err;
+};
+
+__device__ __forceinline__ void tile_coords4(int tile, const Gemm4Args& a, int& mb, int& nb) {
+  const int group_size = GROUP_M4 * a.num_n;
+  const int group = tile / group_size;
+  const int first_m = group * GROUP_M4;
+  const int gm = min(a.num_m - first_m, GROUP_M4);
+  const int r = tile - group * group_size;
+  mb = first_m + r % gm;
+  nb = r / gm;
+}
+
+__device__ __forceinline__ float silu_f(float g) { return g / (1.0f + __expf(-g)); }
+
+template <bool NV, bool SWIGLU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
+    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const Gemm4Args a) {
+  constexpr int ATOM_STEPS = NV ? 1 : 2;  // products that a scale tile serves
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES4 * STAGE4_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B4_NUM);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B4_NUM; ++i) {
+      uint32_t count = 1;
+      if (i < B4_EMPTY) count = leader ? 2 : 1;  // with the odd CTA's relay
+      if (i == B4_SHARED) count = 2 * EPI_WARPS;
+      mbar_init(bar(i), count);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // products and scale tiles of stage kb
+  auto steps_of = [&](int kb) { return min(4, (a.K - kb * STAGE_CODES + 63) / 64); };
+  auto atoms_of = [&](int kb) { return (steps_of(kb) + ATOM_STEPS - 1) / ATOM_STEPS; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int issued = 0;
+      bool ok = true;
+      for (int tile = pair; tile < a.num_tiles && ok; tile += pairs) {
+        int mb, nb;
+        tile_coords4(tile, a, mb, nb);
+        const int a_blk = 2 * mb + static_cast<int>(rank);
+        // the pair's two blocks of 128 rows of B: neighbours, or gate and up
+        const int b_blk0 = SWIGLU ? nb : 2 * nb;
+        const int b_blk1 = SWIGLU ? a.up_rows / ROWS + nb : 2 * nb + 1;
+        const int b_row = (leader ? b_blk0 : b_blk1) * ROWS;
+        const bool a_in = a_blk < a.a_blocks, b1_in = b_blk1 < a.b_blocks;
+        for (int kb = 0; kb < a.num_k; ++kb) {
+          const int st = issued % STAGES4;
+          if (!mbar_wait(bar(B4_EMPTY + st), (static_cast<uint32_t>(issued / STAGES4) & 1u) ^ 1u,
+                         a.err, ERR_WAIT_GEMM_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = bar(B4_FULL + st);
+          const uint32_t dst = smem_u32(smem + st * STAGE4_BYTES);
+          const uint32_t sf = static_cast<uint32_t>(atoms_of(kb)) * 512u;
+          mbar_arrive_expect_tx(full, 2 * OP_BYTES + sf * (1u + (a_in ? 1u : 0u) + (b1_in ? 1u : 0u)));
+          const int kx = kb * (STAGE_CODES / 2);
+          tma_load_2d(dst, &tmA, full, kx, a_blk * ROWS);
+          tma_load_2d(dst + OP_BYTES, &tmB, full, kx, b_row);
+          const int64_t k_tile = static_cast<int64_t>(kb) * (4 / ATOM_STEPS);
+          const uint32_t sfa = dst + 2 * OP_BYTES, sfb = sfa + SFA_BYTES;
+          if (a_in)
+            bulk_load(sfa, a.sfa + (static_cast<int64_t>(a_blk) * a.sf_tiles + k_tile) * 512, sf, full);
+          bulk_load(sfb, a.sfb + (static_cast<int64_t>(b_blk0) * a.sf_tiles + k_tile) * 512, sf, full);
+          if (b1_in)
+            bulk_load(sfb + 2048, a.sfb + (static_cast<int64_t>(b_blk1) * a.sf_tiles + k_tile) * 512,
+                      sf, full);
+          ++issued;
+        }
+      }
+      // no copy of this CTA may still be landing when it exits
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = issued > STAGES4 ? issued - STAGES4 : 0; i < issued; ++i)
+        mbar_wait_drain(bar(B4_FULL + i % STAGES4), static_cast<uint32_t>(i / STAGES4) & 1u, t0,
+                        drain_limit_ns(a.err));
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc0 = idesc_e2m1(2 * ROWS, BN4, !NV, 0);
+      constexpr uint32_t idesc2 = idesc_e2m1(2 * ROWS, BN4, !NV, 2);
+      constexpr uint16_t kBoth = 3;
+      const uint64_t da = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t ds = sdesc_rows16(smem_u32(smem) + 2 * OP_BYTES);
+      auto wait = [&](int b, uint32_t parity) {
+        return mbar_wait_warp(bar(b), parity, a.err, ERR_WAIT_GEMM_MMA);
+      };
+      int it = 0;    // stages so far
+      int done = 0;  // tiles so far
+      bool ok = true;
+      for (int tile = pair; tile < a.num_tiles && ok; tile += pairs, ++done) {
+        // the columns this accumulator shares with the tile before are read
+        if (done > 0 && !wait(B4_SHARED, static_cast<uint32_t>(done - 1) & 1u)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (done & 1 ? T4_ACC1 : 0u);
+        for (int kb = 0; kb < a.num_k; ++kb, ++it) {
+          const int st = it % STAGES4;
+          if (!wait(B4_FULL + st, static_cast<uint32_t>(it / STAGES4) & 1u) ||
+              (it >= 2 &&
+               !wait(B4_EMPTY + (it - 2) % STAGES4, static_cast<uint32_t>((it - 2) / STAGES4) & 1u))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t off = static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
+          const uint32_t sf = tmem + T4_SF + static_cast<uint32_t>(it & 1) * T4_SF_COLS;
+          const int steps = steps_of(kb), atoms = atoms_of(kb);
+#pragma unroll
+          for (int t = 0; t < 4 / ATOM_STEPS; ++t) {
+            if (t < atoms) {
+              const uint64_t s = ds + off + static_cast<uint32_t>(t * (512 >> 4));
+              scale_copy_pair_el(sf + t * 4, s);
+              scale_copy_pair_el(sf + T4_SFB + t * 8, s + (SFA_BYTES >> 4));
+              scale_copy_pair_el(sf + T4_SFB + t * 8 + 4, s + ((SFA_BYTES + 2048) >> 4));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k < steps) {
+              const uint64_t ad = da + off + static_cast<uint32_t>(k * 2);
+              mma_fp4_pair_el<NV>(d, ad, ad + (OP_BYTES >> 4),
+                                  (!NV && (k & 1)) ? idesc2 : idesc0, sf + (k / ATOM_STEPS) * 4,
+                                  sf + T4_SFB + (k / ATOM_STEPS) * 8, (kb | k) != 0 ? 1u : 0u);
+            }
+          }
+          mma_commit_pair_mc_el(bar(B4_EMPTY + st), kBoth);
+        }
+        if (!ok) break;
+        mma_commit_pair_mc_el(bar(B4_TFULL + (done & 1)), kBoth);
+      }
+      // every product must be done with both CTAs' memories before either frees them
+      mma_commit_pair_mc_el(bar(B4_DRAIN), 1);
+      mbar_wait_drain(bar(B4_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(a.err));
+    } else if (lane == 0) {
+      // ------------------------------------------------------------ relay
+      int it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < a.num_tiles && ok; tile += pairs)
+        for (int kb = 0; kb < a.num_k; ++kb, ++it) {
+          const int st = it % STAGES4;
+          if (!mbar_wait(bar(B4_FULL + st), static_cast<uint32_t>(it / STAGES4) & 1u, a.err,
+                         ERR_WAIT_GEMM_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_remote(mapa_shared(bar(B4_FULL + st), 0));
+        }
+    }
+  } else {
+    // ------------------------------------------------------ epilogue warps
+    const int quarter = warp & 3;     // TMEM lane quarter this warp may access
+    const int side = (warp - 2) >> 2; // which of the quarter's two warps
+    int done = 0;
+    for (int tile = pair; tile < a.num_tiles; tile += pairs, ++done) {
+      int mb, nb;
+      tile_coords4(tile, a, mb, nb);
+      const int acc = done & 1;
+      if (!mbar_wait_warp(bar(B4_TFULL + acc), static_cast<uint32_t>(done >> 1) & 1u, a.err,
+                          ERR_WAIT_GEMM_EPILOGUE))
+        break;
+      tc_fence_after();
+      const int row = (2 * mb + static_cast<int>(rank)) * ROWS + quarter * 32 + lane;
+      const bool row_ok = row < a.M;
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (acc ? T4_ACC1 : 0u);
+      const float ra = NV ? (row_ok ? __ldg(a.ra + row) : 0.f) : 1.f;
+      __nv_bfloat16* crow = a.C + static_cast<int64_t>(row_ok ? row : 0) * a.N;
+      auto tell = [&]() {  // the shared columns are in registers
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            mbar_arrive(bar(B4_SHARED));
+          else
+            mbar_arrive_remote(mapa_shared(bar(B4_SHARED), 0));
+        }
+      };
+      if constexpr (SWIGLU) {
+        // four pairs of chunks, those with shared columns first; two per warp
+#pragma unroll 1
+        for (int i = side; i < 4; i += 2) {
+          const int c = acc ? i : (i + 1) & 3;
+          uint32_t g[32], u[32];
+          tmem_ld32(t_row + c * 32, g);
+          tmem_ld32(t_row + BN4 / 2 + c * 32, u);
+          tmem_ld_wait();
+          tmem_reg_fence(g);
+          tmem_reg_fence(u);
+          if (i == (side == 0 ? 2 : 1)) tell();  // the last of its first three
+          const int col = nb * (BN4 / 2) + c * 32;
+          if (!row_ok) continue;
+          if constexpr (NV) {
+            const float4* sg = reinterpret_cast<const float4*>(a.rb + col);
+            const float4* su = reinterpret_cast<const float4*>(a.rb + a.up_rows + col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 x = __ldg(sg + j), y = __ldg(su + j);
+              const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                g[4 * j + t] = __float_as_uint(__uint_as_float(g[4 * j + t]) * ra * xs[t]);
+                u[4 * j + t] = __float_as_uint(__uint_as_float(u[4 * j + t]) * ra * ys[t]);
+              }
+            }
+          }
+          uint32_t o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float g0 = round_to_bf16(__uint_as_float(g[2 * j]));
+            const float g1 = round_to_bf16(__uint_as_float(g[2 * j + 1]));
+            const float u0 = round_to_bf16(__uint_as_float(u[2 * j]));
+            const float u1 = round_to_bf16(__uint_as_float(u[2 * j + 1]));
+            o[j] = pack_bf16x2(silu_f(g0) * u0, silu_f(g1) * u1);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(crow + col);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = side; i < 8; i += 2) {
+          const int c = acc ? i : (i + 8 - SHARED_CHUNKS) & 7;
+          uint32_t v[32];
+          tmem_ld32(t_row + c * 32, v);
+          tmem_ld_wait();
+          tmem_reg_fence(v);
+          if (i == (side == 0 ? 2 : 1)) tell();
+          const int col = nb * BN4 + c * 32;
+          if (!row_ok) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (col + 8 * j < a.N) {
+              float f[8];
+#pragma unroll
+              for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(v[8 * j + t]);
+              if constexpr (NV) {
+                const float4* sb = reinterpret_cast<const float4*>(a.rb + col + 8 * j);
+                const float4 x = __ldg(sb), y = __ldg(sb + 1);
+                const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * s[t];
+              }
+              *reinterpret_cast<uint4*>(crow + col + 8 * j) =
+                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            }
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <bool NV, bool SWIGLU>
+h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int N, int K,
+                  cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  h3_status st = set_smem_limit(done, gemm_fp4_kernel<NV, SWIGLU>, SMEM4_BYTES,
+                                "fp4 gemm: set shared memory size");
+  if (st != H3_OK) return st;
+  const int b_rows = SWIGLU ? 2 * N : N;
+  const int tile_n = SWIGLU ? BN4 / 2 : BN4;
+  Gemm4Args a{};
+  a.C = static_cast<__nv_bfloat16*>(C);
+  a.sfa = static_cast<const uint8_t*>(A.scales);
+  a.sfb = static_cast<const uint8_t*>(B.scales);
+  a.ra = A.row_scale;
+  a.rb = B.row_scale;
+  a.M = L;
+  a.N = N;
+  a.K = K;
+  a.num_m = (L + 2 * ROWS - 1) / (2 * ROWS);
+  a.num_n = (N + tile_n - 1) / tile_n;
+  a.num_k = (K + STAGE_CODES - 1) / STAGE_CODES;
+  a.num_tiles = a.num_m * a.num_n;
+  a.sf_tiles = fp4_tiles(K, NV);
+  a.a_blocks = (L + ROWS - 1) / ROWS;
+  a.b_blocks = (b_rows + ROWS - 1) / ROWS;
+  a.up_rows = SWIGLU ? N : 0;
+  if ((st = dev_err(&a.err)) != H3_OK) return st;
+  CUtensorMap tmA, tmB;
+  const uint64_t row_bytes = static_cast<uint64_t>(K) / 2;
+  if ((st = make_tmap_u8_2d(&tmA, A.codes, row_bytes, L, row_bytes, 128, ROWS)) != H3_OK) return st;
+  if ((st = make_tmap_u8_2d(&tmB, B.codes, row_bytes, b_rows, row_bytes, 128, ROWS)) != H3_OK)
+    return st;
+  const int grid = 2 * std::min(a.num_tiles, num_sms() / 2);
+  gemm_fp4_kernel<NV, SWIGLU><<<grid, THREADS4, SMEM4_BYTES, s>>>(tmA, tmB, a);
+  return cuda_fail(cudaGetLastError(), "fp4 gemm launch");
+}
+
+}  // namespace
+
+h3_status launch_gemm_fp4(const Fp4Operand& a, const Fp4Operand& b, void* C, int L, int N, int K,
+                          bool nv, bool swiglu, cudaStream_t s) {
+  if (nv)
+    return swiglu ? launch4<true, true>(a, b, C, L, N, K, s) : launch4<true, false>(a, b, C, L, N, K, s);
+  return swiglu ? launch4<false, true>(a, b, C, L, N, K, s) : launch4<false, false>(a, b, C, L, N, K, s);
+}
+
+}  // namespace h3

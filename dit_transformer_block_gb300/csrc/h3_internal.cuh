@@ -80,6 +80,14 @@ h3_status launch_mod_norm_residual(float* resid, const void* delta, const float*
                                    const RopeRequest* rope = nullptr, uint8_t* codes = nullptr,
                                    float* code_scale = nullptr);
 
+// Norms before and after a branch (h3_norms.cu); see h3_sandwich_norm.
+h3_status launch_sandwich_norm(const float* resid, const void* delta, float* resid_out,
+                               void* normed, bool post_norm, const float* post_gain,
+                               const float* gate, float resid_scale, const float* pre_gain,
+                               const float* shift, const float* scale, const int32_t* seg,
+                               int num_seg, int64_t seg_stride, bool rms, int L, int D, float eps,
+                               cudaStream_t s);
+
 // (cos, sin) of every RoPE angle of rows [0, L): out[i * 64 + p] for channel
 // pair p of a 128-channel head, the angle formed and reduced exactly as
 // launch_qk_norm_rope does.

@@ -1,0 +1,219 @@
+// Norms before and after a branch, fused with the branch's gate and the scaled
+// residual: one CTA per row, which stays in registers from its loads to its stores.
+//
+// Per row: p = n(delta) * post_gain, r = resid_scale * resid + gate * p,
+// h = n(r) * pre_gain * (1 + scale) + shift, with n a LayerNorm without affine or a
+// division by the root mean square. Everything between the loads and the stores is
+// FP32, and the mean is taken before the squares (two passes over registers), so a
+// row far from zero loses nothing. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "h3_internal.cuh"
+
+namespace h3 {
+namespace {
+
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  float t = (lane < T / 32) ? red[lane] : 0.f;
+#pragma unroll
+  for (int m = T / 64; m >= 1; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+  return __shfl_sync(0xffffffffu, t, 0);
+}
+
+// x <- n(x) over a row of D values, VPT float4 of it in this thread's registers
+// (zeros beyond the row). red: two buffers of T / 32 floats, the second reduction's
+// being free of the first's readers.
+template <int T, int VPT, bool RMS>
+__device__ __forceinline__ void norm_row(float4 (&x)[VPT], int D4, float inv_d, float eps,
+                                         float* red) {
+  if constexpr (!RMS) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) s += (x[v].x + x[v].y) + (x[v].z + x[v].w);
+    const float mean = row_sum<T>(s, red) * inv_d;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (static_cast<int>(threadIdx.x) + v * T < D4) {
+        x[v].x -= mean;
+        x[v].y -= mean;
+        x[v].z -= mean;
+        x[v].w -= mean;
+      }
+    }
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    q += (x[v].x * x[v].x + x[v].y * x[v].y) + (x[v].z * x[v].z + x[v].w * x[v].w);
+  const float rstd = rsqrtf(row_sum<T>(q, red + T / 32) * inv_d + eps);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    x[v].x *= rstd;
+    x[v].y *= rstd;
+    x[v].z *= rstd;
+    x[v].w *= rstd;
+  }
+}
+
+struct NormArgs {
+  const float* resid;
+  const __nv_bfloat16* delta;
+  float* resid_out;
+  __nv_bfloat16* normed;
+  const float* post_gain;
+  const float* gate;
+  const float* pre_gain;
+  const float* shift;
+  const float* scale;
+  const int32_t* seg;
+  int num_seg;
+  int64_t seg_stride;
+  float resid_scale, eps, inv_d;
+  int D4;
+};
+
+template <int T, int VPT, bool RMS, bool POST>
+__global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
+  __shared__ float red[4 * (T / 32)];
+  const int64_t row = blockIdx.x;
+  const int D4 = a.D4;
+  const float4* rrow = reinterpret_cast<const float4*>(a.resid) + row * D4;
+  float4 x[VPT], y[VPT];
+  // every load of the row is requested before the first use
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = threadIdx.x + v * T;
+    x[v] = c < D4 ? __ldcs(rrow + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const bool branch = a.delta != nullptr;
+  if (branch) {
+    const uint2* drow = reinterpret_cast<const uint2*>(a.delta) + row * D4;
+    uint2 d[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = threadIdx.x + v * T;
+      d[v] = c < D4 ? __ldcs(drow + c) : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      y[v] = make_float4(bf16_lo(d[v].x), bf16_hi(d[v].x), bf16_lo(d[v].y), bf16_hi(d[v].y));
+  }
+  int64_t off = 0;
+  if (a.seg != nullptr)
+    off = static_cast<int64_t>(min(max(__ldg(a.seg + row), 0), a.num_seg - 1)) * a.seg_stride;
+  auto vec = [](const float* p, int c) { return __ldg(reinterpret_cast<const float4*>(p) + c); };
+
+  if (branch) {
+    if constexpr (POST) norm_row<T, VPT, RMS>(y, D4, a.inv_d, a.eps, red);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = threadIdx.x + v * T;
+      if (c < D4) {
+        if (POST && a.post_gain != nullptr) {
+          const float4 g = vec(a.post_gain, c);
+          y[v].x *= g.x;
+          y[v].y *= g.y;
+          y[v].z *= g.z;
+          y[v].w *= g.w;
+        }
+        float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (a.gate != nullptr) g = vec(a.gate + off, c);
+        x[v].x = fmaf(g.x, y[v].x, a.resid_scale * x[v].x);
+        x[v].y = fmaf(g.y, y[v].y, a.resid_scale * x[v].y);
+        x[v].z = fmaf(g.z, y[v].z, a.resid_scale * x[v].z);
+        x[v].w = fmaf(g.w, y[v].w, a.resid_scale * x[v].w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      x[v].x *= a.resid_scale;
+      x[v].y *= a.resid_scale;
+      x[v].z *= a.resid_scale;
+      x[v].w *= a.resid_scale;
+    }
+  }
+  if (a.resid_out != nullptr) {
+    float4* orow = reinterpret_cast<float4*>(a.resid_out) + row * D4;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = threadIdx.x + v * T;
+      if (c < D4) __stcs(orow + c, x[v]);
+    }
+  }
+  if (a.normed == nullptr) return;
+  norm_row<T, VPT, RMS>(x, D4, a.inv_d, a.eps, red + 2 * (T / 32));
+  uint2* hrow = reinterpret_cast<uint2*>(a.normed) + row * D4;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = threadIdx.x + v * T;
+    if (c < D4) {
+      float4 m = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.scale != nullptr) {
+        const float4 s = vec(a.scale + off, c);
+        m = make_float4(1.f + s.x, 1.f + s.y, 1.f + s.z, 1.f + s.w);
+      }
+      if (a.pre_gain != nullptr) {
+        const float4 g = vec(a.pre_gain, c);
+        m.x *= g.x;
+        m.y *= g.y;
+        m.z *= g.z;
+        m.w *= g.w;
+      }
+      if (a.shift != nullptr) b = vec(a.shift + off, c);
+      __stcs(hrow + c, make_uint2(pack_bf16x2(fmaf(x[v].x, m.x, b.x), fmaf(x[v].y, m.y, b.y)),
+                                  pack_bf16x2(fmaf(x[v].z, m.z, b.z), fmaf(x[v].w, m.w, b.w))));
+    }
+  }
+}
+
+template <int T, int VPT>
+void launch_width(const NormArgs& a, int L, bool rms, bool post, cudaStream_t s) {
+  if (rms) {
+    if (post)
+      sandwich_norm_kernel<T, VPT, true, true><<<L, T, 0, s>>>(a);
+    else
+      sandwich_norm_kernel<T, VPT, true, false><<<L, T, 0, s>>>(a);
+  } else {
+    if (post)
+      sandwich_norm_kernel<T, VPT, false, true><<<L, T, 0, s>>>(a);
+    else
+      sandwich_norm_kernel<T, VPT, false, false><<<L, T, 0, s>>>(a);
+  }
+}
+
+}  // namespace
+
+h3_status launch_sandwich_norm(const float* resid, const void* delta, float* resid_out,
+                               void* normed, bool post_norm, const float* post_gain,
+                               const float* gate, float resid_scale, const float* pre_gain,
+                               const float* shift, const float* scale, const int32_t* seg,
+                               int num_seg, int64_t seg_stride, bool rms, int L, int D, float eps,
+                               cudaStream_t s) {
+  const NormArgs a{resid, static_cast<const __nv_bfloat16*>(delta),
+                   resid_out, static_cast<__nv_bfloat16*>(normed),
+                   post_gain, gate, pre_gain, shift, scale, seg, num_seg, seg_stride,
+                   resid_scale, eps, 1.0f / static_cast<float>(D), D / 4};
+  // as few threads as hold the row in at most four float4 each
+  const int d4 = D / 4;
+#define H3_NORM(T, V) launch_width<T, V>(a, L, rms, post_norm, s)
+  if (d4 <= 128) H3_NORM(128, 1);
+  else if (d4 <= 256) H3_NORM(128, 2);
+  else if (d4 <= 512) H3_NORM(256, 2);
+  else if (d4 <= 768) H3_NORM(256, 3);
+  else if (d4 <= 1024) H3_NORM(512, 2);
+  else if (d4 <= 1536) H3_NORM(512, 3);
+  else H3_NORM(512, 4);
+#undef H3_NORM
+  return cuda_fail(cudaGetLastError(), "sandwich_norm launch");
+}
+
+}  // namespace h3

@@ -113,6 +113,17 @@ _SIGS = {
     "h3_attention_paged": (_I, [_P, _I64, _P, _I64, _I, _F, _I, _P, _P, _P, _SZ, _P]),
     "h3_attention_paged_prefix": (_I, [_P, _I64, _P, _I64, _I, _F, _I, _P, _P, _P, _I, _P, _SZ,
                                        _P]),
+    "h3_sandwich_norm": (_I, [_P, _P, _P, _P, _I, _P, _P, _F, _P, _P, _P, _P, _I, _I64, _I, _I, _I,
+                              _I, _F, _P]),
+    "h3_fp4_scale_bytes": (_SZ, [_I, _I, _I]),
+    "h3_quantize_fp4_rows": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _P]),
+    "h3_linear_fp4": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "h3_linear_swiglu_fp4": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "h3_block_scores_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "h3_block_scores": (_I, [_P, _I64, _P, _I64, _P, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P]),
+    "h3_block_select": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "h3_attention_blocks": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I, _I, _I, _I,
+                                 _I, _I, _I, _F, _P]),
     "h3_stack_forward": (_I, [ctypes.POINTER(BlockConfig), ctypes.POINTER(BlockWeights), _I, _P,
                               _P, _I, _P, _P, _P, _SZ, _P]),
 }
@@ -691,3 +702,238 @@ def block_forward(cfg: BlockConfig, weights, resid, mod, pos, workspace, stream=
     _check("block_forward_events", lib().h3_block_forward_events(
         ctypes.byref(cfg), ctypes.byref(w), _p(resid), _p(mod), _p(pos), _p(workspace), nbytes,
         _s(stream), arr, len(events)))
+
+
+# Norms around a branch, 4-bit rows and block-sparse attention: like the paged calls they run
+# several times per layer, so their checks are attribute reads.
+def _vec(t, name, dev, D, groups):
+    """Pointer of a [D] f32 vector, or with groups of a [groups, D] table's first row."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.shape != ((D,) if groups is None else (groups, D)) or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {[D] if groups is None else [groups, D]} with "
+                         f"neighbouring values, got {list(t.shape)}")
+    _on(t, name, dev)
+    return t.data_ptr()
+
+
+def sandwich_norm(resid, delta=None, normed=None, resid_out=None, post_norm=True, post_gain=None,
+                  gate=None, resid_scale=1.0, pre_gain=None, shift=None, scale=None, seg=None,
+                  rms=False, L=None, eps=1e-6, stream=None):
+    """r = resid_scale * resid + gate * n(delta) * post_gain (post_norm False: delta as it
+    is), stored to resid_out (default: resid itself where there is a delta or a
+    resid_scale); normed <- bf16(n(r) * pre_gain * (1 + scale) + shift); n: LayerNorm
+    without affine, or with rms the division by the root mean square. resid, resid_out
+    [S,D] f32, delta, normed [S,D] bf16; vectors [D] f32, left out where None. With seg [S]
+    int32, gate, shift and scale are [G,D] tables (rows equally far apart, as columns of a
+    [G,6,D] one are) and row i takes row seg[i] of them."""
+    dev = _device()
+    S, D = resid.shape
+    _flat(resid, "resid", torch.float32, dev)
+    for n, t, dtype in (("delta", delta, torch.bfloat16), ("normed", normed, torch.bfloat16),
+                        ("resid_out", resid_out, torch.float32)):
+        if t is not None:
+            if t.shape != resid.shape:
+                raise ValueError(f"{n} must be {[S, D]}, got {list(t.shape)}")
+            _flat(t, n, dtype, dev)
+    if delta is None:
+        post_norm = False
+    if resid_out is None and (delta is not None or resid_scale != 1.0):
+        resid_out = resid
+    groups, stride, pseg = None, 0, None
+    if seg is not None:
+        if seg.shape != (S,):
+            raise ValueError(f"seg must be [{S}], got {list(seg.shape)}")
+        _flat(seg, "seg", torch.int32, dev)
+        pseg, groups, stride = seg.data_ptr(), 1, D
+        tables = [t for t in (gate, shift, scale) if t is not None]
+        if tables:
+            groups = tables[0].shape[0]
+            stride = tables[0].stride(0) if groups > 1 else D
+            if groups > 1 and any(t.dim() != 2 or t.stride(0) != stride for t in tables):
+                raise ValueError("the rows of gate, shift and scale must be equally far apart")
+    _check("sandwich_norm", lib().h3_sandwich_norm(
+        resid.data_ptr(), None if delta is None else delta.data_ptr(),
+        None if resid_out is None else resid_out.data_ptr(),
+        None if normed is None else normed.data_ptr(), int(post_norm),
+        _vec(post_gain, "post_gain", dev, D, None), _vec(gate, "gate", dev, D, groups),
+        resid_scale, _vec(pre_gain, "pre_gain", dev, D, None), _vec(shift, "shift", dev, D, groups),
+        _vec(scale, "scale", dev, D, groups), pseg, groups or 1, stride, int(rms), S,
+        S if L is None else L, D, eps, _raw_stream(stream, dev)))
+
+
+FP4_FORMATS = {"mx": 0, "nv": 1}
+
+
+class Fp4Rows:
+    """A matrix [R, K] of 4-bit rows: codes [R, K/2] uint8, scales (bytes, in the library's
+    tiles), row_scale [R] f32 ("nv") or None ("mx"). fp4_rows makes room for one."""
+    __slots__ = ("codes", "scales", "row_scale", "format", "R", "K", "device")
+
+    def __init__(self, codes, scales, row_scale, format):
+        if format not in FP4_FORMATS:
+            raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
+        dev = codes.get_device()
+        _flat(codes, "codes", torch.uint8, dev)
+        _flat(scales, "scales", torch.uint8, dev)
+        if codes.dim() != 2:
+            raise ValueError(f"codes must be [R, K/2], got {list(codes.shape)}")
+        self.R, self.K = codes.shape[0], codes.shape[1] * 2
+        need = fp4_scale_bytes(self.R, self.K, format)
+        if scales.numel() < need:
+            raise ValueError(f"scales have {scales.numel()} bytes, {need} are needed")
+        if (row_scale is not None) != (format == "nv"):
+            raise ValueError('row_scale belongs to format "nv", and only to it')
+        if row_scale is not None:
+            _flat(row_scale, "row_scale", torch.float32, dev)
+            if row_scale.shape != (self.R,):
+                raise ValueError(f"row_scale must be [{self.R}], got {list(row_scale.shape)}")
+        self.codes, self.scales, self.row_scale = codes, scales, row_scale
+        self.format, self.device = format, dev
+
+    def _pointers(self, dev, name):
+        if self.device != dev or dev < 0:
+            raise ValueError(f"{name} must be on the current CUDA device, is on device "
+                             f"{self.device}")
+        return (self.codes.data_ptr(), self.scales.data_ptr(),
+                None if self.row_scale is None else self.row_scale.data_ptr())
+
+
+def fp4_scale_bytes(R: int, K: int, format: str = "nv") -> int:
+    n = lib().h3_fp4_scale_bytes(R, K, FP4_FORMATS[format])
+    if n == 0:
+        raise H3Error("fp4_scale_bytes", 1, last_error())
+    return n
+
+
+def fp4_rows(R: int, K: int, format: str = "nv", device=None) -> Fp4Rows:
+    """Room for [R, K] 4-bit rows on a device (default: the current one): "nv" (16 values
+    share an E4M3 scale, a row an FP32 one) or "mx" (32 share a power of two)."""
+    if format not in FP4_FORMATS:
+        raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
+    device = torch.device("cuda") if device is None else device
+    n = fp4_scale_bytes(R, K, format)
+    return Fp4Rows(torch.empty(R, K // 2, dtype=torch.uint8, device=device),
+                   torch.empty(n, dtype=torch.uint8, device=device),
+                   torch.empty(R, dtype=torch.float32, device=device) if format == "nv" else None,
+                   format)
+
+
+def quantize_fp4_rows(x, out: Fp4Rows, L=None, stream=None):
+    """x [R, K] bf16 (rows may be strided) -> out, its first L rows."""
+    dev = _device()
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
+    if x.shape != (out.R, out.K) or x.stride(1) != 1:
+        raise ValueError(f"x must be {[out.R, out.K]} with neighbouring values, got "
+                         f"{list(x.shape)}")
+    _on(x, "x", dev)
+    L = out.R if L is None else L
+    if not 0 <= L <= out.R:
+        raise ValueError(f"L={L} exceeds the {out.R} rows")
+    _check("quantize_fp4_rows", lib().h3_quantize_fp4_rows(
+        x.data_ptr(), x.stride(0) if out.R > 1 else out.K, *out._pointers(dev, "out"), L, out.K,
+        FP4_FORMATS[out.format], _raw_stream(stream, dev)))
+
+
+def _fp4_product(name, x, w, y, N, L, stream):
+    dev = _device()
+    if x.format != w.format or x.K != w.K:
+        raise ValueError(f"x is {x.format!r} rows of {x.K}, the weights {w.format!r} of {w.K}")
+    if y.shape != (x.R, N):
+        raise ValueError(f"the output must be {[x.R, N]}, got {list(y.shape)}")
+    _flat(y, "the output", torch.bfloat16, dev)
+    _check(name, getattr(lib(), "h3_" + name)(
+        *x._pointers(dev, "x"), *w._pointers(dev, "the weights"), y.data_ptr(), x.R,
+        x.R if L is None else L, N, x.K, FP4_FORMATS[x.format], _raw_stream(stream, dev)))
+
+
+def linear_fp4(x: Fp4Rows, w: Fp4Rows, y, L=None, stream=None):
+    """y[:L] = x w^T of 4-bit rows x [S, K], w [N, K]; y [S, N] bf16."""
+    _fp4_product("linear_fp4", x, w, y, w.R, L, stream)
+
+
+def linear_swiglu_fp4(x: Fp4Rows, w_gu: Fp4Rows, out, L=None, stream=None):
+    """out[:L] = SiLU(x Wg^T) * (x Wu^T) of 4-bit rows x [S, K], w_gu [2F, K] (rows
+    [gate | up]); out [S, F] bf16."""
+    if w_gu.R % 2:
+        raise ValueError(f"the weights have {w_gu.R} rows, an odd number")
+    _fp4_product("linear_swiglu_fp4", x, w_gu, out, w_gu.R // 2, L, stream)
+
+
+QUERY_BLOCK = 256
+
+
+def block_scores_workspace_bytes(Lq: int, Lk: int, H: int, Hkv: int, k_block: int = 64) -> int:
+    n = lib().h3_block_scores_workspace_bytes(Lq, Lk, H, Hkv, k_block)
+    if n == 0:
+        raise H3Error("block_scores_workspace_bytes", 1, last_error())
+    return n
+
+
+def _block_shape(Lq, Lk, H, k_block):
+    if k_block not in (64, 128):
+        raise ValueError(f"k_block must be 64 or 128, got {k_block}")
+    return H, -(-Lq // QUERY_BLOCK), -(-Lk // k_block)
+
+
+def block_scores(q, k, scores, workspace, k_block=64, scale=None, stream=None):
+    """scores [H, nq, nk] f32 of every (block of QUERY_BLOCK query rows, block of k_block
+    keys): scale times the product of their mean rows. q [Lq,H,128], k [Lk,Hkv,128] bf16
+    (rows may be strided), workspace of block_scores_workspace_bytes."""
+    dev = _device()
+    Lq, Lk = q.shape[0], k.shape[0]
+    ldq, H = _heads(q, "q", Lq, dev)
+    ldk, Hkv = _heads(k, "k", Lk, dev)
+    if scores.shape != _block_shape(Lq, Lk, H, k_block):
+        raise ValueError(f"scores must be {list(_block_shape(Lq, Lk, H, k_block))}, got "
+                         f"{list(scores.shape)}")
+    _flat(scores, "scores", torch.float32, dev)
+    _on(workspace, "workspace", dev)
+    _check("block_scores", lib().h3_block_scores(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, scores.data_ptr(), Lq, Lk, H, Hkv, 128, k_block,
+        128 ** -0.5 if scale is None else scale, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
+
+
+def block_select(scores, ids, counts, keep_first=0, keep_last=0, stream=None):
+    """The best-scored blocks of every row of scores [..., nk] f32: ids [..., max_blocks]
+    int32 in ascending order (then -1), counts [...] int32. The first keep_first and the
+    last keep_last blocks are always among them; -inf and NaN never are otherwise."""
+    dev = _device()
+    nk, most = scores.shape[-1], ids.shape[-1]
+    if ids.shape[:-1] != scores.shape[:-1] or counts.shape != scores.shape[:-1]:
+        raise ValueError(f"scores [..., nk], ids [..., max_blocks] and counts [...] wanted, got "
+                         f"{list(scores.shape)}, {list(ids.shape)} and {list(counts.shape)}")
+    _flat(scores, "scores", torch.float32, dev)
+    _flat(ids, "ids", torch.int32, dev)
+    _flat(counts, "counts", torch.int32, dev)
+    _check("block_select", lib().h3_block_select(
+        scores.data_ptr(), ids.data_ptr(), counts.data_ptr(), counts.numel(), nk, most, keep_first,
+        keep_last, _raw_stream(stream, dev)))
+
+
+def attention_blocks(q, k, v, o, ids, counts, k_block=64, scale=None, stream=None):
+    """Attention of every block of QUERY_BLOCK query rows over its listed key blocks: ids
+    [H, nq, max_blocks], counts [H, nq] int32 (block_select's), q, o [Lq,H,128], k, v
+    [Lk,Hkv,128] bf16 (rows may be strided)."""
+    dev = _device()
+    Lq, Lk = q.shape[0], k.shape[0]
+    ldq, H = _heads(q, "q", Lq, dev)
+    ldk, Hkv = _heads(k, "k", Lk, dev)
+    ldv, hv = _heads(v, "v", Lk, dev)
+    ldo, ho = _heads(o, "o", Lq, dev)
+    if hv != Hkv or ho != H:
+        raise ValueError(f"q and o have {H} and {ho} heads, k and v {Hkv} and {hv}")
+    shape = _block_shape(Lq, Lk, H, k_block)[:2]
+    if counts.shape != shape or ids.shape[:2] != shape or ids.dim() != 3:
+        raise ValueError(f"ids must be {list(shape)} x max_blocks and counts {list(shape)}, got "
+                         f"{list(ids.shape)} and {list(counts.shape)}")
+    _flat(ids, "ids", torch.int32, dev)
+    _flat(counts, "counts", torch.int32, dev)
+    _check("attention_blocks", lib().h3_attention_blocks(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, o.data_ptr(), ldo,
+        ids.data_ptr(), counts.data_ptr(), ids.shape[2], Lq, Lk, H, Hkv, 128, k_block,
+        128 ** -0.5 if scale is None else scale, _raw_stream(stream, dev)))

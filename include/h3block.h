@@ -92,6 +92,36 @@ h3_status h3_mod_norm_residual(float* resid, const void* delta, const float* gat
                                int S, int L, int D, float eps, h3_stream_t stream);
 
 /*
+ * Norms before and after a branch (next step beside a1: blocks whose branches are
+ * normed on both sides), with the branch's gate and the scaled residual, one pass
+ * per row, all in FP32 between its loads and its stores:
+ *   p = delta[i,:], or n(delta[i,:]) * post_gain[:] with post_norm != 0
+ *   r = resid_scale * resid[i,:] + gate[:] * p      -> resid_out[i,:]
+ *   normed[i,:] <- bf16( n(r) * pre_gain[:] * (1 + scale[:]) + shift[:] )
+ * where n(x) is LayerNorm without affine (rms == 0) or x / sqrt(mean(x^2) + eps)
+ * (rms != 0). A vector that is NULL is left out of its formula (a gain of 1, a gate
+ * of 1, a scale or shift of 0).
+ *   resid      [S, D] float32
+ *   delta      [S, D] bf16, or NULL (then r = resid_scale * resid and post_norm is 0)
+ *   resid_out  [S, D] float32, may be resid itself; NULL: r is not stored (without
+ *              delta, where resid_scale is 1)
+ *   normed     [S, D] bf16, or NULL: only the residual (then delta or another
+ *              resid_scale than 1 is given)
+ *   post_gain, pre_gain [D] float32
+ *   gate, shift, scale  [D] float32; with seg, row i takes them from group seg[i] of
+ *              tables whose groups are seg_stride floats apart, as
+ *              h3_mod_norm_residual_seg
+ * resid_out and normed overlap no input (but resid_out may be resid) and not each other.
+ * D % 8 == 0, D <= 8192. Rows >= L of every tensor are left alone.
+ */
+h3_status h3_sandwich_norm(const float* resid, const void* delta, float* resid_out, void* normed,
+                           int post_norm, const float* post_gain, const float* gate,
+                           float resid_scale, const float* pre_gain, const float* shift,
+                           const float* scale, const int32_t* seg, int num_seg,
+                           int64_t seg_stride, int rms, int S, int L, int D, float eps,
+                           h3_stream_t stream);
+
+/*
  * a2 — per-head Q/K RMSNorm followed by rotary position embedding, in place
  * (blog section 3.2, #5990; RoPE rows from per-token positions, section 3.1).
  * For every valid row i, head h and x in {q, k} (gain g_q / g_k):
@@ -213,6 +243,59 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
                                 const float* sk, const float* sv, void* o, int S, int L, int H,
                                 int Dh, float softmax_scale, float skip_eps, int32_t* kept_tiles,
                                 h3_stream_t stream);
+
+/*
+ * Attention over chosen key blocks (next step beside Skip-Softmax: block-sparse video
+ * attention, a coarse score of pooled blocks choosing the fine blocks of every query
+ * block). Query rows are taken in blocks of H3_QUERY_BLOCK rows from row 0, keys in blocks
+ * of k_block (64 or 128) rows from row 0; the last block of each may be short. With
+ * nq = ceil(Lq / H3_QUERY_BLOCK) and nk = ceil(Lk / k_block):
+ *
+ * h3_block_scores: scores[h, t, b] = softmax_scale * mean(q rows of block t, head h)
+ *   . mean(k rows of block b, head h / (H / Hkv)), means and products in FP32.
+ *   q       [Lq, H, Dh] bf16, row stride ld_q elements; k [Lk, Hkv, Dh], ld_k
+ *   scores  [H, nq, nk] float32
+ *   workspace  device memory of h3_block_scores_workspace_bytes(...) bytes, 256-byte
+ *           aligned, overwritten; calls that may overlap on the GPU need one each
+ *
+ * h3_block_select: the list of every row of scores [rows, nk] (rows = H * nq): the first
+ *   keep_first and the last keep_last blocks, whatever their scores are, and then those
+ *   with the largest scores, max_blocks in all at most. Equal scores go to the lower
+ *   index; a score of -inf or NaN is not selected. ids [rows, max_blocks] int32 receives
+ *   them in ascending order, then -1; counts [rows] int32 their number (0 where a row has
+ *   nothing to select). Scores of -inf written between the two calls mask blocks out.
+ *   keep_first + keep_last at most max_blocks.
+ *
+ * h3_attention_blocks: for i < Lq, t = i / H3_QUERY_BLOCK, and every head h
+ *   o[i,h,:] = sum_j softmax_j(q[i,h,:] . k[j,g,:] * softmax_scale) v[j,g,:],
+ *   g = h / (H / Hkv), over the keys j < Lk of the first counts[h, t] blocks listed in
+ *   ids[h, t, :]. A block listed twice counts twice; an id outside [0, nk) is left out (a
+ *   count is taken as at least 0 and at most max_blocks), so what the lists hold, which is
+ *   read when the call runs, never leads outside the tensors. A query block without a key
+ *   gives zeros; a row with a score of NaN or +inf, or whose scores are all -inf, gives NaN.
+ *   q, o    [Lq, H, Dh] bf16, row strides ld_q, ld_o; k, v [Lk, Hkv, Dh], ld_k, ld_v
+ *           (multiples of 8; q, k and v may be columns of one buffer). o overlaps nothing.
+ *   ids     [H, nq, max_blocks] int32; counts [H, nq] int32
+ * bf16 tensor-core products, FP32 softmax and accumulation, weights rounded to bf16 before
+ * their product (2^-8 of the sum of weight times |v|), bf16 out.
+ *
+ * Dh == 128, H a multiple of Hkv, at most 65,535. A call with Lq or Lk 0: no scores and
+ * nothing done; h3_attention_blocks with Lk 0 writes zeros. max_blocks >= 1, rows * max_blocks
+ * and rows * nk below 2^31 (rows = H * nq), nq and nk at most 2^20.
+ */
+#define H3_QUERY_BLOCK 256
+size_t h3_block_scores_workspace_bytes(int Lq, int Lk, int H, int Hkv, int k_block);
+h3_status h3_block_scores(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                          float* scores, int Lq, int Lk, int H, int Hkv, int Dh, int k_block,
+                          float softmax_scale, void* workspace, size_t workspace_bytes,
+                          h3_stream_t stream);
+h3_status h3_block_select(const float* scores, int32_t* ids, int32_t* counts, int rows, int nk,
+                          int max_blocks, int keep_first, int keep_last, h3_stream_t stream);
+h3_status h3_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                              const void* v, int64_t ld_v, void* o, int64_t ld_o,
+                              const int32_t* ids, const int32_t* counts, int max_blocks, int Lq,
+                              int Lk, int H, int Hkv, int Dh, int k_block, float softmax_scale,
+                              h3_stream_t stream);
 
 /*
  * Paged key/value cache. The block reads keys and values of its own rows only
@@ -534,6 +617,62 @@ h3_status h3_linear_fp8(const void* qx, const float* sx, const void* qw, const f
  * are scaled and rounded to bf16 before the SiLU. F % 128 == 0, K % 128 == 0. */
 h3_status h3_linear_swiglu_fp8(const void* qx, const float* sx, const void* qw_gu,
                                const float* sw_gu, void* out, int S, int L, int F, int K,
+                               h3_stream_t stream);
+
+/*
+ * 4-bit projections (next step after FP8; microscaled E2M1 weights and activations, the
+ * base product of 4-bit checkpoints). A matrix [R, K] is held as
+ *   codes   [R, K / 2] bytes: value k of a row in the low (k even) or high half of byte
+ *           k / 2, bit 3 the sign, 0..7 of the rest 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales  one byte for every block of values of a row, in tiles of 128 rows and 4
+ *           blocks: the scale of row r and block b is byte
+ *           ((r / 128) * ceil(nb / 4) + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4
+ *           where a row has nb blocks; h3_fp4_scale_bytes(R, K, format) bytes
+ * in one of two formats:
+ *   H3_FP4_MX  blocks of 32 values, the scale a power of two 2^(byte - 127) (255: NaN);
+ *              value = code * scale. row_scale is NULL.
+ *   H3_FP4_NV  blocks of 16 values, the scale an E4M3 number (>= 0), and a float32 scale
+ *              of the row, row_scale [R]; value = code * scale * row_scale. (One scale for
+ *              all of a matrix is the same number in every row.)
+ *
+ * h3_quantize_fp4_rows: x [R, K] bf16, rows ld_x elements apart, into that form. amax is the
+ * largest magnitude of a block, ties of every rounding go to the even code, values beyond
+ * 6 become 6:
+ *   MX  e = max(floor(log2(amax)) - 2, -127) (-127 for a block of zeros), code = E2M1(x * 2^-e)
+ *   NV  with amax_row the largest finite magnitude of the row's blocks that are all finite,
+ *       each step rounded in float32: row_scale = amax_row / 2688,
+ *       scale = E4M3(amax * (448 / amax_row)), code = E2M1(x * ((2688 / amax_row) / scale));
+ *       a row with amax_row below 2^-100 has scales and row_scale 0, and a scale of 0 has
+ *       codes of 0
+ * A block with a NaN or an infinity gets a scale of NaN (and codes of 0), so that it shows in
+ * every product it takes part in. Scale bytes of rows below R beyond a row's blocks, up to a
+ * multiple of 4, are written as 0; those of rows >= R are left as they were.
+ *   K % 32 == 0, K <= 16384, ld_x a multiple of 8; x and codes 16-byte, scales 128-byte
+ *   aligned, none overlapping.
+ */
+typedef enum h3_fp4_format { H3_FP4_MX = 0, H3_FP4_NV = 1 } h3_fp4_format;
+size_t h3_fp4_scale_bytes(int R, int K, int format);
+h3_status h3_quantize_fp4_rows(const void* x, int64_t ld_x, void* codes, void* scales,
+                               float* row_scale, int R, int K, int format, h3_stream_t stream);
+
+/*
+ * y[i, j] = bf16( rx[i] * rw[j] * sum over K of value(x)[i,:] * value(w)[j,:] / (rx[i] * rw[j]) )
+ * for i < L: a projection of 4-bit rows on tcgen05 (block-scaled products, FP32
+ * accumulation); rx and rw are the row scales (1 in H3_FP4_MX, where they are NULL).
+ *   x_codes [S, K / 2], x_scales, rx [S]; w_codes [N, K / 2], w_scales, rw [N]; y [S, N] bf16
+ *   K % 32 == 0, N % 8 == 0; both operands in the same format; codes and y 16-byte,
+ *   scales 128-byte aligned; y overlaps nothing.
+ */
+h3_status h3_linear_fp4(const void* x_codes, const void* x_scales, const float* rx,
+                        const void* w_codes, const void* w_scales, const float* rw, void* y,
+                        int S, int L, int N, int K, int format, h3_stream_t stream);
+
+/* 4-bit gate/up projection with SwiGLU in the epilogue: as h3_linear_swiglu with 4-bit
+ * operands (w_gu [2F, K], rows [gate | up]); the two products are scaled and rounded to bf16
+ * before the SiLU. F % 128 == 0, K % 32 == 0. */
+h3_status h3_linear_swiglu_fp4(const void* x_codes, const void* x_scales, const float* rx,
+                               const void* w_codes, const void* w_scales, const float* rw,
+                               void* out, int S, int L, int F, int K, int format,
                                h3_stream_t stream);
 
 /* Block weights with FP8 projections (codes from h3_quantize_fp8_rows). */
