@@ -169,6 +169,23 @@ static h3_status make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void
   return H3_OK;
 }
 
+h3_status make_tmap_u32_rows(CUtensorMap* m, const void* base, uint32_t inner, uint64_t outer,
+                             uint32_t box_outer) {
+  h3_status st = load_encode();
+  if (st != H3_OK) return st;
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {inner * 4ull};
+  const cuuint32_t box[2] = {inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(H3_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %u x %llu words",
+                static_cast<int>(r), inner, static_cast<unsigned long long>(outer));
+  return H3_OK;
+}
+
 h3_status make_tmap_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1,
                             uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1,
                             uint32_t b2) {
@@ -1233,7 +1250,8 @@ static h3_status fp4_product(const Fp4Operand& x, const Fp4Operand& w, void* y, 
              "codes, y and the weights' row scales must be 16-byte, scales 128-byte aligned");
   H3_REQUIRE(y != x.codes && y != w.codes, H3_ERR_INVALID_ARG, "y overlaps an operand");
   const int64_t tiles = ((static_cast<int64_t>(L) + 255) / 256) * ((static_cast<int64_t>(N) + 127) / 128);
-  H3_REQUIRE(tiles < (int64_t{1} << 30), H3_ERR_UNSUPPORTED, "L=%d x N=%d is too large", L, N);
+  H3_REQUIRE(tiles * ((K + 255) / 256) < (int64_t{1} << 31), H3_ERR_UNSUPPORTED,
+             "L=%d x N=%d x K=%d is too large", L, N, K);
   if (L == 0) return H3_OK;
   return launch_gemm_fp4(x, w, y, L, N, K, nv, swiglu, reinterpret_cast<cudaStream_t>(stream));
 }

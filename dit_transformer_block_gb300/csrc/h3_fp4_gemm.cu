@@ -34,23 +34,31 @@ constexpr int OP_BYTES = ROWS * STAGE_CODES / 2;  // 16 KB
 constexpr int SFA_BYTES = 2048, SFB_BYTES = 2 * 2048;
 constexpr int STAGE4_BYTES = 2 * OP_BYTES + SFA_BYTES + SFB_BYTES;
 constexpr int STAGES4 = 5;
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS4 = 64 + EPI_WARPS * 32;
+constexpr int EPI_WARPS = 8, COPY_WARPS = 2;
+constexpr int THREADS4 = (2 + EPI_WARPS + COPY_WARPS) * 32;
 constexpr int GROUP_M4 = 16;                 // raster: 16 x 256 rows per sweep of the columns
 constexpr size_t SMEM4_BYTES = 1024 + STAGES4 * STAGE4_BYTES + 256;
 static_assert(SMEM4_BYTES <= 227 * 1024, "fp4 gemm shared memory");
 
-// tensor-memory columns
-constexpr uint32_t T4_ACC1 = 160, T4_SF = 416, T4_SF_COLS = 48, T4_SFB = 16;
-constexpr int SHARED_CHUNKS = 3;             // 32-column chunks the accumulators share
+// Tensor memory: accumulators of 256 columns at 0 and ACC1, sharing SHARED chunks of 32,
+// then SF_BUFS buffers of a stage's scales: SFB columns into one A's, then B's.
+template <bool NV>
+struct Tmem4 {
+  static constexpr int SF_BUFS = NV ? 3 : 4;
+  static constexpr uint32_t SFB = NV ? 16 : 8, SF_COLS = 3 * SFB;
+  static constexpr int SHARED = NV ? 5 : 3;
+  static constexpr uint32_t ACC1 = 256 - 32 * SHARED, SF = ACC1 + 256;
+  static_assert(SF + SF_BUFS * SF_COLS <= 512, "tensor memory");
+};
 
 enum Bar4 {
-  B4_FULL = 0,
-  B4_EMPTY = B4_FULL + STAGES4,
-  B4_TFULL = B4_EMPTY + STAGES4,  // accumulator written [2]
-  B4_SHARED = B4_TFULL + 2,       // shared columns read (16 warps)
-  B4_DRAIN = B4_SHARED + 1,
-  B4_NUM = B4_DRAIN + 1
+  B4_FULL = 0,                    // stage landed in both CTAs (even CTA)
+  B4_EMPTY = B4_FULL + STAGES4,   // stage read by the products
+  B4_SF = B4_EMPTY + STAGES4,     // stage's scales in tensor memory (even CTA) [4]
+  B4_TFULL = B4_SF + 4,           // accumulator written [2]
+  B4_SHARED = B4_TFULL + 2,       // shared columns read (16 warps, even CTA)
+  B4_DRAIN = B4_SHARED + 1,       // [1 + COPY_WARPS]
+  B4_NUM = B4_DRAIN + 1 + COPY_WARPS
 };
 static_assert(B4_NUM * 8 + 8 <= 256, "barrier region");
 
@@ -96,27 +104,25 @@ __device__ __forceinline__ void mma_fp4_pair_el(uint32_t d, uint64_t a, uint64_t
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
-// Untiled copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+// 2D tiled load into this CTA's shared memory, counted on a barrier of either CTA of the
+// pair (its shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m,
+                                                 uint32_t cluster_bar, int32_t x, int32_t y) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
 
 struct Gemm4Args {
   __nv_bfloat16* C;
-  const uint8_t* sfa;
-  const uint8_t* sfb;
   const float* ra;  // row scales (NV)
   const float* rb;
   int M, N, K;
   int num_m, num_n, num_k;  // tiles of 256 rows, of columns, stages
   int num_tiles;
   int sf_tiles;             // scale tiles along K
-  int a_blocks, b_blocks;   // scale tiles along the rows
   int up_rows;              // SwiGLU: first row of the up half of B
   DevErr err;
 };
@@ -136,8 +142,13 @@ __device__ __forceinline__ float silu_f(float g) { return g / (1.0f + __expf(-g)
 template <bool NV, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                     const Gemm4Args a) {
+  using TM = Tmem4<NV>;
   constexpr int ATOM_STEPS = NV ? 1 : 2;  // products that a scale tile serves
+  constexpr int ATOMS = 4 / ATOM_STEPS;   // scale tiles of a stage and 128 rows
+  // bytes of a stage in one CTA
+  constexpr uint32_t LOADED = 2 * OP_BYTES + 3 * ATOMS * 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -154,13 +165,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < B4_NUM; ++i) {
       uint32_t count = 1;
-      if (i < B4_EMPTY) count = leader ? 2 : 1;  // with the odd CTA's relay
       if (i == B4_SHARED) count = 2 * EPI_WARPS;
       mbar_init(bar(i), count);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -171,15 +183,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // products and scale tiles of stage kb
-  auto steps_of = [&](int kb) { return min(4, (a.K - kb * STAGE_CODES + 63) / 64); };
-  auto atoms_of = [&](int kb) { return (steps_of(kb) + ATOM_STEPS - 1) / ATOM_STEPS; };
+  // stages of this pair, over all of its tiles
+  const int total = (a.num_tiles - pair + pairs - 1) / pairs * a.num_k;
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int issued = 0;
+      int issued = 0, st = 0;
+      uint32_t phase = 1;
       bool ok = true;
+      const uint32_t full0 = mapa_shared(bar(B4_FULL), 0);  // the even CTA's
       for (int tile = pair; tile < a.num_tiles && ok; tile += pairs) {
         int mb, nb;
         tile_coords4(tile, a, mb, nb);
@@ -188,109 +201,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
         const int b_blk0 = SWIGLU ? nb : 2 * nb;
         const int b_blk1 = SWIGLU ? a.up_rows / ROWS + nb : 2 * nb + 1;
         const int b_row = (leader ? b_blk0 : b_blk1) * ROWS;
-        const bool a_in = a_blk < a.a_blocks, b1_in = b_blk1 < a.b_blocks;
+        // (blocks past the operands' rows, and a row's scales past its end, which no product
+        // uses, come from wherever they lie in the scales, or as zeros from past their end)
+        int sa = a_blk * a.sf_tiles, sb0 = b_blk0 * a.sf_tiles, sb1 = b_blk1 * a.sf_tiles;
         for (int kb = 0; kb < a.num_k; ++kb) {
-          const int st = issued % STAGES4;
-          if (!mbar_wait(bar(B4_EMPTY + st), (static_cast<uint32_t>(issued / STAGES4) & 1u) ^ 1u,
-                         a.err, ERR_WAIT_GEMM_PRODUCER)) {
+          if (!mbar_wait(bar(B4_EMPTY + st), phase, a.err, ERR_WAIT_GEMM_PRODUCER)) {
             ok = false;
             break;
           }
-          const uint32_t full = bar(B4_FULL + st);
+          const uint32_t full = full0 + st * 8;
           const uint32_t dst = smem_u32(smem + st * STAGE4_BYTES);
-          const uint32_t sf = static_cast<uint32_t>(atoms_of(kb)) * 512u;
-          mbar_arrive_expect_tx(full, 2 * OP_BYTES + sf * (1u + (a_in ? 1u : 0u) + (b1_in ? 1u : 0u)));
+          if (leader) mbar_arrive_expect_tx(bar(B4_FULL + st), 2 * LOADED);
           const int kx = kb * (STAGE_CODES / 2);
-          tma_load_2d(dst, &tmA, full, kx, a_blk * ROWS);
-          tma_load_2d(dst + OP_BYTES, &tmB, full, kx, b_row);
-          const int64_t k_tile = static_cast<int64_t>(kb) * (4 / ATOM_STEPS);
-          const uint32_t sfa = dst + 2 * OP_BYTES, sfb = sfa + SFA_BYTES;
-          if (a_in)
-            bulk_load(sfa, a.sfa + (static_cast<int64_t>(a_blk) * a.sf_tiles + k_tile) * 512, sf, full);
-          bulk_load(sfb, a.sfb + (static_cast<int64_t>(b_blk0) * a.sf_tiles + k_tile) * 512, sf, full);
-          if (b1_in)
-            bulk_load(sfb + 2048, a.sfb + (static_cast<int64_t>(b_blk1) * a.sf_tiles + k_tile) * 512,
-                      sf, full);
+          tma_load_2d_pair(dst, &tmA, full, kx, a_blk * ROWS);
+          tma_load_2d_pair(dst + OP_BYTES, &tmB, full, kx, b_row);
+          tma_load_2d_pair(dst + 2 * OP_BYTES, &tmSA, full, 0, sa);
+          tma_load_2d_pair(dst + 2 * OP_BYTES + SFA_BYTES, &tmSB, full, 0, sb0);
+          tma_load_2d_pair(dst + 2 * OP_BYTES + SFA_BYTES + 2048, &tmSB, full, 0, sb1);
+          sa += ATOMS, sb0 += ATOMS, sb1 += ATOMS;
           ++issued;
+          if (++st == STAGES4) {
+            st = 0;
+            phase ^= 1u;
+          }
         }
       }
-      // no copy of this CTA may still be landing when it exits
-      const uint64_t t0 = globaltimer_ns();
-      for (int i = issued > STAGES4 ? issued - STAGES4 : 0; i < issued; ++i)
-        mbar_wait_drain(bar(B4_FULL + i % STAGES4), static_cast<uint32_t>(i / STAGES4) & 1u, t0,
-                        drain_limit_ns(a.err));
+      // No copy may still be landing when a CTA exits. The even CTA's barriers count those of
+      // both, and neither leaves before the other; where a wait ran out they may never
+      // complete, and the time of this wait is what the copies have to land.
+      if (leader) {
+        const uint64_t t0 = globaltimer_ns();
+        for (int i = issued > STAGES4 ? issued - STAGES4 : 0; i < issued; ++i)
+          mbar_wait_drain(bar(B4_FULL + i % STAGES4), static_cast<uint32_t>(i / STAGES4) & 1u, t0,
+                          drain_limit_ns(a.err));
+      } else if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
     }
   } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer
     if (leader) {
-      // ------------------------------------------------------ MMA issuer
       constexpr uint32_t idesc0 = idesc_e2m1(2 * ROWS, BN4, !NV, 0);
       constexpr uint32_t idesc2 = idesc_e2m1(2 * ROWS, BN4, !NV, 2);
       constexpr uint16_t kBoth = 3;
-      const uint64_t da = sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t ds = sdesc_rows16(smem_u32(smem) + 2 * OP_BYTES);
-      auto wait = [&](int b, uint32_t parity) {
-        return mbar_wait_warp(bar(b), parity, a.err, ERR_WAIT_GEMM_MMA);
+      const uint64_t da0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        return mbar_wait_warp(b, parity, a.err, ERR_WAIT_GEMM_MMA);
       };
-      int it = 0;    // stages so far
-      int done = 0;  // tiles so far
+      int st = 0, buf = 0, done = 0;
+      uint32_t phase = 0, sf_phase = 0;
       bool ok = true;
       for (int tile = pair; tile < a.num_tiles && ok; tile += pairs, ++done) {
         // the columns this accumulator shares with the tile before are read
-        if (done > 0 && !wait(B4_SHARED, static_cast<uint32_t>(done - 1) & 1u)) break;
+        if (done > 0 && !wait(bar(B4_SHARED), static_cast<uint32_t>(done - 1) & 1u)) break;
         tc_fence_after();
-        const uint32_t d = tmem + (done & 1 ? T4_ACC1 : 0u);
-        for (int kb = 0; kb < a.num_k; ++kb, ++it) {
-          const int st = it % STAGES4;
-          if (!wait(B4_FULL + st, static_cast<uint32_t>(it / STAGES4) & 1u) ||
-              (it >= 2 &&
-               !wait(B4_EMPTY + (it - 2) % STAGES4, static_cast<uint32_t>((it - 2) / STAGES4) & 1u))) {
+        const uint32_t d = tmem + (done & 1 ? TM::ACC1 : 0u);
+        for (int kb = 0; kb < a.num_k; ++kb) {
+          if (!wait(bar(B4_FULL) + st * 8, phase) || !wait(bar(B4_SF) + buf * 8, sf_phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t off = static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
-          const uint32_t sf = tmem + T4_SF + static_cast<uint32_t>(it & 1) * T4_SF_COLS;
-          const int steps = steps_of(kb), atoms = atoms_of(kb);
-#pragma unroll
-          for (int t = 0; t < 4 / ATOM_STEPS; ++t) {
-            if (t < atoms) {
-              const uint64_t s = ds + off + static_cast<uint32_t>(t * (512 >> 4));
-              scale_copy_pair_el(sf + t * 4, s);
-              scale_copy_pair_el(sf + T4_SFB + t * 8, s + (SFA_BYTES >> 4));
-              scale_copy_pair_el(sf + T4_SFB + t * 8 + 4, s + ((SFA_BYTES + 2048) >> 4));
-            }
-          }
+          const uint64_t ad = da0 + static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
+          const uint64_t bd = ad + (OP_BYTES >> 4);
+          const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(buf) * TM::SF_COLS;
+          const int steps = (a.K - kb * STAGE_CODES + 63) / 64;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (k < steps) {
-              const uint64_t ad = da + off + static_cast<uint32_t>(k * 2);
-              mma_fp4_pair_el<NV>(d, ad, ad + (OP_BYTES >> 4),
-                                  (!NV && (k & 1)) ? idesc2 : idesc0, sf + (k / ATOM_STEPS) * 4,
-                                  sf + T4_SFB + (k / ATOM_STEPS) * 8, (kb | k) != 0 ? 1u : 0u);
-            }
+            if (k == 0 || k < steps)
+              mma_fp4_pair_el<NV>(d, ad + k * 2, bd + k * 2, (!NV && (k & 1)) ? idesc2 : idesc0,
+                                  sf + (k / ATOM_STEPS) * 4, sf + TM::SFB + (k / ATOM_STEPS) * 8,
+                                  (kb | k) != 0 ? 1u : 0u);
           }
-          mma_commit_pair_mc_el(bar(B4_EMPTY + st), kBoth);
+          mma_commit_pair_mc_el(bar(B4_EMPTY) + st * 8, kBoth);
+          if (++st == STAGES4) {
+            st = 0;
+            phase ^= 1u;
+          }
+          if (++buf == TM::SF_BUFS) {
+            buf = 0;
+            sf_phase ^= 1u;
+          }
         }
         if (!ok) break;
-        mma_commit_pair_mc_el(bar(B4_TFULL + (done & 1)), kBoth);
+        mma_commit_pair_mc_el(bar(B4_TFULL) + (done & 1) * 8, kBoth);
       }
       // every product must be done with both CTAs' memories before either frees them
       mma_commit_pair_mc_el(bar(B4_DRAIN), 1);
       mbar_wait_drain(bar(B4_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(a.err));
-    } else if (lane == 0) {
-      // ------------------------------------------------------------ relay
-      int it = 0;
-      bool ok = true;
-      for (int tile = pair; tile < a.num_tiles && ok; tile += pairs)
-        for (int kb = 0; kb < a.num_k; ++kb, ++it) {
-          const int st = it % STAGES4;
-          if (!mbar_wait(bar(B4_FULL + st), static_cast<uint32_t>(it / STAGES4) & 1u, a.err,
-                         ERR_WAIT_GEMM_PRODUCER)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_remote(mapa_shared(bar(B4_FULL + st), 0));
+    }
+  } else if (warp >= 2 + EPI_WARPS) {
+    // ------------------------------------------------------ scale copies
+    // two warps, a stage each in turn: issuing a stage's copies takes longer than its products
+    if (leader) {
+      const int c = warp - 2 - EPI_WARPS;
+      const uint64_t ds0 = sdesc_rows16(smem_u32(smem) + 2 * OP_BYTES);
+      auto wait = [&](int b, uint32_t parity) {
+        return mbar_wait_warp(bar(b), parity, a.err, ERR_WAIT_GEMM_MMA);
+      };
+      for (int it = c; it < total; it += COPY_WARPS) {
+        const int st = it % STAGES4, buf = it % TM::SF_BUFS, old = it - TM::SF_BUFS;
+        // the products that read this buffer last
+        if (old >= 0 &&
+            !wait(B4_EMPTY + old % STAGES4, static_cast<uint32_t>(old / STAGES4) & 1u))
+          break;
+        if (!wait(B4_FULL + st, static_cast<uint32_t>(it / STAGES4) & 1u)) break;
+        tc_fence_after();
+        const uint64_t s = ds0 + static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
+        const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(buf) * TM::SF_COLS;
+#pragma unroll
+        for (int t = 0; t < ATOMS; ++t) {
+          scale_copy_pair_el(sf + t * 4, s + t * (512 >> 4));
+          scale_copy_pair_el(sf + TM::SFB + t * 8, s + ((SFA_BYTES + t * 512) >> 4));
+          scale_copy_pair_el(sf + TM::SFB + t * 8 + 4, s + ((SFA_BYTES + 2048 + t * 512) >> 4));
         }
+        mma_commit_pair_mc_el(bar(B4_SF + buf), 1);
+      }
+      mma_commit_pair_mc_el(bar(B4_DRAIN + 1 + c), 1);
+      mbar_wait_drain(bar(B4_DRAIN + 1 + c), 0u, globaltimer_ns(), drain_limit_ns(a.err));
     }
   } else {
     // ------------------------------------------------------ epilogue warps
@@ -307,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
       tc_fence_after();
       const int row = (2 * mb + static_cast<int>(rank)) * ROWS + quarter * 32 + lane;
       const bool row_ok = row < a.M;
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (acc ? T4_ACC1 : 0u);
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (acc ? TM::ACC1 : 0u);
       const float ra = NV ? (row_ok ? __ldg(a.ra + row) : 0.f) : 1.f;
       __nv_bfloat16* crow = a.C + static_cast<int64_t>(row_ok ? row : 0) * a.N;
       auto tell = [&]() {  // the shared columns are in registers
@@ -321,7 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
         }
       };
       if constexpr (SWIGLU) {
-        // four pairs of chunks, those with shared columns first; two per warp
+        // four pairs of chunks, two per warp. Of the shared columns each of them has some (NV),
+        // or, in order, the first three (MX)
 #pragma unroll 1
         for (int i = side; i < 4; i += 2) {
           const int c = acc ? i : (i + 1) & 3;
@@ -331,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
           tmem_ld_wait();
           tmem_reg_fence(g);
           tmem_reg_fence(u);
-          if (i == (side == 0 ? 2 : 1)) tell();  // the last of its first three
+          if (i == (side == 0 || TM::SHARED > 3 ? side + 2 : side)) tell();
           const int col = nb * (BN4 / 2) + c * 32;
           if (!row_ok) continue;
           if constexpr (NV) {
@@ -365,12 +396,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
       } else {
 #pragma unroll 1
         for (int i = side; i < 8; i += 2) {
-          const int c = acc ? i : (i + 8 - SHARED_CHUNKS) & 7;
+          const int c = acc ? i : (i + 8 - TM::SHARED) & 7;  // the shared chunks first
           uint32_t v[32];
           tmem_ld32(t_row + c * 32, v);
           tmem_ld_wait();
           tmem_reg_fence(v);
-          if (i == (side == 0 ? 2 : 1)) tell();
+          if (i == (TM::SHARED - 1 - side) / 2 * 2 + side) tell();  // its last shared chunk
           const int col = nb * BN4 + c * 32;
           if (!row_ok) continue;
 #pragma unroll
@@ -416,8 +447,6 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   const int tile_n = SWIGLU ? BN4 / 2 : BN4;
   Gemm4Args a{};
   a.C = static_cast<__nv_bfloat16*>(C);
-  a.sfa = static_cast<const uint8_t*>(A.scales);
-  a.sfb = static_cast<const uint8_t*>(B.scales);
   a.ra = A.row_scale;
   a.rb = B.row_scale;
   a.M = L;
@@ -428,17 +457,21 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   a.num_k = (K + STAGE_CODES - 1) / STAGE_CODES;
   a.num_tiles = a.num_m * a.num_n;
   a.sf_tiles = fp4_tiles(K, NV);
-  a.a_blocks = (L + ROWS - 1) / ROWS;
-  a.b_blocks = (b_rows + ROWS - 1) / ROWS;
   a.up_rows = SWIGLU ? N : 0;
   if ((st = dev_err(&a.err)) != H3_OK) return st;
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmSA, tmSB;
   const uint64_t row_bytes = static_cast<uint64_t>(K) / 2;
   if ((st = make_tmap_u8_2d(&tmA, A.codes, row_bytes, L, row_bytes, 128, ROWS)) != H3_OK) return st;
   if ((st = make_tmap_u8_2d(&tmB, B.codes, row_bytes, b_rows, row_bytes, 128, ROWS)) != H3_OK)
     return st;
+  // scales: rows of a tile each, a stage's at a time
+  const uint64_t ta = static_cast<uint64_t>((L + ROWS - 1) / ROWS) * a.sf_tiles;
+  const uint64_t tb = static_cast<uint64_t>((b_rows + ROWS - 1) / ROWS) * a.sf_tiles;
+  constexpr uint32_t atoms = NV ? 4 : 2;
+  if ((st = make_tmap_u32_rows(&tmSA, A.scales, 128, ta, atoms)) != H3_OK) return st;
+  if ((st = make_tmap_u32_rows(&tmSB, B.scales, 128, tb, atoms)) != H3_OK) return st;
   const int grid = 2 * std::min(a.num_tiles, num_sms() / 2);
-  gemm_fp4_kernel<NV, SWIGLU><<<grid, THREADS4, SMEM4_BYTES, s>>>(tmA, tmB, a);
+  gemm_fp4_kernel<NV, SWIGLU><<<grid, THREADS4, SMEM4_BYTES, s>>>(tmA, tmB, tmSA, tmSB, a);
   return cuda_fail(cudaGetLastError(), "fp4 gemm launch");
 }
 
