@@ -8,15 +8,15 @@
 // 128 cycles, three quarters of what it can; as a pair it is 8 KB.
 //   * stage: 256 values of K (128 bytes per row, 128-byte swizzle) of both operands and
 //     their scales, which lie in memory as the tensor cores want them (tiles of 128 rows x
-//     4 scales, 512 bytes), so a stage's are one contiguous copy per 128 rows;
-//   * warp 0: TMA producer (one lane); warp 1 of the even CTA: issues, per stage, the
-//     copies of the scales from shared to tensor memory (both CTAs' at once) and four
-//     products of K = 64; of the odd CTA: tells the even one when its stage has landed;
-//     warps 2-9: epilogue, two per lane quarter;
-//   * tensor memory: the scales of two stages (2 x 48 columns) leave 416 columns for two
-//     accumulators of 256, so they share 96: a tile's epilogue reads the shared columns
-//     first, and the next tile's products start when they are read. A buffer of scales
-//     is written again when the products of the stage before last are done.
+//     4 scales, 512 bytes);
+//   * warp 0 of each CTA: TMA producer (one lane), counted on the even CTA's barriers; of the
+//     even CTA, warp 1 issues four products of K = 64 per stage, and two warps the copies of
+//     a stage's scales from shared to tensor memory (both CTAs' at once) in turn: twelve (NV)
+//     or six (MX) copies take longer to issue than the products to run;
+//   * warps 2-9: epilogue, two per lane quarter. A warp reads its 128 columns of the
+//     accumulator at once, so that the next tile's products wait for one read and not for
+//     the stores, then writes bf16 through 4 KB of shared memory of its own with TMA;
+//   * tensor memory: 256 columns of accumulator, a buffer of scales per stage.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -37,27 +37,24 @@ constexpr int STAGES4 = 5;
 constexpr int EPI_WARPS = 8, COPY_WARPS = 2;
 constexpr int THREADS4 = (2 + EPI_WARPS + COPY_WARPS) * 32;
 constexpr int GROUP_M4 = 16;                 // raster: 16 x 256 rows per sweep of the columns
-constexpr size_t SMEM4_BYTES = 1024 + STAGES4 * STAGE4_BYTES + 256;
+constexpr int OUT_BYTES = 32 * 128;          // a warp's 32 rows x 64 columns of output
+constexpr size_t SMEM4_BYTES = 1024 + STAGES4 * STAGE4_BYTES + EPI_WARPS * OUT_BYTES + 256;
 static_assert(SMEM4_BYTES <= 227 * 1024, "fp4 gemm shared memory");
 
-// Tensor memory: accumulators of 256 columns at 0 and ACC1, sharing SHARED chunks of 32,
-// then SF_BUFS buffers of a stage's scales: SFB columns into one A's, then B's.
+// Tensor memory: the accumulator, then a buffer of scales per stage: A's, from SFB on B's.
 template <bool NV>
 struct Tmem4 {
-  static constexpr int SF_BUFS = NV ? 3 : 4;
-  static constexpr uint32_t SFB = NV ? 16 : 8, SF_COLS = 3 * SFB;
-  static constexpr int SHARED = NV ? 5 : 3;
-  static constexpr uint32_t ACC1 = 256 - 32 * SHARED, SF = ACC1 + 256;
-  static_assert(SF + SF_BUFS * SF_COLS <= 512, "tensor memory");
+  static constexpr uint32_t SFB = NV ? 16 : 8, SF_COLS = 3 * SFB, SF = BN4;
+  static_assert(SF + STAGES4 * SF_COLS <= 512, "tensor memory");
 };
 
 enum Bar4 {
   B4_FULL = 0,                    // stage landed in both CTAs (even CTA)
   B4_EMPTY = B4_FULL + STAGES4,   // stage read by the products
-  B4_SF = B4_EMPTY + STAGES4,     // stage's scales in tensor memory (even CTA) [4]
-  B4_TFULL = B4_SF + 4,           // accumulator written [2]
-  B4_SHARED = B4_TFULL + 2,       // shared columns read (16 warps, even CTA)
-  B4_DRAIN = B4_SHARED + 1,       // [1 + COPY_WARPS]
+  B4_SF = B4_EMPTY + STAGES4,     // stage's scales in tensor memory (even CTA)
+  B4_TFULL = B4_SF + STAGES4,     // accumulator written
+  B4_TEMPTY = B4_TFULL + 1,       // accumulator read (16 warps, even CTA)
+  B4_DRAIN = B4_TEMPTY + 1,       // [1 + COPY_WARPS]
   B4_NUM = B4_DRAIN + 1 + COPY_WARPS
 };
 static_assert(B4_NUM * 8 + 8 <= 256, "barrier region");
@@ -115,8 +112,37 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// 32 rows x 64 columns from shared memory (128-byte swizzle) to the output, clipped at its
+// edges.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int32_t x,
+                                             int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(x), "r"(y), "r"(src)
+      : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// This thread's stores have read their shared memory / are done.
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
 struct Gemm4Args {
-  __nv_bfloat16* C;
   const float* ra;  // row scales (NV)
   const float* rb;
   int M, N, K;
@@ -143,7 +169,7 @@ template <bool NV, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                    const Gemm4Args a) {
+                    const __grid_constant__ CUtensorMap tmC, const Gemm4Args a) {
   using TM = Tmem4<NV>;
   constexpr int ATOM_STEPS = NV ? 1 : 2;  // products that a scale tile serves
   constexpr int ATOMS = 4 / ATOM_STEPS;   // scale tiles of a stage and 128 rows
@@ -152,7 +178,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES4 * STAGE4_BYTES);
+  uint8_t* sOut = smem + STAGES4 * STAGE4_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + EPI_WARPS * OUT_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B4_NUM);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
@@ -165,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < B4_NUM; ++i) {
       uint32_t count = 1;
-      if (i == B4_SHARED) count = 2 * EPI_WARPS;
+      if (i == B4_TEMPTY) count = 2 * EPI_WARPS;
       mbar_init(bar(i), count);
     }
     fence_mbar_init();
@@ -173,6 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
+    tma_prefetch_desc(&tmC);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -250,28 +278,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
       auto wait = [&](uint32_t b, uint32_t parity) {
         return mbar_wait_warp(b, parity, a.err, ERR_WAIT_GEMM_MMA);
       };
-      int st = 0, buf = 0, done = 0;
-      uint32_t phase = 0, sf_phase = 0;
+      int st = 0;
+      uint32_t phase = 0, acc_phase = 1;
       bool ok = true;
-      for (int tile = pair; tile < a.num_tiles && ok; tile += pairs, ++done) {
-        // the columns this accumulator shares with the tile before are read
-        if (done > 0 && !wait(bar(B4_SHARED), static_cast<uint32_t>(done - 1) & 1u)) break;
+      for (int tile = pair; tile < a.num_tiles && ok; tile += pairs, acc_phase ^= 1u) {
+        if (!wait(bar(B4_TEMPTY), acc_phase)) break;
         tc_fence_after();
-        const uint32_t d = tmem + (done & 1 ? TM::ACC1 : 0u);
         for (int kb = 0; kb < a.num_k; ++kb) {
-          if (!wait(bar(B4_FULL) + st * 8, phase) || !wait(bar(B4_SF) + buf * 8, sf_phase)) {
+          if (!wait(bar(B4_FULL) + st * 8, phase) || !wait(bar(B4_SF) + st * 8, phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t ad = da0 + static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
           const uint64_t bd = ad + (OP_BYTES >> 4);
-          const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(buf) * TM::SF_COLS;
+          const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(st) * TM::SF_COLS;
           const int steps = (a.K - kb * STAGE_CODES + 63) / 64;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (k == 0 || k < steps)
-              mma_fp4_pair_el<NV>(d, ad + k * 2, bd + k * 2, (!NV && (k & 1)) ? idesc2 : idesc0,
+              mma_fp4_pair_el<NV>(tmem, ad + k * 2, bd + k * 2, (!NV && (k & 1)) ? idesc2 : idesc0,
                                   sf + (k / ATOM_STEPS) * 4, sf + TM::SFB + (k / ATOM_STEPS) * 8,
                                   (kb | k) != 0 ? 1u : 0u);
           }
@@ -280,13 +306,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
             st = 0;
             phase ^= 1u;
           }
-          if (++buf == TM::SF_BUFS) {
-            buf = 0;
-            sf_phase ^= 1u;
-          }
         }
         if (!ok) break;
-        mma_commit_pair_mc_el(bar(B4_TFULL) + (done & 1) * 8, kBoth);
+        mma_commit_pair_mc_el(bar(B4_TFULL), kBoth);
       }
       // every product must be done with both CTAs' memories before either frees them
       mma_commit_pair_mc_el(bar(B4_DRAIN), 1);
@@ -302,22 +324,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
         return mbar_wait_warp(bar(b), parity, a.err, ERR_WAIT_GEMM_MMA);
       };
       for (int it = c; it < total; it += COPY_WARPS) {
-        const int st = it % STAGES4, buf = it % TM::SF_BUFS, old = it - TM::SF_BUFS;
-        // the products that read this buffer last
-        if (old >= 0 &&
-            !wait(B4_EMPTY + old % STAGES4, static_cast<uint32_t>(old / STAGES4) & 1u))
-          break;
+        // (the stage was loaded again only after the products that read its buffer)
+        const int st = it % STAGES4;
         if (!wait(B4_FULL + st, static_cast<uint32_t>(it / STAGES4) & 1u)) break;
         tc_fence_after();
         const uint64_t s = ds0 + static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
-        const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(buf) * TM::SF_COLS;
+        const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(st) * TM::SF_COLS;
 #pragma unroll
         for (int t = 0; t < ATOMS; ++t) {
           scale_copy_pair_el(sf + t * 4, s + t * (512 >> 4));
           scale_copy_pair_el(sf + TM::SFB + t * 8, s + ((SFA_BYTES + t * 512) >> 4));
           scale_copy_pair_el(sf + TM::SFB + t * 8 + 4, s + ((SFA_BYTES + 2048 + t * 512) >> 4));
         }
-        mma_commit_pair_mc_el(bar(B4_SF + buf), 1);
+        mma_commit_pair_mc_el(bar(B4_SF + st), 1);
       }
       mma_commit_pair_mc_el(bar(B4_DRAIN + 1 + c), 1);
       mbar_wait_drain(bar(B4_DRAIN + 1 + c), 0u, globaltimer_ns(), drain_limit_ns(a.err));
@@ -326,105 +345,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
     // ------------------------------------------------------ epilogue warps
     const int quarter = warp & 3;     // TMEM lane quarter this warp may access
     const int side = (warp - 2) >> 2; // which of the quarter's two warps
-    int done = 0;
-    for (int tile = pair; tile < a.num_tiles; tile += pairs, ++done) {
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    // this lane's row of the warp's 32 x 64 columns, 16-byte pieces swizzled as TMA reads them
+    const uint32_t out = smem_u32(sOut + (warp - 2) * OUT_BYTES);
+    auto put = [&](int piece, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+      st_shared_v4(out + lane * 128 + ((piece ^ (lane & 7)) << 4), x, y, z, w);
+    };
+    uint32_t phase = 0;
+    for (int tile = pair; tile < a.num_tiles; tile += pairs, phase ^= 1u) {
       int mb, nb;
       tile_coords4(tile, a, mb, nb);
-      const int acc = done & 1;
-      if (!mbar_wait_warp(bar(B4_TFULL + acc), static_cast<uint32_t>(done >> 1) & 1u, a.err,
-                          ERR_WAIT_GEMM_EPILOGUE))
-        break;
+      if (!mbar_wait_warp(bar(B4_TFULL), phase, a.err, ERR_WAIT_GEMM_EPILOGUE)) break;
       tc_fence_after();
-      const int row = (2 * mb + static_cast<int>(rank)) * ROWS + quarter * 32 + lane;
-      const bool row_ok = row < a.M;
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (acc ? TM::ACC1 : 0u);
-      const float ra = NV ? (row_ok ? __ldg(a.ra + row) : 0.f) : 1.f;
-      __nv_bfloat16* crow = a.C + static_cast<int64_t>(row_ok ? row : 0) * a.N;
-      auto tell = [&]() {  // the shared columns are in registers
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader)
-            mbar_arrive(bar(B4_SHARED));
-          else
-            mbar_arrive_remote(mapa_shared(bar(B4_SHARED), 0));
+      const int row0 = (2 * mb + static_cast<int>(rank)) * ROWS + quarter * 32;
+      // chunks of 32 columns: the warp's half of the tile; gate and up of its half
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tmem_ld32(t_row + (SWIGLU ? (c >> 1) * (BN4 / 2) + side * 64 + (c & 1) * 32
+                                  : side * (BN4 / 2) + c * 32),
+                  v[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_reg_fence(v[c]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(bar(B4_TEMPTY));
+        else
+          mbar_arrive_remote(mapa_shared(bar(B4_TEMPTY), 0));
+      }
+      if (row0 >= a.M) continue;
+      const float ra = NV ? (row0 + lane < a.M ? __ldg(a.ra + row0 + lane) : 0.f) : 1.f;
+      // eight products of v[c][8 j ..], B's rows from b on, scaled
+      auto scaled = [&](int c, int j, int b, float (&f)[8]) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(v[c][8 * j + t]);
+        if constexpr (NV) {
+          const float4* sb = reinterpret_cast<const float4*>(a.rb + b);
+          const float4 x = __ldg(sb), y = __ldg(sb + 1);
+          const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * s[t];
         }
       };
-      if constexpr (SWIGLU) {
-        // four pairs of chunks, two per warp. Of the shared columns each of them has some (NV),
-        // or, in order, the first three (MX)
-#pragma unroll 1
-        for (int i = side; i < 4; i += 2) {
-          const int c = acc ? i : (i + 1) & 3;
-          uint32_t g[32], u[32];
-          tmem_ld32(t_row + c * 32, g);
-          tmem_ld32(t_row + BN4 / 2 + c * 32, u);
-          tmem_ld_wait();
-          tmem_reg_fence(g);
-          tmem_reg_fence(u);
-          if (i == (side == 0 || TM::SHARED > 3 ? side + 2 : side)) tell();
-          const int col = nb * (BN4 / 2) + c * 32;
-          if (!row_ok) continue;
-          if constexpr (NV) {
-            const float4* sg = reinterpret_cast<const float4*>(a.rb + col);
-            const float4* su = reinterpret_cast<const float4*>(a.rb + a.up_rows + col);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 x = __ldg(sg + j), y = __ldg(su + j);
-              const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                g[4 * j + t] = __float_as_uint(__uint_as_float(g[4 * j + t]) * ra * xs[t]);
-                u[4 * j + t] = __float_as_uint(__uint_as_float(u[4 * j + t]) * ra * ys[t]);
-              }
-            }
-          }
-          uint32_t o[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float g0 = round_to_bf16(__uint_as_float(g[2 * j]));
-            const float g1 = round_to_bf16(__uint_as_float(g[2 * j + 1]));
-            const float u0 = round_to_bf16(__uint_as_float(u[2 * j]));
-            const float u1 = round_to_bf16(__uint_as_float(u[2 * j + 1]));
-            o[j] = pack_bf16x2(silu_f(g0) * u0, silu_f(g1) * u1);
-          }
-          uint4* dst = reinterpret_cast<uint4*>(crow + col);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      auto send = [&](int col) {  // what is put, to the output's columns from col on
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tmC, out, col, row0);
+          store_commit();
+          store_wait_read();
         }
-      } else {
-#pragma unroll 1
-        for (int i = side; i < 8; i += 2) {
-          const int c = acc ? i : (i + 8 - TM::SHARED) & 7;  // the shared chunks first
-          uint32_t v[32];
-          tmem_ld32(t_row + c * 32, v);
-          tmem_ld_wait();
-          tmem_reg_fence(v);
-          if (i == (TM::SHARED - 1 - side) / 2 * 2 + side) tell();  // its last shared chunk
-          const int col = nb * BN4 + c * 32;
-          if (!row_ok) continue;
+        __syncwarp();
+      };
+      if constexpr (SWIGLU) {
+        const int col0 = nb * (BN4 / 2) + side * 64;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (col + 8 * j < a.N) {
+            float g[8], u[8];
+            scaled(c, j, col0 + c * 32 + 8 * j, g);
+            scaled(2 + c, j, a.up_rows + col0 + c * 32 + 8 * j, u);
+            uint32_t o[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              o[t] = pack_bf16x2(
+                  silu_f(round_to_bf16(g[2 * t])) * round_to_bf16(u[2 * t]),
+                  silu_f(round_to_bf16(g[2 * t + 1])) * round_to_bf16(u[2 * t + 1]));
+            put(c * 4 + j, o[0], o[1], o[2], o[3]);
+          }
+        }
+        send(col0);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col0 = nb * BN4 + side * (BN4 / 2) + h * 64;
+          if (col0 < a.N) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
               float f[8];
-#pragma unroll
-              for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(v[8 * j + t]);
-              if constexpr (NV) {
-                const float4* sb = reinterpret_cast<const float4*>(a.rb + col + 8 * j);
-                const float4 x = __ldg(sb), y = __ldg(sb + 1);
-                const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * s[t];
+              if (col0 + 8 * p < a.N) {
+                scaled(2 * h + (p >> 2), p & 3, col0 + 8 * p, f);
+                put(p, pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
               }
-              *reinterpret_cast<uint4*>(crow + col + 8 * j) =
-                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
             }
+            send(col0);
           }
         }
       }
     }
+    if (lane == 0) store_wait();
   }
 
   __syncwarp();
@@ -446,7 +460,6 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   const int b_rows = SWIGLU ? 2 * N : N;
   const int tile_n = SWIGLU ? BN4 / 2 : BN4;
   Gemm4Args a{};
-  a.C = static_cast<__nv_bfloat16*>(C);
   a.ra = A.row_scale;
   a.rb = B.row_scale;
   a.M = L;
@@ -459,7 +472,7 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   a.sf_tiles = fp4_tiles(K, NV);
   a.up_rows = SWIGLU ? N : 0;
   if ((st = dev_err(&a.err)) != H3_OK) return st;
-  CUtensorMap tmA, tmB, tmSA, tmSB;
+  CUtensorMap tmA, tmB, tmSA, tmSB, tmC;
   const uint64_t row_bytes = static_cast<uint64_t>(K) / 2;
   if ((st = make_tmap_u8_2d(&tmA, A.codes, row_bytes, L, row_bytes, 128, ROWS)) != H3_OK) return st;
   if ((st = make_tmap_u8_2d(&tmB, B.codes, row_bytes, b_rows, row_bytes, 128, ROWS)) != H3_OK)
@@ -470,8 +483,9 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   constexpr uint32_t atoms = NV ? 4 : 2;
   if ((st = make_tmap_u32_rows(&tmSA, A.scales, 128, ta, atoms)) != H3_OK) return st;
   if ((st = make_tmap_u32_rows(&tmSB, B.scales, 128, tb, atoms)) != H3_OK) return st;
+  if ((st = make_tmap_bf16_2d(&tmC, C, N, L, static_cast<uint64_t>(N) * 2, 64, 32)) != H3_OK) return st;
   const int grid = 2 * std::min(a.num_tiles, num_sms() / 2);
-  gemm_fp4_kernel<NV, SWIGLU><<<grid, THREADS4, SMEM4_BYTES, s>>>(tmA, tmB, tmSA, tmSB, a);
+  gemm_fp4_kernel<NV, SWIGLU><<<grid, THREADS4, SMEM4_BYTES, s>>>(tmA, tmB, tmSA, tmSB, tmC, a);
   return cuda_fail(cudaGetLastError(), "fp4 gemm launch");
 }
 
