@@ -278,6 +278,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
       auto wait = [&](uint32_t b, uint32_t parity) {
         return mbar_wait_warp(b, parity, a.err, ERR_WAIT_GEMM_MMA);
       };
+      // stages with all of their four products, and the products of one behind them
+      const int whole = a.K / STAGE_CODES + (a.K % STAGE_CODES > 192 ? 1 : 0);
+      const int last = (a.K - whole * STAGE_CODES + 63) / 64;
       int st = 0;
       uint32_t phase = 0, acc_phase = 1;
       bool ok = true;
@@ -293,13 +296,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
           const uint64_t ad = da0 + static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
           const uint64_t bd = ad + (OP_BYTES >> 4);
           const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(st) * TM::SF_COLS;
-          const int steps = (a.K - kb * STAGE_CODES + 63) / 64;
+          auto product = [&](int k) {
+            mma_fp4_pair_el<NV>(tmem, ad + k * 2, bd + k * 2, (!NV && (k & 1)) ? idesc2 : idesc0,
+                                sf + (k / ATOM_STEPS) * 4, sf + TM::SFB + (k / ATOM_STEPS) * 8,
+                                (kb | k) != 0 ? 1u : 0u);
+          };
+          // a whole stage without a branch between its products (with one before each the
+          // pipe ran at 0.79 of this: 7,250 against 9,220 TFLOP/s without loads and stores)
+          if (kb < whole) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k == 0 || k < steps)
-              mma_fp4_pair_el<NV>(tmem, ad + k * 2, bd + k * 2, (!NV && (k & 1)) ? idesc2 : idesc0,
-                                  sf + (k / ATOM_STEPS) * 4, sf + TM::SFB + (k / ATOM_STEPS) * 8,
-                                  (kb | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) product(k);
+          } else {
+            product(0);
+            if (last > 1) product(1);
+            if (last > 2) product(2);
           }
           mma_commit_pair_mc_el(bar(B4_EMPTY) + st * 8, kBoth);
           if (++st == STAGES4) {
