@@ -6,11 +6,12 @@
 // has 1 / block of the attention's own Q K^T to do, in FP32 on the CUDA cores, since a
 // score that is rounded to fewer bits changes which blocks are chosen.
 //
-// Selection: a radix search for the max_blocks-th largest score (8 bits a pass), then one
-// pass that writes the chosen indices in ascending order. A CTA per row of scores.
+// Selection: the max_blocks-th largest score is found by counting, then one pass writes
+// the chosen indices in ascending order. A warp per row of scores, longer ones a CTA.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "h3_blocks.cuh"
 #include "h3_internal.cuh"
@@ -82,63 +83,95 @@ __global__ void __launch_bounds__(POOL_WARPS * 32)
 }
 
 // ------------------------------------------------------------------ product
-constexpr int SC_T = 64;     // query blocks x key blocks of a CTA
-constexpr int SC_LD = 68;    // floats between two channels' rows of a tile
-constexpr size_t SC_SMEM = 2 * DHB * SC_LD * sizeof(float);
+constexpr int SC_N = 128;    // key blocks of a CTA
+constexpr int SC_K = 32;     // channels per step
+constexpr int SC_THREADS = 128;
 
-// scores[h] = scale * mq[h] mk[g]^T: 64 x 64 of it per CTA, 8 x 4 per thread, both
-// tiles whole (128 channels) in shared memory, channel by channel.
-__global__ void __launch_bounds__(128)
+// (d0, d1) += (a, a) * (b0, b1)
+__device__ __forceinline__ void ffma2_acc(uint64_t& d, float a, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "fma.rn.f32x2 %0, x, y, %0;\n\t}"
+      : "+l"(d)
+      : "f"(a), "f"(b0), "f"(b1));
+}
+
+// scores[h] = scale * mq[h] mk[g]^T: TMQ x 128 of it per CTA. A thread has TMQ / 8 neighbouring
+// query blocks and eight key blocks 16 apart, two to a packed FMA; both operands lie
+// channel by channel in shared memory, 32 channels at a time, the next ones on their way.
+template <int TMQ>
+__global__ void __launch_bounds__(SC_THREADS)
     block_scores_kernel(const float* __restrict__ mq, const float* __restrict__ mk,
                         float* __restrict__ scores, int nq, int nk, int group, float scale) {
-  extern __shared__ float sm[];
-  float* sa = sm;
-  float* sb = sm + DHB * SC_LD;
+  constexpr int RQ = TMQ / 8;              // rows of a thread
+  constexpr int AV = TMQ * SC_K / 4 / SC_THREADS;  // float4 that a thread loads of A
+  constexpr int BV = SC_N * SC_K / 4 / SC_THREADS;
+  __shared__ __align__(16) float sa[SC_K][TMQ + 4];
+  __shared__ __align__(16) float sb[SC_K][SC_N + 4];
   const int h = blockIdx.z, g = h / group;
-  const int t0 = blockIdx.y * SC_T, b0 = blockIdx.x * SC_T;
-  const float* qa = mq + static_cast<int64_t>(h) * nq * DHB;
-  const float* kb = mk + static_cast<int64_t>(g) * nk * DHB;
-  {
-    const int row = threadIdx.x & 63, half = threadIdx.x >> 6;
-    const bool qok = t0 + row < nq, kok = b0 + row < nk;
-    const float4* qp = reinterpret_cast<const float4*>(qa + static_cast<int64_t>(t0 + row) * DHB);
-    const float4* kp = reinterpret_cast<const float4*>(kb + static_cast<int64_t>(b0 + row) * DHB);
+  const int t0 = blockIdx.y * TMQ, b0 = blockIdx.x * SC_N;
+  const float4* qa = reinterpret_cast<const float4*>(mq + (static_cast<int64_t>(h) * nq + t0) * DHB);
+  const float4* kb = reinterpret_cast<const float4*>(mk + (static_cast<int64_t>(g) * nk + b0) * DHB);
+  const int tid = threadIdx.x;
+  // A: thread's row tid % TMQ, its AV float4 from (tid / TMQ) * AV on; B: row tid, all of them
+  const int ar = tid % TMQ, ac = tid / TMQ * AV;
+  const bool a_in = t0 + ar < nq, b_in = b0 + tid < nk;
+  float4 av[AV], bv[BV];
+  auto fetch = [&](int k4) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < AV; ++i) av[i] = a_in ? __ldg(qa + ar * (DHB / 4) + k4 + ac + i) : z;
+#pragma unroll
+    for (int i = 0; i < BV; ++i) bv[i] = b_in ? __ldg(kb + tid * (DHB / 4) + k4 + i) : z;
+  };
+  uint64_t acc[RQ][4];
+#pragma unroll
+  for (int i = 0; i < RQ; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
+  const int ty = tid >> 4, tx = tid & 15;
+  fetch(0);
+#pragma unroll 1
+  for (int k0 = 0; k0 < DHB; k0 += SC_K) {
+    if (k0 > 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < AV; ++i) {
+      const float w[4] = {av[i].x, av[i].y, av[i].z, av[i].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sa[4 * (ac + i) + c][ar] = w[c] * scale;
+    }
+#pragma unroll
+    for (int i = 0; i < BV; ++i) {
+      const float w[4] = {bv[i].x, bv[i].y, bv[i].z, bv[i].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sb[4 * i + c][tid] = w[c];
+    }
+    __syncthreads();
+    if (k0 + SC_K < DHB) fetch((k0 + SC_K) / 4);
 #pragma unroll 8
-    for (int i = 0; i < 16; ++i) {
-      const int c = half * 16 + i;
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 u = qok ? __ldg(qp + c) : z;
-      const float4 w = kok ? __ldg(kp + c) : z;
-      float* pa = sa + 4 * c * SC_LD + row;
-      float* pb = sb + 4 * c * SC_LD + row;
-      pa[0] = u.x * scale, pa[SC_LD] = u.y * scale;
-      pa[2 * SC_LD] = u.z * scale, pa[3 * SC_LD] = u.w * scale;
-      pb[0] = w.x, pb[SC_LD] = w.y, pb[2 * SC_LD] = w.z, pb[3 * SC_LD] = w.w;
+    for (int c = 0; c < SC_K; ++c) {
+      float x[RQ], y[8];
+#pragma unroll
+      for (int i = 0; i < RQ; ++i) x[i] = sa[c][ty * RQ + i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = sb[c][tx + 16 * j];
+#pragma unroll
+      for (int i = 0; i < RQ; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ffma2_acc(acc[i][j], x[i], y[2 * j], y[2 * j + 1]);
     }
   }
-  __syncthreads();
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  float acc[8][4] = {};
-#pragma unroll 4
-  for (int c = 0; c < DHB; ++c) {
-    const float4 a0 = *reinterpret_cast<const float4*>(sa + c * SC_LD + ty * 8);
-    const float4 a1 = *reinterpret_cast<const float4*>(sa + c * SC_LD + ty * 8 + 4);
-    const float4 b = *reinterpret_cast<const float4*>(sb + c * SC_LD + tx * 4);
-    const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-    const float bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int t = t0 + ty * 8 + i;
+  for (int i = 0; i < RQ; ++i) {
+    const int t = t0 + ty * RQ + i;
     if (t >= nq) break;
-    float* o = scores + (static_cast<int64_t>(h) * nq + t) * nk + b0 + tx * 4;
+    float* o = scores + (static_cast<int64_t>(h) * nq + t) * nk + b0 + tx;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (b0 + tx * 4 + j < nk) o[j] = acc[i][j];
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t w = static_cast<uint32_t>(acc[i][j >> 1] >> (32 * (j & 1)));
+      if (b0 + tx + 16 * j < nk) o[16 * j] = __uint_as_float(w);
+    }
   }
 }
 
@@ -152,6 +185,134 @@ __device__ __forceinline__ uint32_t select_key(float f, bool kept) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+constexpr uint32_t KEPT = 0xffffffffu;
+constexpr int SEL_WARPS = 4;
+
+// Rows of at most 32 * IPT scores: a warp per row, whose keys stay in its registers. The
+// threshold T (the least selected key) is looked for between lo and hi, of which at least
+// and fewer than `most` keys are not below; every step counts the keys from a place between them
+// on. The first place is where a normal distribution of the row's mean and deviation has
+// `most` (z deviations above the mean), the second as far from it as that density says, a
+// dozen keys further, and from then on the middle: rows as scores are take two or three
+// steps, any others at most 32 more. With at most 32 keys left between lo and hi, a lane
+// takes one and ranks it among them.
+template <int IPT>
+__global__ void __launch_bounds__(SEL_WARPS * 32)
+    block_select_warp_kernel(const float* __restrict__ scores, int32_t* __restrict__ ids,
+                             int32_t* __restrict__ counts, int rows, int nk, int most, int first,
+                             int last, float z, float density) {
+  __shared__ uint32_t left[SEL_WARPS][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * SEL_WARPS + warp;
+  if (row >= rows) return;
+  const float* s = scores + static_cast<int64_t>(row) * nk;
+  int32_t* out = ids + static_cast<int64_t>(row) * most;
+  uint32_t key[IPT];
+  float sum = 0.f, sum2 = 0.f;
+  int valid = 0, kept = 0;
+  {
+    float f[IPT];
+#pragma unroll
+    for (int r = 0; r < IPT; ++r) {
+      const int i = r * 32 + lane;
+      f[r] = i < nk ? __ldcs(s + i) : -INFINITY;
+    }
+#pragma unroll
+    for (int r = 0; r < IPT; ++r) {
+      const int i = r * 32 + lane;
+      key[r] = select_key(f[r], i < nk && (i < first || i >= nk - last));
+      valid += key[r] != 0u;
+      kept += key[r] == KEPT;
+      const float v = key[r] != 0u && key[r] != KEPT ? f[r] : 0.f;
+      sum += v;
+      sum2 = fmaf(v, v, sum2);
+    }
+  }
+  valid = __reduce_add_sync(0xffffffffu, valid);
+  kept = __reduce_add_sync(0xffffffffu, kept);
+  // T, and how many of the keys equal to it are selected (the first of them)
+  uint32_t T = 0;
+  int equal = 0;
+  if (kept >= most) {
+    T = KEPT - 1u;
+  } else if (valid > most) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      sum2 += __shfl_xor_sync(0xffffffffu, sum2, m);
+    }
+    const float n = static_cast<float>(valid - kept);
+    const float mean = sum / n;
+    const float dev = sqrtf(fmaxf(sum2 / n - mean * mean, 0.f));
+    uint32_t lo = 1u, hi = KEPT;
+    int c_lo = valid, c_hi = kept;  // keys from lo, from hi on
+    float at = fmaf(z, dev, mean);
+    for (int step = 0;; ++step) {
+      uint32_t place = lo + (hi - lo) / 2;
+      if (step < 2 && at > -INFINITY && at < INFINITY) {
+        const uint32_t k = select_key(at, false);
+        if (k > lo && k < hi) place = k;
+      }
+      int c = 0;
+#pragma unroll
+      for (int r = 0; r < IPT; ++r) c += key[r] >= place;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c >= most) {
+        lo = place, c_lo = c;
+        if (c == most) break;
+        at += (c - most + 12) * dev / (n * density);
+      } else {
+        hi = place, c_hi = c;
+        at -= (most - c + 12) * dev / (n * density);
+      }
+      if (c_lo - c_hi <= 32 || hi - lo == 1u) break;
+    }
+    const int need = most - c_hi;
+    if (c_lo == most) {
+      T = lo - 1u;  // all from lo on
+    } else if (hi - lo == 1u) {
+      T = lo;
+      equal = need;
+    } else {
+      int base = 0;
+#pragma unroll
+      for (int r = 0; r < IPT; ++r) {
+        const bool in = key[r] >= lo && key[r] < hi;
+        const uint32_t b = __ballot_sync(0xffffffffu, in);
+        if (in) left[warp][base + __popc(b & ((1u << lane) - 1u))] = key[r];
+        base += __popc(b);
+      }
+      __syncwarp();
+      const uint32_t mine = lane < base ? left[warp][lane] : 0u;
+      int above = 0, rank = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mine, j);
+        above += other > mine;
+        rank += other > mine || (other == mine && j < lane);
+      }
+      const uint32_t b = __ballot_sync(0xffffffffu, rank == need - 1 && lane < base);
+      const int who = __ffs(b) - 1;
+      T = __shfl_sync(0xffffffffu, mine, who);
+      equal = need - __shfl_sync(0xffffffffu, above, who);
+    }
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  int n = 0, eq = 0;
+#pragma unroll
+  for (int r = 0; r < IPT; ++r) {
+    const uint32_t same = __ballot_sync(0xffffffffu, key[r] == T && T != 0u);
+    const bool in = key[r] > T || (key[r] == T && T != 0u && eq + __popc(same & below) < equal);
+    const uint32_t b = __ballot_sync(0xffffffffu, in);
+    if (in) out[n + __popc(b & below)] = r * 32 + lane;
+    n += __popc(b);
+    eq += __popc(same);
+  }
+  for (int i = n + lane; i < most; i += 32) out[i] = -1;
+  if (lane == 0) counts[row] = n;
+}
+
+// Longer rows: a CTA per row, a radix search of 8 bits a pass over the scores in L1 and L2.
 template <int T>
 __global__ void __launch_bounds__(T)
     block_select_kernel(const float* __restrict__ scores, int32_t* __restrict__ ids,
@@ -258,10 +419,7 @@ size_t block_scores_workspace_bytes(int nq, int nk, int H, int Hkv) {
 h3_status launch_block_scores(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
                               float* scores, int Lq, int Lk, int H, int Hkv, int k_block,
                               float scale, void* workspace, cudaStream_t s) {
-  static std::atomic<bool> done[64];
-  h3_status st = set_smem_limit(done, block_scores_kernel, SC_SMEM,
-                                "block scores: set shared memory size");
-  if (st != H3_OK) return st;
+  h3_status st;
   const int nq = (Lq + H3_QUERY_BLOCK - 1) / H3_QUERY_BLOCK, nk = (Lk + k_block - 1) / k_block;
   float* mq = static_cast<float*>(workspace);
   float* mk = mq + static_cast<int64_t>(nq) * H * DHB;
@@ -272,20 +430,45 @@ h3_status launch_block_scores(const void* q, int64_t ld_q, const void* k, int64_
   const int q_ctas = nq * qs.pairs;
   pool_kernel<<<q_ctas + nk * ks.pairs, POOL_WARPS * 32, 0, s>>>(qs, ks, q_ctas);
   if ((st = cuda_fail(cudaGetLastError(), "block pooling launch")) != H3_OK) return st;
-  const dim3 grid((nk + SC_T - 1) / SC_T, (nq + SC_T - 1) / SC_T, H);
-  block_scores_kernel<<<grid, 128, SC_SMEM, s>>>(mq, mk, scores, nq, nk, H / Hkv, scale);
+  const int tile = nq <= 16 ? 16 : 64;
+  const dim3 grid((nk + SC_N - 1) / SC_N, (nq + tile - 1) / tile, H);
+  if (tile == 16)
+    block_scores_kernel<16><<<grid, SC_THREADS, 0, s>>>(mq, mk, scores, nq, nk, H / Hkv, scale);
+  else
+    block_scores_kernel<64><<<grid, SC_THREADS, 0, s>>>(mq, mk, scores, nq, nk, H / Hkv, scale);
   return cuda_fail(cudaGetLastError(), "block scores launch");
 }
 
 h3_status launch_block_select(const float* scores, int32_t* ids, int32_t* counts, int rows,
                               int nk, int max_blocks, int keep_first, int keep_last,
                               cudaStream_t s) {
-  if (nk <= 2048)
-    block_select_kernel<128><<<rows, 128, 0, s>>>(scores, ids, counts, nk, max_blocks, keep_first,
-                                                  keep_last);
-  else
+  if (nk <= 2048) {
+    // z: where a normal distribution has max_blocks / nk of it above (Abramowitz and Stegun,
+    // Handbook of Mathematical Functions, 26.2.23: off by less than 4.5e-4), and its density there
+    const double share = std::min(0.999, std::max(1e-6, static_cast<double>(max_blocks) / nk));
+    const double p = std::min(share, 1.0 - share);
+    const double t = std::sqrt(-2.0 * std::log(p));
+    double z = t - (2.515517 + t * (0.802853 + t * 0.010328)) /
+                       (1.0 + t * (1.432788 + t * (0.189269 + t * 0.001308)));
+    const double density = 0.3989422804014327 * std::exp(-0.5 * z * z);
+    if (share > 0.5) z = -z;
+    const int grid = (rows + SEL_WARPS - 1) / SEL_WARPS;
+    const float zf = static_cast<float>(z), df = static_cast<float>(std::max(density, 1e-4));
+#define H3_SELECT(I)                                                                            \
+  block_select_warp_kernel<I><<<grid, SEL_WARPS * 32, 0, s>>>(scores, ids, counts, rows, nk,    \
+                                                              max_blocks, keep_first, keep_last, \
+                                                              zf, df)
+    if (nk <= 128) H3_SELECT(4);
+    else if (nk <= 256) H3_SELECT(8);
+    else if (nk <= 512) H3_SELECT(16);
+    else if (nk <= 768) H3_SELECT(24);
+    else if (nk <= 1024) H3_SELECT(32);
+    else H3_SELECT(64);
+#undef H3_SELECT
+  } else {
     block_select_kernel<512><<<rows, 512, 0, s>>>(scores, ids, counts, nk, max_blocks, keep_first,
                                                   keep_last);
+  }
   return cuda_fail(cudaGetLastError(), "block select launch");
 }
 
