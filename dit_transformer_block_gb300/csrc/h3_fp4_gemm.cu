@@ -163,7 +163,10 @@ __device__ __forceinline__ void tile_coords4(int tile, const Gemm4Args& a, int& 
   nb = r / gm;
 }
 
-__device__ __forceinline__ float silu_f(float g) { return g / (1.0f + __expf(-g)); }
+// (the division within 2 units of FP32's last place; its IEEE form takes a subroutine for
+// operands out of the ordinary and made the epilogue of a tile 4 us longer, 12 where rows
+// beyond the last one hold NaN)
+__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 template <bool NV, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
@@ -365,9 +368,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
     for (int tile = pair; tile < a.num_tiles; tile += pairs, phase ^= 1u) {
       int mb, nb;
       tile_coords4(tile, a, mb, nb);
+      const int row0 = (2 * mb + static_cast<int>(rank)) * ROWS + quarter * 32;
+      // scales of the row and, a lane four of them, of the warp's 128 columns (or 64 and 64),
+      // asked for while the products run
+      float ra = 1.f;
+      float4 rb = make_float4(0.f, 0.f, 0.f, 0.f);
+      if constexpr (NV) {
+        if (row0 + lane < a.M) ra = __ldg(a.ra + row0 + lane);
+        const int b = SWIGLU ? (lane >> 4) * a.up_rows + nb * (BN4 / 2) + side * 64 + (lane & 15) * 4
+                             : nb * BN4 + side * (BN4 / 2) + lane * 4;
+        if (SWIGLU || b < a.N) rb = __ldg(reinterpret_cast<const float4*>(a.rb + b));
+      }
       if (!mbar_wait_warp(bar(B4_TFULL), phase, a.err, ERR_WAIT_GEMM_EPILOGUE)) break;
       tc_fence_after();
-      const int row0 = (2 * mb + static_cast<int>(rank)) * ROWS + quarter * 32;
       // chunks of 32 columns: the warp's half of the tile; gate and up of its half
       uint32_t v[4][32];
 #pragma unroll
@@ -387,17 +400,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
           mbar_arrive_remote(mapa_shared(bar(B4_TEMPTY), 0));
       }
       if (row0 >= a.M) continue;
-      const float ra = NV ? (row0 + lane < a.M ? __ldg(a.ra + row0 + lane) : 0.f) : 1.f;
-      // eight products of v[c][8 j ..], B's rows from b on, scaled
-      auto scaled = [&](int c, int j, int b, float (&f)[8]) {
+      // eight products, v[c][8 j ..], scaled
+      auto scaled = [&](int c, int j, float (&f)[8]) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(v[c][8 * j + t]);
         if constexpr (NV) {
-          const float4* sb = reinterpret_cast<const float4*>(a.rb + b);
-          const float4 x = __ldg(sb), y = __ldg(sb + 1);
-          const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * s[t];
+          for (int t = 0; t < 8; ++t) {
+            const float mine = (t & 3) == 0 ? rb.x : (t & 3) == 1 ? rb.y : (t & 3) == 2 ? rb.z : rb.w;
+            f[t] = f[t] * ra * __shfl_sync(0xffffffffu, mine, c * 8 + 2 * j + (t >> 2));
+          }
         }
       };
       auto send = [&](int col) {  // what is put, to the output's columns from col on
@@ -417,8 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float g[8], u[8];
-            scaled(c, j, col0 + c * 32 + 8 * j, g);
-            scaled(2 + c, j, a.up_rows + col0 + c * 32 + 8 * j, u);
+            scaled(c, j, g);
+            scaled(2 + c, j, u);
             uint32_t o[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -437,11 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
               float f[8];
-              if (col0 + 8 * p < a.N) {
-                scaled(2 * h + (p >> 2), p & 3, col0 + 8 * p, f);
-                put(p, pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-              }
+              scaled(2 * h + (p >> 2), p & 3, f);
+              put(p, pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                  pack_bf16x2(f[6], f[7]));
             }
             send(col0);
           }

@@ -669,7 +669,8 @@ h3_status h3_linear_fp4(const void* x_codes, const void* x_scales, const float* 
 
 /* 4-bit gate/up projection with SwiGLU in the epilogue: as h3_linear_swiglu with 4-bit
  * operands (w_gu [2F, K], rows [gate | up]); the two products are scaled and rounded to bf16
- * before the SiLU. F % 128 == 0, K % 32 == 0. */
+ * before the SiLU, whose division is within 2 units of the last place of FP32 (h3_swiglu
+ * divides exactly, so a value may round to the neighbouring bf16). F % 128 == 0, K % 32 == 0. */
 h3_status h3_linear_swiglu_fp4(const void* x_codes, const void* x_scales, const float* rx,
                                const void* w_codes, const void* w_scales, const float* rw,
                                void* out, int S, int L, int F, int K, int format,

@@ -7,8 +7,9 @@ within
   + (K / 16 + 4) 2^-23 A      the FP32 sum: at least 16 values of K meet in one addition, each
                               of them off by one unit of the last place of what was summed so
                               far, A = the sum of the products' magnitudes; and the scaling
-SwiGLU: the same on both products, each rounded once more to bf16, through SiLU (slope at
-most 1.1) and the product."""
+SwiGLU, given the two rounded products g and u: 2^-8 for its own rounding and 2^-20 (an exponential
+off by 2 units of FP32's last place and 2^-24 |g|, a division off by 2, three roundings), relative to
+SiLU(g) u; where exp(-g) passes 2^126 it may be 0 instead of less than 2^-119 |u|."""
 import numpy as np
 import pytest
 import torch
@@ -269,14 +270,38 @@ def test_linear_swiglu_is_product_then_gate(h3lib, S, L, F, K, fmt):
     qx = quantize(h3lib, draw(S, K, seed=S), fmt)
     qw = quantize(h3lib, draw(2 * F, K, seed=F, std=0.02), fmt)
     gu = torch.empty(S, 2 * F, dtype=torch.bfloat16, device=dev)
-    want = torch.full((S, F), SENT, dtype=torch.bfloat16, device=dev)
     out = torch.full((S, F), SENT, dtype=torch.bfloat16, device=dev)
     h3lib.linear_fp4(qx, qw, gu, L)
-    h3lib.swiglu(gu, want, L)
     h3lib.linear_swiglu_fp4(qx, qw, out, L)
     h3lib.check_device_error()
     check_linear(gu, qx, qw, np.arange(L), "gate and up")
-    assert torch.equal(out, want)  # the same products, the same roundings
+    check_swiglu(out[:L], gu[:L])
+    assert bool((out[L:] == SENT).all())
+
+
+def check_swiglu(out, gu):
+    g, u = gu.double().chunk(2, 1)
+    want = g * torch.sigmoid(g) * u
+    bound = (2.0 ** -8 + 2.0 ** -20 + 2.0 ** -23 * g.abs()) * want.abs() + 2.0 ** -119 * u.abs()
+    assert ((out.double() - want).abs() <= bound).all()
+
+
+def test_swiglu_of_large_products(h3lib):
+    # gates from -300 to 300: the exponential's overflow, and its end
+    S, F, K = 64, 128, 64
+    x, w = torch.zeros(S, K, device=dev), torch.zeros(2 * F, K, device=dev)
+    x[:, 0] = torch.linspace(-6, 6, S, device=dev)
+    x[:, 1] = 1
+    w[:F, 0] = torch.linspace(0, 50, F, device=dev)
+    w[F:, 1] = torch.linspace(-3, 3, F, device=dev)
+    qx, qw = (quantize(h3lib, t.to(torch.bfloat16), "mx") for t in (x, w))
+    gu = torch.empty(S, 2 * F, dtype=torch.bfloat16, device=dev)
+    out = torch.empty(S, F, dtype=torch.bfloat16, device=dev)
+    h3lib.linear_fp4(qx, qw, gu)
+    h3lib.linear_swiglu_fp4(qx, qw, out)
+    h3lib.check_device_error()
+    assert gu[:, :F].min() < -250 and gu[:, :F].max() > 250 and torch.isfinite(out).all()
+    check_swiglu(out, gu)
 
 
 def test_zero_rows_and_columns(h3lib):
