@@ -20,6 +20,7 @@
 
 #include "h3_attn_common.cuh"
 #include "h3_blocks.cuh"
+#include "h3_launch.cuh"
 
 namespace h3 {
 namespace {
@@ -160,14 +161,7 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
   const int h = blockIdx.y;
   const int q0 = qb * 2 * BQ;
   const bool two = q0 + BQ < a.Lq;  // the second query tile has rows
-  const int64_t item = static_cast<int64_t>(h) * a.nq + qb;
-  const int32_t* list = a.ids + item * a.most;
   const int per_tile = BKV / a.kb;  // listed blocks of a key tile
-  const int count = min(max(__ldg(a.counts + item), 0), a.most);
-  // this CTA's key tiles
-  const int tiles = (count + per_tile - 1) / per_tile;
-  const int tile0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / a.cluster);
-  const int n = static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / a.cluster) - tile0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < BB_NUM; ++i) mbar_init(bar(i), (i >= BB_SFREE && i < BB_PVD) ? 4 : 1);
@@ -181,6 +175,14 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_previous();
+  const int64_t item = static_cast<int64_t>(h) * a.nq + qb;
+  const int32_t* list = a.ids + item * a.most;
+  const int count = min(max(*(a.counts + item), 0), a.most);
+  // this CTA's key tiles
+  const int tiles = (count + per_tile - 1) / per_tile;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / a.cluster);
+  const int n = static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / a.cluster) - tile0;
 
   float m = -INFINITY, l = 0.f;  // softmax warps: the row's maximum and sum
   bool ok = true;
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
       auto rows_of = [&](int j, int (&row)[2], int (&real)[2]) {
         for (int e = 0; e < per_tile; ++e) {
           const int at = (tile0 + j) * per_tile + e;
-          const int id = at < count ? __ldg(list + at) : -1;
+          const int id = at < count ? *(list + at) : -1;
           const bool in = id >= 0 && id < a.nk;
           row[e] = in ? id * a.kb : a.Lk;
           real[e] = in ? min(a.kb, a.Lk - row[e]) : 0;
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
         }
         if (j > 0 && !load(&tmV, row[(j - 1) & 1])) break;
       }
+      launch_next();
       // no copy of this CTA may still be landing when it exits
       const uint64_t t0 = globaltimer_ns();
       const uint64_t lim = drain_limit_ns(a.err);
@@ -468,29 +471,26 @@ h3_status launch_attention_blocks(const void* q, int64_t ld_q, const void* k, in
   a.group = H / Hkv;
   a.scale_log2 = scale * 1.4426950408889634f;
   if ((st = dev_err(&a.err)) != H3_OK) return st;
-  // a list is shared by as many CTAs as there are SMs for, of two key tiles each at least
+  // a list is shared by as many CTAs as all of them find room for, two key tiles each at least
   const int64_t items = static_cast<int64_t>(a.nq) * H;
   const int64_t tiles = (static_cast<int64_t>(max_blocks) * k_block + BKV - 1) / BKV;
+  static std::atomic<int> room[64][9];
   a.cluster = 1;
-  while (a.cluster < 8 && items * a.cluster * 2 <= num_sms() && tiles >= a.cluster * 4) a.cluster *= 2;
+  for (int c = 8; c >= 2; --c) {
+    if (items * c > num_sms() || tiles < 2 * c) continue;
+    if (clusters_at_once(room, attention_blocks_kernel, Q2_THREADS, BS_SMEM_BYTES, c) >= items) {
+      a.cluster = c;
+      break;
+    }
+  }
   CUtensorMap tq, tk, tv;
   const uint64_t wq = static_cast<uint64_t>(H) * DH, wk = static_cast<uint64_t>(Hkv) * DH;
   if ((st = make_tmap_bf16_2d(&tq, q, wq, Lq, ld_q * 2, 64, BQ)) != H3_OK) return st;
   if ((st = make_tmap_bf16_2d(&tk, k, wk, Lk, ld_k * 2, 64, k_block)) != H3_OK) return st;
   if ((st = make_tmap_bf16_2d(&tv, v, wk, Lk, ld_v * 2, 64, k_block)) != H3_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.nq) * a.cluster, H);
-  cfg.blockDim = dim3(Q2_THREADS);
-  cfg.dynamicSmemBytes = BS_SMEM_BYTES;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_fail(cudaLaunchKernelEx(&cfg, attention_blocks_kernel, tq, tk, tv, a),
+  return cuda_fail(launch_overlapped(attention_blocks_kernel,
+                                     dim3(static_cast<unsigned>(a.nq) * a.cluster, H), Q2_THREADS,
+                                     BS_SMEM_BYTES, a.cluster, s, tq, tk, tv, a),
                    "block attention launch");
 }
 

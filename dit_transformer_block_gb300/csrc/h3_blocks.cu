@@ -15,6 +15,7 @@
 
 #include "h3_blocks.cuh"
 #include "h3_internal.cuh"
+#include "h3_launch.cuh"
 
 namespace h3 {
 namespace {
@@ -41,7 +42,9 @@ __global__ void __launch_bounds__(POOL_WARPS * 32)
   const PoolSide& s = is_q ? q : k;
   const int id = static_cast<int>(blockIdx.x) - (is_q ? 0 : q_ctas);
   const int blk = id / s.pairs, head0 = id % s.pairs * 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_previous();
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
   const int row0 = blk * s.block;
   const int rows = min(s.block, s.L - row0);
   const bool real = head0 + (lane >> 4) < s.heads;
@@ -62,12 +65,13 @@ __global__ void __launch_bounds__(POOL_WARPS * 32)
     for (; r + (U - 1) * POOL_WARPS < rows; r += U * POOL_WARPS, p += U * step) {
       uint4 v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(p + u * step));
+      for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const uint4*>(p + u * step);
 #pragma unroll
       for (int u = 0; u < U; ++u) add(v[u]);
     }
-    for (; r < rows; r += POOL_WARPS, p += step) add(__ldg(reinterpret_cast<const uint4*>(p)));
+    for (; r < rows; r += POOL_WARPS, p += step) add(*reinterpret_cast<const uint4*>(p));
   }
+  launch_next();
   float4* mine = reinterpret_cast<float4*>(&part[warp][lane * 8]);
   mine[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
   mine[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -102,8 +106,8 @@ __device__ __forceinline__ void ffma2_acc(uint64_t& d, float a, float b0, float 
 // channel by channel in shared memory, 32 channels at a time, the next ones on their way.
 template <int TMQ>
 __global__ void __launch_bounds__(SC_THREADS)
-    block_scores_kernel(const float* __restrict__ mq, const float* __restrict__ mk,
-                        float* __restrict__ scores, int nq, int nk, int group, float scale) {
+    block_scores_kernel(const float* mq, const float* mk,
+                        float* scores, int nq, int nk, int group, float scale) {
   constexpr int RQ = TMQ / 8;              // rows of a thread
   constexpr int AV = TMQ * SC_K / 4 / SC_THREADS;  // float4 that a thread loads of A
   constexpr int BV = SC_N * SC_K / 4 / SC_THREADS;
@@ -113,6 +117,7 @@ __global__ void __launch_bounds__(SC_THREADS)
   const int t0 = blockIdx.y * TMQ, b0 = blockIdx.x * SC_N;
   const float4* qa = reinterpret_cast<const float4*>(mq + (static_cast<int64_t>(h) * nq + t0) * DHB);
   const float4* kb = reinterpret_cast<const float4*>(mk + (static_cast<int64_t>(g) * nk + b0) * DHB);
+  wait_previous();
   const int tid = threadIdx.x;
   // A: thread's row tid % TMQ, its AV float4 from (tid / TMQ) * AV on; B: row tid, all of them
   const int ar = tid % TMQ, ac = tid / TMQ * AV;
@@ -121,9 +126,9 @@ __global__ void __launch_bounds__(SC_THREADS)
   auto fetch = [&](int k4) {
     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < AV; ++i) av[i] = a_in ? __ldg(qa + ar * (DHB / 4) + k4 + ac + i) : z;
+    for (int i = 0; i < AV; ++i) av[i] = a_in ? qa[ar * (DHB / 4) + k4 + ac + i] : z;
 #pragma unroll
-    for (int i = 0; i < BV; ++i) bv[i] = b_in ? __ldg(kb + tid * (DHB / 4) + k4 + i) : z;
+    for (int i = 0; i < BV; ++i) bv[i] = b_in ? kb[tid * (DHB / 4) + k4 + i] : z;
   };
   uint64_t acc[RQ][4];
 #pragma unroll
@@ -162,6 +167,7 @@ __global__ void __launch_bounds__(SC_THREADS)
         for (int j = 0; j < 4; ++j) ffma2_acc(acc[i][j], x[i], y[2 * j], y[2 * j + 1]);
     }
   }
+  launch_next();
 #pragma unroll
   for (int i = 0; i < RQ; ++i) {
     const int t = t0 + ty * RQ + i;
@@ -198,11 +204,13 @@ constexpr int SEL_WARPS = 4;
 // takes one and ranks it among them.
 template <int IPT>
 __global__ void __launch_bounds__(SEL_WARPS * 32)
-    block_select_warp_kernel(const float* __restrict__ scores, int32_t* __restrict__ ids,
-                             int32_t* __restrict__ counts, int rows, int nk, int most, int first,
+    block_select_warp_kernel(const float* scores, int32_t* ids,
+                             int32_t* counts, int rows, int nk, int most, int first,
                              int last, float z, float density) {
   __shared__ uint32_t left[SEL_WARPS][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_previous();
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x * SEL_WARPS + warp;
   if (row >= rows) return;
   const float* s = scores + static_cast<int64_t>(row) * nk;
@@ -297,6 +305,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32)
       equal = need - __shfl_sync(0xffffffffu, above, who);
     }
   }
+  launch_next();
   const uint32_t below = (1u << lane) - 1u;
   int n = 0, eq = 0;
 #pragma unroll
@@ -315,16 +324,17 @@ __global__ void __launch_bounds__(SEL_WARPS * 32)
 // Longer rows: a CTA per row, a radix search of 8 bits a pass over the scores in L1 and L2.
 template <int T>
 __global__ void __launch_bounds__(T)
-    block_select_kernel(const float* __restrict__ scores, int32_t* __restrict__ ids,
-                        int32_t* __restrict__ counts, int nk, int most, int first, int last) {
+    block_select_kernel(const float* scores, int32_t* ids,
+                        int32_t* counts, int nk, int most, int first, int last) {
   __shared__ int hist[256];
   __shared__ int found[3];       // bin, still needed in it, how many it holds
   __shared__ int warp_gt[T / 32], warp_eq[T / 32];
   const int64_t row = blockIdx.x;
   const float* s = scores + row * nk;
   int32_t* out = ids + row * most;
+  wait_previous();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto key = [&](int i) { return select_key(__ldg(s + i), i < first || i >= nk - last); };
+  auto key = [&](int i) { return select_key(*(s + i), i < first || i >= nk - last); };
 
   // threshold: what is above it is selected, and of what is equal to it the first `equal`
   uint32_t prefix = 0, mask = 0, threshold = 0;
@@ -400,6 +410,7 @@ __global__ void __launch_bounds__(T)
     if (w < warp) sg += warp_gt[w], se += warp_eq[w];
     total_gt += warp_gt[w];
   }
+  launch_next();
   const int n = total_gt + equal;
   int at = sg + min(se, equal);
   for (int i = i0; i < i1; ++i) {
@@ -419,7 +430,6 @@ size_t block_scores_workspace_bytes(int nq, int nk, int H, int Hkv) {
 h3_status launch_block_scores(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
                               float* scores, int Lq, int Lk, int H, int Hkv, int k_block,
                               float scale, void* workspace, cudaStream_t s) {
-  h3_status st;
   const int nq = (Lq + H3_QUERY_BLOCK - 1) / H3_QUERY_BLOCK, nk = (Lk + k_block - 1) / k_block;
   float* mq = static_cast<float*>(workspace);
   float* mk = mq + static_cast<int64_t>(nq) * H * DHB;
@@ -428,20 +438,22 @@ h3_status launch_block_scores(const void* q, int64_t ld_q, const void* k, int64_
   const PoolSide ks{static_cast<const __nv_bfloat16*>(k), ld_k, Lk, Hkv, k_block, nk,
                     (Hkv + 1) / 2, mk};
   const int q_ctas = nq * qs.pairs;
-  pool_kernel<<<q_ctas + nk * ks.pairs, POOL_WARPS * 32, 0, s>>>(qs, ks, q_ctas);
-  if ((st = cuda_fail(cudaGetLastError(), "block pooling launch")) != H3_OK) return st;
+  h3_status st = cuda_fail(launch_overlapped(pool_kernel, dim3(q_ctas + nk * ks.pairs),
+                                             POOL_WARPS * 32, 0, 1, s, qs, ks, q_ctas),
+                           "block pooling launch");
+  if (st != H3_OK) return st;
   const int tile = nq <= 16 ? 16 : 64;
   const dim3 grid((nk + SC_N - 1) / SC_N, (nq + tile - 1) / tile, H);
-  if (tile == 16)
-    block_scores_kernel<16><<<grid, SC_THREADS, 0, s>>>(mq, mk, scores, nq, nk, H / Hkv, scale);
-  else
-    block_scores_kernel<64><<<grid, SC_THREADS, 0, s>>>(mq, mk, scores, nq, nk, H / Hkv, scale);
-  return cuda_fail(cudaGetLastError(), "block scores launch");
+  return cuda_fail(launch_overlapped(tile == 16 ? block_scores_kernel<16> : block_scores_kernel<64>,
+                                     grid, SC_THREADS, 0, 1, s, mq, mk, scores, nq, nk, H / Hkv,
+                                     scale),
+                   "block scores launch");
 }
 
 h3_status launch_block_select(const float* scores, int32_t* ids, int32_t* counts, int rows,
                               int nk, int max_blocks, int keep_first, int keep_last,
                               cudaStream_t s) {
+  cudaError_t e;
   if (nk <= 2048) {
     // z: where a normal distribution has max_blocks / nk of it above (Abramowitz and Stegun,
     // Handbook of Mathematical Functions, 26.2.23: off by less than 4.5e-4), and its density there
@@ -454,22 +466,19 @@ h3_status launch_block_select(const float* scores, int32_t* ids, int32_t* counts
     if (share > 0.5) z = -z;
     const int grid = (rows + SEL_WARPS - 1) / SEL_WARPS;
     const float zf = static_cast<float>(z), df = static_cast<float>(std::max(density, 1e-4));
-#define H3_SELECT(I)                                                                            \
-  block_select_warp_kernel<I><<<grid, SEL_WARPS * 32, 0, s>>>(scores, ids, counts, rows, nk,    \
-                                                              max_blocks, keep_first, keep_last, \
-                                                              zf, df)
-    if (nk <= 128) H3_SELECT(4);
-    else if (nk <= 256) H3_SELECT(8);
-    else if (nk <= 512) H3_SELECT(16);
-    else if (nk <= 768) H3_SELECT(24);
-    else if (nk <= 1024) H3_SELECT(32);
-    else H3_SELECT(64);
-#undef H3_SELECT
+    auto kernel = nk <= 128    ? block_select_warp_kernel<4>
+                  : nk <= 256  ? block_select_warp_kernel<8>
+                  : nk <= 512  ? block_select_warp_kernel<16>
+                  : nk <= 768  ? block_select_warp_kernel<24>
+                  : nk <= 1024 ? block_select_warp_kernel<32>
+                               : block_select_warp_kernel<64>;
+    e = launch_overlapped(kernel, dim3(grid), SEL_WARPS * 32, 0, 1, s, scores, ids, counts, rows, nk,
+                          max_blocks, keep_first, keep_last, zf, df);
   } else {
-    block_select_kernel<512><<<rows, 512, 0, s>>>(scores, ids, counts, nk, max_blocks, keep_first,
-                                                  keep_last);
+    e = launch_overlapped(block_select_kernel<512>, dim3(rows), 512, 0, 1, s, scores, ids, counts, nk,
+                          max_blocks, keep_first, keep_last);
   }
-  return cuda_fail(cudaGetLastError(), "block select launch");
+  return cuda_fail(e, "block select launch");
 }
 
 }  // namespace h3

@@ -12,6 +12,7 @@
 
 #include "h3_fp4.cuh"
 #include "h3_internal.cuh"
+#include "h3_launch.cuh"
 
 namespace h3 {
 namespace {
@@ -41,19 +42,21 @@ __device__ __forceinline__ uint32_t top_bits(const uint4& v) {
 
 template <bool NV, int T, int VPT>
 __global__ void __launch_bounds__(T)
-    quantize_fp4_kernel(const __nv_bfloat16* __restrict__ x, int64_t ldx,
-                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                        float* __restrict__ row_scale, int K) {
+    quantize_fp4_kernel(const __nv_bfloat16* x, int64_t ldx,
+                        uint8_t* codes, uint8_t* scales,
+                        float* row_scale, int K) {
   __shared__ uint32_t red[T / 32];
   const int row = blockIdx.x;
   const int K8 = K >> 3;
   // lanes' worth of a row, whole tiles of four scales
   const int K8s = NV ? (K8 + 7) & ~7 : (K8 + 15) & ~15;
   const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(row) * ldx);
+  wait_previous();
+  const int tid = threadIdx.x;
   uint4 v[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = threadIdx.x + i * T;
+    const int c = tid + i * T;
     v[i] = c < K8 ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
   }
   uint32_t top[VPT], row_top = 0;
@@ -80,13 +83,14 @@ __global__ void __launch_bounds__(T)
     }
     if (threadIdx.x == 0) row_scale[row] = some ? __fdiv_rn(amax, 2688.0f) : 0.f;
   }
+  launch_next();
   const int per = NV ? 2 : 4;  // lanes of a block
   uint8_t* srow = scales + static_cast<int64_t>(row >> 7) * (K8s / (4 * per)) * 512 +
                   (row & 31) * 16 + ((row & 127) >> 5) * 4;
   uint32_t* dst = reinterpret_cast<uint32_t*>(codes + static_cast<int64_t>(row) * (K >> 1));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = threadIdx.x + i * T;
+    const int c = tid + i * T;
     if (c >= K8s) break;
     const bool bad = top[i] >= BF16_INF;
     float mul;
@@ -125,16 +129,16 @@ h3_status launch(const void* x, int64_t ldx, void* codes, void* scales, float* r
   auto* ss = static_cast<uint8_t*>(scales);
   const int k8s = (K / 8 + 15) & ~15;
 #define H3_Q4(T, V) \
-  quantize_fp4_kernel<NV, T, V><<<R, T, 0, s>>>(xx, ldx, cc, ss, row_scale, K)
-  if (k8s <= 128) H3_Q4(128, 1);
-  else if (k8s <= 256) H3_Q4(256, 1);
-  else if (k8s <= 512) H3_Q4(256, 2);
-  else if (k8s <= 768) H3_Q4(256, 3);
-  else if (k8s <= 1024) H3_Q4(256, 4);
-  else if (k8s <= 1536) H3_Q4(256, 6);
-  else H3_Q4(256, 8);
+  launch_overlapped(quantize_fp4_kernel<NV, T, V>, dim3(R), T, 0, 1, s, xx, ldx, cc, ss, row_scale, K)
+  const cudaError_t e = k8s <= 128    ? H3_Q4(128, 1)
+                        : k8s <= 256  ? H3_Q4(256, 1)
+                        : k8s <= 512  ? H3_Q4(256, 2)
+                        : k8s <= 768  ? H3_Q4(256, 3)
+                        : k8s <= 1024 ? H3_Q4(256, 4)
+                        : k8s <= 1536 ? H3_Q4(256, 6)
+                                      : H3_Q4(256, 8);
 #undef H3_Q4
-  return cuda_fail(cudaGetLastError(), "quantize_fp4_rows launch");
+  return cuda_fail(e, "quantize_fp4_rows launch");
 }
 
 }  // namespace

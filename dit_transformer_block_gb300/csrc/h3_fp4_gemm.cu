@@ -17,12 +17,16 @@
 //     accumulator at once, so that the next tile's products wait for one read and not for
 //     the stores, then writes bf16 through 4 KB of shared memory of its own with TMA;
 //   * tensor memory: 256 columns of accumulator, a buffer of scales per stage.
+// A CTA gets its operands at a rate that its copies in flight allow, so where there are few
+// tiles (few rows: the weights' bytes count) several pairs in a cluster share one tile's K. They
+// put their sums into shared memory and each adds up a share of the columns, in the order of K.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "h3_fp4.cuh"
 #include "h3_internal.cuh"
+#include "h3_launch.cuh"
 
 namespace h3 {
 namespace {
@@ -143,12 +147,14 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 }
 
 struct Gemm4Args {
+  __nv_bfloat16* C;  // (SPLIT)
   const float* ra;  // row scales (NV)
   const float* rb;
   int M, N, K;
   int num_m, num_n, num_k;  // tiles of 256 rows, of columns, stages
   int num_tiles;
   int sf_tiles;             // scale tiles along K
+  int parts;                // pairs that share a tile's K
   int up_rows;              // SwiGLU: first row of the up half of B
   DevErr err;
 };
@@ -168,8 +174,9 @@ __device__ __forceinline__ void tile_coords4(int tile, const Gemm4Args& a, int& 
 // beyond the last one hold NaN)
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-template <bool NV, bool SWIGLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
+// SPLIT: the cluster's pairs share one tile; else a pair takes one tile after another.
+template <bool NV, bool SWIGLU, bool SPLIT>
+__global__ void __launch_bounds__(THREADS4, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                     const __grid_constant__ CUtensorMap tmC, const Gemm4Args a) {
@@ -186,11 +193,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B4_NUM);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1u;         // in the pair
+  const uint32_t even = crank & ~1u;        // the pair's even CTA
   const bool leader = rank == 0;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int part = SPLIT ? static_cast<int>(crank >> 1) : 0;
+  const int pair = SPLIT ? static_cast<int>(blockIdx.x) / (2 * a.parts) : blockIdx.x >> 1;
+  const int pairs = SPLIT ? a.num_tiles : gridDim.x >> 1;
+  // this pair's stages of K
+  const int kb0 = SPLIT ? a.num_k * part / a.parts : 0;
+  const int kb1 = SPLIT ? a.num_k * (part + 1) / a.parts : a.num_k;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B4_NUM; ++i) {
@@ -213,9 +227,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_previous();
 
   // stages of this pair, over all of its tiles
-  const int total = (a.num_tiles - pair + pairs - 1) / pairs * a.num_k;
+  const int total = (a.num_tiles - pair + pairs - 1) / pairs * (kb1 - kb0);
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
@@ -223,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
       int issued = 0, st = 0;
       uint32_t phase = 1;
       bool ok = true;
-      const uint32_t full0 = mapa_shared(bar(B4_FULL), 0);  // the even CTA's
+      const uint32_t full0 = mapa_shared(bar(B4_FULL), even);  // the even CTA's
       for (int tile = pair; tile < a.num_tiles && ok; tile += pairs) {
         int mb, nb;
         tile_coords4(tile, a, mb, nb);
@@ -234,8 +249,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
         const int b_row = (leader ? b_blk0 : b_blk1) * ROWS;
         // (blocks past the operands' rows, and a row's scales past its end, which no product
         // uses, come from wherever they lie in the scales, or as zeros from past their end)
-        int sa = a_blk * a.sf_tiles, sb0 = b_blk0 * a.sf_tiles, sb1 = b_blk1 * a.sf_tiles;
-        for (int kb = 0; kb < a.num_k; ++kb) {
+        const int k_tile = kb0 * ATOMS;
+        int sa = a_blk * a.sf_tiles + k_tile;
+        int sb0 = b_blk0 * a.sf_tiles + k_tile, sb1 = b_blk1 * a.sf_tiles + k_tile;
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(bar(B4_EMPTY + st), phase, a.err, ERR_WAIT_GEMM_PRODUCER)) {
             ok = false;
             break;
@@ -257,6 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
           }
         }
       }
+      launch_next();
       // No copy may still be landing when a CTA exits. The even CTA's barriers count those of
       // both, and neither leaves before the other; where a wait ran out they may never
       // complete, and the time of this wait is what the copies have to land.
@@ -276,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
     if (leader) {
       constexpr uint32_t idesc0 = idesc_e2m1(2 * ROWS, BN4, !NV, 0);
       constexpr uint32_t idesc2 = idesc_e2m1(2 * ROWS, BN4, !NV, 2);
-      constexpr uint16_t kBoth = 3;
+      const uint16_t both = static_cast<uint16_t>(3u << even);
       const uint64_t da0 = sdesc_sw128(smem_u32(smem), 16, 1024);
       auto wait = [&](uint32_t b, uint32_t parity) {
         return mbar_wait_warp(b, parity, a.err, ERR_WAIT_GEMM_MMA);
@@ -290,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
       for (int tile = pair; tile < a.num_tiles && ok; tile += pairs, acc_phase ^= 1u) {
         if (!wait(bar(B4_TEMPTY), acc_phase)) break;
         tc_fence_after();
-        for (int kb = 0; kb < a.num_k; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait(bar(B4_FULL) + st * 8, phase) || !wait(bar(B4_SF) + st * 8, phase)) {
             ok = false;
             break;
@@ -302,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
           auto product = [&](int k) {
             mma_fp4_pair_el<NV>(tmem, ad + k * 2, bd + k * 2, (!NV && (k & 1)) ? idesc2 : idesc0,
                                 sf + (k / ATOM_STEPS) * 4, sf + TM::SFB + (k / ATOM_STEPS) * 8,
-                                (kb | k) != 0 ? 1u : 0u);
+                                (kb > kb0 || k > 0) ? 1u : 0u);
           };
           // a whole stage without a branch between its products (with one before each the
           // pipe ran at 0.79 of this: 7,250 against 9,220 TFLOP/s without loads and stores)
@@ -314,17 +332,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
             if (last > 1) product(1);
             if (last > 2) product(2);
           }
-          mma_commit_pair_mc_el(bar(B4_EMPTY) + st * 8, kBoth);
+          mma_commit_pair_mc_el(bar(B4_EMPTY) + st * 8, both);
           if (++st == STAGES4) {
             st = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        mma_commit_pair_mc_el(bar(B4_TFULL), kBoth);
+        mma_commit_pair_mc_el(bar(B4_TFULL), both);
       }
       // every product must be done with both CTAs' memories before either frees them
-      mma_commit_pair_mc_el(bar(B4_DRAIN), 1);
+      mma_commit_pair_mc_el(bar(B4_DRAIN), static_cast<uint16_t>(1u << even));
       mbar_wait_drain(bar(B4_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(a.err));
     }
   } else if (warp >= 2 + EPI_WARPS) {
@@ -349,9 +367,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
           scale_copy_pair_el(sf + TM::SFB + t * 8, s + ((SFA_BYTES + t * 512) >> 4));
           scale_copy_pair_el(sf + TM::SFB + t * 8 + 4, s + ((SFA_BYTES + 2048 + t * 512) >> 4));
         }
-        mma_commit_pair_mc_el(bar(B4_SF + st), 1);
+        mma_commit_pair_mc_el(bar(B4_SF + st), static_cast<uint16_t>(1u << even));
       }
-      mma_commit_pair_mc_el(bar(B4_DRAIN + 1 + c), 1);
+      mma_commit_pair_mc_el(bar(B4_DRAIN + 1 + c), static_cast<uint16_t>(1u << even));
       mbar_wait_drain(bar(B4_DRAIN + 1 + c), 0u, globaltimer_ns(), drain_limit_ns(a.err));
     }
   } else {
@@ -374,10 +392,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
       float ra = 1.f;
       float4 rb = make_float4(0.f, 0.f, 0.f, 0.f);
       if constexpr (NV) {
-        if (row0 + lane < a.M) ra = __ldg(a.ra + row0 + lane);
+        if (row0 + lane < a.M) ra = *(a.ra + row0 + lane);
         const int b = SWIGLU ? (lane >> 4) * a.up_rows + nb * (BN4 / 2) + side * 64 + (lane & 15) * 4
                              : nb * BN4 + side * (BN4 / 2) + lane * 4;
-        if (SWIGLU || b < a.N) rb = __ldg(reinterpret_cast<const float4*>(a.rb + b));
+        if (SWIGLU || b < a.N) rb = *reinterpret_cast<const float4*>(a.rb + b);
       }
       if (!mbar_wait_warp(bar(B4_TFULL), phase, a.err, ERR_WAIT_GEMM_EPILOGUE)) break;
       tc_fence_after();
@@ -397,7 +415,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
         if (leader)
           mbar_arrive(bar(B4_TEMPTY));
         else
-          mbar_arrive_remote(mapa_shared(bar(B4_TEMPTY), 0));
+          mbar_arrive_remote(mapa_shared(bar(B4_TEMPTY), even));
+      }
+      if constexpr (SPLIT) {
+        // to shared memory, where no load and no product is under way any more: 16 bytes c of row
+        // r at c ^ (r & 31)
+        if (row0 < a.M) {
+          const uint32_t sums = smem_u32(smem) + (quarter * 32 + lane) * (BN4 * 4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col = SWIGLU ? (c >> 1) * (BN4 / 2) + side * 64 + (c & 1) * 32
+                                   : side * (BN4 / 2) + c * 32;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(sums + (((col / 4 + j) ^ lane) << 4), v[c][4 * j], v[c][4 * j + 1],
+                           v[c][4 * j + 2], v[c][4 * j + 3]);
+          }
+        }
+        continue;
       }
       if (row0 >= a.M) continue;
       // eight products, v[c][8 j ..], scaled
@@ -464,6 +499,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();
+  if constexpr (SPLIT) {
+    // this pair's share of the tile's columns, eight of a row to a thread
+    constexpr int WIDTH = SWIGLU ? BN4 / 2 : BN4;
+    int mb, nb;
+    tile_coords4(pair, a, mb, nb);
+    const int g0 = WIDTH / 8 * part / a.parts, groups = WIDTH / 8 * (part + 1) / a.parts - g0;
+    const int first = (2 * mb + static_cast<int>(rank)) * ROWS;
+    const int rows = min(ROWS, a.M - first);
+    const uint32_t sums = smem_u32(smem);
+    for (int i = threadIdx.x; i < rows * groups; i += THREADS4) {
+      const int r = i / groups, g = g0 + i % groups;
+      const int col = nb * WIDTH + g * 8;
+      if (col >= a.N) continue;
+      auto sum8 = [&](int piece, int b, float (&f)[8]) {  // columns 4 piece .. + 7, B's rows b ..
+#pragma unroll
+        for (int t = 0; t < 8; ++t) f[t] = 0.f;
+        for (int p = 0; p < a.parts; ++p) {
+          const uint32_t at = mapa_shared(sums + r * (BN4 * 4), 2 * p + rank);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float4 y;
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                         : "r"(at + (((piece + u) ^ (r & 31)) << 4))
+                         : "memory");
+            f[4 * u] += y.x, f[4 * u + 1] += y.y, f[4 * u + 2] += y.z, f[4 * u + 3] += y.w;
+          }
+        }
+        if constexpr (NV) {
+          const float ra = *(a.ra + first + r);
+          const float4 x = *reinterpret_cast<const float4*>(a.rb + b);
+          const float4 y = reinterpret_cast<const float4*>(a.rb + b)[1];
+          const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * s[t];
+        }
+      };
+      float f[8];
+      sum8(2 * g, col, f);
+      if constexpr (SWIGLU) {
+        float u[8];
+        sum8(BN4 / 8 + 2 * g, a.up_rows + col, u);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) f[t] = silu_f(round_to_bf16(f[t])) * round_to_bf16(u[t]);
+      }
+      *reinterpret_cast<uint4*>(a.C + static_cast<int64_t>(first + r) * a.N + col) =
+          make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                     pack_bf16x2(f[6], f[7]));
+    }
+    cluster_sync_all();  // a peer may still be reading this CTA's sums
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
@@ -473,13 +559,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS4, 1)
 template <bool NV, bool SWIGLU>
 h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int N, int K,
                   cudaStream_t s) {
-  static std::atomic<bool> done[64];
-  h3_status st = set_smem_limit(done, gemm_fp4_kernel<NV, SWIGLU>, SMEM4_BYTES,
+  static std::atomic<bool> done[64], done_split[64];
+  h3_status st = set_smem_limit(done, gemm_fp4_kernel<NV, SWIGLU, false>, SMEM4_BYTES,
                                 "fp4 gemm: set shared memory size");
   if (st != H3_OK) return st;
   const int b_rows = SWIGLU ? 2 * N : N;
   const int tile_n = SWIGLU ? BN4 / 2 : BN4;
   Gemm4Args a{};
+  a.C = static_cast<__nv_bfloat16*>(C);
   a.ra = A.row_scale;
   a.rb = B.row_scale;
   a.M = L;
@@ -504,9 +591,26 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   if ((st = make_tmap_u32_rows(&tmSA, A.scales, 128, ta, atoms)) != H3_OK) return st;
   if ((st = make_tmap_u32_rows(&tmSB, B.scales, 128, tb, atoms)) != H3_OK) return st;
   if ((st = make_tmap_bf16_2d(&tmC, C, N, L, static_cast<uint64_t>(N) * 2, 64, 32)) != H3_OK) return st;
-  const int grid = 2 * std::min(a.num_tiles, num_sms() / 2);
-  gemm_fp4_kernel<NV, SWIGLU><<<grid, THREADS4, SMEM4_BYTES, s>>>(tmA, tmB, tmSA, tmSB, tmC, a);
-  return cuda_fail(cudaGetLastError(), "fp4 gemm launch");
+  // as many pairs to a tile as all tiles find room for, four stages each at least
+  static std::atomic<int> room[64][9];
+  a.parts = 1;
+  for (int p = 4; p >= 2; --p) {
+    if (a.num_tiles * 2 * p > num_sms() || a.num_k < 4 * p) continue;
+    st = set_smem_limit(done_split, gemm_fp4_kernel<NV, SWIGLU, true>, SMEM4_BYTES,
+                        "fp4 gemm: set shared memory size");
+    if (st != H3_OK) return st;
+    if (clusters_at_once(room, gemm_fp4_kernel<NV, SWIGLU, true>, THREADS4, SMEM4_BYTES, 2 * p) >=
+        a.num_tiles) {
+      a.parts = p;
+      break;
+    }
+  }
+  const int grid = 2 * (a.parts > 1 ? a.num_tiles * a.parts : std::min(a.num_tiles, num_sms() / 2));
+  return cuda_fail(
+      launch_overlapped(a.parts > 1 ? gemm_fp4_kernel<NV, SWIGLU, true>
+                                    : gemm_fp4_kernel<NV, SWIGLU, false>,
+                        dim3(grid), THREADS4, SMEM4_BYTES, 2 * a.parts, s, tmA, tmB, tmSA, tmSB, tmC, a),
+      "fp4 gemm launch");
 }
 
 }  // namespace

@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "h3_internal.cuh"
+#include "h3_launch.cuh"
 
 namespace h3 {
 namespace {
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
       if (c < D4) __stcs(orow + c, x[v]);
     }
   }
+  launch_next();
   if (a.normed == nullptr) return;
   norm_row<T, VPT, RMS>(x, D4, a.inv_d, a.eps, red + 2 * (T / 32));
   uint2* hrow = reinterpret_cast<uint2*>(a.normed) + row * D4;

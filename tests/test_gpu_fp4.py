@@ -343,3 +343,24 @@ def test_graph_and_side_stream(h3lib):
         h3lib.linear_fp4(q, qw, y)
     torch.cuda.synchronize()
     assert torch.equal(y, want[1])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("S,N,K", [(1, 256, 2048), (22, 2560, 4096), (128, 3840, 4128), (130, 1288, 5376),
+                                   (300, 2048, 8192), (22, 5376, 5376), (256, 9216, 2080), (22, 24, 16384)])
+def test_few_tiles_share_their_k(h3lib, S, N, K, fmt):
+    # one tile of 256 x 256 to a cluster of two, three and four pairs, and not quite few enough
+    qx = quantize(h3lib, draw(S, K, seed=S + N), fmt)
+    qw = quantize(h3lib, draw(N, K, seed=K, std=0.02), fmt)
+    buf = torch.full((S + 2, N), SENT, dtype=torch.bfloat16, device=dev)
+    y, again = buf[1:S + 1], torch.empty(S, N, dtype=torch.bfloat16, device=dev)
+    h3lib.linear_fp4(qx, qw, y)
+    h3lib.linear_fp4(qx, qw, again)
+    h3lib.check_device_error()
+    check_linear(y, qx, qw, np.arange(S), f"{fmt} {S}x{N}x{K}")
+    assert torch.equal(again, y) and (buf[0] == SENT).all() and (buf[-1] == SENT).all()
+    if N % 256 == 0:
+        out = torch.empty(S, N // 2, dtype=torch.bfloat16, device=dev)
+        h3lib.linear_swiglu_fp4(qx, qw, out)
+        h3lib.check_device_error()
+        check_swiglu(out, y)
