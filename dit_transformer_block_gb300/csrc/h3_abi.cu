@@ -128,6 +128,12 @@ h3_status make_tmap_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, ui
                       box_inner, box_outer);
 }
 
+h3_status make_tmap_f32_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, inner, outer, row_stride_bytes,
+                      box_inner, box_outer);
+}
+
 h3_status make_tmap_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer) {
   return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, outer, row_stride_bytes,

@@ -2,9 +2,10 @@
 // selection of the best of every query block.
 //
 // Scores: the mean row of every query block and key block (FP32), then one product of
-// the means per head. The pooling reads q and k once and is bound by HBM; the product
-// has 1 / block of the attention's own Q K^T to do, in FP32 on the CUDA cores, since a
-// score that is rounded to fewer bits changes which blocks are chosen.
+// the means per head. The pooling reads q and k once and is bound by HBM. A product with
+// rounded means would choose other blocks, so it has FP32's accuracy: each mean is the sum
+// of two TF32 numbers, and three products of those (all but that of the two smaller parts)
+// run on the tensor cores; of few query blocks it runs on the CUDA cores.
 //
 // Selection: the max_blocks-th largest score is found by counting, then one pass writes
 // the chosen indices in ascending order. A warp per row of scores, longer ones a CTA.
@@ -31,7 +32,13 @@ struct PoolSide {
   int L, heads, block, blocks;
   int pairs;   // pairs of heads
   float* out;  // [heads][blocks][128]
+  float* low;  // as out, or NULL: out is then rounded to TF32, and this is what that leaves
 };
+
+// The nearest number of 11 significant bits (ties away from zero).
+__device__ __forceinline__ float to_tf32(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
+}
 
 // A CTA takes a block of rows and two neighbouring heads: a warp reads 512 contiguous
 // bytes of a row, its rows POOL_WARPS apart, and the warps' sums meet in shared memory.
@@ -81,8 +88,16 @@ __global__ void __launch_bounds__(POOL_WARPS * 32)
     float t = 0.f;
 #pragma unroll
     for (int w = 0; w < POOL_WARPS; ++w) t += part[w][threadIdx.x];
-    s.out[(static_cast<int64_t>(head) * s.blocks + blk) * DHB + (threadIdx.x & 127)] =
-        t / static_cast<float>(rows);
+    const float mean = t / static_cast<float>(rows);
+    const int64_t at = (static_cast<int64_t>(head) * s.blocks + blk) * DHB + (threadIdx.x & 127);
+    if (s.low != nullptr) {
+      // (NaN and infinity go whole into the first part)
+      const float hi = fabsf(mean) < INFINITY ? to_tf32(mean) : mean;
+      s.out[at] = hi;
+      s.low[at] = fabsf(mean) < INFINITY ? to_tf32(mean - hi) : 0.f;
+    } else {
+      s.out[at] = mean;
+    }
   }
 }
 
@@ -101,38 +116,34 @@ __device__ __forceinline__ void ffma2_acc(uint64_t& d, float a, float b0, float 
       : "f"(a), "f"(b0), "f"(b1));
 }
 
-// scores[h] = scale * mq[h] mk[g]^T: TMQ x 128 of it per CTA. A thread has TMQ / 8 neighbouring
-// query blocks and eight key blocks 16 apart, two to a packed FMA; both operands lie
+// Few query blocks: scores[h] = scale * mq[h] mk[g]^T, 16 x 128 of it per CTA. A thread has two
+// query blocks and four pairs of key blocks 32 apart, a pair to a packed FMA; both operands lie
 // channel by channel in shared memory, 32 channels at a time, the next ones on their way.
-template <int TMQ>
+constexpr int SC_M = 16;
 __global__ void __launch_bounds__(SC_THREADS)
-    block_scores_kernel(const float* mq, const float* mk,
-                        float* scores, int nq, int nk, int group, float scale) {
-  constexpr int RQ = TMQ / 8;              // rows of a thread
-  constexpr int AV = TMQ * SC_K / 4 / SC_THREADS;  // float4 that a thread loads of A
-  constexpr int BV = SC_N * SC_K / 4 / SC_THREADS;
-  __shared__ __align__(16) float sa[SC_K][TMQ + 4];
+    block_scores_few_kernel(const float* mq, const float* mk, float* scores, int nq, int nk, int group,
+                            float scale) {
+  constexpr int BV = SC_N * SC_K / 4 / SC_THREADS;  // float4 that a thread loads of B; of A, one
+  __shared__ __align__(16) float sa[SC_K][SC_M + 4];
   __shared__ __align__(16) float sb[SC_K][SC_N + 4];
   const int h = blockIdx.z, g = h / group;
-  const int t0 = blockIdx.y * TMQ, b0 = blockIdx.x * SC_N;
+  const int t0 = blockIdx.y * SC_M, b0 = blockIdx.x * SC_N;
   const float4* qa = reinterpret_cast<const float4*>(mq + (static_cast<int64_t>(h) * nq + t0) * DHB);
   const float4* kb = reinterpret_cast<const float4*>(mk + (static_cast<int64_t>(g) * nk + b0) * DHB);
   wait_previous();
   const int tid = threadIdx.x;
-  // A: thread's row tid % TMQ, its AV float4 from (tid / TMQ) * AV on; B: row tid, all of them
-  const int ar = tid % TMQ, ac = tid / TMQ * AV;
+  const int ar = tid % SC_M, ac = tid / SC_M;  // A: its row and float4 of a step; B: row tid
   const bool a_in = t0 + ar < nq, b_in = b0 + tid < nk;
-  float4 av[AV], bv[BV];
+  float4 av, bv[BV];
   auto fetch = [&](int k4) {
     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < AV; ++i) av[i] = a_in ? qa[ar * (DHB / 4) + k4 + ac + i] : z;
+    av = a_in ? qa[ar * (DHB / 4) + k4 + ac] : z;
 #pragma unroll
     for (int i = 0; i < BV; ++i) bv[i] = b_in ? kb[tid * (DHB / 4) + k4 + i] : z;
   };
-  uint64_t acc[RQ][4];
+  uint64_t acc[2][4];
 #pragma unroll
-  for (int i = 0; i < RQ; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
   const int ty = tid >> 4, tx = tid & 15;
@@ -140,125 +151,285 @@ __global__ void __launch_bounds__(SC_THREADS)
 #pragma unroll 1
   for (int k0 = 0; k0 < DHB; k0 += SC_K) {
     if (k0 > 0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < AV; ++i) {
-      const float w[4] = {av[i].x, av[i].y, av[i].z, av[i].w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) sa[4 * (ac + i) + c][ar] = w[c] * scale;
-    }
+    sa[4 * ac][ar] = av.x * scale, sa[4 * ac + 1][ar] = av.y * scale;
+    sa[4 * ac + 2][ar] = av.z * scale, sa[4 * ac + 3][ar] = av.w * scale;
 #pragma unroll
     for (int i = 0; i < BV; ++i) {
-      const float w[4] = {bv[i].x, bv[i].y, bv[i].z, bv[i].w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) sb[4 * i + c][tid] = w[c];
+      sb[4 * i][tid] = bv[i].x, sb[4 * i + 1][tid] = bv[i].y;
+      sb[4 * i + 2][tid] = bv[i].z, sb[4 * i + 3][tid] = bv[i].w;
     }
     __syncthreads();
     if (k0 + SC_K < DHB) fetch((k0 + SC_K) / 4);
 #pragma unroll 8
     for (int c = 0; c < SC_K; ++c) {
-      float x[RQ], y[8];
+      const float2 x = *reinterpret_cast<const float2*>(&sa[c][ty * 2]);
 #pragma unroll
-      for (int i = 0; i < RQ; ++i) x[i] = sa[c][ty * RQ + i];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = sb[c][tx + 16 * j];
-#pragma unroll
-      for (int i = 0; i < RQ; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ffma2_acc(acc[i][j], x[i], y[2 * j], y[2 * j + 1]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = *reinterpret_cast<const float2*>(&sb[c][2 * tx + 32 * j]);
+        ffma2_acc(acc[0][j], x.x, y.x, y.y);
+        ffma2_acc(acc[1][j], x.y, y.x, y.y);
+      }
     }
   }
   launch_next();
 #pragma unroll
-  for (int i = 0; i < RQ; ++i) {
-    const int t = t0 + ty * RQ + i;
+  for (int i = 0; i < 2; ++i) {
+    const int t = t0 + ty * 2 + i;
     if (t >= nq) break;
-    float* o = scores + (static_cast<int64_t>(h) * nq + t) * nk + b0 + tx;
+    const int b = b0 + 2 * tx;
+    float* o = scores + (static_cast<int64_t>(h) * nq + t) * nk + b;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t w = static_cast<uint32_t>(acc[i][j >> 1] >> (32 * (j & 1)));
-      if (b0 + tx + 16 * j < nk) o[16 * j] = __uint_as_float(w);
+    for (int j = 0; j < 4; ++j) {
+      if (b + 32 * j < nk) o[32 * j] = __uint_as_float(static_cast<uint32_t>(acc[i][j]));
+      if (b + 32 * j + 1 < nk) o[32 * j + 1] = __uint_as_float(static_cast<uint32_t>(acc[i][j] >> 32));
     }
   }
 }
 
-// ---------------------------------------------------------------- selection
-// Scores as integers of the same order: 0 for what is never selected (-inf, NaN), the
-// largest for the blocks that always are; -0 and +0 are the same.
-__device__ __forceinline__ uint32_t select_key(float f, bool kept) {
-  if (kept) return 0xffffffffu;
-  if (!(f > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(f == 0.f ? 0.f : f);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+// The tensor-core form: 128 query blocks x 128 key blocks of a head per CTA (230 x 919 blocks of 42
+// heads in 30 us, and 75 us by FP32 FMAs; three CTAs to an SM of one stage each are no faster).
+// A stage is 32
+// channels (128 bytes a row) of both parts of both operands; warp 0 loads (TMA), warp 1
+// issues, per 8 channels, three products into one FP32 accumulator, and warps 2 to 5 write the
+// scores, row by row through shared memory, since a row of them starts at any 4 bytes.
+constexpr int TC_TILE = 128, TC_STAGES = 3, TC_STEPS = DHB / 32;
+constexpr int TC_PART = TC_TILE * 128;         // 16 KB: 128 rows x 32 channels
+constexpr int TC_STAGE_BYTES = 4 * TC_PART;    // A high, A low, B high, B low
+constexpr int TC_THREADS = 192;
+constexpr size_t TC_SMEM_BYTES = 1024 + TC_STAGES * TC_STAGE_BYTES + 128;
+static_assert(TC_SMEM_BYTES <= 227 * 1024, "block scores shared memory");
+enum BarTc { BT_FULL = 0, BT_EMPTY = TC_STAGES, BT_DONE = 2 * TC_STAGES, BT_NUM = BT_DONE + 1 };
+
+__device__ __forceinline__ void mma_tf32_el(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
-constexpr uint32_t KEPT = 0xffffffffu;
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    block_scores_kernel(const __grid_constant__ CUtensorMap tmQh, const __grid_constant__ CUtensorMap tmQl,
+                        const __grid_constant__ CUtensorMap tmKh, const __grid_constant__ CUtensorMap tmKl,
+                        float* scores, int nq, int nk, int group, float scale, const DevErr err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + TC_STAGES * TC_STAGE_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BT_NUM);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.z, t0 = blockIdx.y * TC_TILE, b0 = blockIdx.x * TC_TILE;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < BT_NUM; ++i) mbar_init(bar(i), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), TC_TILE);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  wait_previous();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // (rows past the head's last block are the next head's, or zeros; nothing is stored of them)
+      const int qrow = h * nq + t0, krow = h / group * nk + b0;
+      int issued = 0;
+      for (int c = 0; c < TC_STEPS; ++c) {
+        const int st = c % TC_STAGES;
+        if (!mbar_wait(bar(BT_EMPTY + st), (static_cast<uint32_t>(c / TC_STAGES) & 1u) ^ 1u, err,
+                       ERR_WAIT_GEMM_PRODUCER))
+          break;
+        const uint32_t full = bar(BT_FULL + st), dst = smem_u32(smem + st * TC_STAGE_BYTES);
+        mbar_arrive_expect_tx(full, TC_STAGE_BYTES);
+        tma_load_2d(dst, &tmQh, full, c * 32, qrow);
+        tma_load_2d(dst + TC_PART, &tmQl, full, c * 32, qrow);
+        tma_load_2d(dst + 2 * TC_PART, &tmKh, full, c * 32, krow);
+        tma_load_2d(dst + 3 * TC_PART, &tmKl, full, c * 32, krow);
+        issued = c + 1;
+      }
+      launch_next();
+      const uint64_t at = globaltimer_ns();
+      for (int c = issued > TC_STAGES ? issued - TC_STAGES : 0; c < issued; ++c)
+        mbar_wait_drain(bar(BT_FULL + c % TC_STAGES), static_cast<uint32_t>(c / TC_STAGES) & 1u, at,
+                        drain_limit_ns(err));
+    }
+  } else if (warp == 1) {
+    // instruction descriptor: f32 accumulator, TF32 operands (format 2), both K-major
+    constexpr uint32_t idesc = (1u << 4) | (2u << 7) | (2u << 10) |
+                               (static_cast<uint32_t>(TC_TILE >> 3) << 17) |
+                               (static_cast<uint32_t>(TC_TILE >> 4) << 24);
+    const uint64_t base = sdesc_sw128(smem_u32(smem), 16, 1024);
+    for (int c = 0; c < TC_STEPS; ++c) {
+      const int st = c % TC_STAGES;
+      if (!mbar_wait_warp(bar(BT_FULL + st), static_cast<uint32_t>(c / TC_STAGES) & 1u, err,
+                          ERR_WAIT_GEMM_MMA))
+        break;
+      tc_fence_after();
+      const uint64_t ah = base + static_cast<uint32_t>(st * (TC_STAGE_BYTES >> 4));
+      const uint64_t al = ah + (TC_PART >> 4), bh = ah + (2 * TC_PART >> 4);
+      const uint64_t bl = ah + (3 * TC_PART >> 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        mma_tf32_el(tmem, ah + k * 2, bl + k * 2, idesc, (c | k) != 0 ? 1u : 0u);
+        mma_tf32_el(tmem, al + k * 2, bh + k * 2, idesc, 1u);
+        mma_tf32_el(tmem, ah + k * 2, bh + k * 2, idesc, 1u);
+      }
+      mma_commit_el(bar(BT_EMPTY + st));
+    }
+    mma_commit_el(bar(BT_DONE));
+    mbar_wait_drain(bar(BT_DONE), 0u, globaltimer_ns(), drain_limit_ns(err));
+  } else {
+    const int quarter = warp & 3;
+    if (mbar_wait_warp(bar(BT_DONE), 0u, err, ERR_WAIT_GEMM_EPILOGUE)) {
+      tc_fence_after();
+      // the warp's 32 rows x 128 scores, float4 c of row r at c ^ (r & 31): no load and no product
+      // is under way any more
+      float4* rows = reinterpret_cast<float4*>(smem) + (warp - 2) * 32 * (TC_TILE / 4);
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        tmem_ld32(t_row + c * 32, v);
+        tmem_ld_wait();
+        tmem_reg_fence(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          rows[lane * (TC_TILE / 4) + ((c * 8 + j) ^ lane)] =
+              make_float4(__uint_as_float(v[4 * j]) * scale, __uint_as_float(v[4 * j + 1]) * scale,
+                          __uint_as_float(v[4 * j + 2]) * scale, __uint_as_float(v[4 * j + 3]) * scale);
+      }
+      __syncwarp();
+      const int first = t0 + quarter * 32, n = min(32, nq - first);
+      const float* words = reinterpret_cast<const float*>(rows);
+      for (int r = 0; r < n; ++r) {
+        float* o = scores + (static_cast<int64_t>(h) * nq + first + r) * nk + b0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int b = j * 32 + lane;
+          if (b0 + b < nk) o[b] = words[r * TC_TILE + (((b >> 2) ^ r) << 2) + (b & 3)];
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TC_TILE);
+  }
+}
+
+// ---------------------------------------------------------------- selection
+// Scores as integers of the same order, -0 as +0; NONE for what is never selected (-inf, NaN),
+// below all others, and KEPT for the blocks that always are, above them.
+constexpr uint32_t NONE = 0x007fffffu, KEPT = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t select_key(float f) {
+  const uint32_t u = __float_as_uint(fmaxf(f, -INFINITY) + 0.f);  // (of a NaN the maximum is -inf)
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
 constexpr int SEL_WARPS = 4;
 
-// Rows of at most 32 * IPT scores: a warp per row, whose keys stay in its registers. The
-// threshold T (the least selected key) is looked for between lo and hi, of which at least
-// and fewer than `most` keys are not below; every step counts the keys from a place between them
-// on. The first place is where a normal distribution of the row's mean and deviation has
-// `most` (z deviations above the mean), the second as far from it as that density says, a
-// dozen keys further, and from then on the middle: rows as scores are take two or three
-// steps, any others at most 32 more. With at most 32 keys left between lo and hi, a lane
-// takes one and ranks it among them.
+// Rows r of a 32 x 32 bit matrix, one in every lane, to its columns.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  constexpr uint32_t keep[5] = {0x0000ffffu, 0x00ff00ffu, 0x0f0f0f0fu, 0x33333333u, 0x55555555u};
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int m = 16 >> i;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, m);
+    x = (lane & m) != 0 ? (x & ~keep[i]) | ((y >> m) & keep[i]) : (x & keep[i]) | ((y & keep[i]) << m);
+  }
+  return x;
+}
+
+// Sum of v over the lanes before this one.
+__device__ __forceinline__ int lanes_before(int v, int lane) {
+  int t = v;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, t, m);
+    if (lane >= m) t += o;
+  }
+  return t - v;
+}
+
+// Rows of at most 32 * IPT scores (IPT up to 32): a warp per row, whose keys stay in its
+// registers. The threshold T (the least selected key) is looked for between lo and hi, of
+// which at least and fewer than `most` keys are not below; every step counts the keys from a
+// place between them on. The first place is where a normal distribution of the row's mean and
+// deviation (of every other 32 scores) has `most` (z deviations above the mean), the second as
+// far from it as that density says, a dozen keys further, and from then on the middle: rows
+// as scores are take two or three steps, any others at most 32 more. With at most 32 keys left
+// between lo and hi, a lane takes one, and they go from the largest down. Bound by
+// instructions, most of them at half rate; so indices are not written 32 scores at a time but
+// from each lane's bits, a 32 x 32 matrix that is transposed, where a lane then has 32
+// neighbouring ones. (9,660 rows of 919 scores in 21 us, 6 for their bytes; 27 with the
+// indices written by a vote per 32 scores.)
 template <int IPT>
 __global__ void __launch_bounds__(SEL_WARPS * 32)
-    block_select_warp_kernel(const float* scores, int32_t* ids,
-                             int32_t* counts, int rows, int nk, int most, int first,
-                             int last, float z, float density) {
+    block_select_warp_kernel(const float* scores, int32_t* ids, int32_t* counts, int rows, int nk,
+                             int most, int first, int last, float z, float density) {
   __shared__ uint32_t left[SEL_WARPS][32];
   wait_previous();
-  const int tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * SEL_WARPS + warp;
   if (row >= rows) return;
   const float* s = scores + static_cast<int64_t>(row) * nk;
   int32_t* out = ids + static_cast<int64_t>(row) * most;
   uint32_t key[IPT];
   float sum = 0.f, sum2 = 0.f;
-  int valid = 0, kept = 0;
-  {
-    float f[IPT];
 #pragma unroll
-    for (int r = 0; r < IPT; ++r) {
-      const int i = r * 32 + lane;
-      f[r] = i < nk ? __ldcs(s + i) : -INFINITY;
-    }
+  for (int r = 0; r < IPT; ++r)
+    key[r] = __float_as_uint(r * 32 + lane < nk ? s[r * 32 + lane] : -INFINITY);
 #pragma unroll
-    for (int r = 0; r < IPT; ++r) {
-      const int i = r * 32 + lane;
-      key[r] = select_key(f[r], i < nk && (i < first || i >= nk - last));
-      valid += key[r] != 0u;
-      kept += key[r] == KEPT;
-      const float v = key[r] != 0u && key[r] != KEPT ? f[r] : 0.f;
+  for (int r = 0; r < IPT; ++r) {
+    const float f = __uint_as_float(key[r]);
+    if ((r & 1) == 0) {
+      const float v = f > -INFINITY ? f : 0.f;
       sum += v;
       sum2 = fmaf(v, v, sum2);
     }
+    key[r] = select_key(f);
   }
-  valid = __reduce_add_sync(0xffffffffu, valid);
-  kept = __reduce_add_sync(0xffffffffu, kept);
+  const int kept = min(first + last, nk);
+  if (kept > 0) {
+#pragma unroll
+    for (int r = 0; r < IPT; ++r)
+      if (r * 32 < first || r * 32 + 32 > nk - last) {
+        const int i = r * 32 + lane;
+        if (i < nk && (i < first || i >= nk - last)) key[r] = KEPT;
+      }
+  }
   // T, and how many of the keys equal to it are selected (the first of them)
-  uint32_t T = 0;
+  uint32_t T = NONE;
   int equal = 0;
   if (kept >= most) {
     T = KEPT - 1u;
-  } else if (valid > most) {
+  } else if (nk > most) {
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, m);
       sum2 += __shfl_xor_sync(0xffffffffu, sum2, m);
     }
-    const float n = static_cast<float>(valid - kept);
+    const float n = static_cast<float>((nk + 63) / 64 * 32);  // (of the mean; a guess is enough)
     const float mean = sum / n;
     const float dev = sqrtf(fmaxf(sum2 / n - mean * mean, 0.f));
-    uint32_t lo = 1u, hi = KEPT;
-    int c_lo = valid, c_hi = kept;  // keys from lo, from hi on
+    const float per_key = dev / (static_cast<float>(nk) * density);
+    uint32_t lo = NONE, hi = KEPT;
+    int c_lo = nk, c_hi = kept;  // keys from lo, from hi on
     float at = fmaf(z, dev, mean);
     for (int step = 0;; ++step) {
       uint32_t place = lo + (hi - lo) / 2;
-      if (step < 2 && at > -INFINITY && at < INFINITY) {
-        const uint32_t k = select_key(at, false);
+      if (step < 2) {
+        const uint32_t k = select_key(at);
         if (k > lo && k < hi) place = k;
       }
       int c = 0;
@@ -268,54 +439,69 @@ __global__ void __launch_bounds__(SEL_WARPS * 32)
       if (c >= most) {
         lo = place, c_lo = c;
         if (c == most) break;
-        at += (c - most + 12) * dev / (n * density);
+        at = fmaf(static_cast<float>(c - most + 12), per_key, at);
       } else {
         hi = place, c_hi = c;
-        at -= (most - c + 12) * dev / (n * density);
+        at = fmaf(static_cast<float>(c - most - 12), per_key, at);
       }
       if (c_lo - c_hi <= 32 || hi - lo == 1u) break;
     }
-    const int need = most - c_hi;
+    int need = most - c_hi;
     if (c_lo == most) {
       T = lo - 1u;  // all from lo on
     } else if (hi - lo == 1u) {
       T = lo;
       equal = need;
     } else {
-      int base = 0;
+      // the keys between, read again where they lie
+      uint32_t bits = 0;
 #pragma unroll
-      for (int r = 0; r < IPT; ++r) {
-        const bool in = key[r] >= lo && key[r] < hi;
-        const uint32_t b = __ballot_sync(0xffffffffu, in);
-        if (in) left[warp][base + __popc(b & ((1u << lane) - 1u))] = key[r];
-        base += __popc(b);
+      for (int r = 0; r < IPT; ++r) bits |= key[r] - lo < hi - lo ? 1u << r : 0u;
+      uint32_t mine = transpose_bits(bits, lane);  // scores 32 lane .. 32 lane + 31
+      if (lane * 32 + 32 > nk) mine &= lane * 32 < nk ? (1u << (nk & 31)) - 1u : 0u;
+      int at_left = lanes_before(__popc(mine), lane);
+      while (mine != 0u) {
+        const int j = __ffs(mine) - 1;
+        mine &= mine - 1u;
+        left[warp][at_left++] = select_key(s[lane * 32 + j]);
       }
       __syncwarp();
-      const uint32_t mine = lane < base ? left[warp][lane] : 0u;
-      int above = 0, rank = 0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t other = __shfl_sync(0xffffffffu, mine, j);
-        above += other > mine;
-        rank += other > mine || (other == mine && j < lane);
+      uint32_t k = lane < c_lo - c_hi ? left[warp][lane] : 0u;
+      for (;;) {
+        T = __reduce_max_sync(0xffffffffu, k);
+        const int same = __popc(__ballot_sync(0xffffffffu, k == T));
+        if (same >= need || T == 0u) {
+          equal = same == need ? 0 : need;
+          if (same == need) --T;  // all of them: what is above T - 1
+          break;
+        }
+        need -= same;
+        if (k == T) k = 0u;
       }
-      const uint32_t b = __ballot_sync(0xffffffffu, rank == need - 1 && lane < base);
-      const int who = __ffs(b) - 1;
-      T = __shfl_sync(0xffffffffu, mine, who);
-      equal = need - __shfl_sync(0xffffffffu, above, who);
     }
+    if (T <= NONE) T = NONE, equal = 0;  // fewer than wanted: all but -inf and NaN
   }
   launch_next();
-  const uint32_t below = (1u << lane) - 1u;
-  int n = 0, eq = 0;
+  uint32_t bits = 0, same = 0;
 #pragma unroll
-  for (int r = 0; r < IPT; ++r) {
-    const uint32_t same = __ballot_sync(0xffffffffu, key[r] == T && T != 0u);
-    const bool in = key[r] > T || (key[r] == T && T != 0u && eq + __popc(same & below) < equal);
-    const uint32_t b = __ballot_sync(0xffffffffu, in);
-    if (in) out[n + __popc(b & below)] = r * 32 + lane;
-    n += __popc(b);
-    eq += __popc(same);
+  for (int r = 0; r < IPT; ++r) bits |= key[r] > T ? 1u << r : 0u;
+  bits = transpose_bits(bits, lane);
+  if (equal > 0) {
+#pragma unroll
+    for (int r = 0; r < IPT; ++r) same |= key[r] == T ? 1u << r : 0u;
+    same = transpose_bits(same, lane);
+    int take = min(max(equal - lanes_before(__popc(same), lane), 0), __popc(same));
+    while (take-- > 0) {  // the first of them
+      bits |= same & (0u - same);
+      same &= same - 1u;
+    }
+  }
+  const int mine = __popc(bits);
+  int at = lanes_before(mine, lane);
+  const int n = __shfl_sync(0xffffffffu, at + mine, 31);
+  while (bits != 0u) {
+    out[at++] = lane * 32 + __ffs(bits) - 1;
+    bits &= bits - 1u;
   }
   for (int i = n + lane; i < most; i += 32) out[i] = -1;
   if (lane == 0) counts[row] = n;
@@ -334,17 +520,17 @@ __global__ void __launch_bounds__(T)
   int32_t* out = ids + row * most;
   wait_previous();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto key = [&](int i) { return select_key(*(s + i), i < first || i >= nk - last); };
+  auto key = [&](int i) { return i < first || i >= nk - last ? KEPT : select_key(s[i]); };
 
   // threshold: what is above it is selected, and of what is equal to it the first `equal`
-  uint32_t prefix = 0, mask = 0, threshold = 0;
+  uint32_t prefix = 0, mask = 0, threshold = NONE;
   int need = most, equal = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
     for (int i = tid; i < 256; i += T) hist[i] = 0;
     __syncthreads();
     for (int i = tid; i < nk; i += T) {
       const uint32_t k = key(i);
-      if (k != 0u && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+      if (k > NONE && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
     }
     __syncthreads();
     if (warp == 0) {
@@ -375,12 +561,12 @@ __global__ void __launch_bounds__(T)
       }
     }
     __syncthreads();
-    if (found[0] < 0) break;  // threshold 0
+    if (found[0] < 0) break;  // threshold NONE
     prefix |= static_cast<uint32_t>(found[0]) << shift;
     mask |= 255u << shift;
     need = found[1];
     if (need == found[2]) {  // all of the bin
-      threshold = prefix != 0u ? prefix - 1u : 0u;
+      threshold = max(prefix, NONE + 1u) - 1u;
       equal = 0;
       break;
     }
@@ -423,30 +609,54 @@ __global__ void __launch_bounds__(T)
 
 }  // namespace
 
+// Query blocks up to which the product runs on the CUDA cores: one tile of theirs, where the
+// tensor cores' 128 rows would be mostly empty.
+constexpr int SCORES_FEW = SC_M;
+
 size_t block_scores_workspace_bytes(int nq, int nk, int H, int Hkv) {
-  return (static_cast<size_t>(nq) * H + static_cast<size_t>(nk) * Hkv) * DHB * sizeof(float);
+  const size_t means = static_cast<size_t>(nq) * H + static_cast<size_t>(nk) * Hkv;
+  return means * DHB * sizeof(float) * (nq > SCORES_FEW ? 2 : 1);
 }
 
 h3_status launch_block_scores(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
                               float* scores, int Lq, int Lk, int H, int Hkv, int k_block,
                               float scale, void* workspace, cudaStream_t s) {
   const int nq = (Lq + H3_QUERY_BLOCK - 1) / H3_QUERY_BLOCK, nk = (Lk + k_block - 1) / k_block;
+  const bool few = nq <= SCORES_FEW;
+  const int64_t q_rows = static_cast<int64_t>(nq) * H, k_rows = static_cast<int64_t>(nk) * Hkv;
   float* mq = static_cast<float*>(workspace);
-  float* mk = mq + static_cast<int64_t>(nq) * H * DHB;
+  float* mk = mq + q_rows * DHB;
+  float* lq = few ? nullptr : mk + k_rows * DHB;
+  float* lk = few ? nullptr : lq + q_rows * DHB;
   const PoolSide qs{static_cast<const __nv_bfloat16*>(q), ld_q, Lq, H, H3_QUERY_BLOCK, nq,
-                    (H + 1) / 2, mq};
+                    (H + 1) / 2, mq, lq};
   const PoolSide ks{static_cast<const __nv_bfloat16*>(k), ld_k, Lk, Hkv, k_block, nk,
-                    (Hkv + 1) / 2, mk};
+                    (Hkv + 1) / 2, mk, lk};
   const int q_ctas = nq * qs.pairs;
   h3_status st = cuda_fail(launch_overlapped(pool_kernel, dim3(q_ctas + nk * ks.pairs),
                                              POOL_WARPS * 32, 0, 1, s, qs, ks, q_ctas),
                            "block pooling launch");
   if (st != H3_OK) return st;
-  const int tile = nq <= 16 ? 16 : 64;
-  const dim3 grid((nk + SC_N - 1) / SC_N, (nq + tile - 1) / tile, H);
-  return cuda_fail(launch_overlapped(tile == 16 ? block_scores_kernel<16> : block_scores_kernel<64>,
-                                     grid, SC_THREADS, 0, 1, s, mq, mk, scores, nq, nk, H / Hkv,
-                                     scale),
+  if (few) {
+    const dim3 grid((nk + SC_N - 1) / SC_N, (nq + SC_M - 1) / SC_M, H);
+    return cuda_fail(launch_overlapped(block_scores_few_kernel, grid, SC_THREADS, 0, 1, s, mq, mk,
+                                       scores, nq, nk, H / Hkv, scale),
+                     "block scores launch");
+  }
+  static std::atomic<bool> done[64];
+  st = set_smem_limit(done, block_scores_kernel, TC_SMEM_BYTES, "block scores: set shared memory size");
+  if (st != H3_OK) return st;
+  DevErr err;
+  if ((st = dev_err(&err)) != H3_OK) return st;
+  CUtensorMap t[4];
+  const float* parts[4] = {mq, lq, mk, lk};
+  for (int i = 0; i < 4; ++i)
+    if ((st = make_tmap_f32_2d(&t[i], parts[i], DHB, i < 2 ? q_rows : k_rows, DHB * 4, 32, TC_TILE)) !=
+        H3_OK)
+      return st;
+  const dim3 grid((nk + TC_TILE - 1) / TC_TILE, (nq + TC_TILE - 1) / TC_TILE, H);
+  return cuda_fail(launch_overlapped(block_scores_kernel, grid, TC_THREADS, TC_SMEM_BYTES, 1, s, t[0],
+                                     t[1], t[2], t[3], scores, nq, nk, H / Hkv, scale, err),
                    "block scores launch");
 }
 
@@ -454,7 +664,7 @@ h3_status launch_block_select(const float* scores, int32_t* ids, int32_t* counts
                               int nk, int max_blocks, int keep_first, int keep_last,
                               cudaStream_t s) {
   cudaError_t e;
-  if (nk <= 2048) {
+  if (nk <= 1024) {
     // z: where a normal distribution has max_blocks / nk of it above (Abramowitz and Stegun,
     // Handbook of Mathematical Functions, 26.2.23: off by less than 4.5e-4), and its density there
     const double share = std::min(0.999, std::max(1e-6, static_cast<double>(max_blocks) / nk));
@@ -470,8 +680,7 @@ h3_status launch_block_select(const float* scores, int32_t* ids, int32_t* counts
                   : nk <= 256  ? block_select_warp_kernel<8>
                   : nk <= 512  ? block_select_warp_kernel<16>
                   : nk <= 768  ? block_select_warp_kernel<24>
-                  : nk <= 1024 ? block_select_warp_kernel<32>
-                               : block_select_warp_kernel<64>;
+                               : block_select_warp_kernel<32>;
     e = launch_overlapped(kernel, dim3(grid), SEL_WARPS * 32, 0, 1, s, scores, ids, counts, rows, nk,
                           max_blocks, keep_first, keep_last, zf, df);
   } else {

@@ -46,6 +46,10 @@ h3_status make_tmap_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, ui
 h3_status make_tmap_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// Same for a tensor of float32.
+h3_status make_tmap_f32_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+
 // `outer` contiguous rows of `inner` 32-bit words (at most 256), boxes of box_outer whole
 // rows, no swizzle, zero fill past the last row.
 h3_status make_tmap_u32_rows(CUtensorMap* m, const void* base, uint32_t inner, uint64_t outer,

@@ -705,16 +705,38 @@ def block_forward(cfg: BlockConfig, weights, resid, mod, pos, workspace, stream=
 
 
 # Norms around a branch, 4-bit rows and block-sparse attention: like the paged calls they run
-# several times per layer, so their checks are attribute reads.
-def _vec(t, name, dev, D, groups):
-    """Pointer of a [D] f32 vector, or with groups of a [groups, D] table's first row."""
+# several times per layer, so a tensor that is as it should be costs a few attribute reads.
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _here(t, name) -> int:
+    """The device of the first tensor of a call, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current CUDA device, is on {t.device}")
+    return dev
+
+
+def _tensor(t, name, dtype, shape, dev):
+    """Pointer of a contiguous tensor of this type and shape, or NULL for None."""
     if t is None:
         return None
-    if t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
-    if t.shape != ((D,) if groups is None else (groups, D)) or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be {[D] if groups is None else [groups, D]} with "
-                         f"neighbouring values, got {list(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        _flat(t, name, dtype, dev)
+    return t.data_ptr()
+
+
+def _table(t, name, shape, stride, dev):
+    """Pointer of the first row of a [groups, D] f32 table, or NULL for None."""
+    if t is None:
+        return None
+    if t.dtype is not _F32:
+        raise TypeError(f"{name} must be {_F32}, got {t.dtype}")
+    if t.shape != shape or t.stride(1) != 1 or (shape[0] > 1 and t.stride(0) != stride):
+        raise ValueError(f"{name} must be {list(shape)} with neighbouring values and rows as far "
+                         f"apart as the other tables', got {list(t.shape)} of strides {t.stride()}")
     _on(t, name, dev)
     return t.data_ptr()
 
@@ -729,39 +751,38 @@ def sandwich_norm(resid, delta=None, normed=None, resid_out=None, post_norm=True
     [S,D] f32, delta, normed [S,D] bf16; vectors [D] f32, left out where None. With seg [S]
     int32, gate, shift and scale are [G,D] tables (rows equally far apart, as columns of a
     [G,6,D] one are) and row i takes row seg[i] of them."""
-    dev = _device()
-    S, D = resid.shape
-    _flat(resid, "resid", torch.float32, dev)
-    for n, t, dtype in (("delta", delta, torch.bfloat16), ("normed", normed, torch.bfloat16),
-                        ("resid_out", resid_out, torch.float32)):
-        if t is not None:
-            if t.shape != resid.shape:
-                raise ValueError(f"{n} must be {[S, D]}, got {list(t.shape)}")
-            _flat(t, n, dtype, dev)
+    shape = resid.shape
+    S, D = shape
+    dev = _here(resid, "resid")
+    pr = _tensor(resid, "resid", _F32, shape, dev)
+    pd = _tensor(delta, "delta", _BF16, shape, dev)
+    pn = _tensor(normed, "normed", _BF16, shape, dev)
     if delta is None:
         post_norm = False
-    if resid_out is None and (delta is not None or resid_scale != 1.0):
-        resid_out = resid
-    groups, stride, pseg = None, 0, None
-    if seg is not None:
-        if seg.shape != (S,):
-            raise ValueError(f"seg must be [{S}], got {list(seg.shape)}")
-        _flat(seg, "seg", torch.int32, dev)
-        pseg, groups, stride = seg.data_ptr(), 1, D
-        tables = [t for t in (gate, shift, scale) if t is not None]
-        if tables:
-            groups = tables[0].shape[0]
-            stride = tables[0].stride(0) if groups > 1 else D
-            if groups > 1 and any(t.dim() != 2 or t.stride(0) != stride for t in tables):
-                raise ValueError("the rows of gate, shift and scale must be equally far apart")
-    _check("sandwich_norm", lib().h3_sandwich_norm(
-        resid.data_ptr(), None if delta is None else delta.data_ptr(),
-        None if resid_out is None else resid_out.data_ptr(),
-        None if normed is None else normed.data_ptr(), int(post_norm),
-        _vec(post_gain, "post_gain", dev, D, None), _vec(gate, "gate", dev, D, groups),
-        resid_scale, _vec(pre_gain, "pre_gain", dev, D, None), _vec(shift, "shift", dev, D, groups),
-        _vec(scale, "scale", dev, D, groups), pseg, groups or 1, stride, int(rms), S,
-        S if L is None else L, D, eps, _raw_stream(stream, dev)))
+    if resid_out is None:
+        po = pr if delta is not None or resid_scale != 1.0 else None
+    else:
+        po = _tensor(resid_out, "resid_out", _F32, shape, dev)
+    vec = (D,)
+    if seg is None:
+        pseg, groups, stride = None, 1, 0
+        pg = _tensor(gate, "gate", _F32, vec, dev)
+        ph = _tensor(shift, "shift", _F32, vec, dev)
+        pc = _tensor(scale, "scale", _F32, vec, dev)
+    else:
+        pseg = _tensor(seg, "seg", _I32, (S,), dev)
+        first = gate if gate is not None else shift if shift is not None else scale
+        groups = 1 if first is None else first.shape[0]
+        stride = D if groups == 1 else first.stride(0)
+        pg = _table(gate, "gate", (groups, D), stride, dev)
+        ph = _table(shift, "shift", (groups, D), stride, dev)
+        pc = _table(scale, "scale", (groups, D), stride, dev)
+    status = (_lib or lib()).h3_sandwich_norm(
+        pr, pd, po, pn, post_norm, _tensor(post_gain, "post_gain", _F32, vec, dev), pg, resid_scale,
+        _tensor(pre_gain, "pre_gain", _F32, vec, dev), ph, pc, pseg, groups, stride, rms, S,
+        S if L is None else L, D, eps, _raw_stream(stream, dev))
+    if status:
+        _check("sandwich_norm", status)
 
 
 FP4_FORMATS = {"mx": 0, "nv": 1}
@@ -770,7 +791,8 @@ FP4_FORMATS = {"mx": 0, "nv": 1}
 class Fp4Rows:
     """A matrix [R, K] of 4-bit rows: codes [R, K/2] uint8, scales (bytes, in the library's
     tiles), row_scale [R] f32 ("nv") or None ("mx"). fp4_rows makes room for one."""
-    __slots__ = ("codes", "scales", "row_scale", "format", "R", "K", "device")
+    __slots__ = ("codes", "scales", "row_scale", "format", "R", "K", "shape", "device", "pointers",
+                 "number")
 
     def __init__(self, codes, scales, row_scale, format):
         if format not in FP4_FORMATS:
@@ -791,14 +813,10 @@ class Fp4Rows:
             if row_scale.shape != (self.R,):
                 raise ValueError(f"row_scale must be [{self.R}], got {list(row_scale.shape)}")
         self.codes, self.scales, self.row_scale = codes, scales, row_scale
-        self.format, self.device = format, dev
-
-    def _pointers(self, dev, name):
-        if self.device != dev or dev < 0:
-            raise ValueError(f"{name} must be on the current CUDA device, is on device "
-                             f"{self.device}")
-        return (self.codes.data_ptr(), self.scales.data_ptr(),
-                None if self.row_scale is None else self.row_scale.data_ptr())
+        self.format, self.number, self.device = format, FP4_FORMATS[format], dev
+        self.shape = (self.R, self.K)
+        self.pointers = (codes.data_ptr(), scales.data_ptr(),
+                         None if row_scale is None else row_scale.data_ptr())
 
 
 def fp4_scale_bytes(R: int, K: int, format: str = "nv") -> int:
@@ -821,38 +839,53 @@ def fp4_rows(R: int, K: int, format: str = "nv", device=None) -> Fp4Rows:
                    format)
 
 
+def _same_device(q: Fp4Rows, name, dev):
+    if q.device != dev:
+        raise ValueError(f"{name} must be on the current CUDA device, is on device {q.device}")
+
+
 def quantize_fp4_rows(x, out: Fp4Rows, L=None, stream=None):
     """x [R, K] bf16 (rows may be strided) -> out, its first L rows."""
-    dev = _device()
-    if x.dtype is not torch.bfloat16:
-        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
-    if x.shape != (out.R, out.K) or x.stride(1) != 1:
-        raise ValueError(f"x must be {[out.R, out.K]} with neighbouring values, got "
-                         f"{list(x.shape)}")
-    _on(x, "x", dev)
-    L = out.R if L is None else L
-    if not 0 <= L <= out.R:
-        raise ValueError(f"L={L} exceeds the {out.R} rows")
-    _check("quantize_fp4_rows", lib().h3_quantize_fp4_rows(
-        x.data_ptr(), x.stride(0) if out.R > 1 else out.K, *out._pointers(dev, "out"), L, out.K,
-        FP4_FORMATS[out.format], _raw_stream(stream, dev)))
+    dev = _here(x, "x")
+    if x.dtype is not _BF16:
+        raise TypeError(f"x must be {_BF16}, got {x.dtype}")
+    if x.shape != out.shape:
+        raise ValueError(f"x must be {list(out.shape)}, got {list(x.shape)}")
+    ld, one = x.stride()
+    if one != 1:
+        raise ValueError("the values of a row of x must be neighbours")
+    if out.device != dev:
+        _same_device(out, "out", dev)
+    R = out.R
+    if L is None:
+        L = R
+    elif not 0 <= L <= R:
+        raise ValueError(f"L={L} exceeds the {R} rows")
+    codes, scales, row_scale = out.pointers
+    status = (_lib or lib()).h3_quantize_fp4_rows(
+        x.data_ptr(), ld if R > 1 else out.K, codes, scales, row_scale, L, out.K, out.number,
+        _raw_stream(stream, dev))
+    if status:
+        _check("quantize_fp4_rows", status)
 
 
-def _fp4_product(name, x, w, y, N, L, stream):
-    dev = _device()
-    if x.format != w.format or x.K != w.K:
+def _fp4_product(name, call, x, w, y, N, L, stream):
+    dev = _here(y, "the output")
+    if x.number != w.number or x.K != w.K:
         raise ValueError(f"x is {x.format!r} rows of {x.K}, the weights {w.format!r} of {w.K}")
-    if y.shape != (x.R, N):
-        raise ValueError(f"the output must be {[x.R, N]}, got {list(y.shape)}")
-    _flat(y, "the output", torch.bfloat16, dev)
-    _check(name, getattr(lib(), "h3_" + name)(
-        *x._pointers(dev, "x"), *w._pointers(dev, "the weights"), y.data_ptr(), x.R,
-        x.R if L is None else L, N, x.K, FP4_FORMATS[x.format], _raw_stream(stream, dev)))
+    py = _tensor(y, "the output", _BF16, (x.R, N), dev)
+    if x.device != dev or w.device != dev:
+        _same_device(x, "x", dev)
+        _same_device(w, "the weights", dev)
+    status = call(*x.pointers, *w.pointers, py, x.R, x.R if L is None else L, N, x.K, x.number,
+                  _raw_stream(stream, dev))
+    if status:
+        _check(name, status)
 
 
 def linear_fp4(x: Fp4Rows, w: Fp4Rows, y, L=None, stream=None):
     """y[:L] = x w^T of 4-bit rows x [S, K], w [N, K]; y [S, N] bf16."""
-    _fp4_product("linear_fp4", x, w, y, w.R, L, stream)
+    _fp4_product("linear_fp4", (_lib or lib()).h3_linear_fp4, x, w, y, w.R, L, stream)
 
 
 def linear_swiglu_fp4(x: Fp4Rows, w_gu: Fp4Rows, out, L=None, stream=None):
@@ -860,7 +893,8 @@ def linear_swiglu_fp4(x: Fp4Rows, w_gu: Fp4Rows, out, L=None, stream=None):
     [gate | up]); out [S, F] bf16."""
     if w_gu.R % 2:
         raise ValueError(f"the weights have {w_gu.R} rows, an odd number")
-    _fp4_product("linear_swiglu_fp4", x, w_gu, out, w_gu.R // 2, L, stream)
+    _fp4_product("linear_swiglu_fp4", (_lib or lib()).h3_linear_swiglu_fp4, x, w_gu, out,
+                 w_gu.R // 2, L, stream)
 
 
 QUERY_BLOCK = 256
@@ -883,43 +917,44 @@ def block_scores(q, k, scores, workspace, k_block=64, scale=None, stream=None):
     """scores [H, nq, nk] f32 of every (block of QUERY_BLOCK query rows, block of k_block
     keys): scale times the product of their mean rows. q [Lq,H,128], k [Lk,Hkv,128] bf16
     (rows may be strided), workspace of block_scores_workspace_bytes."""
-    dev = _device()
+    dev = _here(scores, "scores")
     Lq, Lk = q.shape[0], k.shape[0]
     ldq, H = _heads(q, "q", Lq, dev)
     ldk, Hkv = _heads(k, "k", Lk, dev)
-    if scores.shape != _block_shape(Lq, Lk, H, k_block):
-        raise ValueError(f"scores must be {list(_block_shape(Lq, Lk, H, k_block))}, got "
-                         f"{list(scores.shape)}")
-    _flat(scores, "scores", torch.float32, dev)
-    _on(workspace, "workspace", dev)
-    _check("block_scores", lib().h3_block_scores(
-        q.data_ptr(), ldq, k.data_ptr(), ldk, scores.data_ptr(), Lq, Lk, H, Hkv, 128, k_block,
+    ps = _tensor(scores, "scores", _F32, _block_shape(Lq, Lk, H, k_block), dev)
+    if workspace.get_device() != dev:
+        _on(workspace, "workspace", dev)
+    status = (_lib or lib()).h3_block_scores(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, ps, Lq, Lk, H, Hkv, 128, k_block,
         128 ** -0.5 if scale is None else scale, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+    if status:
+        _check("block_scores", status)
 
 
 def block_select(scores, ids, counts, keep_first=0, keep_last=0, stream=None):
     """The best-scored blocks of every row of scores [..., nk] f32: ids [..., max_blocks]
     int32 in ascending order (then -1), counts [...] int32. The first keep_first and the
     last keep_last blocks are always among them; -inf and NaN never are otherwise."""
-    dev = _device()
-    nk, most = scores.shape[-1], ids.shape[-1]
-    if ids.shape[:-1] != scores.shape[:-1] or counts.shape != scores.shape[:-1]:
+    shape, listed, rows = scores.shape, ids.shape, counts.shape
+    nk, most = shape[-1], listed[-1]
+    if listed[:-1] != rows or shape[:-1] != rows:
         raise ValueError(f"scores [..., nk], ids [..., max_blocks] and counts [...] wanted, got "
-                         f"{list(scores.shape)}, {list(ids.shape)} and {list(counts.shape)}")
-    _flat(scores, "scores", torch.float32, dev)
-    _flat(ids, "ids", torch.int32, dev)
-    _flat(counts, "counts", torch.int32, dev)
-    _check("block_select", lib().h3_block_select(
-        scores.data_ptr(), ids.data_ptr(), counts.data_ptr(), counts.numel(), nk, most, keep_first,
-        keep_last, _raw_stream(stream, dev)))
+                         f"{list(shape)}, {list(listed)} and {list(rows)}")
+    dev = _here(scores, "scores")
+    status = (_lib or lib()).h3_block_select(
+        _tensor(scores, "scores", _F32, shape, dev), _tensor(ids, "ids", _I32, listed, dev),
+        _tensor(counts, "counts", _I32, rows, dev), counts.numel(), nk, most, keep_first, keep_last,
+        _raw_stream(stream, dev))
+    if status:
+        _check("block_select", status)
 
 
 def attention_blocks(q, k, v, o, ids, counts, k_block=64, scale=None, stream=None):
     """Attention of every block of QUERY_BLOCK query rows over its listed key blocks: ids
     [H, nq, max_blocks], counts [H, nq] int32 (block_select's), q, o [Lq,H,128], k, v
     [Lk,Hkv,128] bf16 (rows may be strided)."""
-    dev = _device()
+    dev = _here(counts, "counts")
     Lq, Lk = q.shape[0], k.shape[0]
     ldq, H = _heads(q, "q", Lq, dev)
     ldk, Hkv = _heads(k, "k", Lk, dev)
@@ -928,12 +963,13 @@ def attention_blocks(q, k, v, o, ids, counts, k_block=64, scale=None, stream=Non
     if hv != Hkv or ho != H:
         raise ValueError(f"q and o have {H} and {ho} heads, k and v {Hkv} and {hv}")
     shape = _block_shape(Lq, Lk, H, k_block)[:2]
-    if counts.shape != shape or ids.shape[:2] != shape or ids.dim() != 3:
-        raise ValueError(f"ids must be {list(shape)} x max_blocks and counts {list(shape)}, got "
-                         f"{list(ids.shape)} and {list(counts.shape)}")
-    _flat(ids, "ids", torch.int32, dev)
-    _flat(counts, "counts", torch.int32, dev)
-    _check("attention_blocks", lib().h3_attention_blocks(
+    if ids.dim() != 3:
+        raise ValueError(f"ids must be {list(shape)} x max_blocks, got {list(ids.shape)}")
+    most = ids.shape[2]
+    status = (_lib or lib()).h3_attention_blocks(
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, o.data_ptr(), ldo,
-        ids.data_ptr(), counts.data_ptr(), ids.shape[2], Lq, Lk, H, Hkv, 128, k_block,
-        128 ** -0.5 if scale is None else scale, _raw_stream(stream, dev)))
+        _tensor(ids, "ids", _I32, (*shape, most), dev), _tensor(counts, "counts", _I32, shape, dev),
+        most, Lq, Lk, H, Hkv, 128, k_block, 128 ** -0.5 if scale is None else scale,
+        _raw_stream(stream, dev))
+    if status:
+        _check("attention_blocks", status)

@@ -252,7 +252,8 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
  * nq = ceil(Lq / H3_QUERY_BLOCK) and nk = ceil(Lk / k_block):
  *
  * h3_block_scores: scores[h, t, b] = softmax_scale * mean(q rows of block t, head h)
- *   . mean(k rows of block b, head h / (H / Hkv)), means and products in FP32.
+ *   . mean(k rows of block b, head h / (H / Hkv)), the means in FP32, their products with at
+ *   most 2^-20 of the sum of the products' magnitudes beside what FP32 sums have.
  *   q       [Lq, H, Dh] bf16, row stride ld_q elements; k [Lk, Hkv, Dh], ld_k
  *   scores  [H, nq, nk] float32
  *   workspace  device memory of h3_block_scores_workspace_bytes(...) bytes, 256-byte

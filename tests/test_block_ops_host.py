@@ -109,6 +109,7 @@ def test_fp4_products(lib, name, N, odd):
 def test_block_scores_and_workspace(lib):
     n = lib.h3_block_scores_workspace_bytes
     assert n(257, 129, 4, 2, 64) == (2 * 4 + 3 * 2) * 512 and n(0, 0, 4, 2, 64) > 0
+    assert n(4097, 129, 4, 2, 64) == (17 * 4 + 3 * 2) * 1024   # means in two parts
     for a in ((-1, 5, 4, 2, 64), (5, 5, 4, 3, 64), (5, 5, 0, 1, 64), (5, 5, 4, 2, 32), (5, (1 << 26) + 1, 4, 2, 64)):
         assert n(*a) == 0 and h3.last_error()
     f = lib.h3_block_scores
