@@ -188,58 +188,81 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
   bool ok = true;
   if (warp == 8) {
     // ---------------------------------------------------------- lists and loads
-    if (lane == 0 && n > 0) {
+    // The whole warp goes along, since a lane reads one of 32 entries of the list, a batch ahead
+    // of their use; lane 0 waits and loads.
+    if (n > 0) {
       const int colq = h * DH, colk = h / a.group * DH;
-      mbar_arrive_expect_tx(bar(BB_Q), (two ? 2 : 1) * TILE_BYTES);
-      for (int i = 0; i < (two ? 2 : 1); ++i)
-        for (int c = 0; c < 2; ++c)
-          tma_load_2d(smem_u32(sQ + i * TILE_BYTES + c * BOX_BYTES), &tmQ, bar(BB_Q), colq + c * 64,
-                      q0 + i * BQ);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(BB_Q), (two ? 2 : 1) * TILE_BYTES);
+        for (int i = 0; i < (two ? 2 : 1); ++i)
+          for (int c = 0; c < 2; ++c)
+            tma_load_2d(smem_u32(sQ + i * TILE_BYTES + c * BOX_BYTES), &tmQ, bar(BB_Q), colq + c * 64,
+                        q0 + i * BQ);
+      }
+      const int first = tile0 * per_tile, end = min(count, (tile0 + n) * per_tile);
+      auto entry = [&](int i) { return first + i < end ? list[first + i] : -1; };
+      int now = entry(lane), next = entry(32 + lane);
       int issued = 0;
       // the first rows of a tile's blocks; past the last key where there is none
       auto rows_of = [&](int j, int (&row)[2], int (&real)[2]) {
-        for (int e = 0; e < per_tile; ++e) {
-          const int at = (tile0 + j) * per_tile + e;
-          const int id = at < count ? *(list + at) : -1;
-          const bool in = id >= 0 && id < a.nk;
-          row[e] = in ? id * a.kb : a.Lk;
-          real[e] = in ? min(a.kb, a.Lk - row[e]) : 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (e < per_tile) {
+            const int at = j * per_tile + e;
+            const int id = __shfl_sync(0xffffffffu, now, at & 31);
+            if ((at & 31) == 31) {
+              now = next;
+              next = entry(at + 33 + lane);
+            }
+            const bool in = id >= 0 && id < a.nk;
+            row[e] = in ? id * a.kb : a.Lk;
+            real[e] = in ? min(a.kb, a.Lk - row[e]) : 0;
+          }
         }
       };
       auto load = [&](const CUtensorMap* map, const int (&row)[2]) {
         const int st = issued % BS_SLOTS;
-        if (!mbar_wait(bar(BB_EMPTY + st), (static_cast<uint32_t>(issued / BS_SLOTS) & 1u) ^ 1u,
-                       a.err, ERR_WAIT_ATTN_PRODUCER))
-          return false;
-        const uint32_t full = bar(BB_FULL + st);
-        mbar_arrive_expect_tx(full, TILE_BYTES);
-        const uint32_t dst = smem_u32(sKV + st * TILE_BYTES);
-        for (int e = 0; e < per_tile; ++e)
-          for (int c = 0; c < 2; ++c)
-            tma_load_2d(dst + c * BOX_BYTES + e * a.kb * 128, map, full, colk + c * 64, row[e]);
-        ++issued;
-        return true;
-      };
-      int row[2][2] = {}, real[2] = {};
-      for (int j = 0; j <= n; ++j) {  // K_j, then V_{j-1}
-        if (j < n) {
-          rows_of(j, row[j & 1], real);
-          keys[j % BS_COUNTS] = a.kb == 64
-                                    ? static_cast<uint32_t>(real[0]) | static_cast<uint32_t>(real[1]) << 16
-                                    : static_cast<uint32_t>(min(real[0], 64)) |
-                                          static_cast<uint32_t>(max(real[0] - 64, 0)) << 16;
-          if (!load(&tmK, row[j & 1])) break;
+        int done = 1;
+        if (lane == 0) {
+          done = mbar_wait(bar(BB_EMPTY + st), (static_cast<uint32_t>(issued / BS_SLOTS) & 1u) ^ 1u,
+                           a.err, ERR_WAIT_ATTN_PRODUCER);
+          if (done) {
+            const uint32_t full = bar(BB_FULL + st);
+            mbar_arrive_expect_tx(full, TILE_BYTES);
+            const uint32_t dst = smem_u32(sKV + st * TILE_BYTES);
+            for (int e = 0; e < per_tile; ++e)
+              for (int c = 0; c < 2; ++c)
+                tma_load_2d(dst + c * BOX_BYTES + e * a.kb * 128, map, full, colk + c * 64, row[e]);
+          }
         }
-        if (j > 0 && !load(&tmV, row[(j - 1) & 1])) break;
+        done = __shfl_sync(0xffffffffu, done, 0);
+        issued += done;
+        return done != 0;
+      };
+      int row[2] = {}, before[2] = {}, real[2] = {};
+      for (int j = 0; j <= n; ++j) {  // K_j, then V_{j-1}
+        before[0] = row[0], before[1] = row[1];
+        if (j < n) {
+          rows_of(j, row, real);
+          if (lane == 0)
+            keys[j % BS_COUNTS] = a.kb == 64
+                                      ? static_cast<uint32_t>(real[0]) | static_cast<uint32_t>(real[1]) << 16
+                                      : static_cast<uint32_t>(min(real[0], 64)) |
+                                            static_cast<uint32_t>(max(real[0] - 64, 0)) << 16;
+          if (!load(&tmK, row)) break;
+        }
+        if (j > 0 && !load(&tmV, before)) break;
       }
-      launch_next();
-      // no copy of this CTA may still be landing when it exits
-      const uint64_t t0 = globaltimer_ns();
-      const uint64_t lim = drain_limit_ns(a.err);
-      mbar_wait_drain(bar(BB_Q), 0u, t0, lim);
-      for (int i = issued > BS_SLOTS ? issued - BS_SLOTS : 0; i < issued; ++i)
-        mbar_wait_drain(bar(BB_FULL + i % BS_SLOTS), static_cast<uint32_t>(i / BS_SLOTS) & 1u, t0,
-                        lim);
+      if (lane == 0) {
+        launch_next();
+        // no copy of this CTA may still be landing when it exits
+        const uint64_t t0 = globaltimer_ns();
+        const uint64_t lim = drain_limit_ns(a.err);
+        mbar_wait_drain(bar(BB_Q), 0u, t0, lim);
+        for (int i = issued > BS_SLOTS ? issued - BS_SLOTS : 0; i < issued; ++i)
+          mbar_wait_drain(bar(BB_FULL + i % BS_SLOTS), static_cast<uint32_t>(i / BS_SLOTS) & 1u, t0,
+                          lim);
+      }
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------- MMA issuer
