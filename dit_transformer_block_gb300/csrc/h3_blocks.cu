@@ -5,7 +5,7 @@
 // the means per head. The pooling reads q and k once and is bound by HBM. A product with
 // rounded means would choose other blocks, so it has FP32's accuracy: each mean is the sum
 // of two TF32 numbers, and three products of those (all but that of the two smaller parts)
-// run on the tensor cores; of few query blocks it runs on the CUDA cores.
+// run on the tensor cores; for few query blocks it runs on the CUDA cores.
 //
 // Selection: the max_blocks-th largest score is found by counting, then one pass writes
 // the chosen indices in ascending order. A warp per row of scores, longer ones a CTA.
@@ -24,13 +24,27 @@ namespace {
 constexpr int DHB = 128;
 
 // ------------------------------------------------------------------ pooling
+// One CTA per SM goes over (block of rows, two neighbouring heads) after the other. Its rows
+// come in pieces of at most 128 rows x 256 channels (64 KB) by TMA, three of them under way,
+// so that HBM is read without a pause whatever the sums do. Each of eight warps sums 32 of the
+// channels, eight rows at a time, and has their mean without another warp's: four boxes
+// of 64 channels, swizzled, so that its eight rows lie in different banks.
+// (1,896 + 29,034 rows of 40 and 8 heads, 79 MB, with their product: 20 us; 24 where every CTA
+// loads its block into
+// registers, 28 with the rows of a piece spread over the warps, which then have to meet. 58,758
+// rows of 42 + 42 heads, 1.26 GB: 200 us, 195 and 206.)
 constexpr int POOL_WARPS = 8;
+constexpr int POOL_THREADS = POOL_WARPS * 32 + 32;  // and a warp that loads
+constexpr int POOL_ROWS = 128, POOL_SLOTS = 3;
+constexpr int POOL_BOX_BYTES = POOL_ROWS * 128;     // 64 channels
+constexpr int POOL_SLOT_BYTES = 4 * POOL_BOX_BYTES;
+constexpr size_t POOL_SMEM_BYTES = 1024 + POOL_SLOTS * POOL_SLOT_BYTES + 2 * POOL_SLOTS * 8;
+static_assert(POOL_SMEM_BYTES <= 227 * 1024, "pooling shared memory");
 
 struct PoolSide {
-  const __nv_bfloat16* x;
-  int64_t ld;
   int L, heads, block, blocks;
   int pairs;   // pairs of heads
+  int items;   // blocks * pairs
   float* out;  // [heads][blocks][128]
   float* low;  // as out, or NULL: out is then rounded to TF32, and this is what that leaves
 };
@@ -40,153 +54,171 @@ __device__ __forceinline__ float to_tf32(float x) {
   return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
 }
 
-// A CTA takes a block of rows and two neighbouring heads: a warp reads 512 contiguous
-// bytes of a row, its rows POOL_WARPS apart, and the warps' sums meet in shared memory.
-__global__ void __launch_bounds__(POOL_WARPS * 32)
-    pool_kernel(const PoolSide q, const PoolSide k, const int q_ctas) {
-  __shared__ float part[POOL_WARPS][2 * DHB];
-  const bool is_q = static_cast<int>(blockIdx.x) < q_ctas;
-  const PoolSide& s = is_q ? q : k;
-  const int id = static_cast<int>(blockIdx.x) - (is_q ? 0 : q_ctas);
-  const int blk = id / s.pairs, head0 = id % s.pairs * 2;
+__global__ void __launch_bounds__(POOL_THREADS, 1)
+    pool_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const PoolSide q, const PoolSide k, const DevErr err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + POOL_SLOTS * POOL_SLOT_BYTES);  // full, empty
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < POOL_SLOTS; ++i) {
+      mbar_init(bar(i), 1);
+      mbar_init(bar(POOL_SLOTS + i), POOL_WARPS);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
   wait_previous();
-  const int tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
-  const int row0 = blk * s.block;
-  const int rows = min(s.block, s.L - row0);
-  const bool real = head0 + (lane >> 4) < s.heads;
-  float acc[8] = {};
-  if (real) {
-    const __nv_bfloat16* p = s.x + static_cast<int64_t>(row0 + warp) * s.ld + head0 * DHB + lane * 8;
-    const int64_t step = POOL_WARPS * s.ld;
-    int r = warp;
-    auto add = [&](const uint4& v) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int items = q.items + k.items;
+
+  if (warp == POOL_WARPS) {
+    if (lane == 0) {
+      int st = 0, issued = 0;
+      uint32_t phase = 1;
+      bool ok = true;
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const bool is_q = item < q.items;
+        const PoolSide& s = is_q ? q : k;
+        const int id = item - (is_q ? 0 : q.items);
+        const int row0 = id / s.pairs * s.block, head0 = id % s.pairs * 2;
+        const int rows = min(s.block, s.L - row0), box = min(s.block, POOL_ROWS);
+        for (int r = 0; r < rows; r += POOL_ROWS) {
+          ok = mbar_wait(bar(POOL_SLOTS + st), phase, err, ERR_WAIT_GEMM_PRODUCER);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(st), box * 2 * DHB * 2);
+          for (int c = 0; c < 4; ++c)
+            tma_load_2d(smem_u32(smem + st * POOL_SLOT_BYTES + c * POOL_BOX_BYTES), is_q ? &tmQ : &tmK,
+                        bar(st), head0 * DHB + c * 64, row0 + r);
+          ++issued;
+          if (++st == POOL_SLOTS) {
+            st = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      launch_next();
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = issued > POOL_SLOTS ? issued - POOL_SLOTS : 0; i < issued; ++i)
+        mbar_wait_drain(bar(i % POOL_SLOTS), static_cast<uint32_t>(i / POOL_SLOTS) & 1u, t0,
+                        drain_limit_ns(err));
+    }
+    return;
+  }
+  // lane: row lane / 4 of eight, channels 8 (lane % 4) .. of the warp's 32: half of a box's row
+  const int sub = lane >> 2, chunk = (warp & 1) * 4 + (lane & 3);
+  const uint32_t off = (warp >> 1) * POOL_BOX_BYTES + sub * 128 + ((chunk ^ sub) << 4);
+  int st = 0;
+  uint32_t phase = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const bool is_q = item < q.items;
+    const PoolSide& s = is_q ? q : k;
+    const int id = item - (is_q ? 0 : q.items);
+    const int blk = id / s.pairs, head = id % s.pairs * 2 + (warp >> 2);
+    const int rows = min(s.block, s.L - blk * s.block);
+    float acc[8] = {};
+    for (int r0 = 0; r0 < rows; r0 += POOL_ROWS) {
+      // (where a wait runs out, this one returns and so does every later one, soon)
+      mbar_wait(bar(st), phase, err, ERR_WAIT_GEMM_EPILOGUE);
+      const uint8_t* x = smem + st * POOL_SLOT_BYTES + off;
+      const int n = min(POOL_ROWS, rows - r0);
+#pragma unroll 8
+      for (int r = sub; r < n; r += 8, x += 1024) {
+        const uint4 v = *reinterpret_cast<const uint4*>(x);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[2 * j] += bf16_lo(w[j]);
+          acc[2 * j + 1] += bf16_hi(w[j]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(POOL_SLOTS + st));
+      if (++st == POOL_SLOTS) {
+        st = 0;
+        phase ^= 1u;
+      }
+    }
+    // over the eight rows, each step leaving a lane half of its channels; then channel
+    // 8 (lane % 4) + sub is lane's
+#pragma unroll
+    for (int m = 4, n = 4; m >= 1; m >>= 1, n >>= 1) {
+      const bool high = (sub & m) != 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        acc[2 * j] += bf16_lo(w[j]);
-        acc[2 * j + 1] += bf16_hi(w[j]);
+        if (j < n) {
+          const float give = high ? acc[j] : acc[j + n], keep = high ? acc[j + n] : acc[j];
+          acc[j] = keep + __shfl_xor_sync(0xffffffffu, give, m * 4);
+        }
       }
-    };
-    constexpr int U = 8;  // rows in flight
-    for (; r + (U - 1) * POOL_WARPS < rows; r += U * POOL_WARPS, p += U * step) {
-      uint4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const uint4*>(p + u * step);
-#pragma unroll
-      for (int u = 0; u < U; ++u) add(v[u]);
     }
-    for (; r < rows; r += POOL_WARPS, p += step) add(*reinterpret_cast<const uint4*>(p));
-  }
-  launch_next();
-  float4* mine = reinterpret_cast<float4*>(&part[warp][lane * 8]);
-  mine[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  mine[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-  __syncthreads();
-  const int head = head0 + (threadIdx.x >> 7);
-  if (head < s.heads) {
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < POOL_WARPS; ++w) t += part[w][threadIdx.x];
-    const float mean = t / static_cast<float>(rows);
-    const int64_t at = (static_cast<int64_t>(head) * s.blocks + blk) * DHB + (threadIdx.x & 127);
-    if (s.low != nullptr) {
-      // (NaN and infinity go whole into the first part)
-      const float hi = fabsf(mean) < INFINITY ? to_tf32(mean) : mean;
-      s.out[at] = hi;
-      s.low[at] = fabsf(mean) < INFINITY ? to_tf32(mean - hi) : 0.f;
-    } else {
-      s.out[at] = mean;
+    if (head < s.heads) {
+      const float mean = acc[0] / static_cast<float>(rows);
+      const int64_t at = (static_cast<int64_t>(head) * s.blocks + blk) * DHB + (warp & 3) * 32 +
+                         (lane & 3) * 8 + sub;
+      if (s.low != nullptr) {
+        // (NaN and infinity go whole into the first part)
+        const float hi = fabsf(mean) < INFINITY ? to_tf32(mean) : mean;
+        s.out[at] = hi;
+        s.low[at] = fabsf(mean) < INFINITY ? to_tf32(mean - hi) : 0.f;
+      } else {
+        s.out[at] = mean;
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------ product
-constexpr int SC_N = 128;    // key blocks of a CTA
-constexpr int SC_K = 32;     // channels per step
-constexpr int SC_THREADS = 128;
+// Few query blocks (at most eight): scores[h] = scale * mq[h] mk[g]^T, a warp 16 key blocks of a
+// head, whose query means its lanes hold, four channels each.
+constexpr int FEW = 8, FEW_WARPS = 4, FEW_KEYS = 16;
 
-// (d0, d1) += (a, a) * (b0, b1)
-__device__ __forceinline__ void ffma2_acc(uint64_t& d, float a, float b0, float b1) {
-  asm("{\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%1, %1};\n\t"
-      "mov.b64 y, {%2, %3};\n\t"
-      "fma.rn.f32x2 %0, x, y, %0;\n\t}"
-      : "+l"(d)
-      : "f"(a), "f"(b0), "f"(b1));
-}
-
-// Few query blocks: scores[h] = scale * mq[h] mk[g]^T, 16 x 128 of it per CTA. A thread has two
-// query blocks and four pairs of key blocks 32 apart, a pair to a packed FMA; both operands lie
-// channel by channel in shared memory, 32 channels at a time, the next ones on their way.
-constexpr int SC_M = 16;
-__global__ void __launch_bounds__(SC_THREADS)
+__global__ void __launch_bounds__(FEW_WARPS * 32)
     block_scores_few_kernel(const float* mq, const float* mk, float* scores, int nq, int nk, int group,
                             float scale) {
-  constexpr int BV = SC_N * SC_K / 4 / SC_THREADS;  // float4 that a thread loads of B; of A, one
-  __shared__ __align__(16) float sa[SC_K][SC_M + 4];
-  __shared__ __align__(16) float sb[SC_K][SC_N + 4];
-  const int h = blockIdx.z, g = h / group;
-  const int t0 = blockIdx.y * SC_M, b0 = blockIdx.x * SC_N;
-  const float4* qa = reinterpret_cast<const float4*>(mq + (static_cast<int64_t>(h) * nq + t0) * DHB);
-  const float4* kb = reinterpret_cast<const float4*>(mk + (static_cast<int64_t>(g) * nk + b0) * DHB);
+  const int lane = threadIdx.x & 31, h = blockIdx.y, g = h / group;
+  const int b0 = (blockIdx.x * FEW_WARPS + (threadIdx.x >> 5)) * FEW_KEYS;
   wait_previous();
-  const int tid = threadIdx.x;
-  const int ar = tid % SC_M, ac = tid / SC_M;  // A: its row and float4 of a step; B: row tid
-  const bool a_in = t0 + ar < nq, b_in = b0 + tid < nk;
-  float4 av, bv[BV];
-  auto fetch = [&](int k4) {
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    av = a_in ? qa[ar * (DHB / 4) + k4 + ac] : z;
+  const float4* kp = reinterpret_cast<const float4*>(mk + static_cast<int64_t>(g) * nk * DHB) + lane;
+  const float4* qp = reinterpret_cast<const float4*>(mq + static_cast<int64_t>(h) * nq * DHB) + lane;
+  float4 x[FEW], y[FEW_KEYS];
 #pragma unroll
-    for (int i = 0; i < BV; ++i) bv[i] = b_in ? kb[tid * (DHB / 4) + k4 + i] : z;
-  };
-  uint64_t acc[2][4];
+  for (int t = 0; t < FEW; ++t)
+    x[t] = t < nq ? qp[t * (DHB / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
-  const int ty = tid >> 4, tx = tid & 15;
-  fetch(0);
-#pragma unroll 1
-  for (int k0 = 0; k0 < DHB; k0 += SC_K) {
-    if (k0 > 0) __syncthreads();
-    sa[4 * ac][ar] = av.x * scale, sa[4 * ac + 1][ar] = av.y * scale;
-    sa[4 * ac + 2][ar] = av.z * scale, sa[4 * ac + 3][ar] = av.w * scale;
-#pragma unroll
-    for (int i = 0; i < BV; ++i) {
-      sb[4 * i][tid] = bv[i].x, sb[4 * i + 1][tid] = bv[i].y;
-      sb[4 * i + 2][tid] = bv[i].z, sb[4 * i + 3][tid] = bv[i].w;
-    }
-    __syncthreads();
-    if (k0 + SC_K < DHB) fetch((k0 + SC_K) / 4);
-#pragma unroll 8
-    for (int c = 0; c < SC_K; ++c) {
-      const float2 x = *reinterpret_cast<const float2*>(&sa[c][ty * 2]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 y = *reinterpret_cast<const float2*>(&sb[c][2 * tx + 32 * j]);
-        ffma2_acc(acc[0][j], x.x, y.x, y.y);
-        ffma2_acc(acc[1][j], x.y, y.x, y.y);
-      }
-    }
-  }
+  for (int i = 0; i < FEW_KEYS; ++i)
+    y[i] = b0 + i < nk ? kp[static_cast<int64_t>(b0 + i) * (DHB / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
   launch_next();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = t0 + ty * 2 + i;
+  for (int t = 0; t < FEW; ++t) {
     if (t >= nq) break;
-    const int b = b0 + 2 * tx;
-    float* o = scores + (static_cast<int64_t>(h) * nq + t) * nk + b;
+    // 16 sums over the lanes, each step leaving a lane half of them: it ends with key block
+    // lane / 2's
+    float d[FEW_KEYS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (b + 32 * j < nk) o[32 * j] = __uint_as_float(static_cast<uint32_t>(acc[i][j]));
-      if (b + 32 * j + 1 < nk) o[32 * j + 1] = __uint_as_float(static_cast<uint32_t>(acc[i][j] >> 32));
+    for (int i = 0; i < FEW_KEYS; ++i)
+      d[i] = fmaf(x[t].x, y[i].x, x[t].y * y[i].y) + fmaf(x[t].z, y[i].z, x[t].w * y[i].w);
+#pragma unroll
+    for (int m = 16, n = 8; n >= 1; m >>= 1, n >>= 1) {
+      const bool high = (lane & m) != 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j < n) {
+          const float give = high ? d[j] : d[j + n], keep = high ? d[j + n] : d[j];
+          d[j] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+        }
+      }
     }
+    const float sum = d[0] + __shfl_xor_sync(0xffffffffu, d[0], 1);
+    const int b = b0 + (lane >> 1);
+    if ((lane & 1) == 0 && b < nk)
+      scores[(static_cast<int64_t>(h) * nq + t) * nk + b] = sum * scale;
   }
 }
 
-// The tensor-core form: 128 query blocks x 128 key blocks of a head per CTA (230 x 919 blocks of 42
+// scores[h] = scale * mq[h] mk[g]^T: 128 query blocks x 128 key blocks of a head per CTA (230 x 919 blocks of 42
 // heads in 30 us, and 75 us by FP32 FMAs; three CTAs to an SM of one stage each are no faster).
 // A stage is 32
 // channels (128 bytes a row) of both parts of both operands; warp 0 loads (TMA), warp 1
@@ -609,45 +641,49 @@ __global__ void __launch_bounds__(T)
 
 }  // namespace
 
-// Query blocks up to which the product runs on the CUDA cores: one tile of theirs, where the
-// tensor cores' 128 rows would be mostly empty.
-constexpr int SCORES_FEW = SC_M;
-
 size_t block_scores_workspace_bytes(int nq, int nk, int H, int Hkv) {
   const size_t means = static_cast<size_t>(nq) * H + static_cast<size_t>(nk) * Hkv;
-  return means * DHB * sizeof(float) * (nq > SCORES_FEW ? 2 : 1);
+  return means * DHB * sizeof(float) * (nq > FEW ? 2 : 1);
 }
 
 h3_status launch_block_scores(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
                               float* scores, int Lq, int Lk, int H, int Hkv, int k_block,
                               float scale, void* workspace, cudaStream_t s) {
   const int nq = (Lq + H3_QUERY_BLOCK - 1) / H3_QUERY_BLOCK, nk = (Lk + k_block - 1) / k_block;
-  const bool few = nq <= SCORES_FEW;
+  const bool few = nq <= FEW;
   const int64_t q_rows = static_cast<int64_t>(nq) * H, k_rows = static_cast<int64_t>(nk) * Hkv;
   float* mq = static_cast<float*>(workspace);
   float* mk = mq + q_rows * DHB;
   float* lq = few ? nullptr : mk + k_rows * DHB;
   float* lk = few ? nullptr : lq + q_rows * DHB;
-  const PoolSide qs{static_cast<const __nv_bfloat16*>(q), ld_q, Lq, H, H3_QUERY_BLOCK, nq,
-                    (H + 1) / 2, mq, lq};
-  const PoolSide ks{static_cast<const __nv_bfloat16*>(k), ld_k, Lk, Hkv, k_block, nk,
-                    (Hkv + 1) / 2, mk, lk};
-  const int q_ctas = nq * qs.pairs;
-  h3_status st = cuda_fail(launch_overlapped(pool_kernel, dim3(q_ctas + nk * ks.pairs),
-                                             POOL_WARPS * 32, 0, 1, s, qs, ks, q_ctas),
-                           "block pooling launch");
+  const PoolSide qs{Lq, H, H3_QUERY_BLOCK, nq, (H + 1) / 2, nq * ((H + 1) / 2), mq, lq};
+  const PoolSide ks{Lk, Hkv, k_block, nk, (Hkv + 1) / 2, nk * ((Hkv + 1) / 2), mk, lk};
+  static std::atomic<bool> done_pool[64];
+  h3_status st = set_smem_limit(done_pool, pool_kernel, POOL_SMEM_BYTES,
+                                "block pooling: set shared memory size");
+  if (st != H3_OK) return st;
+  DevErr err;
+  if ((st = dev_err(&err)) != H3_OK) return st;
+  CUtensorMap tq, tk;
+  if ((st = make_tmap_bf16_2d(&tq, q, static_cast<uint64_t>(H) * DHB, Lq, ld_q * 2, 64,
+                              std::min(H3_QUERY_BLOCK, POOL_ROWS))) != H3_OK)
+    return st;
+  if ((st = make_tmap_bf16_2d(&tk, k, static_cast<uint64_t>(Hkv) * DHB, Lk, ld_k * 2, 64,
+                              std::min(k_block, POOL_ROWS))) != H3_OK)
+    return st;
+  st = cuda_fail(launch_overlapped(pool_kernel, dim3(std::min(qs.items + ks.items, num_sms())),
+                                   POOL_THREADS, POOL_SMEM_BYTES, 1, s, tq, tk, qs, ks, err),
+                 "block pooling launch");
   if (st != H3_OK) return st;
   if (few) {
-    const dim3 grid((nk + SC_N - 1) / SC_N, (nq + SC_M - 1) / SC_M, H);
-    return cuda_fail(launch_overlapped(block_scores_few_kernel, grid, SC_THREADS, 0, 1, s, mq, mk,
+    const dim3 grid((nk + FEW_WARPS * FEW_KEYS - 1) / (FEW_WARPS * FEW_KEYS), H);
+    return cuda_fail(launch_overlapped(block_scores_few_kernel, grid, FEW_WARPS * 32, 0, 1, s, mq, mk,
                                        scores, nq, nk, H / Hkv, scale),
                      "block scores launch");
   }
   static std::atomic<bool> done[64];
   st = set_smem_limit(done, block_scores_kernel, TC_SMEM_BYTES, "block scores: set shared memory size");
   if (st != H3_OK) return st;
-  DevErr err;
-  if ((st = dev_err(&err)) != H3_OK) return st;
   CUtensorMap t[4];
   const float* parts[4] = {mq, lq, mk, lk};
   for (int i = 0; i < 4; ++i)
