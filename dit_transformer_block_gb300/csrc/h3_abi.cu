@@ -861,6 +861,9 @@ h3_status h3_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_
              "softmax_scale must be > 0 and finite");
   st = check_lists(static_cast<int64_t>(query_blocks(Lq)) * H, key_blocks(Lk, k_block), max_blocks);
   if (st != H3_OK) return st;
+  // (a tensor core's FP32 sum is cut off with every 16 keys: low by 2^-11 of values of one sign here)
+  H3_REQUIRE(max_blocks <= (1 << 17) / k_block, H3_ERR_UNSUPPORTED,
+             "lists of %d blocks have more than 2^17 keys", max_blocks);
   if (Lq == 0) return H3_OK;
   if ((st = check_strided("q", q, ld_q, H)) != H3_OK) return st;
   if ((st = check_strided("o", o, ld_o, H)) != H3_OK) return st;
@@ -1243,8 +1246,9 @@ static h3_status fp4_product(const Fp4Operand& x, const Fp4Operand& w, void* y, 
   h3_status st = check_rows(S, L);
   if (st != H3_OK) return st;
   if ((st = check_fp4(K, format)) != H3_OK) return st;
-  H3_REQUIRE(K <= (1 << 20) && N <= (1 << 24), H3_ERR_UNSUPPORTED,
-             "K=%d exceeds 2^20 or N=%d exceeds 2^24", K, N);
+  H3_REQUIRE(K <= 16384, H3_ERR_UNSUPPORTED, "K=%d exceeds 16384", K);
+  H3_REQUIRE(L <= (1 << 30) && N <= (1 << 24), H3_ERR_UNSUPPORTED,
+             "L=%d exceeds 2^30 or N=%d exceeds 2^24", L, N);
   H3_REQUIRE(x.codes && x.scales && w.codes && w.scales && y, H3_ERR_INVALID_ARG,
              "a required pointer is NULL");
   const bool nv = format == H3_FP4_NV;

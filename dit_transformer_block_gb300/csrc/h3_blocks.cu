@@ -30,9 +30,8 @@ constexpr int DHB = 128;
 // channels, eight rows at a time, and has their mean without another warp's: four boxes
 // of 64 channels, swizzled, so that its eight rows lie in different banks.
 // (1,896 + 29,034 rows of 40 and 8 heads, 79 MB, with their product: 20 us; 24 where every CTA
-// loads its block into
-// registers, 28 with the rows of a piece spread over the warps, which then have to meet. 58,758
-// rows of 42 + 42 heads, 1.26 GB: 200 us, 195 and 206.)
+// loads its block into registers, 28 with the rows of a piece spread over the warps, which then
+// have to meet. 58,758 rows of 42 + 42 heads, 1.26 GB: 200 us, 195 and 206.)
 constexpr int POOL_WARPS = 8;
 constexpr int POOL_THREADS = POOL_WARPS * 32 + 32;  // and a warp that loads
 constexpr int POOL_ROWS = 128, POOL_SLOTS = 3;

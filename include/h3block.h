@@ -277,12 +277,15 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
  *   q, o    [Lq, H, Dh] bf16, row strides ld_q, ld_o; k, v [Lk, Hkv, Dh], ld_k, ld_v
  *           (multiples of 8; q, k and v may be columns of one buffer). o overlaps nothing.
  *   ids     [H, nq, max_blocks] int32; counts [H, nq] int32
- * bf16 tensor-core products, FP32 softmax and accumulation, weights rounded to bf16 before
- * their product (2^-8 of the sum of weight times |v|), bf16 out.
+ * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out: relative to the sum of
+ * weight times |v| at most 2^-8 for the weights' rounding before their product and 2^-10 for
+ * the sums, beside what the FP32 scores have. Scores of a block whose mean is infinite (or
+ * rounds to it) are infinite or NaN.
  *
  * Dh == 128, H a multiple of Hkv, at most 65,535. A call with Lq or Lk 0: no scores and
  * nothing done; h3_attention_blocks with Lk 0 writes zeros. max_blocks >= 1, rows * max_blocks
- * and rows * nk below 2^31 (rows = H * nq), nq and nk at most 2^20.
+ * and rows * nk below 2^31 (rows = H * nq), nq and nk at most 2^20; in h3_attention_blocks
+ * max_blocks * k_block at most 2^17.
  */
 #define H3_QUERY_BLOCK 256
 size_t h3_block_scores_workspace_bytes(int Lq, int Lk, int H, int Hkv, int k_block);
@@ -661,8 +664,8 @@ h3_status h3_quantize_fp4_rows(const void* x, int64_t ld_x, void* codes, void* s
  * for i < L: a projection of 4-bit rows on tcgen05 (block-scaled products, FP32
  * accumulation); rx and rw are the row scales (1 in H3_FP4_MX, where they are NULL).
  *   x_codes [S, K / 2], x_scales, rx [S]; w_codes [N, K / 2], w_scales, rw [N]; y [S, N] bf16
- *   K % 32 == 0, N % 8 == 0; both operands in the same format; codes and y 16-byte,
- *   scales 128-byte aligned; y overlaps nothing.
+ *   K % 32 == 0, K <= 16384, N % 8 == 0; both operands in the same format; codes, y and rw
+ *   16-byte, scales 128-byte aligned; y overlaps nothing.
  */
 h3_status h3_linear_fp4(const void* x_codes, const void* x_scales, const float* rx,
                         const void* w_codes, const void* w_scales, const float* rw, void* y,

@@ -101,7 +101,7 @@ def test_fp4_products(lib, name, N, odd):
             (1, "NULL", (NULL, P, P, *W, R_, 8, 8, N, 64, 1)), (1, "NULL", (*X, Q, NULL, Q, R_, 8, 8, N, 64, 1)),
             (1, "row scales", (P, P, NULL, *W, R_, 8, 8, N, 64, 1)), (1, "row scales", (*X, *W, R_, 8, 8, N, 64, 0)),
             (3, "aligned", (PM, P, P, *W, R_, 8, 8, N, 64, 1)), (3, "aligned", (*X, Q, Q, PM, R_, 8, 8, N, 64, 1)),
-            (1, "overlaps", (*X, *W, P, 8, 8, N, 64, 1)), (2, "2^20", (*X, *W, R_, 8, 8, N, (1 << 20) + 32, 1))):
+            (1, "overlaps", (*X, *W, P, 8, 8, N, 64, 1)), (2, "16384", (*X, *W, R_, 8, 8, N, 16416, 1)), (2, "2^30", (*X, *W, R_, (1 << 30) + 1, (1 << 30) + 1, N, 64, 1))):
         assert f(*a, NULL) == status, (a, h3.last_error())
         assert text in h3.last_error()
 
@@ -153,7 +153,8 @@ def test_attention_blocks(lib):
             (1, "scale", dict(scale=F(float("nan")))), (1, "o is q", dict(o=P)), (1, "o is k", dict(o=Q)),
             (1, "v is NULL", dict(v=NULL)), (3, "aligned", dict(ld_v=260)), (1, "row stride", dict(ld_o=504)),
             (1, "ids", dict(ids=NULL)), (3, "4-byte", dict(counts=ctypes.c_void_p(4097))),
-            (2, "65535", dict(H=65536, Hkv=1)), (2, "2^31", dict(Lq=1 << 28, most=1 << 12))):
+            (2, "65535", dict(H=65536, Hkv=1)), (2, "2^31", dict(Lq=1 << 28, most=1 << 12)),
+            (2, "2^17", dict(most=2049)), (2, "2^17", dict(most=1025, kb=128))):
         assert f(*(ok | kw).values()) == status, (kw, h3.last_error())
         assert text in h3.last_error()
 

@@ -267,6 +267,25 @@ def test_large_scores_and_far_blocks(h3lib):
     check_attention(h3lib, q, k, v, ids.flip(-1).contiguous(), n, 64, scale=0.2)
 
 
+def test_the_longest_lists(h3lib):
+    # 2^17 keys in one accumulator, of values of one sign: the tensor cores' sums come out low, by
+    # little over 2^-11; the weights are all 1 and their sum exact
+    g = gen(13)
+    Lk = 1 << 17
+    q = torch.zeros(200, 2, 128, dtype=torch.bfloat16, device=dev)
+    k, v = heads(Lk, 1, g), torch.full((Lk, 1, 128), 1.0, dtype=torch.bfloat16, device=dev)
+    v[:, :, 64:] += torch.rand(Lk, 1, 64, generator=g, device=dev).to(torch.bfloat16)
+    for kb in (64, 128):
+        most = Lk // kb
+        ids = torch.arange(most, dtype=torch.int32, device=dev).expand(2, 1, most).contiguous()
+        n = torch.full((2, 1), most, dtype=torch.int32, device=dev)
+        o = torch.empty_like(q)
+        h3lib.attention_blocks(q, k, v, o, ids, n, k_block=kb)
+        h3lib.check_device_error()
+        ref = v.double().mean(0)
+        assert ((o.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -10) * ref).all()
+
+
 def test_strided_rows_of_one_buffer(h3lib):
     g = gen(9)
     qkv = heads(700, 12, g)

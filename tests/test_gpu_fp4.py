@@ -233,11 +233,12 @@ def test_linear_exact_small_integers(h3lib, fmt):
 def test_linear(h3lib, S, L, N, K, fmt):
     qx = quantize(h3lib, draw(S, K, seed=S + N), fmt)
     qw = quantize(h3lib, draw(N, K, seed=K, std=0.02), fmt)
-    y = torch.full((S, N), SENT, dtype=torch.bfloat16, device=dev)
+    buf = torch.full((S + 2, N), SENT, dtype=torch.bfloat16, device=dev)
+    y = buf[1:S + 1]
     h3lib.linear_fp4(qx, qw, y, L)
     h3lib.check_device_error()
     check_linear(y, qx, qw, np.arange(L), f"{fmt} {S}x{N}x{K}")
-    assert bool((y[L:] == SENT).all())
+    assert bool((buf[L + 1:] == SENT).all()) and bool((buf[0] == SENT).all())
     again = torch.empty_like(y)
     h3lib.linear_fp4(qx, qw, again, L)
     h3lib.check_device_error()

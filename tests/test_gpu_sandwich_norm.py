@@ -181,3 +181,34 @@ def test_same_as_the_modulated_norm(h3lib):
     assert torch.equal(out, r)
     step = 2.0 ** -7 * torch.maximum(h.float().abs(), normed.float().abs())
     assert ((h.float() - normed.float()).abs() <= step + 2.0 ** -22).all()
+
+
+def test_graph_and_side_stream(h3lib):
+    names = ("resid", "delta", "post_gain", "pre_gain", "seg")
+    ins = [draw(300, 1928, seed, groups=2) for seed in (21, 22)]
+    tables = [torch.stack([a["gate"], a["shift"], a["scale"]], 1) for a in ins]     # [groups, 3, D]
+    live, table = {k: ins[0][k].clone() for k in names}, tables[0].clone()
+    out, normed = torch.empty(300, 1928, device=dev), torch.empty(300, 1928, device=dev, dtype=torch.bfloat16)
+
+    def run():
+        h3lib.sandwich_norm(live["resid"], live["delta"], normed, resid_out=out, post_gain=live["post_gain"],
+                            gate=table[:, 0], resid_scale=0.75, pre_gain=live["pre_gain"], shift=table[:, 1],
+                            scale=table[:, 2], seg=live["seg"])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    for i in (1, 0):
+        for k in names:
+            live[k].copy_(ins[i][k])
+        table.copy_(tables[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, normed, ins[i], 300, "replayed")
+        got = out.clone(), normed.clone()
+        with torch.cuda.stream(side):
+            run()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got[0]) and torch.equal(normed, got[1])
