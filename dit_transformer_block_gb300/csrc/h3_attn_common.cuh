@@ -1,7 +1,7 @@
 // Pieces shared by the attention kernels (h3_attention.cu: dense attention
 // by CTA pairs; h3_attention_tiles.cu: Skip-Softmax and FP8 attention;
-// h3_paged_attention.cu: the tile sizes only): tile sizes, the kernel
-// arguments, the O row store. Included by those three files only.
+// h3_paged_attention.cu and h3_block_attention.cu: the tile sizes only): tile
+// sizes, the kernel arguments, the O row store. Included by those files only.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

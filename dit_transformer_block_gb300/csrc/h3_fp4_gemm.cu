@@ -15,7 +15,11 @@
 //     or six (MX) copies take longer to issue than the products to run;
 //   * warps 2-9: epilogue, two per lane quarter. A warp reads its 128 columns of the
 //     accumulator at once, so that the next tile's products wait for one read and not for
-//     the stores, then writes bf16 through 4 KB of shared memory of its own with TMA;
+//     the stores, then writes bf16 through 4 KB of shared memory of its own with TMA. The CTA's
+//     sixteen stores of a tile spread over the next tile's products (128 cycles each at best,
+//     16 x 7 of them from store to store): in one go they hold up the loads, and the products
+//     wait (2,432 tiles of K = 5,120: 239 us instead of 247 in MX, 251 and 257 in NV, of K = 2,560
+//     138 and 147, 144 and 155; 220 and 228 of K = 5,120 if nothing were stored);
 //   * tensor memory: 256 columns of accumulator, a buffer of scales per stage.
 // A CTA gets its operands at a rate that its copies in flight allow, so where there are few
 // tiles (few rows: the weights' bytes count) several pairs in a cluster share one tile's K. They
@@ -42,7 +46,8 @@ constexpr int EPI_WARPS = 8, COPY_WARPS = 2;
 constexpr int THREADS4 = (2 + EPI_WARPS + COPY_WARPS) * 32;
 constexpr int GROUP_M4 = 16;                 // raster: 16 x 256 rows per sweep of the columns
 constexpr int OUT_BYTES = 32 * 128;          // a warp's 32 rows x 64 columns of output
-constexpr size_t SMEM4_BYTES = 1024 + STAGES4 * STAGE4_BYTES + EPI_WARPS * OUT_BYTES + 256;
+constexpr int SCALE_BYTES = 3 * BN4 * 4;          // scales of a tile's columns (NV), three tiles
+constexpr size_t SMEM4_BYTES = 1024 + STAGES4 * STAGE4_BYTES + EPI_WARPS * OUT_BYTES + 256 + SCALE_BYTES;
 static_assert(SMEM4_BYTES <= 227 * 1024, "fp4 gemm shared memory");
 
 // Tensor memory: the accumulator, then a buffer of scales per stage: A's, from SFB on B's.
@@ -156,6 +161,7 @@ struct Gemm4Args {
   int sf_tiles;             // scale tiles along K
   int parts;                // pairs that share a tile's K
   int up_rows;              // SwiGLU: first row of the up half of B
+  int pace;                 // cycles from one of a CTA's sixteen stores of a tile to the next
   DevErr err;
 };
 
@@ -189,7 +195,8 @@ __global__ void __launch_bounds__(THREADS4, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sOut = smem + STAGES4 * STAGE4_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + EPI_WARPS * OUT_BYTES);
+  uint8_t* sScale = sOut + EPI_WARPS * OUT_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + SCALE_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B4_NUM);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
@@ -383,19 +390,24 @@ __global__ void __launch_bounds__(THREADS4, 1)
       st_shared_v4(out + lane * 128 + ((piece ^ (lane & 7)) << 4), x, y, z, w);
     };
     uint32_t phase = 0;
+    int turn = 0;
     for (int tile = pair; tile < a.num_tiles; tile += pairs, phase ^= 1u) {
       int mb, nb;
       tile_coords4(tile, a, mb, nb);
       const int row0 = (2 * mb + static_cast<int>(rank)) * ROWS + quarter * 32;
-      // scales of the row and, a lane four of them, of the warp's 128 columns (or 64 and 64),
-      // asked for while the products run
+      // scales of the row and, in shared memory, of the warp's 128 columns (or 64 and 64), read
+      // while the products run
       float ra = 1.f;
-      float4 rb = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4* rb = nullptr;
       if constexpr (NV) {
         if (row0 + lane < a.M) ra = *(a.ra + row0 + lane);
         const int b = SWIGLU ? (lane >> 4) * a.up_rows + nb * (BN4 / 2) + side * 64 + (lane & 15) * 4
                              : nb * BN4 + side * (BN4 / 2) + lane * 4;
-        if (SWIGLU || b < a.N) rb = *reinterpret_cast<const float4*>(a.rb + b);
+        // (the four warps of a side write the same; none is three tiles behind another)
+        rb = reinterpret_cast<float4*>(sScale) + (turn * 2 + side) * 32;
+        if (SWIGLU || b < a.N) rb[lane] = *reinterpret_cast<const float4*>(a.rb + b);
+        __syncwarp();
+        if (++turn == 3) turn = 0;
       }
       if (!mbar_wait_warp(bar(B4_TFULL), phase, a.err, ERR_WAIT_GEMM_EPILOGUE)) break;
       tc_fence_after();
@@ -435,16 +447,24 @@ __global__ void __launch_bounds__(THREADS4, 1)
         continue;
       }
       if (row0 >= a.M) continue;
+      const long long drained = clock64();
+      // the turn-th sixteenth of the next tile's products
+      auto wait_turn = [&](int turn) {
+        if (tile + pairs < a.num_tiles)
+          while (static_cast<uint64_t>(clock64() - drained) < static_cast<uint32_t>(turn * a.pace))
+            __nanosleep(64);
+        __syncwarp();
+      };
       // eight products, v[c][8 j ..], scaled
       auto scaled = [&](int c, int j, float (&f)[8]) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(v[c][8 * j + t]);
         if constexpr (NV) {
+          float b[8];
+          *reinterpret_cast<float4*>(b) = rb[c * 8 + 2 * j];
+          *reinterpret_cast<float4*>(b + 4) = rb[c * 8 + 2 * j + 1];
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const float mine = (t & 3) == 0 ? rb.x : (t & 3) == 1 ? rb.y : (t & 3) == 2 ? rb.z : rb.w;
-            f[t] = f[t] * ra * __shfl_sync(0xffffffffu, mine, c * 8 + 2 * j + (t >> 2));
-          }
+          for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * b[t];
         }
       };
       auto send = [&](int col) {  // what is put, to the output's columns from col on
@@ -459,6 +479,7 @@ __global__ void __launch_bounds__(THREADS4, 1)
       };
       if constexpr (SWIGLU) {
         const int col0 = nb * (BN4 / 2) + side * 64;
+        wait_turn(2 * (warp - 2));
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -481,6 +502,7 @@ __global__ void __launch_bounds__(THREADS4, 1)
         for (int h = 0; h < 2; ++h) {
           const int col0 = nb * BN4 + side * (BN4 / 2) + h * 64;
           if (col0 < a.N) {
+            wait_turn(warp - 2 + h * EPI_WARPS);
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
               float f[8];
@@ -577,6 +599,7 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   a.num_k = (K + STAGE_CODES - 1) / STAGE_CODES;
   a.num_tiles = a.num_m * a.num_n;
   a.sf_tiles = fp4_tiles(K, NV);
+  a.pace = a.num_k * (STAGE_CODES / 64) * 7;
   a.up_rows = SWIGLU ? N : 0;
   if ((st = dev_err(&a.err)) != H3_OK) return st;
   CUtensorMap tmA, tmB, tmSA, tmSB, tmC;

@@ -1,6 +1,7 @@
 """Small, fixed cases for ncu captures of the library's kernels.
 
     python -m dit_transformer_block_gb300.profile_cases [attention] [gemm] [elementwise] [fp8] [sage] [paged]
+                                                        [norms] [fp4] [blocks]
 
 Each selected kernel runs twice on inputs larger than L2 (129 MB) but a few
 hundred MB in total, so that an `ncu --set full -k <kernel> -s 1 -c 1`
@@ -20,6 +21,12 @@ capture of the second launch ends within a minute or two:
   paged       the paged cache: 16384 rows appended (42 heads, interleaved pairs),
               1896 rows against 16384 keys (42 heads), 64 rows of 4096 keys (40
               heads on 8), and 512 rows of 256 keys (32 heads on 8)
+  norms       norms around a gated branch, 16384 x 5376
+  fp4         4-bit rows: quantisation of 16384 x 5376 (both formats), the QKV
+              projection shape with M = 8192 (both), SwiGLU M = 4096, F = 14336, and
+              16 rows of the QKV shape (few tiles, K shared)
+  blocks      16384 rows of 42 heads: scores of key blocks of 64, selection of 56
+              per query block, attention over them
 """
 from __future__ import annotations
 
@@ -31,7 +38,7 @@ from dit_transformer_block_gb300 import build, h3
 
 
 def main(argv):
-    which = set(argv) or {"attention", "gemm", "elementwise", "fp8", "sage", "paged"}
+    which = set(argv) or {"attention", "gemm", "elementwise", "fp8", "sage", "paged", "norms", "fp4", "blocks"}
     build.build()
     h3.lib()
     dev = "cuda"
@@ -122,6 +129,48 @@ def main(argv):
         attend(1, 1896, 16384, 42, 42)
         attend(64, 1, 4096, 40, 8)
         attend(512, 1, 256, 32, 8)
+    if "norms" in which:
+        S, D = 16384, 5376
+        rn, dn = torch.randn(S, D, generator=g, device=dev), rnd(S, D)
+        on, hn = torch.empty_like(rn), torch.empty_like(dn)
+        vecs = torch.randn(5, D, generator=g, device=dev) * 0.1
+        runs.append(lambda: h3.sandwich_norm(rn, dn, hn, resid_out=on, post_gain=vecs[0], gate=vecs[1],
+                                             pre_gain=vecs[2], shift=vecs[3], scale=vecs[4], rms=True))
+    if "fp4" in which:
+        def rows(R, K, form, std=1.0):
+            x, q = rnd(R, K, std=std), h3.fp4_rows(R, K, format=form)
+            h3.quantize_fp4_rows(x, q)
+            return x, q
+
+        def product(M, N, K, form, swiglu=False):
+            xq, wq = rows(M, K, form)[1], rows(2 * N if swiglu else N, K, form, 0.02)[1]
+            yq = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+            fn = h3.linear_swiglu_fp4 if swiglu else h3.linear_fp4
+            runs.append(lambda: fn(xq, wq, yq))
+
+        def quantise(R, K, form):
+            xq, qq4 = rows(R, K, form)
+            runs.append(lambda: h3.quantize_fp4_rows(xq, qq4))
+
+        for form in ("mx", "nv"):
+            quantise(16384, 5376, form)
+        for form in ("mx", "nv"):
+            product(8192, 16128, 5376, form)
+        product(4096, 14336, 5376, "mx", swiglu=True)
+        product(16, 16128, 5376, "nv")
+    if "blocks" in which:
+        S, H, most = 16384, 42, 56
+        qb, kb, vb = rnd(S, H, 128), rnd(S, H, 128), rnd(S, H, 128)
+        ob = torch.empty_like(qb)
+        nq, nk = S // h3.QUERY_BLOCK, S // 64
+        sc = torch.empty(H, nq, nk, device=dev)
+        ids = torch.empty(H, nq, most, dtype=torch.int32, device=dev)
+        counts = torch.empty(H, nq, dtype=torch.int32, device=dev)
+        wsb = torch.empty(h3.block_scores_workspace_bytes(S, S, H, H, 64), device=dev, dtype=torch.uint8)
+        runs.append(lambda: h3.block_scores(qb, kb, sc, wsb, k_block=64))
+        runs.append(lambda: h3.block_select(sc, ids, counts, keep_first=1, keep_last=1))
+        runs.append(lambda: h3.attention_blocks(qb, kb, vb, ob, ids, counts, k_block=64))
+    torch.cuda.synchronize()
     for _ in range(2):
         for fn in runs:
             fn()
