@@ -361,10 +361,16 @@ __global__ void __launch_bounds__(THREADS4, 1)
       auto wait = [&](int b, uint32_t parity) {
         return mbar_wait_warp(bar(b), parity, a.err, ERR_WAIT_GEMM_MMA);
       };
-      for (int it = c; it < total; it += COPY_WARPS) {
-        // (the stage was loaded again only after the products that read its buffer)
-        const int st = it % STAGES4;
-        if (!wait(B4_FULL + st, static_cast<uint32_t>(it / STAGES4) & 1u)) break;
+      // (the stage was loaded again only after the products that read its buffer)
+      for (int it = 0, st = -1, phase = 0; it < total; ++it) {
+        if (++st == STAGES4) {
+          st = 0;
+          phase ^= 1;
+        }
+        // every stage is waited for, also the other warp's: loads may land out of order, and a
+        // barrier whose phase before is still open looks as if this one were over
+        if (!wait(B4_FULL + st, phase)) break;
+        if (it % COPY_WARPS != c) continue;
         tc_fence_after();
         const uint64_t s = ds0 + static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
         const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(st) * TM::SF_COLS;
