@@ -217,19 +217,28 @@ __global__ void __launch_bounds__(FEW_WARPS * 32)
   }
 }
 
-// scores[h] = scale * mq[h] mk[g]^T: 128 query blocks x 128 key blocks of a head per CTA (230 x 919 blocks of 42
-// heads in 30 us, and 75 us by FP32 FMAs; three CTAs to an SM of one stage each are no faster).
-// A stage is 32
-// channels (128 bytes a row) of both parts of both operands; warp 0 loads (TMA), warp 1
-// issues, per 8 channels, three products into one FP32 accumulator, and warps 2 to 5 write the
-// scores, row by row through shared memory, since a row of them starts at any 4 bytes.
+// scores[h] = scale * mq[h] mk[g]^T: a CTA per SM takes one tile of 128 query blocks x 128 key
+// blocks of a head after the other (230 x 919 blocks of 42 heads in 17 us, 30 with a CTA per tile
+// and 75 by FP32 FMAs). A stage is 32 channels (128 bytes a row) of both parts of both operands;
+// warp 0 loads (TMA), warp 1 issues, per 8 channels, three products into one of two FP32
+// accumulators, and warps 2 to 5 write the other's scores, row by row through shared memory,
+// since a row of them starts at any 4 bytes.
 constexpr int TC_TILE = 128, TC_STAGES = 3, TC_STEPS = DHB / 32;
 constexpr int TC_PART = TC_TILE * 128;         // 16 KB: 128 rows x 32 channels
 constexpr int TC_STAGE_BYTES = 4 * TC_PART;    // A high, A low, B high, B low
 constexpr int TC_THREADS = 192;
-constexpr size_t TC_SMEM_BYTES = 1024 + TC_STAGES * TC_STAGE_BYTES + 128;
+constexpr int TC_OUT = 32 * 128;               // a warp's 32 rows x 32 scores
+constexpr size_t TC_SMEM_BYTES = 1024 + TC_STAGES * TC_STAGE_BYTES + 4 * TC_OUT + 128;
 static_assert(TC_SMEM_BYTES <= 227 * 1024, "block scores shared memory");
-enum BarTc { BT_FULL = 0, BT_EMPTY = TC_STAGES, BT_DONE = 2 * TC_STAGES, BT_NUM = BT_DONE + 1 };
+enum BarTc {
+  BT_FULL = 0,                     // stage landed
+  BT_EMPTY = BT_FULL + TC_STAGES,  // stage read by the products
+  BT_DONE = BT_EMPTY + TC_STAGES,  // [2] accumulator written
+  BT_READ = BT_DONE + 2,           // [2] accumulator read (4 warps)
+  BT_DRAIN = BT_READ + 2,
+  BT_NUM
+};
+static_assert(BT_NUM * 8 + 8 <= 128, "barrier region");
 
 __device__ __forceinline__ void mma_tf32_el(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -240,24 +249,37 @@ __device__ __forceinline__ void mma_tf32_el(uint32_t d, uint64_t a, uint64_t b, 
       : "memory");
 }
 
+struct ScoreSizes {
+  int nq, nk, group;
+  int across, down, tiles;  // tiles of a head along the key blocks, the query blocks; of all heads
+};
+
+// Head, first query block and first key block of a tile.
+__device__ __forceinline__ void score_tile(int tile, const ScoreSizes& z, int& h, int& t0, int& b0) {
+  const int r = tile / z.across;
+  b0 = (tile - r * z.across) * TC_TILE;
+  h = r / z.down;
+  t0 = (r - h * z.down) * TC_TILE;
+}
+
 __global__ void __launch_bounds__(TC_THREADS, 1)
     block_scores_kernel(const __grid_constant__ CUtensorMap tmQh, const __grid_constant__ CUtensorMap tmQl,
                         const __grid_constant__ CUtensorMap tmKh, const __grid_constant__ CUtensorMap tmKl,
-                        float* scores, int nq, int nk, int group, float scale, const DevErr err) {
+                        float* scores, const ScoreSizes z, float scale, const DevErr err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + TC_STAGES * TC_STAGE_BYTES);
+  uint8_t* out = smem + TC_STAGES * TC_STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out + 4 * TC_OUT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BT_NUM);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.z, t0 = blockIdx.y * TC_TILE, b0 = blockIdx.x * TC_TILE;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < BT_NUM; ++i) mbar_init(bar(i), 1);
+    for (int i = 0; i < BT_NUM; ++i) mbar_init(bar(i), i == BT_READ || i == BT_READ + 1 ? 4 : 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), TC_TILE);
+    tmem_alloc(smem_u32(tmem_slot), 2 * TC_TILE);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -268,21 +290,28 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      // (rows past the head's last block are the next head's, or zeros; nothing is stored of them)
-      const int qrow = h * nq + t0, krow = h / group * nk + b0;
-      int issued = 0;
-      for (int c = 0; c < TC_STEPS; ++c) {
-        const int st = c % TC_STAGES;
-        if (!mbar_wait(bar(BT_EMPTY + st), (static_cast<uint32_t>(c / TC_STAGES) & 1u) ^ 1u, err,
-                       ERR_WAIT_GEMM_PRODUCER))
-          break;
-        const uint32_t full = bar(BT_FULL + st), dst = smem_u32(smem + st * TC_STAGE_BYTES);
-        mbar_arrive_expect_tx(full, TC_STAGE_BYTES);
-        tma_load_2d(dst, &tmQh, full, c * 32, qrow);
-        tma_load_2d(dst + TC_PART, &tmQl, full, c * 32, qrow);
-        tma_load_2d(dst + 2 * TC_PART, &tmKh, full, c * 32, krow);
-        tma_load_2d(dst + 3 * TC_PART, &tmKl, full, c * 32, krow);
-        issued = c + 1;
+      int issued = 0, st = 0;
+      uint32_t phase = 1;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < z.tiles && ok; tile += gridDim.x) {
+        // (rows past the head's last block are the next head's, or zeros; nothing is stored of them)
+        int h, t0, b0;
+        score_tile(tile, z, h, t0, b0);
+        const int qrow = h * z.nq + t0, krow = h / z.group * z.nk + b0;
+        for (int c = 0; c < TC_STEPS; ++c) {
+          if (!(ok = mbar_wait(bar(BT_EMPTY + st), phase, err, ERR_WAIT_GEMM_PRODUCER))) break;
+          const uint32_t full = bar(BT_FULL + st), dst = smem_u32(smem + st * TC_STAGE_BYTES);
+          mbar_arrive_expect_tx(full, TC_STAGE_BYTES);
+          tma_load_2d(dst, &tmQh, full, c * 32, qrow);
+          tma_load_2d(dst + TC_PART, &tmQl, full, c * 32, qrow);
+          tma_load_2d(dst + 2 * TC_PART, &tmKh, full, c * 32, krow);
+          tma_load_2d(dst + 3 * TC_PART, &tmKl, full, c * 32, krow);
+          ++issued;
+          if (++st == TC_STAGES) {
+            st = 0;
+            phase ^= 1u;
+          }
+        }
       }
       launch_next();
       const uint64_t at = globaltimer_ns();
@@ -296,55 +325,86 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                (static_cast<uint32_t>(TC_TILE >> 3) << 17) |
                                (static_cast<uint32_t>(TC_TILE >> 4) << 24);
     const uint64_t base = sdesc_sw128(smem_u32(smem), 16, 1024);
-    for (int c = 0; c < TC_STEPS; ++c) {
-      const int st = c % TC_STAGES;
-      if (!mbar_wait_warp(bar(BT_FULL + st), static_cast<uint32_t>(c / TC_STAGES) & 1u, err,
-                          ERR_WAIT_GEMM_MMA))
-        break;
-      tc_fence_after();
-      const uint64_t ah = base + static_cast<uint32_t>(st * (TC_STAGE_BYTES >> 4));
-      const uint64_t al = ah + (TC_PART >> 4), bh = ah + (2 * TC_PART >> 4);
-      const uint64_t bl = ah + (3 * TC_PART >> 4);
+    auto wait = [&](int b, uint32_t parity) {
+      return mbar_wait_warp(bar(b), parity, err, ERR_WAIT_GEMM_MMA);
+    };
+    int st = 0, n = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < z.tiles && ok; tile += gridDim.x, ++n) {
+      const int acc = n & 1;
+      if (!(ok = wait(BT_READ + acc, (static_cast<uint32_t>(n >> 1) & 1u) ^ 1u))) break;
+      for (int c = 0; c < TC_STEPS; ++c) {
+        if (!(ok = wait(BT_FULL + st, phase))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * TC_TILE;
+        const uint64_t ah = base + static_cast<uint32_t>(st * (TC_STAGE_BYTES >> 4));
+        const uint64_t al = ah + (TC_PART >> 4), bh = ah + (2 * TC_PART >> 4);
+        const uint64_t bl = ah + (3 * TC_PART >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        mma_tf32_el(tmem, ah + k * 2, bl + k * 2, idesc, (c | k) != 0 ? 1u : 0u);
-        mma_tf32_el(tmem, al + k * 2, bh + k * 2, idesc, 1u);
-        mma_tf32_el(tmem, ah + k * 2, bh + k * 2, idesc, 1u);
+        for (int k = 0; k < 4; ++k) {
+          mma_tf32_el(d, ah + k * 2, bl + k * 2, idesc, (c | k) != 0 ? 1u : 0u);
+          mma_tf32_el(d, al + k * 2, bh + k * 2, idesc, 1u);
+          mma_tf32_el(d, ah + k * 2, bh + k * 2, idesc, 1u);
+        }
+        mma_commit_el(bar(BT_EMPTY + st));
+        if (++st == TC_STAGES) {
+          st = 0;
+          phase ^= 1u;
+        }
       }
-      mma_commit_el(bar(BT_EMPTY + st));
+      if (ok) mma_commit_el(bar(BT_DONE + acc));
     }
-    mma_commit_el(bar(BT_DONE));
-    mbar_wait_drain(bar(BT_DONE), 0u, globaltimer_ns(), drain_limit_ns(err));
+    mma_commit_el(bar(BT_DRAIN));
+    mbar_wait_drain(bar(BT_DRAIN), 0u, globaltimer_ns(), drain_limit_ns(err));
   } else {
     const int quarter = warp & 3;
-    if (mbar_wait_warp(bar(BT_DONE), 0u, err, ERR_WAIT_GEMM_EPILOGUE)) {
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    // 32 rows x 32 scores: float4 c of row r at c ^ (r & 7)
+    float4* rows = reinterpret_cast<float4*>(out + (warp - 2) * TC_OUT);
+    const float* words = reinterpret_cast<const float*>(rows);
+    int n = 0;
+    for (int tile = blockIdx.x; tile < z.tiles; tile += gridDim.x, ++n) {
+      int h, t0, b0;
+      score_tile(tile, z, h, t0, b0);
+      const int acc = n & 1;
+      if (!mbar_wait_warp(bar(BT_DONE + acc), static_cast<uint32_t>(n >> 1) & 1u, err,
+                          ERR_WAIT_GEMM_EPILOGUE))
+        break;
       tc_fence_after();
-      // the warp's 32 rows x 128 scores, float4 c of row r at c ^ (r & 31): no load and no product
-      // is under way any more
-      float4* rows = reinterpret_cast<float4*>(smem) + (warp - 2) * 32 * (TC_TILE / 4);
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(t_row + acc * TC_TILE + c * 32, v[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_reg_fence(v[c]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BT_READ + acc));
+      const int first = t0 + quarter * 32, m = min(32, z.nq - first);
+      float* o = scores + (static_cast<int64_t>(h) * z.nq + first) * z.nk + b0 + lane;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        tmem_ld32(t_row + c * 32, v);
-        tmem_ld_wait();
-        tmem_reg_fence(v);
+        if (m <= 0 || b0 + c * 32 >= z.nk) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          rows[lane * (TC_TILE / 4) + ((c * 8 + j) ^ lane)] =
-              make_float4(__uint_as_float(v[4 * j]) * scale, __uint_as_float(v[4 * j + 1]) * scale,
-                          __uint_as_float(v[4 * j + 2]) * scale, __uint_as_float(v[4 * j + 3]) * scale);
-      }
-      __syncwarp();
-      const int first = t0 + quarter * 32, n = min(32, nq - first);
-      const float* words = reinterpret_cast<const float*>(rows);
-      for (int r = 0; r < n; ++r) {
-        float* o = scores + (static_cast<int64_t>(h) * nq + first + r) * nk + b0;
+          rows[lane * 8 + (j ^ (lane & 7))] =
+              make_float4(__uint_as_float(v[c][4 * j]) * scale, __uint_as_float(v[c][4 * j + 1]) * scale,
+                          __uint_as_float(v[c][4 * j + 2]) * scale, __uint_as_float(v[c][4 * j + 3]) * scale);
+        __syncwarp();
+        const bool mine = b0 + c * 32 + lane < z.nk;
+        auto store = [&](int r) {
+          if (mine)
+            o[static_cast<int64_t>(r) * z.nk + c * 32] =
+                words[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+        };
+        if (m == 32) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int b = j * 32 + lane;
-          if (b0 + b < nk) o[b] = words[r * TC_TILE + (((b >> 2) ^ r) << 2) + (b & 3)];
+          for (int r = 0; r < 32; ++r) store(r);
+        } else {
+          for (int r = 0; r < m; ++r) store(r);
         }
+        __syncwarp();
       }
     }
   }
@@ -353,7 +413,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TC_TILE);
+    tmem_dealloc(tmem, 2 * TC_TILE);
   }
 }
 
@@ -689,9 +749,10 @@ h3_status launch_block_scores(const void* q, int64_t ld_q, const void* k, int64_
     if ((st = make_tmap_f32_2d(&t[i], parts[i], DHB, i < 2 ? q_rows : k_rows, DHB * 4, 32, TC_TILE)) !=
         H3_OK)
       return st;
-  const dim3 grid((nk + TC_TILE - 1) / TC_TILE, (nq + TC_TILE - 1) / TC_TILE, H);
-  return cuda_fail(launch_overlapped(block_scores_kernel, grid, TC_THREADS, TC_SMEM_BYTES, 1, s, t[0],
-                                     t[1], t[2], t[3], scores, nq, nk, H / Hkv, scale, err),
+  ScoreSizes z{nq, nk, H / Hkv, (nk + TC_TILE - 1) / TC_TILE, (nq + TC_TILE - 1) / TC_TILE, 0};
+  z.tiles = z.across * z.down * H;
+  return cuda_fail(launch_overlapped(block_scores_kernel, dim3(std::min(z.tiles, num_sms())), TC_THREADS,
+                                     TC_SMEM_BYTES, 1, s, t[0], t[1], t[2], t[3], scores, z, scale, err),
                    "block scores launch");
 }
 
