@@ -16,14 +16,20 @@
 //   * warps 2-9: epilogue, two per lane quarter. A warp reads its 128 columns of the
 //     accumulator at once, so that the next tile's products wait for one read and not for
 //     the stores, then writes bf16 through 4 KB of shared memory of its own with TMA. The CTA's
-//     sixteen stores of a tile spread over the next tile's products (128 cycles each at best,
-//     16 x 7 of them from store to store): in one go they hold up the loads, and the products
-//     wait (2,432 tiles of K = 5,120: 239 us instead of 247 in MX, 251 and 257 in NV, of K = 2,560
+//     sixteen stores of a tile spread over the next tile's products (seven cycles apart for
+//     every 64 values of K, whose product takes 128): in one go they hold up the loads, and the
+//     products wait (2,432 tiles of K = 5,120: 239 us instead of 247 in MX, 251 and 257 in NV, of K = 2,560
 //     138 and 147, 144 and 155; 220 and 228 of K = 5,120 if nothing were stored);
 //   * tensor memory: 256 columns of accumulator, a buffer of scales per stage.
 // A CTA gets its operands at a rate that its copies in flight allow, so where there are few
 // tiles (few rows: the weights' bytes count) several pairs in a cluster share one tile's K. They
-// put their sums into shared memory and each adds up a share of the columns, in the order of K.
+// put their sums into shared memory and each adds up a share of the rows, in the order of K
+// (22 x 5,376 x 5,376 with weights in HBM: 10.4 us with the quantisation, of which the weights' 15 MB
+// take 2.3).
+// 58,758 x 16,128 x 5,376: MX 1,436 us (7,100 TFLOP/s), NV 1,515 us (6,730). Products of K = 64 and
+// nothing else run at 9,220 TFLOP/s. With the loads beside them a stage takes 600 cycles instead
+// of 512 with five stages (686 with four, 857 with three, 605 with six), nearly the same where half
+// of B's loads, the scales' loads or their copies are left out; the stores add what is said above.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -130,6 +136,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src,
           reinterpret_cast<uint64_t>(m)),
       "r"(x), "r"(y), "r"(src)
       : "memory");
+}
+// 16 bytes of the shared memory of any CTA of the cluster.
+__device__ __forceinline__ void ld_cluster_v4(float4& v, uint32_t addr) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ void store_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -528,53 +541,55 @@ __global__ void __launch_bounds__(THREADS4, 1)
   tc_fence_before();
   cluster_sync_all();
   if constexpr (SPLIT) {
-    // this pair's share of the tile's columns, eight of a row to a thread
+    // this pair's share of the tile's rows: a warp takes one after the other, a lane four columns
+    // of it, twice (the second of which are the up half's in SwiGLU)
     constexpr int WIDTH = SWIGLU ? BN4 / 2 : BN4;
     int mb, nb;
     tile_coords4(pair, a, mb, nb);
-    const int g0 = WIDTH / 8 * part / a.parts, groups = WIDTH / 8 * (part + 1) / a.parts - g0;
     const int first = (2 * mb + static_cast<int>(rank)) * ROWS;
-    const int rows = min(ROWS, a.M - first);
+    const int rows = max(0, min(ROWS, a.M - first));
     const uint32_t sums = smem_u32(smem);
-    for (int i = threadIdx.x; i < rows * groups; i += THREADS4) {
-      const int r = i / groups, g = g0 + i % groups;
-      const int col = nb * WIDTH + g * 8;
-      if (col >= a.N) continue;
-      auto sum8 = [&](int piece, int b, float (&f)[8]) {  // columns 4 piece .. + 7, B's rows b ..
+    for (int r = rows * part / a.parts + warp; r < rows * (part + 1) / a.parts; r += THREADS4 / 32) {
+      // every part's loads are under way before the first is used
+      float4 y[4][2];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) f[t] = 0.f;
-        for (int p = 0; p < a.parts; ++p) {
+      for (int p = 0; p < 4; ++p) {
+        if (p < a.parts) {
           const uint32_t at = mapa_shared(sums + r * (BN4 * 4), 2 * p + rank);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float4 y;
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                         : "r"(at + (((piece + u) ^ (r & 31)) << 4))
-                         : "memory");
-            f[4 * u] += y.x, f[4 * u + 1] += y.y, f[4 * u + 2] += y.z, f[4 * u + 3] += y.w;
+          for (int u = 0; u < 2; ++u) ld_cluster_v4(y[p][u], at + (((lane + 32 * u) ^ (r & 31)) << 4));
+        }
+      }
+      float f[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) f[u][t] = 0.f;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          if (p < a.parts) {
+            f[u][0] += y[p][u].x, f[u][1] += y[p][u].y;
+            f[u][2] += y[p][u].z, f[u][3] += y[p][u].w;
           }
         }
-        if constexpr (NV) {
+        const int b = nb * WIDTH + lane * 4 + u * (SWIGLU ? a.up_rows : 128);
+        if (NV && (SWIGLU || b < a.N)) {
           const float ra = *(a.ra + first + r);
-          const float4 x = *reinterpret_cast<const float4*>(a.rb + b);
-          const float4 y = reinterpret_cast<const float4*>(a.rb + b)[1];
-          const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * s[t];
+          const float4 rb = *reinterpret_cast<const float4*>(a.rb + b);
+          f[u][0] *= ra, f[u][1] *= ra, f[u][2] *= ra, f[u][3] *= ra;
+          f[u][0] *= rb.x, f[u][1] *= rb.y, f[u][2] *= rb.z, f[u][3] *= rb.w;
         }
-      };
-      float f[8];
-      sum8(2 * g, col, f);
-      if constexpr (SWIGLU) {
-        float u[8];
-        sum8(BN4 / 8 + 2 * g, a.up_rows + col, u);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) f[t] = silu_f(round_to_bf16(f[t])) * round_to_bf16(u[t]);
       }
-      *reinterpret_cast<uint4*>(a.C + static_cast<int64_t>(first + r) * a.N + col) =
-          make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                     pack_bf16x2(f[6], f[7]));
+      __nv_bfloat16* c = a.C + static_cast<int64_t>(first + r) * a.N + nb * WIDTH + lane * 4;
+      if constexpr (SWIGLU) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) f[0][t] = silu_f(round_to_bf16(f[0][t])) * round_to_bf16(f[1][t]);
+      }
+#pragma unroll
+      for (int u = 0; u < (SWIGLU ? 1 : 2); ++u)
+        if (nb * WIDTH + lane * 4 + u * 128 < a.N)
+          *reinterpret_cast<uint2*>(c + u * 128) =
+              make_uint2(pack_bf16x2(f[u][0], f[u][1]), pack_bf16x2(f[u][2], f[u][3]));
     }
     cluster_sync_all();  // a peer may still be reading this CTA's sums
   }
@@ -620,11 +635,16 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   if ((st = make_tmap_u32_rows(&tmSA, A.scales, 128, ta, atoms)) != H3_OK) return st;
   if ((st = make_tmap_u32_rows(&tmSB, B.scales, 128, tb, atoms)) != H3_OK) return st;
   if ((st = make_tmap_bf16_2d(&tmC, C, N, L, static_cast<uint64_t>(N) * 2, 64, 32)) != H3_OK) return st;
-  // as many pairs to a tile as all tiles find room for, four stages each at least
+  // As many pairs to a tile as all tiles find room for, of four stages each at least, or, where
+  // there are more rows for the sums to be exchanged of, eight (4-bit rows and product, weights in
+  // HBM: 22 x 5,376 x 5,376 10.4 us by three pairs, 13.2 by one; 256 rows 14.5 by three of seven stages,
+  // 13.5 by two, 14.3 by one; K and N 2,048 22 rows 8.4 by two pairs of four stages, 8.7 by one, 128
+  // rows 10.3 and 9.5; 512 x 2,560 x 10,240 18.0 by three, 21.7 by one)
+  const int least = L > 64 ? 8 : 4;
   static std::atomic<int> room[64][9];
   a.parts = 1;
   for (int p = 4; p >= 2; --p) {
-    if (a.num_tiles * 2 * p > num_sms() || a.num_k < 4 * p) continue;
+    if (a.num_tiles * 2 * p > num_sms() || a.num_k < least * p) continue;
     st = set_smem_limit(done_split, gemm_fp4_kernel<NV, SWIGLU, true>, SMEM4_BYTES,
                         "fp4 gemm: set shared memory size");
     if (st != H3_OK) return st;

@@ -5,7 +5,11 @@
 // h = n(r) * pre_gain * (1 + scale) + shift, with n a LayerNorm without affine or a
 // division by the root mean square. Everything between the loads and the stores is
 // FP32, and the mean is taken before the squares (two passes over registers), so a
-// row far from zero loses nothing. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out.
+// row far from zero loses nothing. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out
+// (58,758 rows of 5,376, 3.79 GB: 605 us, 6.3 TB/s; 22 rows: 3.9 us, the latency of a load, of four
+// sums over the CTA and of a launch). Launched like an ordinary kernel, since its loads of
+// vectors that all rows share take the read-only path: without it, and launched ahead of the
+// end of the kernel before it, the same rows took 665 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
