@@ -18,7 +18,7 @@
 // and joins its partial results through distributed shared memory, in rank order.
 // Bound by the products of bf16 and by the power they draw: 58,758 rows of 42 heads, 92 blocks of 64
 // keys each, 7.4 TFLOP: 4.45 ms (1,670 TFLOP/s), 4.9 ms in a run of seconds. 22 rows of 40 heads, 23
-// blocks of 128: 13.3 us, of which the keys and values once are 4.6: three or four tiles one after
+// blocks of 128: 13.2 us, of which the keys and values once are 4.6: seven or eight tiles one after
 // another, and the join.
 #include <algorithm>
 
@@ -441,25 +441,34 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
     for (int r = rank * 10 + warp; r < rows; r += a.cluster * 10) {
       float top = -INFINITY, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int p = 0; p < a.cluster; ++p) {
-        float pm, pl;
-        const uint32_t ml = mapa_shared(base + 2 * BQ * DH * 4 + r * 8, p);
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(pm), "=f"(pl) : "r"(ml) : "memory");
-        if (pm == -INFINITY) continue;  // no key there
-        float4 y;
-        const uint32_t at = mapa_shared(base + r * (DH * 4) + ((lane ^ (r & 31)) * 16), p);
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                     : "r"(at)
-                     : "memory");
-        const float next = fmaxf(top, pm);
-        const float f = top == -INFINITY ? 0.f : ex2_approx(top - next), w = ex2_approx(pm - next);
+      // every part's loads are under way before the first is used
+      float2 ml[8];
+      float4 y[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        if (p < a.cluster) {
+          const uint32_t at = mapa_shared(base, p);
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(ml[p].x), "=f"(ml[p].y)
+                       : "r"(at + 2 * BQ * DH * 4 + r * 8)
+                       : "memory");
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(y[p].x), "=f"(y[p].y), "=f"(y[p].z), "=f"(y[p].w)
+                       : "r"(at + r * (DH * 4) + ((lane ^ (r & 31)) * 16))
+                       : "memory");
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        if (p >= a.cluster || ml[p].x == -INFINITY) continue;  // (or no key there: y is anything)
+        const float next = fmaxf(top, ml[p].x);
+        const float f = top == -INFINITY ? 0.f : ex2_approx(top - next), w = ex2_approx(ml[p].x - next);
         top = next;
-        sum = fmaf(pl, w, sum * f);
-        acc.x = fmaf(y.x, w, acc.x * f);
-        acc.y = fmaf(y.y, w, acc.y * f);
-        acc.z = fmaf(y.z, w, acc.z * f);
-        acc.w = fmaf(y.w, w, acc.w * f);
+        sum = fmaf(ml[p].y, w, sum * f);
+        acc.x = fmaf(y[p].x, w, acc.x * f);
+        acc.y = fmaf(y[p].y, w, acc.y * f);
+        acc.z = fmaf(y[p].z, w, acc.z * f);
+        acc.w = fmaf(y[p].w, w, acc.w * f);
       }
       const float inv = top == -INFINITY ? 0.f : 1.0f / sum;
       *reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(q0 + r) * a.ld_o + h * DH + lane * 4) =
