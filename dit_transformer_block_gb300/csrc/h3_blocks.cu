@@ -773,7 +773,7 @@ h3_status launch_block_select(const float* scores, int32_t* ids, int32_t* counts
                        (1.0 + t * (1.432788 + t * (0.189269 + t * 0.001308)));
     const double density = 0.3989422804014327 * std::exp(-0.5 * z * z);
     if (share > 0.5) z = -z;
-    const int grid = (rows + SEL_WARPS - 1) / SEL_WARPS;
+    const int grid = (rows - 1) / SEL_WARPS + 1;
     const float zf = static_cast<float>(z), df = static_cast<float>(std::max(density, 1e-4));
     auto kernel = nk <= 128    ? block_select_warp_kernel<4>
                   : nk <= 256  ? block_select_warp_kernel<8>

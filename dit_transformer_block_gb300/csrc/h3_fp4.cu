@@ -146,7 +146,7 @@ h3_status launch(const void* x, int64_t ldx, void* codes, void* scales, float* r
   auto* ss = static_cast<uint8_t*>(scales);
   const int n = (K / 16 + 7) & ~7;
 #define H3_Q4(T, V)                                                                             \
-  launch_overlapped(quantize_fp4_kernel<NV, T, V>, dim3(T == 32 ? (R + Q4_WARPS - 1) / Q4_WARPS : R), \
+  launch_overlapped(quantize_fp4_kernel<NV, T, V>, dim3(T == 32 ? (R - 1) / Q4_WARPS + 1 : R), \
                     T == 32 ? Q4_WARPS * 32 : T, 0, 1, s, xx, ldx, cc, ss, row_scale, R, K)
   const cudaError_t e = n <= 32    ? H3_Q4(32, 1)
                         : n <= 64  ? H3_Q4(32, 2)
