@@ -17,8 +17,8 @@
 //     accumulator at once, so that the next tile's products wait for one read and not for
 //     the stores, then writes bf16 through 4 KB of shared memory of its own with TMA. The CTA's
 //     sixteen stores of a tile spread over the next tile's products (seven cycles apart for
-//     every 64 values of K, whose product takes 128): in one go they hold up the loads, and the
-//     products wait (2,432 tiles of K = 5,120: 239 us instead of 247 in MX, 251 and 257 in NV, of K = 2,560
+//     every 64 values of K, whose product takes 128, or less in SwiGLU): in one go they hold up the
+//     loads, and the products wait (2,432 tiles of K = 5,120: 239 us instead of 247 in MX, 251 and 257 in NV, of K = 2,560
 //     138 and 147, 144 and 155; 220 and 228 of K = 5,120 if nothing were stored);
 //   * tensor memory: 256 columns of accumulator, a buffer of scales per stage.
 // A CTA gets its operands at a rate that its copies in flight allow, so where there are few
@@ -188,10 +188,30 @@ __device__ __forceinline__ void tile_coords4(int tile, const Gemm4Args& a, int& 
   nb = r / gm;
 }
 
-// (the division within 2 units of FP32's last place; its IEEE form takes a subroutine for
-// operands out of the ordinary and made the epilogue of a tile 4 us longer, 12 where rows
-// beyond the last one hold NaN)
-__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// bf16 SiLU(g) * u of two gates and two ups, rounded to bf16 first: g / (1 + 2^(-g log2 e)), the
+// exponential within 2^-22 of it and the reciprocal within 2^-23, which is flushed to 0 from where
+// the sum is above 2^126. (A tile's epilogue bounds products of few stages: 9,728 x 8,192 x 256 54 us in
+// MX and 74 in NV; 85 and 104 with __expf and __fdividef, which look after subnormal operands,
+// and each value rounded by itself; an IEEE division made a tile's epilogue 4 us longer.)
+__device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float u1) {
+  const uint32_t g = pack_bf16x2(g0, g1), u = pack_bf16x2(u0, u1);
+  auto silu = [](float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(-1.4426950408889634f * x)));
+    return x * r;
+  };
+  return pack_bf16x2(silu(bf16_lo(g)) * bf16_lo(u), silu(bf16_hi(g)) * bf16_hi(u));
+}
+// (a0, a1) * (b0, b1)
+__device__ __forceinline__ void fmul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
 
 // SPLIT: the cluster's pairs share one tile; else a pair takes one tile after another.
 template <bool NV, bool SWIGLU, bool SPLIT>
@@ -483,7 +503,10 @@ __global__ void __launch_bounds__(THREADS4, 1)
           *reinterpret_cast<float4*>(b) = rb[c * 8 + 2 * j];
           *reinterpret_cast<float4*>(b + 4) = rb[c * 8 + 2 * j + 1];
 #pragma unroll
-          for (int t = 0; t < 8; ++t) f[t] = f[t] * ra * b[t];
+          for (int t = 0; t < 8; t += 2) {
+            fmul2(f[t], f[t + 1], ra, ra);
+            fmul2(f[t], f[t + 1], b[t], b[t + 1]);
+          }
         }
       };
       auto send = [&](int col) {  // what is put, to the output's columns from col on
@@ -509,9 +532,7 @@ __global__ void __launch_bounds__(THREADS4, 1)
             uint32_t o[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-              o[t] = pack_bf16x2(
-                  silu_f(round_to_bf16(g[2 * t])) * round_to_bf16(u[2 * t]),
-                  silu_f(round_to_bf16(g[2 * t + 1])) * round_to_bf16(u[2 * t + 1]));
+              o[t] = swiglu2(g[2 * t], g[2 * t + 1], u[2 * t], u[2 * t + 1]);
             put(c * 4 + j, o[0], o[1], o[2], o[3]);
           }
         }
@@ -581,15 +602,16 @@ __global__ void __launch_bounds__(THREADS4, 1)
         }
       }
       __nv_bfloat16* c = a.C + static_cast<int64_t>(first + r) * a.N + nb * WIDTH + lane * 4;
+      auto store = [&](int u, uint32_t x, uint32_t y) {
+        if (nb * WIDTH + lane * 4 + u * 128 < a.N) *reinterpret_cast<uint2*>(c + u * 128) = make_uint2(x, y);
+      };
       if constexpr (SWIGLU) {
+        store(0, swiglu2(f[0][0], f[0][1], f[1][0], f[1][1]), swiglu2(f[0][2], f[0][3], f[1][2], f[1][3]));
+      } else {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) f[0][t] = silu_f(round_to_bf16(f[0][t])) * round_to_bf16(f[1][t]);
+        for (int u = 0; u < 2; ++u)
+          store(u, pack_bf16x2(f[u][0], f[u][1]), pack_bf16x2(f[u][2], f[u][3]));
       }
-#pragma unroll
-      for (int u = 0; u < (SWIGLU ? 1 : 2); ++u)
-        if (nb * WIDTH + lane * 4 + u * 128 < a.N)
-          *reinterpret_cast<uint2*>(c + u * 128) =
-              make_uint2(pack_bf16x2(f[u][0], f[u][1]), pack_bf16x2(f[u][2], f[u][3]));
     }
     cluster_sync_all();  // a peer may still be reading this CTA's sums
   }
@@ -620,7 +642,9 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   a.num_k = (K + STAGE_CODES - 1) / STAGE_CODES;
   a.num_tiles = a.num_m * a.num_n;
   a.sf_tiles = fp4_tiles(K, NV);
-  a.pace = a.num_k * (STAGE_CODES / 64) * 7;
+  // seven eighths of the products' 128 cycles for every 64 values of K; SwiGLU's last warp has that
+  // much to do after its turn (9,728 x 8,192 x 2,048 MX 111 us, 124 without the allowance)
+  a.pace = std::max(0, a.num_k * (STAGE_CODES / 64) * 112 - (SWIGLU ? (NV ? 1800 : 1400) : 0)) / 16;
   a.up_rows = SWIGLU ? N : 0;
   if ((st = dev_err(&a.err)) != H3_OK) return st;
   CUtensorMap tmA, tmB, tmSA, tmSB, tmC;
