@@ -201,6 +201,54 @@ def test_attention(h3lib, Lq, Lk, H, Hkv, most, kb):
 
 
 @pytest.mark.parametrize("kb", [64, 128])
+@pytest.mark.parametrize("Lq,Lk,H,Hkv,most", [
+    (768, 900, 51, 17, 7), (2000, 1500, 20, 4, 9), (1793, 2500, 20, 20, 24), (256, 3000, 160, 32, 41),
+    (200, 700, 155, 5, 5), (256, 64, 153, 1, 1), (2048, 5000, 19, 19, 70)])
+def test_attention_of_many_items(h3lib, Lq, Lk, H, Hkv, most, kb):
+    # two (query block, head)s to a pair of CTAs: an odd number of them, lists of unequal length, some
+    # of them empty, the second half of a block's rows missing
+    g = gen(Lq + Lk + H)
+    q, k, v = heads(Lq, H, g), heads(Lk, Hkv, g), heads(Lk, Hkv, g)
+    nq, nk = -(-Lq // QB), -(-Lk // kb)
+    assert nq * H >= 152
+    for ragged in (False, True):
+        ids, n = lists(H, nq, nk, most, g, ragged)
+        if ragged:
+            n.view(-1)[::7] = 0
+            n.view(-1)[1::14] = 0
+            n.view(-1)[-1] = 1 << 30
+            ids.view(-1, most)[3::5, 0] = nk
+            ids.view(-1, most)[4::9] = -1
+            ids.view(-1, most)[5::9] = nk - 1
+        buf = torch.full((Lq + 2, H, 128), SENT, dtype=torch.bfloat16, device=dev)
+        check_attention(h3lib, q, k, v, ids, n.clamp(max=most) if not ragged else n, kb, o=buf[1:-1])
+        assert (buf[0] == SENT).all() and (buf[-1] == SENT).all()
+
+
+def test_many_items_hold_anything_where_they_do_not_look(h3lib):
+    g = gen(77)
+    Lq, Lk, H, kb = 1000, 1030, 40, 64
+    q, k, v = heads(Lq, H, g), heads(Lk, H, g), heads(Lk, H, g)
+    ids, n = lists(H, 4, 17, 6, g, True)
+    ids %= 10                                   # blocks 10 and on are in no list
+    want = check_attention(h3lib, q, k, v, ids, n, kb)
+    k2, v2 = k.clone(), v.clone()
+    k2[640:], v2[640:] = float("nan"), float("inf")
+    o = torch.empty_like(want)
+    h3lib.attention_blocks(q, k2, v2, o, ids, n, k_block=kb)
+    h3lib.check_device_error()
+    assert torch.equal(o, want)
+    k2[5] = float("nan")                         # a key of block 0: NaN where it is listed
+    h3lib.attention_blocks(q, k2, v2, o, ids, n, k_block=kb)
+    h3lib.check_device_error()
+    for h in range(H):
+        for t in range(4):
+            bad = 0 in ids[h, t, :int(n[h, t])].tolist()
+            rows = o[t * QB:(t + 1) * QB, h]
+            assert torch.isnan(rows).all() if bad else torch.equal(rows, want[t * QB:(t + 1) * QB, h])
+
+
+@pytest.mark.parametrize("kb", [64, 128])
 def test_lists_of_any_content(h3lib, kb):
     g = gen(5)
     for Lq, Lk, most in ((300, 1000, 12), (22, 4000, 40)):
