@@ -175,13 +175,26 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  const int64_t item = static_cast<int64_t>(h) * a.nq + qb;
+  const int32_t* list = a.ids + item * a.most;
+  // the loading warp has the list's first entries before its length is known (a CTA that does not
+  // begin with them reads its own later)
+  int now = -1, next = -1;
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    wait_previous();
+    if (lane < a.most) now = list[lane];
+    if (32 + lane < a.most) next = list[32 + lane];
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   wait_previous();
-  const int64_t item = static_cast<int64_t>(h) * a.nq + qb;
-  const int32_t* list = a.ids + item * a.most;
   const int count = min(max(*(a.counts + item), 0), a.most);
   // this CTA's key tiles
   const int tiles = (count + per_tile - 1) / per_tile;
@@ -205,7 +218,13 @@ __global__ void __launch_bounds__(Q2_THREADS, 1)
       }
       const int first = tile0 * per_tile, end = min(count, (tile0 + n) * per_tile);
       auto entry = [&](int i) { return first + i < end ? list[first + i] : -1; };
-      int now = entry(lane), next = entry(32 + lane);
+      if (first > 0) {
+        now = entry(lane);
+        next = entry(32 + lane);
+      } else {
+        if (lane >= end) now = -1;
+        if (32 + lane >= end) next = -1;
+      }
       int issued = 0;
       // the first rows of a tile's blocks; past the last key where there is none
       auto rows_of = [&](int j, int (&row)[2], int (&real)[2]) {

@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(POOL_THREADS, 1)
       mbar_init(bar(POOL_SLOTS + i), POOL_WARPS);
     }
     fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
   }
   __syncthreads();
   wait_previous();
@@ -280,6 +282,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < BT_NUM; ++i) mbar_init(bar(i), i == BT_READ || i == BT_READ + 1 ? 4 : 1);
     fence_mbar_init();
+    tma_prefetch_desc(&tmQh);
+    tma_prefetch_desc(&tmQl);
+    tma_prefetch_desc(&tmKh);
+    tma_prefetch_desc(&tmKl);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 2 * TC_TILE);
