@@ -1,15 +1,15 @@
 // Norms before and after a branch, fused with the branch's gate and the scaled
-// residual: one CTA per row, which stays in registers from its loads to its stores.
+// residual: a CTA per row, or a warp, which stays in registers from its loads to its stores.
 //
 // Per row: p = n(delta) * post_gain, r = resid_scale * resid + gate * p,
 // h = n(r) * pre_gain * (1 + scale) + shift, with n a LayerNorm without affine or a
 // division by the root mean square. Everything between the loads and the stores is
 // FP32, and the mean is taken before the squares (two passes over registers), so a
 // row far from zero loses nothing. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out
-// (58,758 rows of 5,376, 3.79 GB: 605 us, 6.3 TB/s; 22 rows: 3.9 us, the latency of a load, of four
-// sums over the CTA and of a launch). Launched like an ordinary kernel, since its loads of
-// vectors that all rows share take the read-only path: without it, and launched ahead of the
-// end of the kernel before it, the same rows took 665 us.
+// (58,758 rows of 5,376, 3.79 GB: LayerNorm 591 us, 6.4 TB/s, RMS 545 us, 7.0 TB/s; 22 rows: 3.9 us, the
+// latency of a load, of two or four sums over the CTA and of a launch). Launched like an
+// ordinary kernel, since its loads of vectors that all rows share take the read-only path:
+// without it, and launched ahead of the end of the kernel before it, LayerNorm took 665 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -20,16 +20,31 @@
 namespace h3 {
 namespace {
 
+// Half of the least power of two that is not below n.
+constexpr int warps_half(int n) {
+  int m = 1;
+  while (m < n) m *= 2;
+  return m / 2;
+}
+
+// Threads of a row: a warp (of NORM_WARPS in a CTA), or a CTA.
+constexpr int NORM_WARPS = 4;
+template <int T>
+__device__ __forceinline__ int thread_of() {
+  return static_cast<int>(T == 32 ? threadIdx.x & 31 : threadIdx.x);
+}
+
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  if constexpr (T == 32) return v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) red[warp] = v;
   __syncthreads();
   float t = (lane < T / 32) ? red[lane] : 0.f;
 #pragma unroll
-  for (int m = T / 64; m >= 1; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+  for (int m = warps_half(T / 32); m >= 1; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
   return __shfl_sync(0xffffffffu, t, 0);
 }
 
@@ -46,7 +61,7 @@ __device__ __forceinline__ void norm_row(float4 (&x)[VPT], int D4, float inv_d, 
     const float mean = row_sum<T>(s, red) * inv_d;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if (static_cast<int>(threadIdx.x) + v * T < D4) {
+      if (thread_of<T>() + v * T < D4) {
         x[v].x -= mean;
         x[v].y -= mean;
         x[v].z -= mean;
@@ -82,20 +97,22 @@ struct NormArgs {
   int num_seg;
   int64_t seg_stride;
   float resid_scale, eps, inv_d;
-  int D4;
+  int D4, L;
 };
 
 template <int T, int VPT, bool RMS, bool POST>
-__global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(T == 32 ? NORM_WARPS * 32 : T) sandwich_norm_kernel(const NormArgs a) {
   __shared__ float red[4 * (T / 32)];
-  const int64_t row = blockIdx.x;
+  const int tid = thread_of<T>();
+  const int64_t row = T == 32 ? static_cast<int64_t>(blockIdx.x) * NORM_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  if (T == 32 && row >= a.L) return;
   const int D4 = a.D4;
   const float4* rrow = reinterpret_cast<const float4*>(a.resid) + row * D4;
   float4 x[VPT], y[VPT];
   // every load of the row is requested before the first use
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int c = threadIdx.x + v * T;
+    const int c = tid + v * T;
     x[v] = c < D4 ? __ldcs(rrow + c) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const bool branch = a.delta != nullptr;
@@ -104,7 +121,7 @@ __global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
     uint2 d[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int c = threadIdx.x + v * T;
+      const int c = tid + v * T;
       d[v] = c < D4 ? __ldcs(drow + c) : make_uint2(0, 0);
     }
 #pragma unroll
@@ -120,7 +137,7 @@ __global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
     if constexpr (POST) norm_row<T, VPT, RMS>(y, D4, a.inv_d, a.eps, red);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int c = threadIdx.x + v * T;
+      const int c = tid + v * T;
       if (c < D4) {
         if (POST && a.post_gain != nullptr) {
           const float4 g = vec(a.post_gain, c);
@@ -150,7 +167,7 @@ __global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
     float4* orow = reinterpret_cast<float4*>(a.resid_out) + row * D4;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int c = threadIdx.x + v * T;
+      const int c = tid + v * T;
       if (c < D4) __stcs(orow + c, x[v]);
     }
   }
@@ -160,7 +177,7 @@ __global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
   uint2* hrow = reinterpret_cast<uint2*>(a.normed) + row * D4;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int c = threadIdx.x + v * T;
+    const int c = tid + v * T;
     if (c < D4) {
       float4 m = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
       if (a.scale != nullptr) {
@@ -181,18 +198,40 @@ __global__ void __launch_bounds__(T) sandwich_norm_kernel(const NormArgs a) {
   }
 }
 
-template <int T, int VPT>
-void launch_width(const NormArgs& a, int L, bool rms, bool post, cudaStream_t s) {
-  if (rms) {
-    if (post)
-      sandwich_norm_kernel<T, VPT, true, true><<<L, T, 0, s>>>(a);
-    else
-      sandwich_norm_kernel<T, VPT, true, false><<<L, T, 0, s>>>(a);
+template <int T, int VPT, bool RMS>
+void launch_width(const NormArgs& a, bool post, cudaStream_t s) {
+  const int grid = T == 32 ? (a.L - 1) / NORM_WARPS + 1 : a.L, threads = T == 32 ? NORM_WARPS * 32 : T;
+  if (post)
+    sandwich_norm_kernel<T, VPT, RMS, true><<<grid, threads, 0, s>>>(a);
+  else
+    sandwich_norm_kernel<T, VPT, RMS, false><<<grid, threads, 0, s>>>(a);
+}
+
+// Few threads with many vectors each have less to exchange, and more of a row's registers are of
+// the row; many have more loads under way. A LayerNorm, which exchanges twice as often, takes
+// fewer from 641 float4 on. (58,758 rows, us for LayerNorm / RMS: 512 wide 59 / 59, 74 / 66 with 128
+// threads; 1,152 128 / 125, 187 / 142 with 256; 2,048 210 / 210, 231 / 208 with 256; 4,096 LayerNorm 429, 454
+// with 512, RMS 413, 418 with 256; 5,376 LayerNorm 591, 600 with 512 and 613 with 224, RMS 545, 572 with 384.)
+template <bool RMS>
+void launch_rows(const NormArgs& a, bool post, cudaStream_t s) {
+  const int d4 = a.D4;
+  if (d4 <= 64) return launch_width<32, 2, RMS>(a, post, s);
+  if (d4 <= 128) return launch_width<32, 4, RMS>(a, post, s);
+  if (d4 <= 256) return launch_width<64, 4, RMS>(a, post, s);
+  if (d4 <= 320) return launch_width<64, 5, RMS>(a, post, s);
+  if (d4 <= 384) return launch_width<128, 3, RMS>(a, post, s);
+  if (d4 <= 512) return launch_width<128, 4, RMS>(a, post, s);
+  if (d4 <= 640) return launch_width<160, 4, RMS>(a, post, s);
+  if (d4 > 1536) return launch_width<512, 4, RMS>(a, post, s);
+  if constexpr (RMS) {
+    if (d4 <= 768) return launch_width<256, 3, RMS>(a, post, s);
+    if (d4 <= 1024) return launch_width<512, 2, RMS>(a, post, s);
+    launch_width<512, 3, RMS>(a, post, s);
   } else {
-    if (post)
-      sandwich_norm_kernel<T, VPT, false, true><<<L, T, 0, s>>>(a);
-    else
-      sandwich_norm_kernel<T, VPT, false, false><<<L, T, 0, s>>>(a);
+    if (d4 <= 768) return launch_width<192, 4, RMS>(a, post, s);
+    if (d4 <= 1024) return launch_width<256, 4, RMS>(a, post, s);
+    if (d4 <= 1280) return launch_width<256, 5, RMS>(a, post, s);
+    launch_width<384, 4, RMS>(a, post, s);
   }
 }
 
@@ -207,18 +246,11 @@ h3_status launch_sandwich_norm(const float* resid, const void* delta, float* res
   const NormArgs a{resid, static_cast<const __nv_bfloat16*>(delta),
                    resid_out, static_cast<__nv_bfloat16*>(normed),
                    post_gain, gate, pre_gain, shift, scale, seg, num_seg, seg_stride,
-                   resid_scale, eps, 1.0f / static_cast<float>(D), D / 4};
-  // as few threads as hold the row in at most four float4 each
-  const int d4 = D / 4;
-#define H3_NORM(T, V) launch_width<T, V>(a, L, rms, post_norm, s)
-  if (d4 <= 128) H3_NORM(128, 1);
-  else if (d4 <= 256) H3_NORM(128, 2);
-  else if (d4 <= 512) H3_NORM(256, 2);
-  else if (d4 <= 768) H3_NORM(256, 3);
-  else if (d4 <= 1024) H3_NORM(512, 2);
-  else if (d4 <= 1536) H3_NORM(512, 3);
-  else H3_NORM(512, 4);
-#undef H3_NORM
+                   resid_scale, eps, 1.0f / static_cast<float>(D), D / 4, L};
+  if (rms)
+    launch_rows<true>(a, post_norm, s);
+  else
+    launch_rows<false>(a, post_norm, s);
   return cuda_fail(cudaGetLastError(), "sandwich_norm launch");
 }
 

@@ -86,6 +86,20 @@ def test_against_the_formula(h3lib, S, L, D, rms):
 
 
 @pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("D", [32, 256, 264, 504, 1024, 1152, 1280, 1288, 1536, 1544, 2560, 2568, 3000, 3080,
+                               4096, 4104, 5120, 5128, 6144, 7000])
+def test_every_width(h3lib, D, rms):
+    # each split of a row over threads, full and nearly so
+    a = draw(131, D, D, 2) | dict(rms=rms)
+    out = torch.full((133, D), SENT, device=dev)
+    normed = torch.full((133, D), SENT, device=dev, dtype=torch.bfloat16)
+    call(h3lib, a, out[1:-1], normed[1:-1], 130)
+    check(out[1:-1], normed[1:-1], a, 130, f"131x{D}")
+    for t in (out, normed):
+        assert (t[0] == SENT).all() and (t[131:] == SENT).all()
+
+
+@pytest.mark.parametrize("rms", [False, True])
 def test_parts_left_out(h3lib, rms):
     S, D = 40, 640
     full = draw(S, D, 1, groups=2) | dict(rms=rms)
