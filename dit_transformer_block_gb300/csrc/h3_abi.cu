@@ -861,7 +861,8 @@ h3_status h3_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_
              "softmax_scale must be > 0 and finite");
   st = check_lists(static_cast<int64_t>(query_blocks(Lq)) * H, key_blocks(Lk, k_block), max_blocks);
   if (st != H3_OK) return st;
-  // (a tensor core's FP32 sum is cut off with every 16 keys: low by 2^-11 of values of one sign here)
+  // (a tensor core's FP32 sum is cut off with every 16 keys: low by 2^-11 of values of one sign
+  // here)
   H3_REQUIRE(max_blocks <= (1 << 17) / k_block, H3_ERR_UNSUPPORTED,
              "lists of %d blocks have more than 2^17 keys", max_blocks);
   if (Lq == 0) return H3_OK;

@@ -16,10 +16,10 @@
 //     row (zeros) and its keys are masked, as are those past the end of the last block.
 // Where the (query block, head)s are fewer than the SMs, a cluster of CTAs shares a list
 // and joins its partial results through distributed shared memory, in rank order.
-// Bound by the products of bf16 and by the power they draw: 58,758 rows of 42 heads, 92 blocks of 64
-// keys each, 7.4 TFLOP: 4.43 ms (1,680 TFLOP/s), 4.8 ms in a run of seconds. 22 rows of 40 heads, 23
-// blocks of 128: 13.2 us, of which the keys and values once are 4.6: seven or eight tiles one after
-// another, and the join.
+// Bound by the products of bf16 and by the power they draw: 58,758 rows of 42 heads, 92 blocks of
+// 64 keys each, 7.4 TFLOP: 4.43 ms (1,680 TFLOP/s), 4.8 ms in a run of seconds. 22 rows of 40
+// heads, 23 blocks of 128: 13.2 us, of which the keys and values once are 4.6: seven or eight
+// tiles one after another, and the join.
 #include <algorithm>
 
 #include "h3_attn_common.cuh"

@@ -13,18 +13,18 @@
 //     even CTA, warp 1 issues four products of K = 64 per stage, and two warps the copies of
 //     a stage's scales from shared to tensor memory (both CTAs' at once) in turn: twelve (NV)
 //     or six (MX) copies take longer to issue than the products to run;
-//   * warps 2-9: epilogue, two per lane quarter. A warp reads its 128 columns of the
-//     accumulator at once, so that the next tile's products wait for one read and not for
-//     the stores, then writes bf16 through 4 KB of shared memory of its own with TMA. The CTA's
-//     sixteen stores of a tile spread over the next tile's products (seven cycles apart for
-//     every 64 values of K, whose product takes 128, or less in SwiGLU): in one go they hold up the
-//     loads, and the products wait (2,432 tiles of K = 5,120: 239 us instead of 247 in MX, 251 and 257 in NV, of K = 2,560
-//     138 and 147, 144 and 155; 220 and 228 of K = 5,120 if nothing were stored);
+//   * warps 2-9: epilogue, two per lane quarter. A warp reads its 128 columns of the accumulator
+//     at once, so that the next tile's products wait for one read and not for the stores, then
+//     writes bf16 through 4 KB of shared memory of its own with TMA. The CTA's sixteen stores of
+//     a tile spread over the next tile's products (seven cycles apart for every 64 values of K,
+//     whose product takes 128, or less in SwiGLU): in one go they hold up the loads, and the
+//     products wait (2,432 tiles of K = 5,120: 239 us instead of 247 in MX, 251 and 257 in NV, of
+//     K = 2,560 138 and 147, 144 and 155; 220 and 228 of K = 5,120 if nothing were stored);
 //   * tensor memory: 256 columns of accumulator, a buffer of scales per stage.
-// A CTA gets its operands at a rate that its copies in flight allow, so where there are few
-// tiles (few rows: the weights' bytes count) several pairs in a cluster share one tile's K. They
-// put their sums into shared memory and each adds up a share of the rows, in the order of K
-// (22 x 5,376 x 5,376 with weights in HBM: 10.4 us with the quantisation, of which the weights' 15 MB
+// A CTA gets its operands at a rate that its copies in flight allow, so where there are few tiles
+// (few rows: the weights' bytes count) several pairs in a cluster share one tile's K. They put
+// their sums into shared memory and each adds up a share of the rows, in the order of K (22 x
+// 5,376 x 5,376 with weights in HBM: 10.4 us with the quantisation, of which the weights' 15 MB
 // take 2.3).
 // 58,758 x 16,128 x 5,376: MX 1,436 us (7,100 TFLOP/s), NV 1,515 us (6,730). Products of K = 64 and
 // nothing else run at 9,220 TFLOP/s. With the loads beside them a stage takes 600 cycles instead
@@ -189,10 +189,11 @@ __device__ __forceinline__ void tile_coords4(int tile, const Gemm4Args& a, int& 
 }
 
 // bf16 SiLU(g) * u of two gates and two ups, rounded to bf16 first: g / (1 + 2^(-g log2 e)), the
-// exponential within 2^-22 of it and the reciprocal within 2^-23, which is flushed to 0 from where
-// the sum is above 2^126. (A tile's epilogue bounds products of few stages: 9,728 x 8,192 x 256 54 us in
-// MX and 74 in NV; 85 and 104 with __expf and __fdividef, which look after subnormal operands,
-// and each value rounded by itself; an IEEE division made a tile's epilogue 4 us longer.)
+// exponential within 2^-22 of it and the reciprocal within 2^-23, which is flushed to 0 from
+// where the sum is above 2^126. (A tile's epilogue bounds products of few stages: 9,728 x 8,192 x
+// 256 54 us in MX and 74 in NV; 85 and 104 with __expf and __fdividef, which look after subnormal
+// operands, and each value rounded by itself; an IEEE division made a tile's epilogue 4 us
+// longer.)
 __device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float u1) {
   const uint32_t g = pack_bf16x2(g0, g1), u = pack_bf16x2(u0, u1);
   auto silu = [](float x) {
@@ -603,10 +604,12 @@ __global__ void __launch_bounds__(THREADS4, 1)
       }
       __nv_bfloat16* c = a.C + static_cast<int64_t>(first + r) * a.N + nb * WIDTH + lane * 4;
       auto store = [&](int u, uint32_t x, uint32_t y) {
-        if (nb * WIDTH + lane * 4 + u * 128 < a.N) *reinterpret_cast<uint2*>(c + u * 128) = make_uint2(x, y);
+        if (nb * WIDTH + lane * 4 + u * 128 < a.N)
+          *reinterpret_cast<uint2*>(c + u * 128) = make_uint2(x, y);
       };
       if constexpr (SWIGLU) {
-        store(0, swiglu2(f[0][0], f[0][1], f[1][0], f[1][1]), swiglu2(f[0][2], f[0][3], f[1][2], f[1][3]));
+        store(0, swiglu2(f[0][0], f[0][1], f[1][0], f[1][1]),
+              swiglu2(f[0][2], f[0][3], f[1][2], f[1][3]));
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -660,10 +663,10 @@ h3_status launch4(const Fp4Operand& A, const Fp4Operand& B, void* C, int L, int 
   if ((st = make_tmap_u32_rows(&tmSB, B.scales, 128, tb, atoms)) != H3_OK) return st;
   if ((st = make_tmap_bf16_2d(&tmC, C, N, L, static_cast<uint64_t>(N) * 2, 64, 32)) != H3_OK) return st;
   // As many pairs to a tile as all tiles find room for, of four stages each at least, or, where
-  // there are more rows for the sums to be exchanged of, eight (4-bit rows and product, weights in
-  // HBM: 22 x 5,376 x 5,376 10.4 us by three pairs, 13.2 by one; 256 rows 14.5 by three of seven stages,
-  // 13.5 by two, 14.3 by one; K and N 2,048 22 rows 8.4 by two pairs of four stages, 8.7 by one, 128
-  // rows 10.3 and 9.5; 512 x 2,560 x 10,240 18.0 by three, 21.7 by one)
+  // there are more rows for the sums to be exchanged of, eight (4-bit rows and product, weights
+  // in HBM: 22 x 5,376 x 5,376 10.4 us by three pairs, 13.2 by one; 256 rows 14.5 by three of
+  // seven stages, 13.5 by two, 14.3 by one; K and N 2,048 22 rows 8.4 by two pairs of four
+  // stages, 8.7 by one, 128 rows 10.3 and 9.5; 512 x 2,560 x 10,240 18.0 by three, 21.7 by one)
   const int least = L > 64 ? 8 : 4;
   static std::atomic<int> room[64][9];
   a.parts = 1;

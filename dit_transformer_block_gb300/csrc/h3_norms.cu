@@ -1,15 +1,15 @@
 // Norms before and after a branch, fused with the branch's gate and the scaled
 // residual: a CTA per row, or a warp, which stays in registers from its loads to its stores.
 //
-// Per row: p = n(delta) * post_gain, r = resid_scale * resid + gate * p,
-// h = n(r) * pre_gain * (1 + scale) + shift, with n a LayerNorm without affine or a
-// division by the root mean square. Everything between the loads and the stores is
-// FP32, and the mean is taken before the squares (two passes over registers), so a
-// row far from zero loses nothing. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out
-// (58,758 rows of 5,376, 3.79 GB: LayerNorm 591 us, 6.4 TB/s, RMS 545 us, 7.0 TB/s; 22 rows: 3.9 us, the
-// latency of a load, of two or four sums over the CTA and of a launch). Launched like an
-// ordinary kernel, since its loads of vectors that all rows share take the read-only path:
-// without it, and launched ahead of the end of the kernel before it, LayerNorm took 665 us.
+// Per row: p = n(delta) * post_gain, r = resid_scale * resid + gate * p, h = n(r) * pre_gain * (1
+// + scale) + shift, with n a LayerNorm without affine or a division by the root mean square.
+// Everything between the loads and the stores is FP32, and the mean is taken before the squares
+// (two passes over registers), so a row far from zero loses nothing. Bound by HBM: 4 + 2 bytes
+// per element in, 4 + 2 out (58,758 rows of 5,376, 3.79 GB: LayerNorm 591 us, 6.4 TB/s, RMS 545
+// us, 7.0 TB/s; 22 rows: 3.9 us, the latency of a load, of two or four sums over the CTA and of a
+// launch). Launched like an ordinary kernel, since its loads of vectors that all rows share take
+// the read-only path: without it, and launched ahead of the end of the kernel before it,
+// LayerNorm took 665 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -101,10 +101,12 @@ struct NormArgs {
 };
 
 template <int T, int VPT, bool RMS, bool POST>
-__global__ void __launch_bounds__(T == 32 ? NORM_WARPS * 32 : T) sandwich_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(T == 32 ? NORM_WARPS * 32 : T)
+    sandwich_norm_kernel(const NormArgs a) {
   __shared__ float red[4 * (T / 32)];
   const int tid = thread_of<T>();
-  const int64_t row = T == 32 ? static_cast<int64_t>(blockIdx.x) * NORM_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t row =
+      T == 32 ? static_cast<int64_t>(blockIdx.x) * NORM_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   if (T == 32 && row >= a.L) return;
   const int D4 = a.D4;
   const float4* rrow = reinterpret_cast<const float4*>(a.resid) + row * D4;
@@ -209,9 +211,10 @@ void launch_width(const NormArgs& a, bool post, cudaStream_t s) {
 
 // Few threads with many vectors each have less to exchange, and more of a row's registers are of
 // the row; many have more loads under way. A LayerNorm, which exchanges twice as often, takes
-// fewer from 641 float4 on. (58,758 rows, us for LayerNorm / RMS: 512 wide 59 / 59, 74 / 66 with 128
-// threads; 1,152 128 / 125, 187 / 142 with 256; 2,048 210 / 210, 231 / 208 with 256; 4,096 LayerNorm 429, 454
-// with 512, RMS 413, 418 with 256; 5,376 LayerNorm 591, 600 with 512 and 613 with 224, RMS 545, 572 with 384.)
+// fewer from 641 float4 on. (58,758 rows, us for LayerNorm / RMS: 512 wide 59 / 59, 74 / 66 with
+// 128 threads; 1,152 128 / 125, 187 / 142 with 256; 2,048 210 / 210, 231 / 208 with 256; 4,096
+// LayerNorm 429, 454 with 512, RMS 413, 418 with 256; 5,376 LayerNorm 591, 600 with 512 and 613
+// with 224, RMS 545, 572 with 384.)
 template <bool RMS>
 void launch_rows(const NormArgs& a, bool post, cudaStream_t s) {
   const int d4 = a.D4;
