@@ -49,6 +49,7 @@ constexpr int SFA_BYTES = 2048, SFB_BYTES = 2 * 2048;
 constexpr int STAGE4_BYTES = 2 * OP_BYTES + SFA_BYTES + SFB_BYTES;
 constexpr int STAGES4 = 5;
 constexpr int EPI_WARPS = 8, COPY_WARPS = 2;
+static_assert(COPY_WARPS <= STAGES4, "a copy warp's next stage is at most one round of slots on");
 constexpr int THREADS4 = (2 + EPI_WARPS + COPY_WARPS) * 32;
 constexpr int GROUP_M4 = 16;                 // raster: 16 x 256 rows per sweep of the columns
 constexpr int OUT_BYTES = 32 * 128;          // a warp's 32 rows x 64 columns of output
@@ -396,15 +397,12 @@ __global__ void __launch_bounds__(THREADS4, 1)
         return mbar_wait_warp(bar(b), parity, a.err, ERR_WAIT_GEMM_MMA);
       };
       // (the stage was loaded again only after the products that read its buffer)
-      for (int it = 0, st = -1, phase = 0; it < total; ++it) {
-        if (++st == STAGES4) {
-          st = 0;
-          phase ^= 1;
-        }
-        // every stage is waited for, also the other warp's: loads may land out of order, and a
-        // barrier whose phase before is still open looks as if this one were over
-        if (!wait(B4_FULL + st, phase)) break;
-        if (it % COPY_WARPS != c) continue;
+      for (int it = c, st = c, phase = 0; it < total; it += COPY_WARPS) {
+        // The slot's stage before this one may be the other warp's, and its load the last to land:
+        // while it has not, the barrier's parity is that of the phase this one waits for. So the slot's
+        // copies before this one are waited for first: their barrier goes no further without this warp,
+        // however long it is held (a wait for the other warp's loads could miss one).
+        if (!wait(B4_SF + st, phase ^ 1) || !wait(B4_FULL + st, phase)) break;
         tc_fence_after();
         const uint64_t s = ds0 + static_cast<uint32_t>(st * (STAGE4_BYTES >> 4));
         const uint32_t sf = tmem + TM::SF + static_cast<uint32_t>(st) * TM::SF_COLS;
@@ -415,6 +413,11 @@ __global__ void __launch_bounds__(THREADS4, 1)
           scale_copy_pair_el(sf + TM::SFB + t * 8 + 4, s + ((SFA_BYTES + 2048 + t * 512) >> 4));
         }
         mma_commit_pair_mc_el(bar(B4_SF + st), static_cast<uint16_t>(1u << even));
+        st += COPY_WARPS;
+        if (st >= STAGES4) {
+          st -= STAGES4;
+          phase ^= 1;
+        }
       }
       mma_commit_pair_mc_el(bar(B4_DRAIN + 1 + c), static_cast<uint16_t>(1u << even));
       mbar_wait_drain(bar(B4_DRAIN + 1 + c), 0u, globaltimer_ns(), drain_limit_ns(a.err));
