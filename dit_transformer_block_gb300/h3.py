@@ -828,13 +828,15 @@ def fp4_scale_bytes(R: int, K: int, format: str = "nv") -> int:
 
 def fp4_rows(R: int, K: int, format: str = "nv", device=None) -> Fp4Rows:
     """Room for [R, K] 4-bit rows on a device (default: the current one): "nv" (16 values
-    share an E4M3 scale, a row an FP32 one) or "mx" (32 share a power of two)."""
+    share an E4M3 scale, a row an FP32 one) or "mx" (32 share a power of two). The scales are
+    zeros, so that a program which fills in packed weights itself need not clear the places
+    past a row's last block, which a product reads where K is no multiple of 64."""
     if format not in FP4_FORMATS:
         raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
     device = torch.device("cuda") if device is None else device
     n = fp4_scale_bytes(R, K, format)
     return Fp4Rows(torch.empty(R, K // 2, dtype=torch.uint8, device=device),
-                   torch.empty(n, dtype=torch.uint8, device=device),
+                   torch.zeros(n, dtype=torch.uint8, device=device),
                    torch.empty(R, dtype=torch.float32, device=device) if format == "nv" else None,
                    format)
 

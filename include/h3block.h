@@ -650,7 +650,9 @@ h3_status h3_linear_swiglu_fp8(const void* qx, const float* sx, const void* qw_g
  *       codes of 0
  * A block with a NaN or an infinity gets a scale of NaN (and codes of 0), so that it shows in
  * every product it takes part in. Scale bytes of rows below R beyond a row's blocks, up to a
- * multiple of 4, are written as 0; those of rows >= R are left as they were.
+ * multiple of 4, are written as 0; those of rows >= R are left as they were. A program that
+ * fills in an operand itself has to clear them too: where K is no multiple of 64 a product
+ * takes those up to the next one along, with values of 0, and 0 times a NaN is NaN.
  *   K % 32 == 0, K <= 16384, ld_x a multiple of 8; x and codes 16-byte, scales 128-byte
  *   aligned, none overlapping.
  */
