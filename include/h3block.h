@@ -279,8 +279,9 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
  *   ids     [H, nq, max_blocks] int32; counts [H, nq] int32
  * bf16 tensor-core products, FP32 softmax and accumulation, bf16 out: relative to the sum of
  * weight times |v| at most 2^-8 for the weights' rounding before their product and 2^-10 for
- * the sums, beside what the FP32 scores have. Scores of a block whose mean is infinite (or
- * rounds to it) are infinite or NaN.
+ * the sums, beside what the FP32 scores have. A mean is infinite too where the sum of its
+ * rows is beyond FP32's range; its scores are infinite, or NaN where it meets a 0, a NaN or an
+ * infinity of the other sign.
  *
  * Dh == 128, H a multiple of Hkv, at most 65,535. A call with Lq or Lk 0: no scores and
  * nothing done; h3_attention_blocks with Lk 0 writes zeros. max_blocks >= 1, rows * max_blocks
