@@ -4,8 +4,8 @@
 // Per row: p = n(delta) * post_gain, r = resid_scale * resid + gate * p, h = n(r) * pre_gain * (1
 // + scale) + shift, with n a LayerNorm without affine or a division by the root mean square.
 // Everything between the loads and the stores is FP32, and the mean is taken before the squares
-// (two passes over registers), so a row far from zero loses nothing. Bound by HBM: 4 + 2 bytes
-// per element in, 4 + 2 out (58,758 rows of 5,376, 3.79 GB: LayerNorm 591 us, 6.4 TB/s, RMS 545
+// (two passes over registers), so a row far from zero loses what the rounding of its mean is
+// (some 2^-24 |mean|, off every value) and not the square of that. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out (58,758 rows of 5,376, 3.79 GB: LayerNorm 591 us, 6.4 TB/s, RMS 545
 // us, 7.0 TB/s; 22 rows: 3.9 us, the latency of a load, of two or four sums over the CTA and of a
 // launch). Launched like an ordinary kernel, since its loads of vectors that all rows share take
 // the read-only path: without it, and launched ahead of the end of the kernel before it,
@@ -50,9 +50,10 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 
 // x <- n(x) over a row of D values, VPT float4 of it in this thread's registers
 // (zeros beyond the row). red: two buffers of T / 32 floats, the second reduction's
-// being free of the first's readers.
+// being free of the first's readers. False, the same in every thread of the row, where the sum of
+// the squares is not finite (nor is it where the sum of the values is not): x is of no use then.
 template <int T, int VPT, bool RMS>
-__device__ __forceinline__ void norm_row(float4 (&x)[VPT], int D4, float inv_d, float eps,
+__device__ __forceinline__ bool norm_row(float4 (&x)[VPT], int D4, float inv_d, float eps,
                                          float* red) {
   if constexpr (!RMS) {
     float s = 0.f;
@@ -73,7 +74,9 @@ __device__ __forceinline__ void norm_row(float4 (&x)[VPT], int D4, float inv_d, 
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
     q += (x[v].x * x[v].x + x[v].y * x[v].y) + (x[v].z * x[v].z + x[v].w * x[v].w);
-  const float rstd = rsqrtf(row_sum<T>(q, red + T / 32) * inv_d + eps);
+  const float squares = row_sum<T>(q, red + T / 32);
+  if (!(squares < INFINITY)) return false;
+  const float rstd = rsqrtf(squares * inv_d + eps);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     x[v].x *= rstd;
@@ -81,6 +84,7 @@ __device__ __forceinline__ void norm_row(float4 (&x)[VPT], int D4, float inv_d, 
     x[v].z *= rstd;
     x[v].w *= rstd;
   }
+  return true;
 }
 
 struct NormArgs {
@@ -100,9 +104,106 @@ struct NormArgs {
   int D4, L;
 };
 
+// n(x) = (x * k - mean) * rstd of a row that load(c) gives the float4 c of. k is 1, or 2^-80 where the
+// sums of that are not finite: 8,192 squares of any values times 2^-80 have a finite sum, and of eps
+// there is left what keeps a row of equal values from 0 / 0. (What is infinite or NaN stays so.)
+struct RowNorm {
+  float k, mean, rstd;
+
+  template <int T, bool RMS, class Load>
+  __device__ __forceinline__ void find(const Load& load, const NormArgs& a, float* red) {
+    float eps = a.eps;
+    mean = 0.f;
+#pragma unroll 1
+    for (k = 1.f;;) {
+      float q = 0.f;
+#pragma unroll 1
+      for (int pass = RMS ? 1 : 0; pass < 2; ++pass) {
+        float s = 0.f;
+#pragma unroll 1
+        for (int c = thread_of<T>(); c < a.D4; c += T) {
+          const float4 x = load(c);
+          const float u[4] = {x.x * k - mean, x.y * k - mean, x.z * k - mean, x.w * k - mean};
+          s += pass == 0 ? (u[0] + u[1]) + (u[2] + u[3])
+                         : (u[0] * u[0] + u[1] * u[1]) + (u[2] * u[2] + u[3] * u[3]);
+        }
+        if constexpr (T > 32) __syncthreads();  // the last sum's parts are read
+        q = row_sum<T>(s, red) * a.inv_d;
+        if (pass == 0) mean = q;
+      }
+      rstd = rsqrtf(q + eps);
+      if (q < INFINITY || k < 1.f) return;
+      k = 8.271806125530277e-25f;                       // 2^-80
+      if (eps > 0.f) eps = 1.1754943508222875e-38f;  // 2^-126
+      mean = 0.f;
+    }
+  }
+  __device__ __forceinline__ float4 operator()(float4 x) const {
+    return make_float4((x.x * k - mean) * rstd, (x.y * k - mean) * rstd, (x.z * k - mean) * rstd,
+                       (x.w * k - mean) * rstd);
+  }
+};
+
+// A row some of whose sums are not finite, once more and from memory, a float4 at a time: from the branch
+// on, or (stored) from the new residual on, which then lies in resid_out, or in resid where there is none.
+// Out of line: on the rows' registers, inlined, 58,758 x 5,376 RMS took 636 us instead of 540.
+template <int T, bool RMS, bool POST>
+__device__ __noinline__ void large_row(const NormArgs& a, int64_t row, bool stored, float* red) {
+  const float4* rrow = reinterpret_cast<const float4*>(a.resid) + row * a.D4;
+  const uint2* drow = reinterpret_cast<const uint2*>(a.delta) + row * a.D4;
+  float4* orow = reinterpret_cast<float4*>(a.resid_out) + row * a.D4;
+  int64_t off = 0;
+  if (a.seg != nullptr)
+    off = static_cast<int64_t>(min(max(a.seg[row], 0), a.num_seg - 1)) * a.seg_stride;
+  auto vec = [](const float* p, int c, float d) {
+    return p != nullptr ? reinterpret_cast<const float4*>(p)[c] : make_float4(d, d, d, d);
+  };
+  const float* gate = a.gate != nullptr ? a.gate + off : nullptr;
+  RowNorm n{1.f, 0.f, 1.f};
+  if (!stored) {  // (there is a branch, and its sums are not finite)
+    auto branch = [&](int c) {
+      const uint2 d = drow[c];
+      return make_float4(bf16_lo(d.x), bf16_hi(d.x), bf16_lo(d.y), bf16_hi(d.y));
+    };
+    if constexpr (POST) n.find<T, RMS>(branch, a, red);
+#pragma unroll 1
+    for (int c = thread_of<T>(); c < a.D4; c += T) {
+      const float4 p = n(branch(c)), b = vec(POST ? a.post_gain : nullptr, c, 1.f), g = vec(gate, c, 1.f);
+      const float4 x = rrow[c];
+      const float f = a.resid_scale;
+      orow[c] = make_float4(fmaf(g.x, p.x * b.x, f * x.x), fmaf(g.y, p.y * b.y, f * x.y),
+                            fmaf(g.z, p.z * b.z, f * x.z), fmaf(g.w, p.w * b.w, f * x.w));
+    }
+  }
+  launch_next();
+  if (a.normed == nullptr) return;
+  // (a thread reads what it has stored itself)
+  const float4* from = a.resid_out != nullptr ? orow : rrow;
+  auto value = [&](int c) { return from[c]; };
+  n.find<T, RMS>(value, a, red);
+  uint2* hrow = reinterpret_cast<uint2*>(a.normed) + row * a.D4;
+  const float* scale = a.scale != nullptr ? a.scale + off : nullptr;
+  const float* shift = a.shift != nullptr ? a.shift + off : nullptr;
+#pragma unroll 1
+  for (int c = thread_of<T>(); c < a.D4; c += T) {
+    const float4 x = n(value(c)), s = vec(scale, c, 0.f), g = vec(a.pre_gain, c, 1.f), b = vec(shift, c, 0.f);
+    hrow[c] = make_uint2(
+        pack_bf16x2(fmaf(x.x, (1.f + s.x) * g.x, b.x), fmaf(x.y, (1.f + s.y) * g.y, b.y)),
+        pack_bf16x2(fmaf(x.z, (1.f + s.z) * g.z, b.z), fmaf(x.w, (1.f + s.w) * g.w, b.w)));
+  }
+}
+
+// CTAs that an SM holds: as many as the row's registers leave, which the call of large_row would lessen
+// (58,758 rows, us with it left out / in and bounded / in: 5,376 LayerNorm 585 / 593 / 596, RMS 540 /
+// 543 / 629; 4,096 RMS 409 / 406 / 443; the others alike).
+constexpr int norm_ctas(int threads, int vpt) {
+  return 65536 / (threads * (vpt == 2 ? 32 : vpt == 3 ? 42 : vpt == 4 ? 56 : 64));
+}
+
 template <int T, int VPT, bool RMS, bool POST>
-__global__ void __launch_bounds__(T == 32 ? NORM_WARPS * 32 : T)
-    sandwich_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(T == 32 ? NORM_WARPS * 32 : T,
+                                  norm_ctas(T == 32 ? NORM_WARPS * 32 : T, VPT))
+    sandwich_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[4 * (T / 32)];
   const int tid = thread_of<T>();
   const int64_t row =
@@ -136,7 +237,12 @@ __global__ void __launch_bounds__(T == 32 ? NORM_WARPS * 32 : T)
   auto vec = [](const float* p, int c) { return __ldg(reinterpret_cast<const float4*>(p) + c); };
 
   if (branch) {
-    if constexpr (POST) norm_row<T, VPT, RMS>(y, D4, a.inv_d, a.eps, red);
+    if constexpr (POST) {
+      if (!norm_row<T, VPT, RMS>(y, D4, a.inv_d, a.eps, red)) {
+        large_row<T, RMS, POST>(a, row, false, red);
+        return;
+      }
+    }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = tid + v * T;
@@ -175,7 +281,10 @@ __global__ void __launch_bounds__(T == 32 ? NORM_WARPS * 32 : T)
   }
   launch_next();
   if (a.normed == nullptr) return;
-  norm_row<T, VPT, RMS>(x, D4, a.inv_d, a.eps, red + 2 * (T / 32));
+  if (!norm_row<T, VPT, RMS>(x, D4, a.inv_d, a.eps, red + 2 * (T / 32))) {
+    large_row<T, RMS, POST>(a, row, true, red);
+    return;
+  }
   uint2* hrow = reinterpret_cast<uint2*>(a.normed) + row * D4;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {

@@ -112,7 +112,10 @@ h3_status h3_mod_norm_residual(float* resid, const void* delta, const float* gat
  *              tables whose groups are seg_stride floats apart, as
  *              h3_mod_norm_residual_seg
  * resid_out and normed overlap no input (but resid_out may be resid) and not each other.
- * D % 8 == 0, D <= 8192. Rows >= L of every tensor are left alone.
+ * D % 8 == 0, D <= 8192. Rows >= L of every tensor are left alone. A row of finite values has
+ * finite norms, also where the sums of its values or of their squares are beyond FP32's range;
+ * eps plus the mean of the squares should be no less than 2^-126, which eps sees to but where it
+ * is 0.
  */
 h3_status h3_sandwich_norm(const float* resid, const void* delta, float* resid_out, void* normed,
                            int post_norm, const float* post_gain, const float* gate,
