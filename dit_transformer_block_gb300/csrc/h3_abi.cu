@@ -83,6 +83,11 @@ const char* err_code_name(uint32_t c) {
     case ERR_WAIT_ATTN_MMA: return "attention MMA issuer";
     case ERR_WAIT_ATTN_SOFTMAX: return "attention softmax";
     case ERR_WAIT_PROBE: return "wait-timeout probe";
+    case ERR_WAIT_POOL_PRODUCER: return "block pooling TMA producer";
+    case ERR_WAIT_POOL_SUMS: return "block pooling sums";
+    case ERR_WAIT_SCORES_PRODUCER: return "block scores TMA producer";
+    case ERR_WAIT_SCORES_MMA: return "block scores MMA issuer";
+    case ERR_WAIT_SCORES_EPILOGUE: return "block scores epilogue";
     default: return "unknown";
   }
 }

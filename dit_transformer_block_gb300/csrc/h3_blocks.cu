@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1)
         const int row0 = id / s.pairs * s.block, head0 = id % s.pairs * 2;
         const int rows = min(s.block, s.L - row0), box = min(s.block, POOL_ROWS);
         for (int r = 0; r < rows; r += POOL_ROWS) {
-          ok = mbar_wait(bar(POOL_SLOTS + st), phase, err, ERR_WAIT_GEMM_PRODUCER);
+          ok = mbar_wait(bar(POOL_SLOTS + st), phase, err, ERR_WAIT_POOL_PRODUCER);
           if (!ok) break;
           mbar_arrive_expect_tx(bar(st), box * 2 * DHB * 2);
           for (int c = 0; c < 4; ++c)
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1)
     float acc[8] = {};
     for (int r0 = 0; r0 < rows; r0 += POOL_ROWS) {
       // (where a wait runs out, this one returns and so does every later one, soon)
-      mbar_wait(bar(st), phase, err, ERR_WAIT_GEMM_EPILOGUE);
+      mbar_wait(bar(st), phase, err, ERR_WAIT_POOL_SUMS);
       const uint8_t* x = smem + st * POOL_SLOT_BYTES + off;
       const int n = min(POOL_ROWS, rows - r0);
 #pragma unroll 8
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         score_tile(tile, z, h, t0, b0);
         const int qrow = h * z.nq + t0, krow = h / z.group * z.nk + b0;
         for (int c = 0; c < TC_STEPS; ++c) {
-          if (!(ok = mbar_wait(bar(BT_EMPTY + st), phase, err, ERR_WAIT_GEMM_PRODUCER))) break;
+          if (!(ok = mbar_wait(bar(BT_EMPTY + st), phase, err, ERR_WAIT_SCORES_PRODUCER))) break;
           const uint32_t full = bar(BT_FULL + st), dst = smem_u32(smem + st * TC_STAGE_BYTES);
           mbar_arrive_expect_tx(full, TC_STAGE_BYTES);
           tma_load_2d(dst, &tmQh, full, c * 32, qrow);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                (static_cast<uint32_t>(TC_TILE >> 4) << 24);
     const uint64_t base = sdesc_sw128(smem_u32(smem), 16, 1024);
     auto wait = [&](int b, uint32_t parity) {
-      return mbar_wait_warp(bar(b), parity, err, ERR_WAIT_GEMM_MMA);
+      return mbar_wait_warp(bar(b), parity, err, ERR_WAIT_SCORES_MMA);
     };
     int st = 0, n = 0;
     uint32_t phase = 0;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       score_tile(tile, z, h, t0, b0);
       const int acc = n & 1;
       if (!mbar_wait_warp(bar(BT_DONE + acc), static_cast<uint32_t>(n >> 1) & 1u, err,
-                          ERR_WAIT_GEMM_EPILOGUE))
+                          ERR_WAIT_SCORES_EPILOGUE))
         break;
       tc_fence_after();
       uint32_t v[4][32];

@@ -20,6 +20,11 @@ enum : uint32_t {
   ERR_WAIT_ATTN_MMA = 0x202,
   ERR_WAIT_ATTN_SOFTMAX = 0x203,
   ERR_WAIT_PROBE = 0x301,
+  ERR_WAIT_POOL_PRODUCER = 0x401,
+  ERR_WAIT_POOL_SUMS = 0x402,
+  ERR_WAIT_SCORES_PRODUCER = 0x501,
+  ERR_WAIT_SCORES_MMA = 0x502,
+  ERR_WAIT_SCORES_EPILOGUE = 0x503,
 };
 
 struct DevErr {
