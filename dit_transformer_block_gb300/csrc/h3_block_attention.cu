@@ -8,7 +8,10 @@
 // keys, or two of 64.
 //   * tensor memory: S (128 columns, the two query tiles in turn), O and P (bf16) of both;
 //     a softmax reads S into registers and frees it at once, so the other tile's Q K^T
-//     overlaps it, and P V reads P from tensor memory;
+//     overlaps it, and P V reads P from tensor memory. P has
+//     the 8 bits of V's type, since both operands of a product have one type: 0.0023 of the output's
+//     norm off 64 bits, of which its own rounding to bf16 is 0.0017. (P in two parts would be half
+//     as much tensor work again.) The sum that O is divided by is of the weights before rounding;
 //   * warps 0-3 / 4-7: softmax of query tile 0 / 1 (thread = row); warp 8: lists and TMA loads,
 //     keys and values in five 32 KB slots in the order in which they are used; warp 9:
 //     issues the products;
@@ -17,9 +20,10 @@
 // Where the (query block, head)s are fewer than the SMs, a cluster of CTAs shares a list
 // and joins its partial results through distributed shared memory, in rank order.
 // Bound by the products of bf16 and by the power they draw: 58,758 rows of 42 heads, 92 blocks of
-// 64 keys each, 7.4 TFLOP: 4.43 ms (1,680 TFLOP/s), 4.8 ms in a run of seconds. 22 rows of 40
-// heads, 23 blocks of 128: 13.2 us, of which the keys and values once are 4.6: seven or eight
-// tiles one after another, and the join.
+// 64 keys each, 7.4 TFLOP: 4.43 ms (1,680 TFLOP/s), 4.8 to 4.95 ms in a run of seconds. 1,896 rows,
+// 96 blocks, 336 items on 152 SMs: 218 us for 128 of products, three waves of which the last is a
+// fifth full. 22 rows of 40 heads, 23 blocks of 128: 12.7 us, of which the keys and values once are
+// 4.6: seven or eight tiles one after another, each with a whole tile's products, and the join.
 #include <algorithm>
 
 #include "h3_attn_common.cuh"

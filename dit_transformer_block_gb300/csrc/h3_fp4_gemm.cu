@@ -24,8 +24,9 @@
 // A CTA gets its operands at a rate that its copies in flight allow, so where there are few tiles
 // (few rows: the weights' bytes count) several pairs in a cluster share one tile's K. They put
 // their sums into shared memory and each adds up a share of the rows, in the order of K (22 x
-// 5,376 x 5,376 with weights in HBM: 10.4 us with the quantisation, of which the weights' 15 MB
-// take 2.3).
+// 5,376 x 5,376 with weights in HBM: 10.7 us with the quantisation; the product alone 8.7, 7.8 with
+// its weights in L2, where HBM would take 2.3 for their 15 MB. What the rest of it is has not been
+// found: a pair's seven stages are two rounds of loads).
 // 58,758 x 16,128 x 5,376: MX 1,436 us (7,100 TFLOP/s), NV 1,515 us (6,730). Products of K = 64 and
 // nothing else run at 9,220 TFLOP/s. With the loads beside them a stage takes 600 cycles instead
 // of 512 with five stages (686 with four, 857 with three, 605 with six), nearly the same where half
@@ -190,8 +191,8 @@ __device__ __forceinline__ void tile_coords4(int tile, const Gemm4Args& a, int& 
 }
 
 // bf16 SiLU(g) * u of two gates and two ups, rounded to bf16 first: g / (1 + 2^(-g log2 e)), the
-// exponential within 2^-22 of it and the reciprocal within 2^-23, which is flushed to 0 from
-// where the sum is above 2^126. (A tile's epilogue bounds products of few stages: 9,728 x 8,192 x
+// exponential within 2^-22 + 2^-23 |g| of it (its argument is a rounded product) and the reciprocal
+// within 2^-23, which is flushed to 0 from where the sum is above 2^126 (SiLU below 2^-119). (A tile's epilogue bounds products of few stages: 9,728 x 8,192 x
 // 256 54 us in MX and 74 in NV; 85 and 104 with __expf and __fdividef, which look after subnormal
 // operands, and each value rounded by itself; an IEEE division made a tile's epilogue 4 us
 // longer.)

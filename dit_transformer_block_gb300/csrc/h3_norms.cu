@@ -4,12 +4,12 @@
 // Per row: p = n(delta) * post_gain, r = resid_scale * resid + gate * p, h = n(r) * pre_gain * (1
 // + scale) + shift, with n a LayerNorm without affine or a division by the root mean square.
 // Everything between the loads and the stores is FP32, and the mean is taken before the squares
-// (two passes over registers), so a row far from zero loses what the rounding of its mean is
-// (some 2^-24 |mean|, off every value) and not the square of that. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out (58,758 rows of 5,376, 3.79 GB: LayerNorm 591 us, 6.4 TB/s, RMS 545
-// us, 7.0 TB/s; 22 rows: 3.9 us, the latency of a load, of two or four sums over the CTA and of a
-// launch). Launched like an ordinary kernel, since its loads of vectors that all rows share take
-// the read-only path: without it, and launched ahead of the end of the kernel before it,
-// LayerNorm took 665 us.
+// (two passes over registers), so a row far from zero loses a few units of 2^-24 |mean|, off
+// every value, and not of |mean|^2. Bound by HBM: 4 + 2 bytes per element in, 4 + 2 out (58,758
+// rows of 5,376, 3.79 GB: LayerNorm 593 us, 6.4 TB/s, RMS 543 us, 7.0 TB/s; 22 rows: 3.6 us, the
+// latency of a load, of two or four sums over the CTA and of a launch). Launched like an ordinary
+// kernel, since its loads of vectors that all rows share take the read-only path: without it, and
+// launched ahead of the end of the kernel before it, LayerNorm took 665 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -23,10 +23,12 @@ capture of the second launch ends within a minute or two:
               heads on 8), and 512 rows of 256 keys (32 heads on 8)
   norms       norms around a gated branch, 16384 x 5376
   fp4         4-bit rows: quantisation of 16384 x 5376 (both formats), the QKV
-              projection shape with M = 8192 (both), SwiGLU M = 4096, F = 14336, and
-              16 rows of the QKV shape (few tiles, K shared)
+              projection shape with M = 8192 (both), SwiGLU M = 4096, F = 14336,
+              16 rows of the QKV shape (63 tiles, a pair of CTAs each), and 22 rows of
+              the output projection (21 tiles, three pairs each)
   blocks      16384 rows of 42 heads: scores of key blocks of 64, selection of 56
-              per query block, attention over them
+              per query block, attention over them; and selection of 92 of 919
+              blocks in 9660 rows
 """
 from __future__ import annotations
 
@@ -158,6 +160,7 @@ def main(argv):
             product(8192, 16128, 5376, form)
         product(4096, 14336, 5376, "mx", swiglu=True)
         product(16, 16128, 5376, "nv")
+        product(22, 5376, 5376, "mx")
     if "blocks" in which:
         S, H, most = 16384, 42, 56
         qb, kb, vb = rnd(S, H, 128), rnd(S, H, 128), rnd(S, H, 128)
@@ -170,6 +173,10 @@ def main(argv):
         runs.append(lambda: h3.block_scores(qb, kb, sc, wsb, k_block=64))
         runs.append(lambda: h3.block_select(sc, ids, counts, keep_first=1, keep_last=1))
         runs.append(lambda: h3.attention_blocks(qb, kb, vb, ob, ids, counts, k_block=64))
+        many = torch.randn(9660, 919, generator=g, device=dev)
+        many_ids = torch.empty(9660, 92, dtype=torch.int32, device=dev)
+        many_counts = torch.empty(9660, dtype=torch.int32, device=dev)
+        runs.append(lambda: h3.block_select(many, many_ids, many_counts, keep_first=1, keep_last=1))
     torch.cuda.synchronize()
     for _ in range(2):
         for fn in runs:

@@ -251,12 +251,15 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
  * Attention over chosen key blocks (next step beside Skip-Softmax: block-sparse video
  * attention, a coarse score of pooled blocks choosing the fine blocks of every query
  * block). Query rows are taken in blocks of H3_QUERY_BLOCK rows from row 0, keys in blocks
- * of k_block (64 or 128) rows from row 0; the last block of each may be short. With
+ * of k_block (64 or 128) rows from row 0; the last block of each may be short. (A model that was
+ * trained with a list for every 64 query rows does not fit: four of its lists would have to be
+ * made one.) With
  * nq = ceil(Lq / H3_QUERY_BLOCK) and nk = ceil(Lk / k_block):
  *
  * h3_block_scores: scores[h, t, b] = softmax_scale * mean(q rows of block t, head h)
  *   . mean(k rows of block b, head h / (H / Hkv)), the means in FP32, their products with at
- *   most 2^-20 of the sum of the products' magnitudes beside what FP32 sums have.
+ *   most 2^-20 of the sum of the products' magnitudes beside what FP32 sums have (that with more
+ *   than eight query blocks only: scores that are nearly equal may change places with Lq).
  *   q       [Lq, H, Dh] bf16, row stride ld_q elements; k [Lk, Hkv, Dh], ld_k
  *   scores  [H, nq, nk] float32
  *   workspace  device memory of h3_block_scores_workspace_bytes(...) bytes, 256-byte
@@ -286,8 +289,9 @@ h3_status h3_attention_fp8_skip(const void* qc, const void* kc, const void* vc, 
  * rows is beyond FP32's range; its scores are infinite, or NaN where it meets a 0, a NaN or an
  * infinity of the other sign.
  *
- * Dh == 128, H a multiple of Hkv, at most 65,535. A call with Lq or Lk 0: no scores and
- * nothing done; h3_attention_blocks with Lk 0 writes zeros. max_blocks >= 1, rows * max_blocks
+ * Dh == 128, H a multiple of Hkv, at most 65,535. h3_block_scores with Lq or Lk 0 and
+ * h3_block_select with rows or nk 0 do nothing (ids and counts stay as they were);
+ * h3_attention_blocks with Lk 0 writes zeros and reads no list. max_blocks >= 1, rows * max_blocks
  * and rows * nk below 2^31 (rows = H * nq), nq and nk at most 2^20; in h3_attention_blocks
  * max_blocks * k_block at most 2^17.
  */
@@ -668,7 +672,8 @@ h3_status h3_quantize_fp4_rows(const void* x, int64_t ld_x, void* codes, void* s
 /*
  * y[i, j] = bf16( rx[i] * rw[j] * sum over K of value(x)[i,:] * value(w)[j,:] / (rx[i] * rw[j]) )
  * for i < L: a projection of 4-bit rows on tcgen05 (block-scaled products, FP32
- * accumulation); rx and rw are the row scales (1 in H3_FP4_MX, where they are NULL).
+ * accumulation); rx and rw are the row scales (1 in H3_FP4_MX, where they are NULL), applied to
+ * the sum one after the other, rx first, in FP32.
  *   x_codes [S, K / 2], x_scales, rx [S]; w_codes [N, K / 2], w_scales, rw [N]; y [S, N] bf16
  *   K % 32 == 0, K <= 16384, N % 8 == 0; both operands in the same format; codes, y and rw
  *   16-byte, scales 128-byte aligned; y overlaps nothing.
@@ -679,8 +684,9 @@ h3_status h3_linear_fp4(const void* x_codes, const void* x_scales, const float* 
 
 /* 4-bit gate/up projection with SwiGLU in the epilogue: as h3_linear_swiglu with 4-bit
  * operands (w_gu [2F, K], rows [gate | up]); the two products are scaled and rounded to bf16
- * before the SiLU, whose division is within 2 units of the last place of FP32 (h3_swiglu
- * divides exactly, so a value may round to the neighbouring bf16). F % 128 == 0, K % 32 == 0. */
+ * before the SiLU, g / (1 + exp(-g)), which is within 2^-20 + 2^-23 |g| of itself (h3_swiglu
+ * divides exactly, so a value may round to the neighbouring bf16), and 0 where exp(-g) passes
+ * 2^126, from g = -87.3 down, where its magnitude is below 2^-119. F % 128 == 0, K % 32 == 0. */
 h3_status h3_linear_swiglu_fp4(const void* x_codes, const void* x_scales, const float* rx,
                                const void* w_codes, const void* w_scales, const float* rw,
                                void* out, int S, int L, int F, int K, int format,
