@@ -924,12 +924,11 @@ def block_scores(q, k, scores, workspace, k_block=64, scale=None, stream=None):
     ldq, H = _heads(q, "q", Lq, dev)
     ldk, Hkv = _heads(k, "k", Lk, dev)
     ps = _tensor(scores, "scores", _F32, _block_shape(Lq, Lk, H, k_block), dev)
-    if workspace.get_device() != dev:
-        _on(workspace, "workspace", dev)
+    _flat(workspace, "workspace", workspace.dtype, dev)
     status = (_lib or lib()).h3_block_scores(
         q.data_ptr(), ldq, k.data_ptr(), ldk, ps, Lq, Lk, H, Hkv, 128, k_block,
-        128 ** -0.5 if scale is None else scale, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+        128 ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(stream, dev))
     if status:
         _check("block_scores", status)
 
