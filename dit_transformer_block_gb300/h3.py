@@ -788,6 +788,12 @@ def sandwich_norm(resid, delta=None, normed=None, resid_out=None, post_norm=True
 FP4_FORMATS = {"mx": 0, "nv": 1}
 
 
+def _fp4_format(format) -> int:
+    if format not in FP4_FORMATS:
+        raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
+    return FP4_FORMATS[format]
+
+
 class Fp4Rows:
     """A matrix [R, K] of 4-bit rows: codes [R, K/2] uint8, scales (bytes, in the library's
     tiles), row_scale [R] f32 ("nv") or None ("mx"). fp4_rows makes room for one."""
@@ -795,8 +801,7 @@ class Fp4Rows:
                  "number")
 
     def __init__(self, codes, scales, row_scale, format):
-        if format not in FP4_FORMATS:
-            raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
+        number = _fp4_format(format)
         dev = codes.get_device()
         _flat(codes, "codes", torch.uint8, dev)
         _flat(scales, "scales", torch.uint8, dev)
@@ -813,14 +818,14 @@ class Fp4Rows:
             if row_scale.shape != (self.R,):
                 raise ValueError(f"row_scale must be [{self.R}], got {list(row_scale.shape)}")
         self.codes, self.scales, self.row_scale = codes, scales, row_scale
-        self.format, self.number, self.device = format, FP4_FORMATS[format], dev
+        self.format, self.number, self.device = format, number, dev
         self.shape = (self.R, self.K)
         self.pointers = (codes.data_ptr(), scales.data_ptr(),
                          None if row_scale is None else row_scale.data_ptr())
 
 
 def fp4_scale_bytes(R: int, K: int, format: str = "nv") -> int:
-    n = lib().h3_fp4_scale_bytes(R, K, FP4_FORMATS[format])
+    n = lib().h3_fp4_scale_bytes(R, K, _fp4_format(format))
     if n == 0:
         raise H3Error("fp4_scale_bytes", 1, last_error())
     return n
@@ -831,8 +836,6 @@ def fp4_rows(R: int, K: int, format: str = "nv", device=None) -> Fp4Rows:
     share an E4M3 scale, a row an FP32 one) or "mx" (32 share a power of two). The scales are
     zeros, so that a program which fills in packed weights itself need not clear the places
     past a row's last block, which a product reads where K is no multiple of 64."""
-    if format not in FP4_FORMATS:
-        raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
     device = torch.device("cuda") if device is None else device
     n = fp4_scale_bytes(R, K, format)
     return Fp4Rows(torch.empty(R, K // 2, dtype=torch.uint8, device=device),

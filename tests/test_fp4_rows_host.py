@@ -21,3 +21,12 @@ def test_scales_begin_as_zeros(monkeypatch, fmt, R, K):
     finally:
         torch.use_deterministic_algorithms(was)
     assert (scales == 0).all() and scales.numel() == h3.fp4_scale_bytes(R, K, fmt)
+
+
+@pytest.mark.parametrize("format", ["int4", "", None, 1])
+def test_a_format_that_is_none_is_refused(format):
+    build.build()
+    for call in (lambda: h3.fp4_scale_bytes(4, 64, format), lambda: h3.fp4_rows(4, 64, format=format, device="cpu"),
+                 lambda: h3.Fp4Rows(torch.empty(4, 32, dtype=torch.uint8), torch.empty(512, dtype=torch.uint8), None, format)):
+        with pytest.raises(ValueError, match="format must be one of"):
+            call()
